@@ -385,6 +385,145 @@ int fl_moe_int4g_ptrs(const void* x, const float* logits, int M, int H, int E, i
                       int32_t* expert_offsets, int32_t* perm,
                       void* ws, size_t ws_bytes, fl_stream_t stream);
 
+/* ------------------------------------- decoder-layer operators: norm */
+
+/* Root-mean-square norm with the residual's addition and an optional output
+ * in 8 bits.  Not on the FastLLM pages: the pieces of a decoder layer around
+ * the int4g linears.  For each of M * heads rows of H elements:
+ *   s = x + residual (fp32; residual NULL: s = x),  residual_out = bf16(s),
+ *   n_i = s_i / sqrt(mean_j s_j^2 + eps) * weight_i   (fp32),
+ *   y = bf16(n),
+ *   codes, scales: for each run of `group` columns (group 0: the whole row)
+ *   scale = max|n| / 448 and code_i = e4m3(n_i / scale), nearest even (a run
+ *   of zeros: scale 0, codes 0).
+ *   x, residual, y, residual_out  bf16; row (m, h) starts at
+ *           m * stride + h * H elements, stride >= heads * H
+ *   weight  bf16 [H], or NULL for ones
+ *   codes   uint8 [M, heads, H] e4m3 bits, or NULL
+ *   scales  fp32 [M, heads, H / group] (group 0: [M, heads])
+ * y and codes may each be NULL, not both; residual_out NULL: not stored.
+ * In place is allowed: y or residual_out may be x or residual (the same
+ * pointer and stride).  heads > 1 norms each head of a projection by itself.
+ * group is 0, 64, 128 or 256 (H % group == 0); 1 <= H <= 32768.  Rows whose
+ * pointers are 16-byte aligned with H and the strides multiples of 8 are read
+ * 16 bytes at a time, others element by element.  Pointers need only their
+ * elements' alignment.  A row with infinities or NaN gives NaN. */
+int fl_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const void* weight,
+               float eps, int M, int heads, int H, void* y, int64_t y_stride, void* residual_out,
+               int64_t residual_out_stride, void* codes, float* scales, int group, fl_stream_t stream);
+
+/* ------------------------------------- decoder-layer operators: rotary */
+
+#define FL_ROPE_HALVES 0   /* pair i is elements i and i + rot/2 */
+#define FL_ROPE_PAIRS  1   /* pair i is elements 2i and 2i + 1 */
+#define FL_ROPE_MAX_AXES 4
+
+/* Rotary positions with up to FL_ROPE_MAX_AXES axes (time, height, width, ...)
+ * for queries and keys in one launch: pair i of every head of token t turns
+ * by the angle positions[a][t] * inv_freq[i], a = the axis of pair i; the
+ * elements from `rot` on are copied.
+ *   q, q_out  bf16 [T, Hq, D] with token strides in elements
+ *   k, k_out  bf16 [T, Hk, D] likewise (Hk 0: none)
+ *   positions int32 [n_axes, T] device (any sign: a negated position is the
+ *             inverse rotation, which is also the gradient's)
+ *   inv_freq  fp64 [rot/2] device, radians a position
+ *   sections  int32 [n_axes] HOST: how many consecutive pairs turn by each
+ *             axis, their sum rot/2; NULL with one axis
+ * In place is allowed (q_out = q, k_out = k with the same strides).  Angles are
+ * reduced to one turn in 64-bit integers, so far positions lose nothing.
+ * rot even, 2 <= rot <= D <= 1024; T >= 1.  Heads whose D and rot / 2 are
+ * multiples of 8, with 16-byte aligned pointers and strides of multiples of 8,
+ * move 16 bytes at a time, others element by element. */
+int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, int64_t k_stride, int Hk, int T, int D, int rot,
+            int style, const int32_t* positions, int n_axes, const int32_t* sections, const double* inv_freq,
+            void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, fl_stream_t stream);
+
+/* ------------------------- decoder-layer operators: 8-bit key/value cache */
+
+#define FL_KV8_E4M3 0   /* codes are e4m3 */
+#define FL_KV8_INT8 1   /* codes are signed 8-bit integers */
+
+/* The cache: keys and values as 8-bit codes in blocks of `block` tokens, each
+ * (block, kv head) with one fp32 scale for its keys and one for its values;
+ * value = code * scale.
+ *   k, v              uint8 [num_blocks, kv_heads, block, head_dim] device
+ *   k_scale, v_scale  fp32  [num_blocks, kv_heads] device, positive
+ * block is 16, 32, 64 or 128; head_dim 64 or 128; num_blocks * kv_heads *
+ * block < 2^31; at most 2^30 tokens a sequence and 2^29 rows a call.  A block need not be initialised before its first write. */
+typedef struct fl_kv8_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks;
+  int block;
+  int kv_heads;
+  int head_dim;
+  int format;               /* FL_KV8_E4M3 or FL_KV8_INT8 */
+} fl_kv8_cache;
+
+/* The sequences of one call: T query (new) tokens, those of sequence b being
+ * rows cu_q[b] .. cu_q[b+1]-1, the LAST tokens of its kv_lens[b] tokens; token
+ * j of sequence b lives in slot j % block of block block_table[b][j / block].
+ *   cu_q        int32 [B+1] device, or NULL: every sequence has T / B rows
+ *   kv_lens     int32 [B] device, lengths with the new tokens
+ *   block_table int32 [B, max_blocks] device
+ *   max_q       the largest number of rows of a sequence (an upper bound)
+ * A sequence may have no rows; kv_lens[b] below its number of rows is allowed:
+ * the first rows then have negative positions (they are not written and see
+ * no key). */
+typedef struct fl_kv8_seqs {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int T;
+  int B;
+  int max_q;
+  int max_blocks;
+} fl_kv8_seqs;
+
+/* Writes the new tokens' keys and values (bf16 [T, kv_heads, head_dim], token
+ * strides in elements, multiples of 8) into the cache.  Per (block, kv head),
+ * keys and values apart: the scale is the least power of two, 2^-126 or more,
+ * that brings the largest magnitude of the tokens the block holds to 448
+ * (e4m3) or 127 (int8) or less, code = nearest even of x / scale.  A block
+ * that holds earlier tokens of the sequence keeps its scale or raises it;
+ * their codes are then rounded again to the new scale.  Powers of two make
+ * the division exact, and raising a scale rounds e4m3 codes only where they
+ * leave the normal range.
+ * An infinity is stored as the largest code, a NaN as 0; either records
+ * FL_ERR_RANGE, a block number outside the cache (not written)
+ * FL_ERR_DEVICE_CHECK, in the 16-byte device status block `status`
+ * (zero-filled before first use; a workspace will do).  A block that two
+ * sequences share must not be written by both in one call. */
+int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const fl_kv8_cache* cache,
+                  const fl_kv8_seqs* seqs, void* status, fl_stream_t stream);
+
+/* Test hook: what the cache kernels make of sequence b, computed on the host
+ * from lists in HOST memory (the same clamping code).  out[0..8] receives its
+ * first row, rows and length as clamped to the arrays; then for the write and
+ * for the attention with `window` the first page, the pages, and how many of
+ * them name no block of the cache.  FL_ERR_ARG for a bad argument. */
+int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int block, int window, int b, long long* out);
+
+/* Workspace bytes needed by fl_kv8_attention. */
+int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out);
+
+/* Attention of the T query rows over the cache.  Row i of sequence b and
+ * query head h reads kv head h / (Hq / kv_heads) and the tokens j <=
+ * p = kv_lens[b] - rows[b] + i, with window > 0 only those j > p - window:
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum exp s_j
+ * fp32 softmax and accumulation; a row with no token gives out 0, lse -inf.
+ *   q    bf16 [T, Hq, head_dim], out likewise (token strides in elements,
+ *        multiples of 8; out must not overlap q)
+ *   lse  fp32 [T, Hq] natural logarithm, or NULL
+ * Hq % kv_heads == 0.  Results do not depend on timing: partial sums are
+ * joined in a fixed order.  A block number outside the cache is not read:
+ * FL_ERR_DEVICE_CHECK in the workspace's status block, its rows undefined. */
+int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const fl_kv8_cache* cache, const fl_kv8_seqs* seqs,
+                     float scale, int window, void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+                     fl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

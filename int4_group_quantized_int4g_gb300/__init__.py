@@ -23,21 +23,42 @@ __all__ = [
     "fl_moe_int4g_workspace", "fl_moe_int4g", "fl_moe_int4g_ptrs", "FlMoeRouting", "fl_int4g_mlp_workspace",
     "fl_moe_router_logits_workspace", "fl_moe_router_logits",
     "fl_int4g_mlp", "fl_int4g_mlp_fused",
+    "FL_KV8_E4M3", "FL_KV8_INT8", "FlKv8Cache", "FlKv8Seqs",
+    "fl_rmsnorm", "fl_rope", "fl_kv8_append", "fl_kv8_attention_workspace", "fl_kv8_attention",
+    "fl_kv8_test_pages",
 ]
 
 GROUP = 128
 FL_SOFTMAX = 0
 FL_SIGMOID = 1
+FL_ROPE_HALVES = 0
+FL_ROPE_PAIRS = 1
+FL_KV8_E4M3 = 0
+FL_KV8_INT8 = 1
 
 _c_size_p = ctypes.POINTER(ctypes.c_size_t)
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_l = ctypes.c_int64
 
 
 class FlMoeRouting(ctypes.Structure):
     """struct fl_moe_routing (routing options of fl_moe_int4g_ex)."""
     _fields_ = [("scoring", ctypes.c_int), ("renorm", ctypes.c_int), ("score_bias", ctypes.c_void_p),
                 ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int), ("routed_scale", ctypes.c_float)]
+
+
+class FlKv8Cache(ctypes.Structure):
+    """struct fl_kv8_cache (the 8-bit key/value cache)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int), ("block", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("format", ctypes.c_int)]
+
+
+class FlKv8Seqs(ctypes.Structure):
+    """struct fl_kv8_seqs (the sequences of one call)."""
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("T", ctypes.c_int), ("B", ctypes.c_int), ("max_q", ctypes.c_int), ("max_blocks", ctypes.c_int)]
 
 
 # C signatures: name -> (restype, argtypes)
@@ -70,6 +91,14 @@ SIGNATURES = {
                              _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "fl_moe_int4g_ptrs": (_i, [_vp, _vp, _i, _i, _i, _i, _i, ctypes.POINTER(FlMoeRouting), _vp, _vp, _vp, _vp,
                                _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fl_rmsnorm": (_i, [_vp, _l, _vp, _l, _vp, ctypes.c_float, _i, _i, _i, _vp, _l, _vp, _l, _vp, _vp, _i, _vp]),
+    "fl_rope": (_i, [_vp, _l, _i, _vp, _l, _i, _i, _i, _i, _i, _vp, _i, ctypes.POINTER(ctypes.c_int32), _vp,
+                     _vp, _l, _vp, _l, _vp]),
+    "fl_kv8_append": (_i, [_vp, _l, _vp, _l, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), _vp, _vp]),
+    "fl_kv8_test_pages": (_i, [ctypes.POINTER(FlKv8Seqs), _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
+    "fl_kv8_attention_workspace": (_i, [_i, _i, _i, _i, _i, _c_size_p]),
+    "fl_kv8_attention": (_i, [_vp, _l, _i, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), ctypes.c_float, _i,
+                              _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _LIB = None
@@ -383,3 +412,194 @@ def fl_moe_router_logits(x, w_router, logits=None, ws=None):
     _check("fl_moe_router_logits", lib().fl_moe_router_logits(_p(x), M, H, _p(w_router), E, _p(logits), _p(ws),
                                                                ws.numel(), _stream()))
     return logits
+
+
+# ------------------------------------------------- decoder-layer operators
+
+def _tokens(t, name):
+    """(pointer, token stride) of bf16 [tokens, heads, width] whose heads are
+    packed; the tokens may be rows of a wider projection."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype is not _torch().bfloat16:
+        raise ValueError(f"{name}: expected bfloat16, got {t.dtype}")
+    n, h, w = t.shape
+    st = t.stride()
+    if (w > 1 and st[2] != 1) or (h > 1 and st[1] != w):
+        raise ValueError(f"{name}: the heads of a token must be packed")
+    return t.data_ptr(), st[0] if n > 1 else h * w   # (the stride of a single token means nothing)
+
+
+def _typed(t, dtype, name):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    return _p(t)
+
+
+def fl_rmsnorm(x, weight=None, eps=1e-6, residual=None, y=None, residual_out=None, out8=False, group=0, need_y=True):
+    """RMS norm of bf16 x [M, H] or [M, heads, H] (each row of H by itself) with
+    the residual's addition.  Returns a dict: "y" (bf16, unless need_y is
+    False), "residual" (bf16(x + residual), with a residual), and with out8
+    "codes" (uint8, e4m3 bits) and "scales" (fp32 [..., H / group], or [..., 1]
+    for group 0).  y and residual_out may be given, and may be x or residual."""
+    torch = _torch()
+    shape = x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("fl_rmsnorm: x is [M, H] or [M, heads, H]")
+
+    def rows(t, name):
+        if t.shape != shape:
+            raise ValueError(f"fl_rmsnorm: {name} and x differ in shape")
+        return _tokens(t if len(shape) == 3 else t.unsqueeze(1), name)
+
+    M, heads, H = shape if len(shape) == 3 else (shape[0], 1, shape[1])
+    xp, xs = rows(x, "x")
+    rp, rs = rows(residual, "residual") if residual is not None else (None, 0)
+    out = {}
+    if y is None and need_y:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    yp, ys = rows(y, "y") if y is not None else (None, 0)
+    op, os_ = rows(residual_out, "residual_out") if residual_out is not None else (None, 0)
+    if y is not None:
+        out["y"] = y
+    if residual_out is not None:
+        out["residual"] = residual_out
+    cp = sp = None
+    if out8:
+        out["codes"] = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        out["scales"] = torch.empty((*shape[:-1], H // group if group else 1), dtype=torch.float32, device=x.device)
+        cp, sp = out["codes"].data_ptr(), out["scales"].data_ptr()
+    if weight is not None and weight.numel() != H:
+        raise ValueError("fl_rmsnorm: weight is [H]")
+    wp = _typed(weight, torch.bfloat16, "weight") if weight is not None else None
+    _check("fl_rmsnorm", lib().fl_rmsnorm(xp, xs, rp, rs, wp, eps, M, heads, H, yp, ys, op, os_, cp, sp,
+                                          group if out8 else 0, _stream()))
+    return out
+
+
+def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k_out=None):
+    """Rotary positions of bf16 q [T, Hq, D] and k [T, Hk, D] (or None).
+    positions: int32 [T] or [n_axes, T]; inv_freq: float64 [rot / 2]; sections:
+    with several axes, how many consecutive pairs turn by each.  halves: pair i
+    is elements i and i + rot / 2, else 2i and 2i + 1.  Returns (q_out, k_out);
+    they may be q and k themselves."""
+    torch = _torch()
+    T, Hq, D = q.shape
+    qp, qs = _tokens(q, "q")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    qop, qos = _tokens(q_out, "q_out")
+    kp, ks, kop, kos, Hk = None, 0, None, 0, 0
+    if k is not None:
+        Hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("fl_rope: q and k differ in tokens or width")
+        kp, ks = _tokens(k, "k")
+        if k_out is None:
+            k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+        if k_out.shape != k.shape:
+            raise ValueError("fl_rope: k_out and k differ in shape")
+        kop, kos = _tokens(k_out, "k_out")
+    if q_out.shape != q.shape:
+        raise ValueError("fl_rope: q_out and q differ in shape")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if positions.shape[-1] != T or (sections is not None and len(sections) != axes):
+        raise ValueError("fl_rope: positions are [n_axes, T], sections [n_axes]")
+    sec = (ctypes.c_int32 * axes)(*sections) if sections is not None else None
+    _check("fl_rope", lib().fl_rope(qp, qs, Hq, kp, ks, Hk, T, D, 2 * inv_freq.numel(),
+                                    FL_ROPE_HALVES if halves else FL_ROPE_PAIRS,
+                                    _typed(positions, torch.int32, "positions"), axes, sec,
+                                    _typed(inv_freq, torch.float64, "inv_freq"), qop, qos, kop, kos, _stream()))
+    return q_out, k_out
+
+
+def _kv8(where, T, heads, dim, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt):
+    """The two structures of a cache call, from its tensors."""
+    torch = _torch()
+    nb, hk, block, d = k_cache.shape
+    B = kv_lens.shape[0]
+    if v_cache.shape != k_cache.shape or k_scale.shape != (nb, hk) or v_scale.shape != (nb, hk):
+        raise ValueError(f"{where}: the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
+    if d != dim or (heads is not None and heads != hk):
+        raise ValueError(f"{where}: the tokens and the cache differ in heads or width")
+    if block_table.dim() != 2 or block_table.shape[0] != B or (cu_q is not None and cu_q.shape != (B + 1,)):
+        raise ValueError(f"{where}: block_table is [B, max_blocks], kv_lens [B], cu_q [B + 1]")
+    if max_q is None:
+        max_q = T // B if cu_q is None else T
+    c = FlKv8Cache(_typed(k_cache, torch.uint8, "k_cache"), _typed(v_cache, torch.uint8, "v_cache"),
+                   _typed(k_scale, torch.float32, "k_scale"), _typed(v_scale, torch.float32, "v_scale"),
+                   nb, block, hk, d, fmt)
+    s = FlKv8Seqs(_typed(cu_q, torch.int32, "cu_q") if cu_q is not None else None,
+                  _typed(kv_lens, torch.int32, "kv_lens"), _typed(block_table, torch.int32, "block_table"),
+                  T, B, max_q, block_table.shape[1])
+    return c, s
+
+
+def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q=None, max_q=None,
+                  fmt=FL_KV8_E4M3, status=None):
+    """Writes bf16 k, v [T, kv_heads, head_dim] into the 8-bit cache (uint8
+    [blocks, kv_heads, block, head_dim], scales fp32 [blocks, kv_heads]).
+    Sequence b's rows cu_q[b] .. cu_q[b+1]-1 (None: T / B each) are the last of
+    its kv_lens[b] tokens; token j lives in block block_table[b][j // block].
+    status: the status block to record device-side errors in (an int32 or uint8
+    CUDA tensor of 16 bytes or a workspace; None: this stream's workspace)."""
+    T, h, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("fl_kv8_append: k and v differ in shape")
+    kp, ks = _tokens(k, "k")
+    vp, vs = _tokens(v, "v")
+    c, s = _kv8("fl_kv8_append", T, h, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
+    if status is None:
+        status = _workspace(256, k.device)
+    _check("fl_kv8_append", lib().fl_kv8_append(kp, ks, vp, vs, ctypes.byref(c), ctypes.byref(s), _p(status), _stream()))
+
+
+def fl_kv8_test_pages(kv_lens, table, T, num_blocks, block, b, cu_q=None, max_q=None, window=0):
+    """Test hook: what the cache kernels make of sequence b, from Python lists
+    and without a GPU: a dict of start, rows, kv, write and read, the last two
+    (first page, pages, pages without a block)."""
+    def arr(v):
+        return (ctypes.c_int32 * max(1, len(v)))(*v)
+    B, flat = len(kv_lens), [i for row in table for i in row]
+    lens, tab, cu = arr(kv_lens), arr(flat), arr(cu_q) if cu_q is not None else None
+
+    def at(a):
+        return ctypes.cast(a, ctypes.c_void_p) if a is not None else None
+    s = FlKv8Seqs(at(cu), at(lens), at(tab), T, B, T if max_q is None else max_q, len(table[0]))
+    out = (ctypes.c_longlong * 9)()
+    _check("fl_kv8_test_pages", lib().fl_kv8_test_pages(ctypes.byref(s), num_blocks, block, window, b, out))
+    return {"start": out[0], "rows": out[1], "kv": out[2], "write": tuple(out[3:6]), "read": tuple(out[6:9])}
+
+
+def fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim):
+    out = ctypes.c_size_t(0)
+    _check("fl_kv8_attention_workspace",
+           lib().fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim, ctypes.byref(out)))
+    return out.value
+
+
+def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q=None, max_q=None,
+                     fmt=FL_KV8_E4M3, scale=None, window=0, out=None, return_lse=False, ws=None):
+    """Attention of bf16 q [T, Hq, head_dim] over the 8-bit cache (tensors as
+    for fl_kv8_append; kv_lens count the tokens already written, the rows of q
+    among them).  Row i of a sequence sees the tokens up to its own position,
+    with window > 0 only the last `window`.  scale: 1 / sqrt(head_dim) by
+    default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32)."""
+    torch = _torch()
+    T, Hq, d = q.shape
+    qp, qs = _tokens(q, "q")
+    c, s = _kv8("fl_kv8_attention", T, None, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("fl_kv8_attention: out and q differ in shape")
+    op, os_ = _tokens(out, "out")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    if ws is None:
+        ws = _workspace(fl_kv8_attention_workspace(T, s.B, Hq, c.kv_heads, d), q.device)
+    _check("fl_kv8_attention",
+           lib().fl_kv8_attention(qp, qs, Hq, ctypes.byref(c), ctypes.byref(s), d ** -0.5 if scale is None else scale,
+                                  window, op, os_, lse.data_ptr() if return_lse else None, _p(ws), ws.numel(), _stream()))
+    return (out, lse) if return_lse else out

@@ -1,0 +1,121 @@
+// Shared pieces of the 8-bit key/value cache: its sequences, its codes.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "fl_common.cuh"
+
+namespace flkv {
+
+using namespace fl;
+
+// Device view of fl_kv8_seqs.  The lists are read with every bound checked,
+// so that no content of theirs can lead outside the arrays.
+struct Seqs {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* table;
+  int T, B, max_q, max_blocks;
+};
+
+// Query rows [start, start + n) of sequence b and its cache length, clamped
+// to the arrays.
+struct SeqInfo {
+  int start, n, kv;
+};
+__host__ __device__ __forceinline__ SeqInfo seq_info(const Seqs& s, int b, int block) {
+  SeqInfo r;
+  if (s.cu_q) {
+    r.start = min(max(s.cu_q[b], 0), s.T);
+    r.n = min(max(s.cu_q[b + 1], r.start), s.T) - r.start;
+  } else {
+    r.n = s.T / s.B;
+    r.start = b * r.n;
+  }
+  r.n = min(r.n, s.max_q);
+  r.kv = min(max(s.kv_lens[b], 0), s.max_blocks * block);
+  return r;
+}
+
+// The cache block of page pg of sequence b, or -1 where the table has no entry
+// or names a block that the cache has not.
+__host__ __device__ __forceinline__ int page_block(const Seqs& s, int b, int pg, int num_blocks) {
+  if (pg < 0 || pg >= s.max_blocks) return -1;
+  const int id = s.table[static_cast<int64_t>(b) * s.max_blocks + pg];
+  return id >= 0 && id < num_blocks ? id : -1;
+}
+
+// Pages [first, first + n) of a sequence that its new tokens are written to.
+struct PageRun {
+  int first, n;
+};
+__host__ __device__ __forceinline__ PageRun written_pages(const SeqInfo& q, int block) {
+  const int p0 = max(q.kv - q.n, 0);
+  return q.kv > p0 ? PageRun{p0 / block, (q.kv - 1) / block - p0 / block + 1} : PageRun{0, 0};
+}
+// The first token that any row sees, and the pages with a token that one sees.
+__host__ __device__ __forceinline__ int first_seen(const SeqInfo& q, int window) {
+  return window ? max(0, q.kv - q.n + 1 - window) : 0;
+}
+__host__ __device__ __forceinline__ PageRun read_pages(const SeqInfo& q, int block, int window) {
+  const int first = first_seen(q, window) / block;
+  return PageRun{first, (q.kv + block - 1) / block - first};
+}
+
+// ------------------------------------------------------------------ codes
+// Two 8-bit codes (the low 16 bits, or with HI the high 16) as an f16 pair.
+// Both formats are exact in f16.
+template <int FMT, bool HI>
+__device__ __forceinline__ uint32_t code_pair_f16(uint32_t w) {
+  if constexpr (FMT == FL_KV8_E4M3) {
+    uint32_t d;
+    const uint16_t h = static_cast<uint16_t>(HI ? w >> 16 : w);
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(h));
+    return d;
+  } else {
+    // w holds code + 128 in every byte: f16 1024 + u has u in its last byte
+    const uint32_t u = __byte_perm(w, 0x64646464u, HI ? 0x4342u : 0x4140u);
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));  // 1152
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+// What code_pair_f16 wants: the raw codes, or for integers code + 128.
+template <int FMT>
+__device__ __forceinline__ uint32_t bias_codes(uint32_t w) {
+  return FMT == FL_KV8_E4M3 ? w : w ^ 0x80808080u;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+}  // namespace flkv
+
+namespace flh {
+
+// Arguments that fl_kv8_append and fl_kv8_attention share.
+inline int kv8_check(const fl_kv8_cache* c, const fl_kv8_seqs* s) {
+  if (!c || !s || !c->k || !c->v || !c->k_scale || !c->v_scale || !s->kv_lens || !s->block_table) return FL_ERR_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(s->cu_q) & 3u) ||
+      (reinterpret_cast<uintptr_t>(s->kv_lens) & 3u) || (reinterpret_cast<uintptr_t>(s->block_table) & 3u))
+    return FL_ERR_ARG;
+  if (c->num_blocks < 1 || c->kv_heads < 1 || s->T < 1 || s->B < 1 || s->max_q < 1 || s->max_blocks < 1) return FL_ERR_ARG;
+  if (c->format != FL_KV8_E4M3 && c->format != FL_KV8_INT8) return FL_ERR_ARG;
+  if (!s->cu_q && s->T % s->B) return FL_ERR_ARG;
+  if ((c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) ||
+      (c->head_dim != 64 && c->head_dim != 128))
+    return FL_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->num_blocks) * c->kv_heads > 0x7fffffffll / c->block) return FL_ERR_UNSUPPORTED;
+  // positions, and their differences with a window, fit 32 bits
+  if (s->T > (1 << 29) || s->max_blocks > (1 << 30) / c->block) return FL_ERR_UNSUPPORTED;
+  return FL_OK;
+}
+
+}  // namespace flh

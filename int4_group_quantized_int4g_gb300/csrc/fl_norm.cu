@@ -1,0 +1,254 @@
+// Root-mean-square norm with the residual's addition, bf16 and / or e4m3 out.
+//
+//   s = x + r,  n = s / sqrt(mean(s^2) + eps) * w,  r' = bf16(s),  y = bf16(n),
+//   code = e4m3(n / scale),  scale = max|n| / 448 over a run of columns.
+//
+// One pass over memory: a team of threads holds its row's s in registers
+// between the sum of squares and the scaling, so every input is read once and
+// every output written once (8 to 9 bytes an element with the residual and
+// the codes); the kernel is bound by HBM.  The sums and n stay in fp32 and
+// each output is rounded once; the norm uses s before its rounding to bf16.
+#include <cuda_fp8.h>
+
+#include "fl_common.cuh"
+
+using namespace fl;
+
+namespace {
+
+struct NormParams {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* r;
+  const __nv_bfloat16* w;
+  __nv_bfloat16* y;
+  __nv_bfloat16* ro;
+  uint8_t* codes;
+  float* scales;
+  int64_t xs, rs, ys, ros;
+  long long rows;
+  int heads, H, group;
+  float eps;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 8 elements from column c on; those at or past H read as 0.
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16* row, int c, int H, float (&v)[8]) {
+  if constexpr (VEC) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (c < H) u = *reinterpret_cast<const uint4*>(row + c);
+    const uint32_t a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < H ? __bfloat162float(row[c + i]) : 0.f;
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int c, int H, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (c < H)
+      *reinterpret_cast<uint4*>(row + c) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < H) row[c + i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// Sum or maximum over the team of TPR threads (a warp, or the whole CTA).
+template <int TPR, bool MAX>
+__device__ __forceinline__ float team_reduce(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < TPR / 32; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+  }
+  return v;
+}
+
+// TPR threads hold one row, V vectors of 8 columns each: thread i has the
+// vectors i, i + TPR, ...  A CTA is one team, or four when a team is a warp.
+template <int TPR, int V, bool VEC>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_rmsnorm(const NormParams p) {
+  __shared__ float red[2][TPR / 32];
+  constexpr int kTeams = TPR == 32 ? 4 : 1;
+  const int t = threadIdx.x % TPR;
+  const long long row = static_cast<long long>(blockIdx.x) * kTeams + threadIdx.x / TPR;
+  if (row >= p.rows) return;   // a whole team at once
+  const long long m = row / p.heads;
+  const int64_t off = (row - m * p.heads) * p.H;
+  const __nv_bfloat16* x = p.x + m * p.xs + off;
+  float s[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) load8<VEC>(x, (i * TPR + t) * 8, p.H, s[i]);
+  if (p.r) {
+    const __nv_bfloat16* r = p.r + m * p.rs + off;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float u[8];
+      load8<VEC>(r, (i * TPR + t) * 8, p.H, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] += u[j];
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(s[i][j], s[i][j], sum);
+  sum = team_reduce<TPR, false>(sum, red[0]);
+  const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+  if (p.ro) {
+    __nv_bfloat16* ro = p.ro + m * p.ros + off;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store8<VEC>(ro, (i * TPR + t) * 8, p.H, s[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float w[8];
+    if (p.w) {
+      load8<VEC>(p.w, (i * TPR + t) * 8, p.H, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * rstd * w[j];
+  }
+  if (p.y) {
+    __nv_bfloat16* y = p.y + m * p.ys + off;
+#pragma unroll
+    for (int i = 0; i < V; ++i) store8<VEC>(y, (i * TPR + t) * 8, p.H, s[i]);
+  }
+  if (p.codes) {
+    float top[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      top[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top[i] = fmaxf(top[i], fabsf(s[i][j]));
+    }
+    if (p.group) {
+      // a run of `group` columns is group / 8 neighbouring lanes
+      for (int o = 1; o < p.group / 8; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+    } else {
+#pragma unroll
+      for (int i = 1; i < V; ++i) top[0] = fmaxf(top[0], top[i]);
+      const float a = team_reduce<TPR, true>(top[0], red[1]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) top[i] = a;
+    }
+    const int ng = p.group ? p.H / p.group : 1;
+    uint8_t* cr = p.codes + row * p.H;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (i * TPR + t) * 8;
+      if (c >= p.H) continue;
+      const float scale = __fdiv_rn(top[i], 448.f);
+      if (p.group ? c % p.group == 0 : c == 0) p.scales[row * ng + (p.group ? c / p.group : 0)] = scale;
+      uint32_t o[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = scale > 0.f ? __fdiv_rn(s[i][j], scale) : s[i][j] + 0.f;   // (a zero of either sign: code 0; NaN stays)
+        o[j >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3)) << (8 * (j & 3));
+      }
+      if constexpr (VEC) {
+        *reinterpret_cast<uint2*>(cr + c) = make_uint2(o[0], o[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < p.H) cr[c + j] = static_cast<uint8_t>(o[j >> 2] >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+template <int TPR, int V>
+int launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
+  constexpr int kTeams = TPR == 32 ? 4 : 1;
+  const long long grid = (p.rows + kTeams - 1) / kTeams;
+  if (grid > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
+  const dim3 g(static_cast<unsigned>(grid)), b(TPR == 32 ? 128 : TPR);
+  if (vec)
+    k_rmsnorm<TPR, V, true><<<g, b, 0, s>>>(p);
+  else
+    k_rmsnorm<TPR, V, false><<<g, b, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+}
+
+template <int V>
+int pick_team(const NormParams& p, int tpr, bool vec, cudaStream_t s) {
+  switch (tpr) {
+    case 32: return launch_norm<32, V>(p, vec, s);
+    case 128: return launch_norm<128, V>(p, vec, s);
+    case 256: return launch_norm<256, V>(p, vec, s);
+    case 512: return launch_norm<512, V>(p, vec, s);
+    default: return launch_norm<1024, V>(p, vec, s);
+  }
+}
+
+bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+extern "C" int fl_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                          const void* weight, float eps, int M, int heads, int H, void* y, int64_t y_stride,
+                          void* residual_out, int64_t residual_out_stride, void* codes, float* scales, int group,
+                          fl_stream_t stream) {
+  if (!x || (!y && !codes) || (codes != nullptr) != (scales != nullptr)) return FL_ERR_ARG;
+  if (M < 1 || heads < 1 || H < 1 || !(eps >= 0.f) || eps > 3.0e38f) return FL_ERR_ARG;
+  if (H > 32768) return FL_ERR_UNSUPPORTED;
+  if (group != 0 && group != 64 && group != 128 && group != 256) return FL_ERR_UNSUPPORTED;
+  if (!codes && group) return FL_ERR_ARG;
+  if (group && H % group) return FL_ERR_ARG;
+  const int64_t w = static_cast<int64_t>(heads) * H;
+  if (x_stride < w || (residual && residual_stride < w) || (y && y_stride < w) ||
+      (residual_out && residual_out_stride < w))
+    return FL_ERR_ARG;
+  const void* ptr[5] = {x, residual, weight, y, residual_out};
+  const int64_t st[5] = {x_stride, residual ? residual_stride : 0, 0, y ? y_stride : 0,
+                         residual_out ? residual_out_stride : 0};
+  bool vec = H % 8 == 0 && aligned_to(codes, 8);
+  for (int i = 0; i < 5; ++i) {
+    if (!aligned_to(ptr[i], 2)) return FL_ERR_ARG;
+    vec = vec && aligned_to(ptr[i], 16) && st[i] % 8 == 0;
+  }
+  if (!aligned_to(scales, 4)) return FL_ERR_ARG;
+  NormParams p;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.r = static_cast<const __nv_bfloat16*>(residual);
+  p.w = static_cast<const __nv_bfloat16*>(weight);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.ro = static_cast<__nv_bfloat16*>(residual_out);
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = scales;
+  p.xs = x_stride, p.rs = residual_stride, p.ys = y_stride, p.ros = residual_out_stride;
+  p.rows = static_cast<long long>(M) * heads;
+  p.heads = heads, p.H = H, p.group = group, p.eps = eps;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int tpr = 32;
+  while (tpr < 1024 && tpr * 32 < H) tpr = tpr == 32 ? 128 : 2 * tpr;   // at most 4 vectors a thread
+  if (tpr * 8 >= H) return pick_team<1>(p, tpr, vec, s);
+  return pick_team<4>(p, tpr, vec, s);
+}
