@@ -26,10 +26,8 @@
 // output's 2^-9) after a factor 2^14 v_scale / v_ref, v_ref the largest value
 // scale so far, so that it keeps its 11 bits down to 2^-28 of the largest
 // weight; the accumulators are in units of v_ref.  Sums are fp32.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "fl_kv8.cuh"
+#include "fl_tc.cuh"
 
 using namespace flkv;
 
@@ -139,13 +137,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
@@ -590,22 +581,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }
-  return fn;
-}
-
 // The codes as rows of head_dim bytes, one page of one head a box.
 bool code_map(CUtensorMap* map, void* base, const fl_kv8_cache& c) {
-  auto enc = encode_fn();
+  auto enc = flh::encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim),
                               static_cast<cuuint64_t>(c.num_blocks) * c.kv_heads * c.block};
