@@ -506,6 +506,14 @@ int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int64_t v_stri
  * them name no block of the cache.  FL_ERR_ARG for a bad argument. */
 int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int block, int window, int b, long long* out);
 
+/* Test hook: how the attention of many rows splits one sequence of n rows a
+ * query head and kv tokens into units (256 rows of a kv head x 128 tokens).
+ * out[0..1] receives the items (runs of 256 rows) of a kv head and its units;
+ * for 0 <= u < units, out[2..7] unit u's item, its index there, the item's
+ * units, its first tile of 128 tokens, and the tokens [out[7], out[6]) that
+ * some row of the item sees. */
+int fl_kv8_test_units(int n, int kv, int group, int heads, int window, long long u, long long* out);
+
 /* Workspace bytes needed by fl_kv8_attention. */
 int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out);
 

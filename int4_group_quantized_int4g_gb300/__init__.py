@@ -25,7 +25,7 @@ __all__ = [
     "fl_int4g_mlp", "fl_int4g_mlp_fused",
     "FL_KV8_E4M3", "FL_KV8_INT8", "FlKv8Cache", "FlKv8Seqs",
     "fl_rmsnorm", "fl_rope", "fl_kv8_append", "fl_kv8_attention_workspace", "fl_kv8_attention",
-    "fl_kv8_test_pages",
+    "fl_kv8_test_pages", "fl_kv8_test_units",
 ]
 
 GROUP = 128
@@ -96,6 +96,7 @@ SIGNATURES = {
                      _vp, _l, _vp, _l, _vp]),
     "fl_kv8_append": (_i, [_vp, _l, _vp, _l, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), _vp, _vp]),
     "fl_kv8_test_pages": (_i, [ctypes.POINTER(FlKv8Seqs), _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
+    "fl_kv8_test_units": (_i, [_i, _i, _i, _i, _i, ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_attention_workspace": (_i, [_i, _i, _i, _i, _i, _c_size_p]),
     "fl_kv8_attention": (_i, [_vp, _l, _i, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), ctypes.c_float, _i,
                               _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
@@ -571,6 +572,14 @@ def fl_kv8_test_pages(kv_lens, table, T, num_blocks, block, b, cu_q=None, max_q=
     out = (ctypes.c_longlong * 9)()
     _check("fl_kv8_test_pages", lib().fl_kv8_test_pages(ctypes.byref(s), num_blocks, block, window, b, out))
     return {"start": out[0], "rows": out[1], "kv": out[2], "write": tuple(out[3:6]), "read": tuple(out[6:9])}
+
+
+def fl_kv8_test_units(n, kv, group, u=-1, window=0):
+    """Test hook: (items, units) of a kv head in the attention of many rows, and
+    for unit u also (item, index, units, first tile, last token + 1, first token)."""
+    out = (ctypes.c_longlong * 8)()
+    _check("fl_kv8_test_units", lib().fl_kv8_test_units(n, kv, group, 1, window, u, out))
+    return tuple(out[:2]) if u < 0 else tuple(out[2:])
 
 
 def fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim):

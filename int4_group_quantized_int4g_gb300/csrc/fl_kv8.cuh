@@ -92,6 +92,107 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+// Arguments of the attention kernels.  A launch serves the sequences whose
+// rows (query heads of a kv head x tokens) number in (rows_lo, rows_hi].
+struct AttnParams {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* out;
+  float* lse;
+  const float* ks;
+  const float* vs;
+  float* part;
+  int32_t* cnt;
+  int32_t* status;
+  int64_t qs, os;
+  Seqs seqs;
+  int num_blocks, block, heads, group, Hq, window;
+  int rows_lo, rows_hi;
+  float scale2;   // scale * log2(e)
+};
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Runs of units: all units of the batch lie in one line, sequence by
+// sequence, and CTA c of P takes [c U / P, (c + 1) U / P).
+__host__ __device__ __forceinline__ long long unit_begin(int c, long long U, int P) { return c * U / P; }
+__host__ __device__ __forceinline__ int cta_of_unit(long long u, long long U, int P) {
+  return static_cast<int>(((u + 1) * P - 1) / U);
+}
+
+// U, P and the sequence that the CTA's first unit lies in (b, and the units
+// before it), by a scan over the sequences.  All THREADS threads take part.
+// P is 0 without units, and at most gridDim.x and ceil(U / least).
+struct Start {
+  long long U, base;
+  int P, b;
+};
+template <int THREADS, typename F>
+__device__ __forceinline__ Start find_start(int B, int least, F&& units_of) {
+  __shared__ long long scan[THREADS / 32];
+  __shared__ long long hit[2];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool one = B <= THREADS;   // with one chunk of sequences the first pass has it all
+  long long U = 0;
+  auto ctas = [&](long long n) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (n + least - 1) / least)); };
+  for (int pass = 0; pass < 2; ++pass) {
+    long long base = 0;
+    for (int c = 0; c < B; c += THREADS) {
+      const long long n = c + tid < B ? units_of(c + tid) : 0;
+      long long inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      long long before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += scan[w];
+        all += scan[w];
+      }
+      if (one) U = all;
+      if (one || pass == 1) {
+        const int P = ctas(U);
+        const long long u0 = static_cast<int>(blockIdx.x) < P ? unit_begin(blockIdx.x, U, P) : U;
+        const long long mine = base + before + inc - n;
+        if (u0 >= mine && u0 < mine + n) {
+          hit[0] = c + tid;
+          hit[1] = mine;
+        }
+      }
+      base += all;
+    }
+    U = base;
+    if (one) break;
+  }
+  __syncthreads();
+  return {U, hit[1], ctas(U), static_cast<int>(hit[0])};
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// The 16-byte chunk c of row r of a swizzled tile of D-byte rows (128-byte
+// rows: c ^ r % 8; 64-byte rows: c ^ (r / 2) % 4).
+template <int D>
+__device__ __forceinline__ int chunk_at(int r, int c) {
+  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+// A query row's power of two: e with its largest magnitude in [2^e, 2^(e+1)),
+// from the largest bf16 magnitude bits.
+__device__ __forceinline__ int row_exponent(uint32_t top) {
+  return top ? min(max(static_cast<int>(top >> 7) - 127, -126), 126) : 0;
+}
+
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 

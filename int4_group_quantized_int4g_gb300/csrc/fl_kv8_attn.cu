@@ -26,7 +26,7 @@
 // output's 2^-9) after a factor 2^14 v_scale / v_ref, v_ref the largest value
 // scale so far, so that it keeps its 11 bits down to 2^-28 of the largest
 // weight; the accumulators are in units of v_ref.  Sums are fp32.
-#include "fl_kv8.cuh"
+#include "fl_kv8_prompt.cuh"
 #include "fl_tc.cuh"
 
 using namespace flkv;
@@ -36,8 +36,10 @@ namespace {
 constexpr int kTile = 128;              // tokens of a unit
 constexpr int kWarps = 8;               // consumer warps
 constexpr int kRowsThreads = 32 * (kWarps + 1);
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kPScale = 16384.f;      // 2^14
+// Most rows of a sequence (query heads of a kv head x tokens) that this kernel
+// takes; sequences with more go to the tcgen05 kernel, in the same call.
+constexpr int kFewRows = 64;
 
 template <int D, int NT>
 struct RowsCfg {
@@ -55,21 +57,6 @@ struct RowsCfg {
   static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O, m, l
 };
 
-struct RowsParams {
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  float* lse;
-  const float* ks;
-  const float* vs;
-  float* part;
-  int32_t* cnt;
-  int32_t* status;
-  int64_t qs, os;
-  Seqs seqs;
-  int num_blocks, block, heads, group, Hq, window;
-  float scale2;   // scale * log2(e)
-};
-
 // The units of one sequence.
 struct SeqWork {
   SeqInfo q;
@@ -77,20 +64,15 @@ struct SeqWork {
   long long units;
 };
 template <int ROWS>
-__device__ __forceinline__ SeqWork seq_work(const RowsParams& p, int b) {
+__device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
   SeqWork w;
   w.q = seq_info(p.seqs, b, p.block);
   w.rows = w.q.n * p.group;
-  w.rt = (w.rows + ROWS - 1) / ROWS;
+  w.rt = w.rows > p.rows_lo && w.rows <= p.rows_hi ? (w.rows + ROWS - 1) / ROWS : 0;
   w.t0 = first_seen(w.q, p.window) / kTile;
   w.nt = max(1, (w.q.kv + kTile - 1) / kTile - w.t0);   // one even without tokens: it stores the zeros
   w.units = static_cast<long long>(p.heads) * w.rt * w.nt;
   return w;
-}
-
-__device__ __forceinline__ long long unit_begin(int c, long long U, int P) { return c * U / P; }
-__device__ __forceinline__ int cta_of_unit(long long u, long long U, int P) {
-  return static_cast<int>(((u + 1) * P - 1) / U);
 }
 
 // A run of tiles of one (sequence, head, row tile) inside the CTA's units.
@@ -103,7 +85,7 @@ struct Walk {
   long long u, end, base;
   int b;
   SeqWork w;
-  __device__ bool next(const RowsParams& p, Segment& s) {
+  __device__ bool next(const AttnParams& p, Segment& s) {
     if (u >= end) return false;
     while (u >= base + w.units) {
       base += w.units;
@@ -134,24 +116,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
   return d;
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-
-// The 16-byte chunk c of row r of a swizzled tile of D-byte rows (128-byte
-// rows: c ^ r % 8; 64-byte rows: c ^ (r / 2) % 4).
-template <int D>
-__device__ __forceinline__ int chunk_at(int r, int c) {
-  return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-}
-
 template <int FMT, int D, int NT>
 __global__ void __launch_bounds__(kRowsThreads, 1)
-    k_kv8_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const RowsParams p) {
+    k_kv8_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
   using C = RowsCfg<D, NT>;
   constexpr int ROWS = C::kRows, NS = C::kStages, KS = D / 16, WB = D / 16;   // WB: words of a lane's keys, m tiles of O^T
   extern __shared__ uint8_t smem_raw[];
@@ -161,8 +128,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff);    // [stage][16 tokens]: key, value scale
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   uint64_t* empty = full + NS;
-  __shared__ long long s_scan[kRowsThreads / 32];
-  __shared__ long long s_hit[2];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -174,52 +139,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     fence_mbar_init();
   }
 
-  // All units of the batch, and the sequence that the CTA's first unit is in.
-  long long U = 0;
-  for (int pass = 0; pass < 2; ++pass) {   // with one chunk of sequences the first pass has it all
-    long long base = 0, u0 = 0;
-    const bool one = p.seqs.B <= kRowsThreads;
-    for (int c = 0; c < p.seqs.B; c += kRowsThreads) {
-      const long long n = c + tid < p.seqs.B ? seq_work<ROWS>(p, c + tid).units : 0;
-      long long inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
-      __syncthreads();
-      long long before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kRowsThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        all += s_scan[w];
-      }
-      if (one) U = all;
-      if (one || pass == 1) {
-        const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
-        u0 = P > 0 && blockIdx.x < P ? unit_begin(blockIdx.x, U, P) : 0;
-        const long long mine = base + before + inc - n;
-        if (u0 >= mine && u0 < mine + n) {
-          s_hit[0] = c + tid;
-          s_hit[1] = mine;
-        }
-      }
-      base += all;
-    }
-    U = base;
-    if (one) break;
-  }
-  __syncthreads();
-  const int P = static_cast<int>(min(static_cast<long long>(gridDim.x), U));
-  if (static_cast<int>(blockIdx.x) >= P) return;
-  const int c = blockIdx.x;
+  const Start start = find_start<kRowsThreads>(p.seqs.B, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
+  const long long U = start.U;
+  const int P = start.P, c = blockIdx.x;
+  if (c >= P) return;
   Walk<ROWS> walk;
   walk.u = unit_begin(c, U, P);
   walk.end = unit_begin(c + 1, U, P);
-  walk.b = static_cast<int>(s_hit[0]);
-  walk.base = s_hit[1];
+  walk.b = start.b;
+  walk.base = start.base;
   walk.w = seq_work<ROWS>(p, walk.b);
   const long long ubeg = walk.u;
 
@@ -319,7 +247,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int i = 0; i < D / 8; ++i) top = max(top, max(a[i] & 0x7fffu, (a[i] >> 16) & 0x7fffu));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = top ? min(max(static_cast<int>(top >> 7) - 127, -126), 126) : 0;
+      const int e = row_exponent(top);
       const float down = pow2i(-e);
 #pragma unroll
       for (int i = 0; i < KS; ++i)
@@ -596,7 +524,7 @@ bool code_map(CUtensorMap* map, void* base, const fl_kv8_cache& c) {
 }
 
 template <int FMT, int D, int NT>
-int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const RowsParams& p, cudaStream_t s) {
+int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, cudaStream_t s) {
   using C = RowsCfg<D, NT>;
   static bool attr_done[64] = {false};
   int dev = 0;
@@ -611,7 +539,7 @@ int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const RowsParams& 
 }
 
 template <int FMT, int D>
-int pick_rows(const CUtensorMap& km, const CUtensorMap& vm, const RowsParams& p, long long rows, cudaStream_t s) {
+int pick_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, long long rows, cudaStream_t s) {
   return rows <= 8 ? launch_rows<FMT, D, 1>(km, vm, p, s) : launch_rows<FMT, D, 2>(km, vm, p, s);
 }
 
@@ -620,8 +548,10 @@ int pick_rows(const CUtensorMap& km, const CUtensorMap& vm, const RowsParams& p,
 extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out) {
   if (!out || T < 1 || B < 1 || Hq < 1 || kv_heads < 1 || Hq % kv_heads) return FL_ERR_ARG;
   if (head_dim != 64 && head_dim != 128) return FL_ERR_UNSUPPORTED;
-  // two partials a CTA: the row tiles that it shares with the CTAs before and after
-  *out = kScratchOff + 2ull * flh::sm_count() * 16 * (head_dim + 2) * 4;
+  // two partials a CTA: the rows that it shares with the CTAs before and after
+  const bool prompt = static_cast<long long>(T) * (Hq / kv_heads) > kFewRows;
+  const size_t slot = prompt ? prompt_slot_floats(head_dim) : 16 * (head_dim + 2);
+  *out = kScratchOff + 2ull * flh::sm_count() * slot * 4;
   return FL_OK;
 }
 
@@ -644,7 +574,7 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   if (rows > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
   CUtensorMap km, vm;
   if (!code_map(&km, cache->k, *cache) || !code_map(&vm, cache->v, *cache)) return FL_ERR_CUDA;
-  RowsParams p;
+  AttnParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
@@ -658,6 +588,13 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   p.group = Hq / cache->kv_heads, p.Hq = Hq, p.window = window;
   p.scale2 = scale * 1.44269504088896340736f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (rows > kFewRows) {
+    // one sequence goes to the one kernel; a batch may hold both kinds
+    p.rows_lo = seqs->B > 1 ? kFewRows : 0, p.rows_hi = 0x7fffffff;
+    const int e = launch_prompt(km, vm, p, cache->format, cache->head_dim, s);
+    if (e != FL_OK || seqs->B == 1) return e;
+  }
+  p.rows_lo = 0, p.rows_hi = kFewRows;
   if (cache->format == FL_KV8_E4M3)
     return cache->head_dim == 64 ? pick_rows<FL_KV8_E4M3, 64>(km, vm, p, rows, s)
                                  : pick_rows<FL_KV8_E4M3, 128>(km, vm, p, rows, s);

@@ -1,0 +1,91 @@
+// The split of a prompt's attention into units, and the launch of its kernel.
+#pragma once
+
+#include <cuda.h>
+
+#include "fl_kv8.cuh"
+
+namespace flkv {
+
+constexpr int kPromptRows = 256;   // rows of an item: two row tiles of 128
+constexpr int kPromptTile = 128;   // tokens of a unit
+
+// sum over i < n of floor((a i + b) / m), for n >= 0, m >= 1, a, b >= 0
+__host__ __device__ __forceinline__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// The units of one sequence: items (kv head, 256 rows) of `tiles(i)` units
+// each, a unit one tile of 128 tokens.  Rows are token-major (token, query
+// head of the group).  A causal sequence's item i ends with the tile of its
+// last row's own position, so that its tiles are those that some row sees:
+//   tiles(i) = floor((past g + 256 (i + 1) - 1) / (128 g)) + 1,
+// summed in closed form (the division by 128 g is one by 128, then one by g).
+// With a window, or with rows before the first token, every item gets the
+// same number of units, some of them without work.
+struct PromptWork {
+  SeqInfo q;
+  int rows, items, g, past, window, nc;   // nc: units of each item, 0 for the causal form
+  long long per_head;
+
+  __host__ __device__ long long before(int i) const {   // units of a head's items before item i
+    if (nc) return static_cast<long long>(i) * nc;
+    if (i >= items) return before(items - 1) + (q.kv + kPromptTile - 1) / kPromptTile;
+    return i + floor_sum(i, g, 2, (static_cast<long long>(past) * g + 255) / 128);
+  }
+  __host__ __device__ int tiles(int i) const { return static_cast<int>(before(i + 1) - before(i)); }
+  __host__ __device__ int item_of(long long u) const {   // the item that unit u of a head lies in
+    int lo = 0, hi = items - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (before(mid) <= u)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+  // Tokens [low, lim) that some row of [r0, r0 + n) sees (lim <= low: none).
+  __host__ __device__ int lim(int r0, int n) const { return past + min(r0 + n - 1, rows - 1) / g + 1; }
+  __host__ __device__ int low(int r0) const { return window ? max(0, past + r0 / g + 1 - window) : 0; }
+  __host__ __device__ int first_tile(int i) const { return low(i * kPromptRows) / kPromptTile; }
+};
+
+__host__ __device__ __forceinline__ PromptWork prompt_work(const SeqInfo& q, int group, int heads, int window, int rows_lo,
+                                                           int rows_hi) {
+  PromptWork w;
+  w.q = q;
+  w.g = group;
+  w.rows = q.n * group;
+  w.items = w.rows > rows_lo && w.rows <= rows_hi ? (w.rows + kPromptRows - 1) / kPromptRows : 0;
+  w.past = q.kv - q.n;
+  w.window = window < q.kv ? window : 0;
+  w.nc = 0;
+  if (w.past < 0 || w.window) {
+    const int all = max(1, (q.kv + kPromptTile - 1) / kPromptTile);
+    // a window's first tile starts up to 127 tokens early, and an item's rows
+    // span up to 256 / g + 1 tokens
+    const int win = w.window ? (w.window + kPromptRows / group + 1) / kPromptTile + 2 : all;
+    w.nc = min(all, win);
+  }
+  w.per_head = w.items ? w.before(w.items) : 0;
+  return w;
+}
+
+int launch_prompt(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int format, int head_dim, cudaStream_t s);
+size_t prompt_slot_floats(int head_dim);
+
+}  // namespace flkv

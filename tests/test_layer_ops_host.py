@@ -147,6 +147,32 @@ def test_pages_of_malformed_lists_stay_inside_the_arrays():
                 assert bad == sum(not 0 <= table[b][i] < nb for i in range(first, first + n))
 
 
+def test_prompt_units_cover_every_visible_token():
+    """Units of the attention of many rows against a count by hand: items in
+    order, each tile with a visible token in exactly one unit, no more units
+    than the causal triangle needs."""
+    rnd = random.Random(9)
+    for _ in range(400):
+        group, window = rnd.choice([1, 2, 3, 5, 7, 8, 16]), rnd.choice([0, 0, 1, 64, 300, 1000, 10 ** 6])
+        n = rnd.randint(1, 700)
+        kv = max(0, n + rnd.choice([-n, -5, 0, 1, 127, 128, 1000, 5000]))
+        items, units = fl.fl_kv8_test_units(n, kv, group, window=window)
+        assert items == -(-n * group // 256)
+        past, u = kv - n, 0
+        for i in range(items):
+            item, index, count, tile0, lim, low = fl.fl_kv8_test_units(n, kv, group, u, window)
+            assert (item, index) == (i, 0)
+            first, last = i * 256 // group, min(i * 256 + 255, n * group - 1) // group
+            assert lim == past + last + 1 and low == (max(0, past + first + 1 - window) if window and window < kv else 0)
+            assert tile0 == low // 128 and (tile0 + count) * 128 >= lim and count >= 1
+            if past >= 0 and not (window and window < kv):
+                assert count == -(-lim // 128)
+            if count > 1:
+                assert fl.fl_kv8_test_units(n, kv, group, u + count - 1, window)[:2] == (i, count - 1)
+            u += count
+        assert u == units
+
+
 # ------------------------------------------------------------- oracle pins
 
 def test_e4m3_rounding_pins():
