@@ -119,21 +119,21 @@ __host__ __device__ __forceinline__ int cta_of_unit(long long u, long long U, in
   return static_cast<int>(((u + 1) * P - 1) / U);
 }
 
-// U, P and the sequence that the CTA's first unit lies in (b, and the units
-// before it), by a scan over the sequences.  All THREADS threads take part.
-// P is 0 without units, and at most gridDim.x and ceil(U / least).
+// U, P and the sequence that the first unit of CTA c of P lies in (b, and the
+// units before it), by a scan over the sequences.  All THREADS threads take
+// part.  P is at most `ctas` and ceil(U / least), 0 without units.
 struct Start {
   long long U, base;
   int P, b;
 };
 template <int THREADS, typename F>
-__device__ __forceinline__ Start find_start(int B, int least, F&& units_of) {
+__device__ __forceinline__ Start find_start(int B, int c0, int ctas, int least, F&& units_of) {
   __shared__ long long scan[THREADS / 32];
   __shared__ long long hit[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool one = B <= THREADS;   // with one chunk of sequences the first pass has it all
   long long U = 0;
-  auto ctas = [&](long long n) { return static_cast<int>(min(static_cast<long long>(gridDim.x), (n + least - 1) / least)); };
+  auto parts = [&](long long n) { return static_cast<int>(min(static_cast<long long>(ctas), (n + least - 1) / least)); };
   for (int pass = 0; pass < 2; ++pass) {
     long long base = 0;
     for (int c = 0; c < B; c += THREADS) {
@@ -155,8 +155,8 @@ __device__ __forceinline__ Start find_start(int B, int least, F&& units_of) {
       }
       if (one) U = all;
       if (one || pass == 1) {
-        const int P = ctas(U);
-        const long long u0 = static_cast<int>(blockIdx.x) < P ? unit_begin(blockIdx.x, U, P) : U;
+        const int P = parts(U);
+        const long long u0 = c0 < P ? unit_begin(c0, U, P) : U;
         const long long mine = base + before + inc - n;
         if (u0 >= mine && u0 < mine + n) {
           hit[0] = c + tid;
@@ -169,7 +169,7 @@ __device__ __forceinline__ Start find_start(int B, int least, F&& units_of) {
     if (one) break;
   }
   __syncthreads();
-  return {U, hit[1], ctas(U), static_cast<int>(hit[0])};
+  return {U, hit[1], parts(U), static_cast<int>(hit[0])};
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     fence_mbar_init();
   }
 
-  const Start start = find_start<kRowsThreads>(p.seqs.B, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
+  const Start start = find_start<kRowsThreads>(p.seqs.B, blockIdx.x, gridDim.x, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
   const long long U = start.U;
   const int P = start.P, c = blockIdx.x;
   if (c >= P) return;

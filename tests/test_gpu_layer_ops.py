@@ -433,6 +433,9 @@ def test_attention_query_range(rows):
 def test_attention_long_context(fmt):
     """Contexts over many CTAs' runs, next to short ones."""
     _close(*_attend([(1, 30000), (1, 5), (2, 9001)], 4, 1, 128, 64, fmt, seed=12))
+    # a few rows more than the single-token form takes, over many CTAs
+    _close(*_attend([(17, 20000)], 4, 1, 128, 64, fmt, seed=15))
+    _close(*_attend([(3, 700), (70, 9000)], 2, 2, 64, 16, fmt, seed=16))
 
 
 def test_attention_many_sequences():
