@@ -121,17 +121,6 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
-// One thread of the (converged) warp, chosen by elect.sync.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile(
-      "{\n\t.reg .pred P;\n\t"
-      "elect.sync _|P, 0xffffffff;\n\t"
-      "selp.b32 %0, 1, 0, P;\n\t}"
-      : "=r"(pred));
-  return pred != 0;
-}
-
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major.
 template <int BN>
 __device__ __forceinline__ uint32_t idesc_bf16() {

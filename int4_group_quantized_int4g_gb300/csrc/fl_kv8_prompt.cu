@@ -16,13 +16,14 @@
 //   0..3, 4..7  softmax of row tile 0, 1: a thread has a row.  The maximum
 //               that weights are taken against moves only when it is passed by
 //               2^8; then the warp rescales its rows of O in tensor memory
-//   8..15       convert: key rows as they are (K-major), values transposed
-//               (tokens along K) with byte permutes; the order of output
+//   8..11       convert key rows as they are (K-major)
+//   12..15      convert values, transposed
+//               (tokens along K) with byte permutes: the order of output
 //               columns is free, so value element 4 l + j goes to row j D/4 + l,
 //               which makes the writes conflict-free
-//   16, 17      issue the MMAs of row tile 0, 1
-//   18          copies pages by TMA into a staging tile for keys and for values
-//   19          walks the CTA's units and publishes their segments to the others
+//   16          issues the MMAs
+//   17          copies pages by TMA into a staging tile for keys and for values
+//   18          walks the CTA's units and publishes their segments to the others
 //
 // Scales: with e_b the power of two in a block's scale and e_ref the largest of
 // the segment's, codes are multiplied by 2^(e_b - e_ref + k) as they
@@ -39,11 +40,11 @@ using namespace flkv;
 namespace {
 
 constexpr int kPrThreads = 640;
-constexpr int kConv0 = 8, kIssue0 = 16, kProd = 18, kPlan = 19;   // first warps of the roles
-constexpr int kConvThreads = 256;
+constexpr int kConv0 = 8, kIssue0 = 16, kProd = 17, kPlan = 18;   // first warps of the roles
+constexpr int kConvWarps = 4;                         // for keys, and for values
 // Registers a thread: all at launch, then by role (warps 16..19 share one count)
 constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsConv = 64, kRegsRest = 96;
-static_assert(256 * kRegsSoftmax + kConvThreads * kRegsConv + 128 * kRegsRest <= kPrThreads * kRegs, "register pool");
+static_assert(256 * kRegsSoftmax + 64 * kConvWarps * kRegsConv + 128 * kRegsRest <= kPrThreads * kRegs, "register pool");
 constexpr int kPromptLeast = 2;                       // fewest units of a CTA
 constexpr float kBias = 6.f;                          // P = 2^(x - m + kBias)
 constexpr float kSlack = 8.f;                         // the maximum may lag by 2^kSlack
@@ -56,8 +57,9 @@ struct PrCfg {
   static constexpr int kKOff = 2 * kQ;         // two stages
   static constexpr int kVOff = kKOff + 2 * kKv;
   static constexpr int kStgOff = kVOff + 2 * kKv;
-  static constexpr int kMetaOff = kStgOff + 2 * kStg;      // [4 units][8 slices of 16 tokens]: key, value scale
-  static constexpr int kSegOff = kMetaOff + 4 * 8 * 8;     // [4] segments
+  static constexpr int kMetaOff = kStgOff + 2 * kStg;      // [8 units][8 slices of 16 tokens]: mantissas of the key, value scale
+  static constexpr int kRatioOff = kMetaOff + 8 * 8 * 8;   // [8][8]: the codes' multipliers, f16 pairs
+  static constexpr int kSegOff = kRatioOff + 8 * 8 * 8;    // [4] segments
   static constexpr int kBarOff = kSegOff + 4 * 64;
   static constexpr int kBars = 4 + 8 + 2 + 2 + 2 + 2 + 8;
   static constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;
@@ -115,6 +117,13 @@ __device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
                :
                : "memory");
 }
+__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  tmem_ld16_issue(taddr, r);
+  tmem_ld_wait(r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -128,6 +137,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+  tmem_st16(taddr, r);
+}
+
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -136,22 +152,11 @@ template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// (x, y) * (a, a) + (b, b), and (x, y) + (z, w): two fp32 lanes an instruction
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float b) {
-  asm("{\n\t.reg .b64 v, s, t;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %2};\n\tmov.b64 t, {%3, %3};\n\t"
-      "fma.rn.f32x2 v, v, s, t;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
-__device__ __forceinline__ void add2(float& x, float& y, float z, float w) {
-  asm("{\n\t.reg .b64 v, s;\n\t"
-      "mov.b64 v, {%0, %1};\n\tmov.b64 s, {%2, %3};\n\t"
-      "add.rn.f32x2 v, v, s;\n\tmov.b64 {%0, %1}, v;\n\t}"
-      : "+f"(x), "+f"(y)
-      : "f"(z), "f"(w));
-}
-
 // A run of units of one item inside the CTA's units, as the roles need it.
 struct __align__(16) Segment {
   int units;       // with work (row tile 0 or 1); -1: no more segments
@@ -244,6 +249,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff);
+  uint2* ratios = reinterpret_cast<uint2*>(smem + C::kRatioOff);
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegOff);
   uint64_t* stg_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);   // [keys, values]
   uint64_t* stg_empty = stg_full + 2;
@@ -264,11 +270,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&stg_full[i], 1);
-      mbar_init(&stg_empty[i], kConvThreads / 32);
-      mbar_init(&k_full[i], kConvThreads / 32);
-      mbar_init(&k_empty[i], 2);
-      mbar_init(&v_full[i], kConvThreads / 32);
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&stg_empty[i], kConvWarps);
+      mbar_init(&k_full[i], kConvWarps);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], kConvWarps);
+      mbar_init(&v_empty[i], 1);
       mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&seg_full[i], 1);
-      mbar_init(&seg_empty[i], kPlan);   // one arrival a warp but the planner
+      mbar_init(&seg_empty[i], kPlan);   // one arrival of every warp before the planner
     }
     fence_mbar_init();
   }
@@ -364,35 +370,39 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       float m = -INFINITY, l = 0.f;   // weights are 2^(x - m); m is kBias below the maximum that it was taken from
       for (int j = 0; j < live; ++j, ++js) {
         const bool mask = hi_all < kPromptTile || lo_all > 0;
-        float x[2][32];   // a quarter of S at work, the next in flight
-        const float2* mt = general ? meta + ((s.meta + j) & 3) * 8 : nullptr;
-        auto careful = [&](float (&v)[32], int k) {
-          if (general) {   // the keys' mantissas
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float mk = scale_mantissa(mt[2 * k + h].x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[16 * h + i] *= mk;
-            }
-          }
-          if (mask) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * k + i >= hi || 32 * k + i < lo) v[i] = -INFINITY;
-          }
-        };
         wait(&s_full[t], js, 61);
         tc_fence_after();
+        // The loops below are kept short on purpose: with everything unrolled
+        // the roles' code no longer fits the instruction cache together, and a
+        // unit took 4.5 us instead of the figures above.
+        if (mask || general) {
+          // S as it is meant, back to its columns: the keys' mantissas, -inf
+          // where this row does not see the token
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            float v[16];
+            tmem_ld16f(ts + 16 * k, v);
+            const float mk = general ? meta[((s.meta + j) & 7) * 8 + k].x : 1.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = 16 * k + i >= hi || 16 * k + i < lo ? -INFINITY : v[i] * mk;
+            tmem_st16f(ts + 16 * k, v);
+          }
+          tmem_wait_st();
+        }
+        float x[2][32];   // a quarter of S at work, the next in flight
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         tmem_ld32_issue(ts, x[0]);
         tmem_ld32_wait(x[0]);
+#pragma unroll 1
+        for (int k = 0; k < 4; k += 2) {
+          tmem_ld32_issue(ts + 32 * (k + 1), x[1]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          tmem_ld32_issue(ts + 32 * ((k + 1) & 3), x[(k + 1) & 1]);   // (the last: the first quarter again)
-          if (mask || general) careful(x[k & 1], k);
+          for (int i = 0; i < 16; ++i) mx4[i & 3] = max3(mx4[i & 3], x[0][2 * i], x[0][2 * i + 1]);
+          tmem_ld32_wait(x[1]);
+          tmem_ld32_issue(ts + 32 * ((k + 2) & 3), x[0]);   // (at last the first quarter again)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], x[k & 1][i]);
-          tmem_ld32_wait(x[(k + 1) & 1]);
+          for (int i = 0; i < 16; ++i) mx4[i & 3] = max3(mx4[i & 3], x[1][2 * i], x[1][2 * i + 1]);
+          tmem_ld32_wait(x[0]);
         }
         const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a;
         if (j == 0) {
@@ -419,33 +429,38 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           tmem_wait_st();
         }
         const float mm = m == -INFINITY ? 0.f : -m;
-        float lx[2] = {0.f, 0.f}, ly[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float (&v)[32] = x[k & 1];
-          if (k < 3) tmem_ld32_issue(ts + 32 * (k + 1), x[(k + 1) & 1]);
-          if (mask || general) careful(v, k);
+        float2 lsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weights = [&](float (&v)[32], int k) {   // a quarter of P from one of S
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            fma2(v[2 * i], v[2 * i + 1], a, mm);
-            v[2 * i] = exp2_approx(v[2 * i]), v[2 * i + 1] = exp2_approx(v[2 * i + 1]);
-            add2(lx[i & 1], ly[i & 1], v[2 * i], v[2 * i + 1]);
+            const float2 e = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(a, a), make_float2(mm, mm));
+            v[2 * i] = exp2_approx(e.x), v[2 * i + 1] = exp2_approx(e.y);
+            lsum[i & 1] = __fadd2_rn(lsum[i & 1], make_float2(v[2 * i], v[2 * i + 1]));
           }
           if (general) {   // the values' mantissas
+            const float m0 = meta[((s.meta + j) & 7) * 8 + 2 * k].y, m1 = meta[((s.meta + j) & 7) * 8 + 2 * k + 1].y;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float mv = scale_mantissa(mt[2 * k + h].y);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[16 * h + i] *= mv;
-            }
+            for (int i = 0; i < 32; ++i) v[i] *= i < 16 ? m0 : m1;
           }
+        };
+        auto store = [&](const float (&v)[32], int k) {   // over columns of S that have been read
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-          if (k < 3) tmem_ld32_wait(x[(k + 1) & 1]);
-          tmem_st16(ts + 16 * k, pk);   // over columns of S that have been read
+          tmem_st16(ts + 16 * k, pk);
+        };
+#pragma unroll 1
+        for (int k = 0; k < 4; k += 2) {
+          tmem_ld32_issue(ts + 32 * (k + 1), x[1]);
+          weights(x[0], k);
+          tmem_ld32_wait(x[1]);
+          store(x[0], k);
+          if (k == 0) tmem_ld32_issue(ts + 64, x[0]);
+          weights(x[1], k + 1);
+          if (k == 0) tmem_ld32_wait(x[0]);
+          store(x[1], k + 1);
         }
-        l += (lx[0] + lx[1]) + (ly[0] + ly[1]);
+        l += (lsum[0].x + lsum[1].x) + (lsum[0].y + lsum[1].y);
         hi -= kPromptTile, hi_all -= kPromptTile, lo -= kPromptTile, lo_all -= kPromptTile;
         tmem_wait_st();
         tc_fence_before();
@@ -514,7 +529,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   } else if (warp < kIssue0) {
     // ---------------- convert
     regs_down<kRegsConv>();
-    const int ct = tid - 32 * kConv0, cw = warp - kConv0;
+    const bool values = warp >= kConv0 + kConvWarps;
+    const int cw = (warp - kConv0) % kConvWarps;
     int i = 0;
     for (int seg = 0; ok; ++seg) {
       wait(&seg_full[seg & 3], seg >> 2, 59);
@@ -522,27 +538,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (!ok || s.units < 0) break;
       SeqInfo q;
       q.kv = s.kv, q.n = s.kv - s.past, q.start = 0;
-      const int ke = s.ke, ve = s.ve;
       const int seen = first_seen(q, p.window), units = s.units;
       int pos = s.tile * kPromptTile;
-      for (int j = 0; j < units; ++j, ++i, pos += kPromptTile) {
-        const int st = i & 1;
-        const float2* mt = meta + (i & 3) * 8;
-        // 2^(e - e_ref + shift), 0 below f16 (pages that are not read have a scale of 1, which may exceed e_ref)
-        auto ratio = [&](float scale, int e_ref) {
-          return __float2half2_rn(pow2i(max(min(scale_exponent(scale) - e_ref, 0) + code_shift<FMT>(), -126)));
-        };
-        // keys
-        wait(&stg_full[0], i, 64);
-        wait(&k_empty[st], (i >> 1) + 1, 65);
-        {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[seg & 3]);
+      if (!values) {
+        for (int j = 0; j < units; ++j, ++i) {
+          const int st = i & 1;
+          wait(&stg_full[0], i, 64);
+          wait(&k_empty[st], (i >> 1) + 1, 65);
           const uint8_t* src = smem + C::kStgOff;
           uint8_t* dst = smem + C::kKOff + st * C::kKv;
-          constexpr int kCh = D / 16, kIt = 128 * kCh / kConvThreads;   // chunks of 16 codes a row, passes
-#pragma unroll
-          for (int it = 0; it < kIt; ++it) {
-            const int task = it * kConvThreads + ct, row = task / kCh, ch = task % kCh;
-            const __half2 r2 = ratio(mt[row >> 4].x, ke), o2 = __hmul2(r2, __float2half2_rn(-1152.f));
+          const uint2* rt = ratios + (i & 7) * 8;
+          // a warp has two slices of 16 tokens; eight lanes take one 16-byte
+          // chunk of eight rows, free of bank conflicts in both layouts
+          constexpr int kCh = D / 16;   // chunks of a row
+#pragma unroll 2
+          for (int it = 0; it < kCh; ++it) {
+            const int task = it * 32 + lane, ch = (task >> 3) % kCh, row = cw * 32 + task / (8 * kCh) * 8 + (lane & 7);
+            const uint32_t rr = rt[row >> 4].x;
+            const __half2 r2 = *reinterpret_cast<const __half2*>(&rr), o2 = __hmul2(r2, __float2half2_rn(-1152.f));
             const uint4 v = *reinterpret_cast<const uint4*>(src + chunk_at<D>(row, ch));
             const uint32_t wd[4] = {bias_codes<FMT>(v.x), bias_codes<FMT>(v.y), bias_codes<FMT>(v.z), bias_codes<FMT>(v.w)};
             uint32_t o[8];
@@ -553,41 +568,44 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             uint8_t* rowp = dst + (ch >> 2) * (128 * 128) + row * 128;
             const int c0 = (ch & 3) * 2;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            // the upper half row writes its second chunk first: no bank conflicts
-            const int sw = ch >> 2;
-            *reinterpret_cast<uint4*>(rowp + (((c0 + sw) ^ (row & 7)) << 4)) = sw ? hi : lo;
-            *reinterpret_cast<uint4*>(rowp + (((c0 + 1 - sw) ^ (row & 7)) << 4)) = sw ? lo : hi;
+            *reinterpret_cast<uint4*>(rowp + ((c0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(rowp + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&stg_empty[0]);
+            mbar_arrive(&k_full[st]);
           }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&k_full[st]);
-          mbar_arrive(&stg_empty[0]);
-        }
-        // values
-        wait(&stg_full[1], i, 66);
-        wait(&v_empty[st], (i >> 1) + 1, 67);
-        {
+      } else {
+        for (int j = 0; j < units; ++j, ++i, pos += kPromptTile) {
+          const int st = i & 1;
+          wait(&stg_full[1], i, 66);
+          wait(&v_empty[st], (i >> 1) + 1, 67);
           const uint8_t* src = smem + C::kStgOff + C::kStg;
           uint8_t* dst = smem + C::kVOff + st * C::kKv;
-          constexpr int kL = D / 4, kPer = 32 / kL * (kConvThreads / 32), kIt = 16 / kPer;   // lanes of a row; groups of 8 tokens a pass
+          const uint2* rt = ratios + (i & 7) * 8;
+          // lanes of a row; groups of 8 tokens a pass; passes
+          constexpr int kL = D / 4, kPer = 32 / kL * kConvWarps, kIt = 16 / kPer;
           const int l = lane % kL;
           const bool edge = pos + kPromptTile > q.kv || pos < seen;
-#pragma unroll
+#pragma unroll 1
           for (int it = 0; it < kIt; ++it) {
             const int grp = it * kPer + cw * (32 / kL) + lane / kL;
-            const __half2 r2 = ratio(mt[grp >> 1].y, ve), o2 = __hmul2(r2, __float2half2_rn(-1152.f));
+            const uint32_t rr = rt[grp >> 1].y;
+            const __half2 r2 = *reinterpret_cast<const __half2*>(&rr), o2 = __hmul2(r2, __float2half2_rn(-1152.f));
             uint32_t wd[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int row = grp * 8 + k;
-              wd[k] = *reinterpret_cast<const uint32_t*>(src + chunk_at<D>(row, l >> 2) + 4 * (l & 3));
+            for (int k = 0; k < 8; ++k) wd[k] = *reinterpret_cast<const uint32_t*>(src + chunk_at<D>(grp * 8 + k, l >> 2) + 4 * (l & 3));
+            if (edge) {
               // slots past the sequence's tokens may hold anything: as 0 they add 0 * 0
-              if (edge && (pos + row >= q.kv || pos + row < seen)) wd[k] = 0;
-              wd[k] = bias_codes<FMT>(wd[k]);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                if (pos + grp * 8 + k >= q.kv || pos + grp * 8 + k < seen) wd[k] = 0;
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wd[k] = bias_codes<FMT>(wd[k]);
             uint32_t o[4][4];   // [element][pair of tokens]
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -596,78 +614,85 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               o[0][k] = scaled_pair<FMT, false>(e01, r2, o2), o[1][k] = scaled_pair<FMT, true>(e01, r2, o2);
               o[2][k] = scaled_pair<FMT, false>(e23, r2, o2), o[3][k] = scaled_pair<FMT, true>(e23, r2, o2);
             }
-            uint8_t* base = dst + (grp >> 3) * (D * 128);
+            uint8_t* base = dst + (grp >> 3) * (D * 128) + l * 128 + (((grp & 7) ^ (l & 7)) << 4);   // (D/4 is a multiple of 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int n = e * (D / 4) + l;
-              *reinterpret_cast<uint4*>(base + n * 128 + (((grp & 7) ^ (n & 7)) << 4)) =
-                  make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
-            }
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(base + e * (D / 4) * 128) = make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&stg_empty[1]);
+            mbar_arrive(&v_full[st]);
           }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&v_full[st]);
-          mbar_arrive(&stg_empty[1]);
-        }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&seg_empty[seg & 3]);
     }
   } else {
     regs_down<kRegsRest>();
-    if (warp < kProd) {
-      // ---------------- the MMAs of row tile t, from one lane
-      const int t = warp - kIssue0;
-      if (lane == 0) {
-        const uint32_t ts = tmem + 128 * t, to = tmem + 256 + D * t;
-        const uint32_t ids = idesc_f16(128), ido = idesc_f16(D);
-        const uint32_t qa = smem_u32(smem + t * C::kQ);
-        int i = 0;
-        uint32_t jt = 0, lived = 0;
-        for (int seg = 0; ok; ++seg) {
-          wait_one(&seg_full[seg & 3], seg >> 2, 59);
-          const Segment& s = segs[seg & 3];
-          const int units = s.units, live = s.live[t];
-          if (!ok || units < 0) break;
-          mbar_arrive(&seg_empty[seg & 3]);
-          if (live > 0) wait_one(&q_full[t], lived++, 68);
-          for (int j = 0; j < units; ++j, ++i) {
-            const int st = i & 1;
-            wait_one(&k_full[st], i >> 1, 69);
-            if (j < live) {
-              if (jt > 0) wait_one(&o_done[t], jt - 1, 70);   // P, which lies over S, has been read
-              if (ok) {
-                tc_fence_after();
-                const uint32_t kb = smem_u32(smem + C::kKOff + st * C::kKv);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  umma_f16_ss(ts, sw128_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32),
-                              sw128_desc(kb + (k >> 2) * (128 * 128) + (k & 3) * 32), ids, k != 0);
-                umma_commit(&k_empty[st]);
-                umma_commit(&s_full[t]);
-              }
-            } else {
-              mbar_arrive(&k_empty[st]);
-            }
-            wait_one(&v_full[st], i >> 1, 71);
-            if (j < live) {
-              wait_one(&p_full[t], jt, 72);
-              if (ok) {
-                tc_fence_after();
-                const uint32_t vb = smem_u32(smem + C::kVOff + st * C::kKv);
+    if (warp == kIssue0) {
+      // ---------------- the MMAs.  Row tile 0's P V and next S go
+      // out before row tile 1's, which keeps the two half a unit apart: while
+      // one is at its softmax the other is at its products.
+      // (The whole warp walks through and an elected lane issues: the
+      // descriptors stay in uniform registers.  With one lane in a branch of its
+      // own an MMA took 110 cycles to issue, 64 is its time.)
+      int i = 0;
+      uint32_t jt0 = 0, jt1 = 0, lived0 = 0, lived1 = 0;   // units and segments with work of each row tile so far
+      for (int seg = 0; ok; ++seg) {
+        wait(&seg_full[seg & 3], seg >> 2, 59);
+        const Segment& s = segs[seg & 3];
+        const int units = __shfl_sync(0xffffffffu, s.units, 0), live0 = __shfl_sync(0xffffffffu, s.live[0], 0);
+        const int live1 = __shfl_sync(0xffffffffu, s.live[1], 0);
+        if (!ok || units < 0) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[seg & 3]);
+        // step -1 has the first S of both tiles, step j their P V and next S
+#pragma unroll 1
+        for (int j = units > 0 ? -1 : 0; j < units; ++j) {
+          const int st = i & 1, nx = j >= 0 ? i + 1 : i;   // nx: the unit of the next S
+          if (j >= 0) wait(&v_full[st], i >> 1, 71);
+          if (j + 1 < units) wait(&k_full[nx & 1], nx >> 1, 69);
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int live = t ? live1 : live0;
+            if (j >= live || live == 0) continue;
+            uint32_t jt = t ? jt1 : jt0;
+            if (j >= 0) {
+              wait(&p_full[t], jt, 72);
+              tc_fence_after();
+              if (ok && elect_one()) {
+                const uint64_t vd = sw128_desc(smem_u32(smem + C::kVOff + st * C::kKv));
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  umma_f16_ts(to, ts + 8 * k, sw128_desc(vb + (k >> 2) * (D * 128) + (k & 3) * 32), ido, j != 0 || k != 0);
-                umma_commit(&v_empty[st]);
+                  umma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, vd + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4),
+                              idesc_f16(D), j != 0 || k != 0);
+                if (t == 1 || j >= live1) umma_commit(&v_empty[st]);
                 umma_commit(&o_done[t]);   // (last: the CTA may end once it has come)
               }
+              __syncwarp();
               ++jt;
+              if (t) jt1 = jt; else jt0 = jt;
             } else {
-              mbar_arrive(&v_empty[st]);
+              wait(&q_full[t], t ? lived1++ : lived0++, 68);
+            }
+            if (j + 1 < live) {
+              if (jt > 0) wait(&o_done[t], jt - 1, 70);   // P, which lies over S, has been read
+              tc_fence_after();
+              if (ok && elect_one()) {
+                const uint64_t qd = sw128_desc(smem_u32(smem + t * C::kQ));
+                const uint64_t kd = sw128_desc(smem_u32(smem + C::kKOff + (nx & 1) * C::kKv));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                  umma_f16_ss(tmem + 128 * t, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                              kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), idesc_f16(128), k != 0);
+                if (t == 1 || j + 1 >= live1) umma_commit(&k_empty[nx & 1]);
+                umma_commit(&s_full[t]);
+              }
+              __syncwarp();
             }
           }
+          if (j >= 0) ++i;
         }
       }
     } else if (warp == kProd) {
@@ -677,7 +702,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       for (int seg = 0; ok; ++seg) {
         wait(&seg_full[seg & 3], seg >> 2, 59);
         const Segment& s = segs[seg & 3];
-        const int units = s.units, b = s.b, h = s.h;
+        const int units = s.units, b = s.b, h = s.h, ke = s.ke, ve = s.ve;
         if (!ok || units < 0) break;
         SeqInfo q;
         q.kv = s.kv, q.n = s.kv - s.past, q.start = 0;
@@ -691,6 +716,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           const int id = page_block(p.seqs, b, pg, p.num_blocks);
           if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 55);
           return id;
+        };
+        // 2^(e - e_ref + shift), 0 below f16 (pages that are not read have a scale of 1, which may exceed e_ref)
+        auto ratio = [&](float scale, int e_ref) {
+          return __float2half2_rn(pow2i(max(min(scale_exponent(scale) - e_ref, 0) + code_shift<FMT>(), -126)));
         };
         auto scales_of = [&](int id) {
           if (id < 0) return make_float2(1.f, 1.f);
@@ -716,7 +745,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             if (i > 0) wait(&stg_empty[hh], i - 1, 73);
             if (ok) {
               if (lane == 0 && valid) mbar_expect_tx(&stg_full[hh], static_cast<uint32_t>(pbytes) * __popc(valid));
-              if (hh == 0 && lane < 8) meta[(i & 3) * 8 + lane] = make_float2(a, v);
+              if (hh == 0 && lane < 8) {
+                const __half2 rk = ratio(a, ke), rv = ratio(v, ve);
+                ratios[(i & 7) * 8 + lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&rk), *reinterpret_cast<const uint32_t*>(&rv));
+                meta[(i & 7) * 8 + lane] = make_float2(scale_mantissa(a), scale_mantissa(v));
+              }
               __syncwarp();
               if (mine)
                 tma_load_2d(smem + C::kStgOff + hh * C::kStg + (lane - k * ppt) * pbytes, hh ? &vmap : &kmap, 0, row,
@@ -730,7 +763,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       // (in the normal course the converters have waited for every copy)
       if (!ok && i > 0)
         for (int h = 0; h < 2; ++h) mbar_wait(&stg_full[h], static_cast<uint32_t>(i - 1) & 1u);
-    } else {
+    } else if (warp == kPlan) {
       // ---------------- the plan, and the scales of each segment's pages
       const int ppt = kPromptTile / p.block;
       PromptWalk walk;
@@ -764,7 +797,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           s.ke = __reduce_max_sync(0xffffffffu, ke);
           s.ve = __reduce_max_sync(0xffffffffu, ve);
           s.general = __any_sync(0xffffffffu, mantissas);
-          s.meta = i & 3;
+          s.meta = i & 7;
           i += s.units;
         }
         if (lane == 0) {
