@@ -13,9 +13,11 @@
 // with the running maximum and sum, P as f16 back into S's columns, O += P V
 // (P from tensor memory, O there too).  Codes become f16 once per CTA and unit,
 // in shared memory, and serve both row tiles.  Warps:
-//   0..3, 4..7  softmax of row tile 0, 1: a thread has a row.  The maximum
-//               that weights are taken against moves only when it is passed by
-//               2^8; then the warp rescales its rows of O in tensor memory
+//   0..3, 4..7  softmax of row tile 0, 1: a thread has a row.  The reference
+//               that weights are taken against moves only when a maximum has
+//               passed it by 2^8, so one pass over S does: the maximum of 64
+//               columns, their weights, P back; where a reference has moved, P,
+//               O and the sum are rescaled by the power of two
 //   8..11       convert key rows as they are (K-major)
 //   12..15      convert values, transposed
 //               (tokens along K) with byte permutes: the order of output
@@ -43,11 +45,11 @@ constexpr int kPrThreads = 640;
 constexpr int kConv0 = 8, kIssue0 = 16, kProd = 17, kPlan = 18;   // first warps of the roles
 constexpr int kConvWarps = 4;                         // for keys, and for values
 // Registers a thread: all at launch, then by role (warps 16..19 share one count)
-constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsConv = 64, kRegsRest = 96;
+constexpr int kRegs = 96, kRegsSoftmax = 136, kRegsConv = 64, kRegsRest = 80;
 static_assert(256 * kRegsSoftmax + 64 * kConvWarps * kRegsConv + 128 * kRegsRest <= kPrThreads * kRegs, "register pool");
 constexpr int kPromptLeast = 2;                       // fewest units of a CTA
-constexpr float kBias = 6.f;                          // P = 2^(x - m + kBias)
-constexpr float kSlack = 8.f;                         // the maximum may lag by 2^kSlack
+constexpr float kBias = 6.f;                          // P is at most 2^kBias when its reference is taken
+constexpr float kSlack = 8.f;                         // and 2^(kBias + kSlack) before it is taken anew
 
 template <int D>
 struct PrCfg {
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   const uint32_t tmem = *tmem_slot;   // S/P of row tile t at 128 t, O at 256 + D t
   bool ok = true;   // false after a wait ran out: nothing is waited for or issued any more
   auto wait_one = [&](uint64_t* bar, uint32_t phase, int where) {
-    if (ok && !mbar_wait(bar, phase & 1u)) {
+    if (ok && !mbar_wait_many(bar, phase & 1u)) {
       set_status(p.status, FL_ERR_TIMEOUT, where);
       ok = false;
     }
@@ -317,21 +319,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + D * t;
     uint32_t js = 0;    // units of this row tile so far
+    // the factor of weights whose reference moves up
+    auto shrink = [](float from, float to) { return from == to ? 1.f : exp2_approx(from - to); };
     for (int seg = 0; ok; ++seg) {
       wait(&seg_full[seg & 3], seg >> 2, 59);
       const Segment& s = segs[seg & 3];
       if (!ok || s.units < 0) break;
       const int live = s.live[t];
-      const int r0 = s.row0 + 128 * t, row = r0 + r, rows = s.rows;
-      const bool real = row < rows, general = s.general != 0;
-      const int tok = min(row, rows - 1) / p.group;
+      const bool general = s.general != 0;
       float a = 0.f;
       if (live > 0) {
         // the row of q, times a power of two and the sign of the scale, as f16
         uint4 x[D / 8];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
-        if (real) {
+        const int row = s.row0 + 128 * t + r, tok = row / p.group;
+        if (row < s.rows) {
           const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.start) + tok) * p.qs +
                                                             static_cast<int64_t>(s.h * p.group + row - tok * p.group) * D);
 #pragma unroll
@@ -362,22 +365,27 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
-      // columns of the first unit that this row sees are [lo, hi), those that every row of the tile sees [lo_all, hi_all)
-      const int pos0 = s.tile * kPromptTile;
-      int hi = s.past + tok + 1 - pos0, hi_all = s.past + r0 / p.group + 1 - pos0;
-      int lo = -0x40000000, lo_all = -0x40000000;
-      if (p.window) lo = hi - p.window, lo_all = s.past + min(r0 + 127, rows - 1) / p.group + 1 - pos0 - p.window;
-      float m = -INFINITY, l = 0.f;   // weights are 2^(x - m); m is kBias below the maximum that it was taken from
+      // units [plain_begin, plain_end) of which every row of the tile sees every token
+      int plain_begin = 0, plain_end;
+      {
+        const int r0 = s.row0 + 128 * t, pos = s.tile * kPromptTile;
+        plain_end = (s.past + r0 / p.group + 1 - pos) >> 7;
+        if (p.window) plain_begin = (s.past + min(r0 + 127, s.rows - 1) / p.group + 1 - p.window - pos + 127) >> 7;
+      }
+      float m = -INFINITY, l = 0.f;   // weights are 2^(x - m); the reference m is an integer, about kBias below a maximum
       for (int j = 0; j < live; ++j, ++js) {
-        const bool mask = hi_all < kPromptTile || lo_all > 0;
         wait(&s_full[t], js, 61);
         tc_fence_after();
-        // The loops below are kept short on purpose: with everything unrolled
-        // the roles' code no longer fits the instruction cache together, and a
-        // unit took 4.5 us instead of the figures above.
-        if (mask || general) {
+        // The loops of all roles are kept short on purpose: unrolled, they do not
+        // fit the instruction cache together, and a unit took twice as long.  And
+        // they spill no register: little of the L1 is left beside the tiles, so
+        // that a spilled value comes back from L2.
+        if (j >= plain_end || j < plain_begin || general) {
           // S as it is meant, back to its columns: the keys' mantissas, -inf
           // where this row does not see the token
+          const int pos = (s.tile + j) * kPromptTile;
+          const int hi = s.past + min(s.row0 + 128 * t + r, s.rows - 1) / p.group + 1 - pos;   // columns [lo, hi) are seen
+          const int lo = p.window ? hi - p.window : -0x40000000;
 #pragma unroll 1
           for (int k = 0; k < 8; ++k) {
             float v[16];
@@ -389,48 +397,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
           tmem_wait_st();
         }
-        float x[2][32];   // a quarter of S at work, the next in flight
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        tmem_ld32_issue(ts, x[0]);
-        tmem_ld32_wait(x[0]);
-#pragma unroll 1
-        for (int k = 0; k < 4; k += 2) {
-          tmem_ld32_issue(ts + 32 * (k + 1), x[1]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mx4[i & 3] = max3(mx4[i & 3], x[0][2 * i], x[0][2 * i + 1]);
-          tmem_ld32_wait(x[1]);
-          tmem_ld32_issue(ts + 32 * ((k + 2) & 3), x[0]);   // (at last the first quarter again)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) mx4[i & 3] = max3(mx4[i & 3], x[1][2 * i], x[1][2 * i + 1]);
-          tmem_ld32_wait(x[0]);
-        }
-        const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a;
-        if (j == 0) {
-          m = top - kBias;
-        } else if (__any_sync(0xffffffffu, top - kBias > m + kSlack)) {
-          // a maximum has outgrown its reference: the warp's rows of O move
-          float f = 1.f;
-          if (top - kBias > m + kSlack) {
-            f = exp2_approx(m - (top - kBias));
-            m = top - kBias;
-          }
-          l *= f;
-          wait(&o_done[t], js - 1, 62);
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < D / 8; ++k) {
-            uint32_t o[8];
-            tmem_ld8_issue(to + 8 * k, o);
-            tmem_ld8_wait(o);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st8(to + 8 * k, o);
-          }
-          tmem_wait_st();
-        }
-        const float mm = m == -INFINITY ? 0.f : -m;
+        float mu = m;   // the reference of this unit's weights
         float2 lsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weights = [&](float (&v)[32], int k) {   // a quarter of P from one of S
+        auto weights = [&](float (&v)[32], int k) {   // columns 32 k .. of S become columns 16 k .. of P
+          const float mm = mu == -INFINITY ? 0.f : -mu;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 e = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(a, a), make_float2(mm, mm));
@@ -442,26 +412,71 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= i < 16 ? m0 : m1;
           }
-        };
-        auto store = [&](const float (&v)[32], int k) {   // over columns of S that have been read
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_f16(v[2 * i], v[2 * i + 1]);
           tmem_st16(ts + 16 * k, pk);
         };
+        // Half of the columns at a time: their maximum and, if it has outgrown
+        // the reference, a new one; then their weights, while the other half loads.
+        float x[2][32];
+        tmem_ld32_issue(ts, x[0]);
+        tmem_ld32_issue(ts + 32, x[1]);
 #pragma unroll 1
         for (int k = 0; k < 4; k += 2) {
-          tmem_ld32_issue(ts + 32 * (k + 1), x[1]);
-          weights(x[0], k);
+          tmem_ld32_wait(x[0]);
           tmem_ld32_wait(x[1]);
-          store(x[0], k);
+          float mx4[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
+#pragma unroll
+          for (int i = 1; i < 16; ++i) {
+            mx4[i & 1] = max3(mx4[i & 1], x[0][2 * i], x[0][2 * i + 1]);
+            mx4[2 + (i & 1)] = max3(mx4[2 + (i & 1)], x[1][2 * i], x[1][2 * i + 1]);
+          }
+          const float top = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * a;
+          if (__any_sync(0xffffffffu, top - kBias > mu + kSlack)) {
+            const float nm = top - kBias > mu + kSlack ? ceilf(top) - kBias : mu;
+            const float g = shrink(mu, nm);
+            lsum[0].x *= g, lsum[0].y *= g, lsum[1].x *= g, lsum[1].y *= g;
+            const __half2 g2 = __float2half2_rn(g);
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c = 0; c < 2 * k; ++c) {   // this unit's P so far, exactly (a power of two)
+              uint32_t o[8];
+              tmem_ld8_issue(ts + 8 * c, o);
+              tmem_ld8_wait(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), g2);
+                o[i] = *reinterpret_cast<const uint32_t*>(&w);
+              }
+              tmem_st8(ts + 8 * c, o);
+            }
+            mu = nm;
+          }
+          weights(x[0], k);
           if (k == 0) tmem_ld32_issue(ts + 64, x[0]);
           weights(x[1], k + 1);
-          if (k == 0) tmem_ld32_wait(x[0]);
-          store(x[1], k + 1);
+          if (k == 0) tmem_ld32_issue(ts + 96, x[1]);
+        }
+        if (__any_sync(0xffffffffu, mu != m)) {   // the rows of O move
+          const float f = shrink(m, mu);
+          l *= f;
+          if (j > 0) {
+            wait(&o_done[t], js - 1, 62);
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < D / 8; ++k) {
+              uint32_t o[8];
+              tmem_ld8_issue(to + 8 * k, o);
+              tmem_ld8_wait(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st8(to + 8 * k, o);
+            }
+          }
+          m = mu;
         }
         l += (lsum[0].x + lsum[1].x) + (lsum[0].y + lsum[1].y);
-        hi -= kPromptTile, hi_all -= kPromptTile, lo -= kPromptTile, lo_all -= kPromptTile;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -475,6 +490,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       const float back = pow2i(max(s.ve - code_shift<FMT>(), -126));
       if (s.slot < 0) {
+        const int row = s.row0 + 128 * t + r, tok = min(row, s.rows - 1) / p.group;
+        const bool real = row < s.rows;
         const float inv = l == 0.f ? 0.f : back / l;   // 0: no token (a NaN is not)
         const int64_t tk = static_cast<int64_t>(s.start) + tok;
         const int hd = s.h * p.group + row - tok * p.group;

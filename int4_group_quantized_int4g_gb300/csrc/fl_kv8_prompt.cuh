@@ -43,8 +43,9 @@ struct PromptWork {
 
   __host__ __device__ long long before(int i) const {   // units of a head's items before item i
     if (nc) return static_cast<long long>(i) * nc;
-    if (i >= items) return before(items - 1) + (q.kv + kPromptTile - 1) / kPromptTile;
-    return i + floor_sum(i, g, 2, (static_cast<long long>(past) * g + 255) / 128);
+    const int k = min(i, items - 1);
+    const long long n = k + floor_sum(k, g, 2, (static_cast<long long>(past) * g + 255) / 128);
+    return i < items ? n : n + (q.kv + kPromptTile - 1) / kPromptTile;
   }
   __host__ __device__ int tiles(int i) const { return static_cast<int>(before(i + 1) - before(i)); }
   __host__ __device__ int item_of(long long u) const {   // the item that unit u of a head lies in

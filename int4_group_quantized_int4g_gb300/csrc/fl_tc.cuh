@@ -73,6 +73,37 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Bounded wait for phase `parity` of `bar`, false when the limit ran out, for
+// kernels with many waiting warps: the plain try (with a suspend-time hint each
+// try compiles to a sleep and a clock read besides) and the clock only every 64
+// of them.
+__device__ __forceinline__ bool mbar_try_plain(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_many(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_plain(bar, parity)) return true;
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t n = 1; !mbar_try_plain(bar, parity); ++n) {
+    if ((n & 63u) == 0) {
+      const unsigned long long now = globaltimer();
+      if (t0 == 0)
+        t0 = now;
+      else if (now - t0 > kWaitLimitNs)
+        return false;
+    }
+  }
+  return true;
+}
+
 // One thread of the (converged) warp, chosen by elect.sync.
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
