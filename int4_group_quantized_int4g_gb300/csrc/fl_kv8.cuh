@@ -126,10 +126,11 @@ struct Start {
   long long U, base;
   int P, b;
 };
+// scratch: shared memory for THREADS / 32 + 2 numbers, free again after a barrier.
 template <int THREADS, typename F>
-__device__ __forceinline__ Start find_start(int B, int c0, int ctas, int least, F&& units_of) {
-  __shared__ long long scan[THREADS / 32];
-  __shared__ long long hit[2];
+__device__ __forceinline__ Start find_start(long long* scratch, int B, int c0, int ctas, int least, F&& units_of) {
+  long long* scan = scratch;
+  long long* hit = scratch + THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool one = B <= THREADS;   // with one chunk of sequences the first pass has it all
   long long U = 0;

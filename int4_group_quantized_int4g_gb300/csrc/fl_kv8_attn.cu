@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     fence_mbar_init();
   }
 
-  const Start start = find_start<kRowsThreads>(p.seqs.B, blockIdx.x, gridDim.x, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
+  __shared__ long long scratch[kRowsThreads / 32 + 2];
+  const Start start = find_start<kRowsThreads>(scratch, p.seqs.B, blockIdx.x, gridDim.x, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
   const long long U = start.U;
   const int P = start.P, c = blockIdx.x;
   if (c >= P) return;

@@ -23,9 +23,9 @@
 //               (tokens along K) with byte permutes: the order of output
 //               columns is free, so value element 4 l + j goes to row j D/4 + l,
 //               which makes the writes conflict-free
-//   16          issues the MMAs
-//   17          copies pages by TMA into a staging tile for keys and for values
-//   18          walks the CTA's units and publishes their segments to the others
+//   16, 17      issue the MMAs of row tile 0, 1
+//   18          copies pages by TMA into a staging tile for keys and for values
+//   19          walks the CTA's units and publishes their segments to the others
 //
 // Scales: with e_b the power of two in a block's scale and e_ref the largest of
 // the segment's, codes are multiplied by 2^(e_b - e_ref + k) as they
@@ -42,7 +42,7 @@ using namespace flkv;
 namespace {
 
 constexpr int kPrThreads = 640;
-constexpr int kConv0 = 8, kIssue0 = 16, kProd = 17, kPlan = 18;   // first warps of the roles
+constexpr int kConv0 = 8, kIssue0 = 16, kProd = 18, kPlan = 19;   // first warps of the roles
 constexpr int kConvWarps = 4;                         // for keys, and for values
 // Registers a thread: all at launch, then by role (warps 16..19 share one count)
 constexpr int kRegs = 96, kRegsSoftmax = 136, kRegsConv = 64, kRegsRest = 80;
@@ -63,8 +63,8 @@ struct PrCfg {
   static constexpr int kRatioOff = kMetaOff + 8 * 8 * 8;   // [8][8]: the codes' multipliers, f16 pairs
   static constexpr int kSegOff = kRatioOff + 8 * 8 * 8;    // [4] segments
   static constexpr int kBarOff = kSegOff + 4 * 64;
-  static constexpr int kBars = 4 + 8 + 2 + 2 + 2 + 2 + 8;
-  static constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;
+  static constexpr int kBars = 4 + 8 + 2 + 4 + 4 + 4 + 8;
+  static constexpr int kSmem = kBarOff + kBars * 8 + 16;
   static constexpr int kSlot = kPromptRows * (D + 2);      // floats of a partial: O [D][256], m, l [256][2]
   static_assert(kSmem <= 232448, "shared memory");
 };
@@ -248,8 +248,9 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
     k_kv8_prompt(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
   using C = PrCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // No static shared memory: the dynamic part begins the CTA's window, on the
+  // 1024-byte boundary that the swizzled tiles need (checked below).
+  extern __shared__ __align__(1024) uint8_t smem[];
   float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff);
   uint2* ratios = reinterpret_cast<uint2*>(smem + C::kRatioOff);
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegOff);
@@ -260,35 +261,40 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + 2;
   uint64_t* q_full = v_empty + 2;        // [row tile]
+  // [row tile][buffer]: with one barrier a tile a phase could complete twice before its waiter looks
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint64_t* seg_full = o_done + 2;       // [4]
+  uint64_t* p_full = s_full + 4;
+  uint64_t* o_done = p_full + 4;
+  uint64_t* seg_full = o_done + 4;       // [4]
   uint64_t* seg_empty = seg_full + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 56);
+    return;
+  }
   pdl_launch_dependents();   // (the joining kernel waits for the end of this one itself)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&stg_full[i], 1);
       mbar_init(&stg_empty[i], kConvWarps);
       mbar_init(&k_full[i], kConvWarps);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 2);
       mbar_init(&v_full[i], kConvWarps);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 2);
       mbar_init(&q_full[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
       mbar_init(&seg_full[i], 1);
       mbar_init(&seg_empty[i], kPlan);   // one arrival of every warp before the planner
     }
     fence_mbar_init();
   }
-  const Start start = find_start<kPrThreads>(p.seqs.B, blockIdx.x, gridDim.x, kPromptLeast, [&](int b) {
+  const Start start = find_start<kPrThreads>(reinterpret_cast<long long*>(smem + C::kStgOff), p.seqs.B, blockIdx.x, gridDim.x, kPromptLeast, [&](int b) {
     return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
   if (static_cast<int>(blockIdx.x) >= start.P) return;
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   tc_fence_before();
   cta_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;   // S/P of row tile t at 128 t, O at 256 + D t
+  const uint32_t tmem = *tmem_slot;   // S of row tile t and half b at 128 t + 64 b, P over it, O at 256 + D t
   bool ok = true;   // false after a wait ran out: nothing is waited for or issued any more
   auto wait_one = [&](uint64_t* bar, uint32_t phase, int where) {
     if (ok && !mbar_wait_many(bar, phase & 1u)) {
@@ -317,10 +323,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     regs_up<kRegsSoftmax>();
     const int t = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + D * t;
-    uint32_t js = 0;    // units of this row tile so far
-    // the factor of weights whose reference moves up
-    auto shrink = [](float from, float to) { return from == to ? 1.f : exp2_approx(from - to); };
+    const uint32_t to = tmem + lanes + 256 + D * t;
+    uint32_t js = 0;    // half units of this row tile so far
     for (int seg = 0; ok; ++seg) {
       wait(&seg_full[seg & 3], seg >> 2, 59);
       const Segment& s = segs[seg & 3];
@@ -365,16 +369,17 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
       }
-      // units [plain_begin, plain_end) of which every row of the tile sees every token
+      // half units [plain_begin, plain_end) of which every row of the tile sees every token
       int plain_begin = 0, plain_end;
       {
         const int r0 = s.row0 + 128 * t, pos = s.tile * kPromptTile;
-        plain_end = (s.past + r0 / p.group + 1 - pos) >> 7;
-        if (p.window) plain_begin = (s.past + min(r0 + 127, s.rows - 1) / p.group + 1 - p.window - pos + 127) >> 7;
+        plain_end = (s.past + r0 / p.group + 1 - pos) >> 6;
+        if (p.window) plain_begin = (s.past + min(r0 + 127, s.rows - 1) / p.group + 1 - p.window - pos + 63) >> 6;
       }
       float m = -INFINITY, l = 0.f;   // weights are 2^(x - m); the reference m is an integer, about kBias below a maximum
-      for (int j = 0; j < live; ++j, ++js) {
-        wait(&s_full[t], js, 61);
+      for (int j = 0; j < 2 * live; ++j, ++js) {
+        const uint32_t ts = tmem + lanes + 128 * t + 64 * (js & 1);
+        wait(&s_full[2 * t + (js & 1)], js >> 1, 61);
         tc_fence_after();
         // The loops of all roles are kept short on purpose: unrolled, they do not
         // fit the instruction cache together, and a unit took twice as long.  And
@@ -383,86 +388,40 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         if (j >= plain_end || j < plain_begin || general) {
           // S as it is meant, back to its columns: the keys' mantissas, -inf
           // where this row does not see the token
-          const int pos = (s.tile + j) * kPromptTile;
+          const int pos = s.tile * kPromptTile + 64 * j;
           const int hi = s.past + min(s.row0 + 128 * t + r, s.rows - 1) / p.group + 1 - pos;   // columns [lo, hi) are seen
           const int lo = p.window ? hi - p.window : -0x40000000;
 #pragma unroll 1
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             float v[16];
             tmem_ld16f(ts + 16 * k, v);
-            const float mk = general ? meta[((s.meta + j) & 7) * 8 + k].x : 1.f;
+            const float mk = general ? meta[((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1) + k].x : 1.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = 16 * k + i >= hi || 16 * k + i < lo ? -INFINITY : v[i] * mk;
             tmem_st16f(ts + 16 * k, v);
           }
           tmem_wait_st();
         }
-        float mu = m;   // the reference of this unit's weights
-        float2 lsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weights = [&](float (&v)[32], int k) {   // columns 32 k .. of S become columns 16 k .. of P
-          const float mm = mu == -INFINITY ? 0.f : -mu;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(a, a), make_float2(mm, mm));
-            v[2 * i] = exp2_approx(e.x), v[2 * i + 1] = exp2_approx(e.y);
-            lsum[i & 1] = __fadd2_rn(lsum[i & 1], make_float2(v[2 * i], v[2 * i + 1]));
-          }
-          if (general) {   // the values' mantissas
-            const float m0 = meta[((s.meta + j) & 7) * 8 + 2 * k].y, m1 = meta[((s.meta + j) & 7) * 8 + 2 * k + 1].y;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= i < 16 ? m0 : m1;
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-          tmem_st16(ts + 16 * k, pk);
-        };
-        // Half of the columns at a time: their maximum and, if it has outgrown
-        // the reference, a new one; then their weights, while the other half loads.
         float x[2][32];
         tmem_ld32_issue(ts, x[0]);
         tmem_ld32_issue(ts + 32, x[1]);
-#pragma unroll 1
-        for (int k = 0; k < 4; k += 2) {
-          tmem_ld32_wait(x[0]);
-          tmem_ld32_wait(x[1]);
-          float mx4[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
+        tmem_ld32_wait(x[0]);
+        tmem_ld32_wait(x[1]);
+        float mx4[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
 #pragma unroll
-          for (int i = 1; i < 16; ++i) {
-            mx4[i & 1] = max3(mx4[i & 1], x[0][2 * i], x[0][2 * i + 1]);
-            mx4[2 + (i & 1)] = max3(mx4[2 + (i & 1)], x[1][2 * i], x[1][2 * i + 1]);
-          }
-          const float top = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * a;
-          if (__any_sync(0xffffffffu, top - kBias > mu + kSlack)) {
-            const float nm = top - kBias > mu + kSlack ? ceilf(top) - kBias : mu;
-            const float g = shrink(mu, nm);
-            lsum[0].x *= g, lsum[0].y *= g, lsum[1].x *= g, lsum[1].y *= g;
-            const __half2 g2 = __float2half2_rn(g);
-            tmem_wait_st();
-#pragma unroll 1
-            for (int c = 0; c < 2 * k; ++c) {   // this unit's P so far, exactly (a power of two)
-              uint32_t o[8];
-              tmem_ld8_issue(ts + 8 * c, o);
-              tmem_ld8_wait(o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __half2 w = __hmul2(*reinterpret_cast<const __half2*>(&o[i]), g2);
-                o[i] = *reinterpret_cast<const uint32_t*>(&w);
-              }
-              tmem_st8(ts + 8 * c, o);
-            }
-            mu = nm;
-          }
-          weights(x[0], k);
-          if (k == 0) tmem_ld32_issue(ts + 64, x[0]);
-          weights(x[1], k + 1);
-          if (k == 0) tmem_ld32_issue(ts + 96, x[1]);
+        for (int i = 1; i < 16; ++i) {
+          mx4[i & 1] = max3(mx4[i & 1], x[0][2 * i], x[0][2 * i + 1]);
+          mx4[2 + (i & 1)] = max3(mx4[2 + (i & 1)], x[1][2 * i], x[1][2 * i + 1]);
         }
-        if (__any_sync(0xffffffffu, mu != m)) {   // the rows of O move
-          const float f = shrink(m, mu);
+        const float top = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * a - kBias;
+        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+          // a maximum has outgrown its reference: the rows of O and the sum move
+          const float nm = top > m + kSlack ? ceilf(top) : m;
+          const float f = nm == m ? 1.f : exp2_approx(m - nm);
+          m = nm;
           l *= f;
           if (j > 0) {
-            wait(&o_done[t], js - 1, 62);
+            wait(&o_done[2 * t + ((js - 1) & 1)], (js - 1) >> 1, 62);
             tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < D / 8; ++k) {
@@ -474,18 +433,39 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               tmem_st8(to + 8 * k, o);
             }
           }
-          m = mu;
+        }
+        const float mm = m == -INFINITY ? 0.f : -m;
+        float2 lsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = __ffma2_rn(make_float2(x[k][2 * i], x[k][2 * i + 1]), make_float2(a, a), make_float2(mm, mm));
+            x[k][2 * i] = exp2_approx(e.x), x[k][2 * i + 1] = exp2_approx(e.y);
+            lsum[i & 1] = __fadd2_rn(lsum[i & 1], make_float2(x[k][2 * i], x[k][2 * i + 1]));
+          }
+          if (general) {   // the values' mantissas
+            const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1) + 2 * k;
+            const float m0 = mt[0].y, m1 = mt[1].y;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[k][i] *= i < 16 ? m0 : m1;
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = pack_f16(x[k][2 * i], x[k][2 * i + 1]);
+          tmem_st16(ts + 16 * k, pk);   // over columns of S that have been read
         }
         l += (lsum[0].x + lsum[1].x) + (lsum[0].y + lsum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[t]);
+        if (lane == 0) mbar_arrive(&p_full[2 * t + (js & 1)]);
       }
 
       // ---------------- the rows' output, or their partial
       if (live > 0) {
-        wait(&o_done[t], js - 1, 63);
+        wait(&o_done[2 * t], (js - 2) >> 1, 63);       // (js is even: the last use of either buffer)
+        wait(&o_done[2 * t + 1], (js - 2) >> 1, 63);
         tc_fence_after();
       }
       const float back = pow2i(max(s.ve - code_shift<FMT>(), -126));
@@ -647,70 +627,81 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
   } else {
     regs_down<kRegsRest>();
-    if (warp == kIssue0) {
-      // ---------------- the MMAs.  Row tile 0's P V and next S go
-      // out before row tile 1's, which keeps the two half a unit apart: while
-      // one is at its softmax the other is at its products.
+    if (warp < kProd) {
+      // ---------------- the MMAs of row tile t, in half units of 64 tokens.  S has
+      // two buffers, so that the softmax finds the next half ready: when P of
+      // half n has come, O += P V of it, then S of half n + 2 into its place.
       // (The whole warp walks through and an elected lane issues: the
       // descriptors stay in uniform registers.  With one lane in a branch of its
       // own an MMA took 110 cycles to issue, 64 is its time.)
-      int i = 0;
-      uint32_t jt0 = 0, jt1 = 0, lived0 = 0, lived1 = 0;   // units and segments with work of each row tile so far
+      const int t = __shfl_sync(0xffffffffu, warp - kIssue0, 0);
+      const uint32_t ts = tmem + 128 * t, to = tmem + 256 + D * t;
+      const uint64_t qd = sw128_desc(smem_u32(smem + t * C::kQ));
+      const uint64_t kd0 = sw128_desc(smem_u32(smem + C::kKOff)), vd0 = sw128_desc(smem_u32(smem + C::kVOff));
+      int i = 0;                       // first unit of the segment
+      uint32_t ju = 0, lived = 0;      // units and segments with work of this row tile so far
       for (int seg = 0; ok; ++seg) {
         wait(&seg_full[seg & 3], seg >> 2, 59);
         const Segment& s = segs[seg & 3];
-        const int units = __shfl_sync(0xffffffffu, s.units, 0), live0 = __shfl_sync(0xffffffffu, s.live[0], 0);
-        const int live1 = __shfl_sync(0xffffffffu, s.live[1], 0);
+        const int units = __shfl_sync(0xffffffffu, s.units, 0), live = __shfl_sync(0xffffffffu, s.live[t], 0);
         if (!ok || units < 0) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&seg_empty[seg & 3]);
-        // step -1 has the first S of both tiles, step j their P V and next S
-#pragma unroll 1
-        for (int j = units > 0 ? -1 : 0; j < units; ++j) {
-          const int st = i & 1, nx = j >= 0 ? i + 1 : i;   // nx: the unit of the next S
-          if (j >= 0) wait(&v_full[st], i >> 1, 71);
-          if (j + 1 < units) wait(&k_full[nx & 1], nx >> 1, 69);
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            const int live = t ? live1 : live0;
-            if (j >= live || live == 0) continue;
-            uint32_t jt = t ? jt1 : jt0;
-            if (j >= 0) {
-              wait(&p_full[t], jt, 72);
-              tc_fence_after();
-              if (ok && elect_one()) {
-                const uint64_t vd = sw128_desc(smem_u32(smem + C::kVOff + st * C::kKv));
+        auto scores = [&](int unit, int b) {   // S of half b of a unit
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint64_t kd = kd0 + (((unit & 1) * C::kKv + b * (64 * 128)) >> 4);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  umma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * k, vd + (((k >> 2) * (D * 128) + (k & 3) * 32) >> 4),
-                              idesc_f16(D), j != 0 || k != 0);
-                if (t == 1 || j >= live1) umma_commit(&v_empty[st]);
-                umma_commit(&o_done[t]);   // (last: the CTA may end once it has come)
-              }
-              __syncwarp();
-              ++jt;
-              if (t) jt1 = jt; else jt0 = jt;
-            } else {
-              wait(&q_full[t], t ? lived1++ : lived0++, 68);
-            }
-            if (j + 1 < live) {
-              if (jt > 0) wait(&o_done[t], jt - 1, 70);   // P, which lies over S, has been read
-              tc_fence_after();
-              if (ok && elect_one()) {
-                const uint64_t qd = sw128_desc(smem_u32(smem + t * C::kQ));
-                const uint64_t kd = sw128_desc(smem_u32(smem + C::kKOff + (nx & 1) * C::kKv));
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                  umma_f16_ss(tmem + 128 * t, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                              kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), idesc_f16(128), k != 0);
-                if (t == 1 || j + 1 >= live1) umma_commit(&k_empty[nx & 1]);
-                umma_commit(&s_full[t]);
-              }
-              __syncwarp();
-            }
+            for (int k = 0; k < D / 16; ++k)
+              umma_f16_ss(ts + 64 * b, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                          kd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), idesc_f16(64), k != 0);
+            if (b) umma_commit(&k_empty[unit & 1]);
+            umma_commit(&s_full[2 * t + b]);
           }
-          if (j >= 0) ++i;
+          __syncwarp();
+        };
+        if (units > 0) wait(&k_full[i & 1], i >> 1, 69);
+        if (live > 0) {
+          wait(&q_full[t], lived++, 68);
+          scores(i, 0);
+          scores(i, 1);
         }
+#pragma unroll 1
+        for (int j = 0; j < units; ++j) {
+          const int unit = i + j, st = unit & 1;
+          wait(&v_full[st], unit >> 1, 71);
+          if (j + 1 < units) wait(&k_full[st ^ 1], (unit + 1) >> 1, 69);
+          if (j < live) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              wait(&p_full[2 * t + b], ju, 72);
+              tc_fence_after();
+              if (ok && elect_one()) {
+                const uint64_t vd = vd0 + ((st * C::kKv + b * (D * 128)) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_f16_ts(to, ts + 64 * b + 8 * k, vd + ((k * 32) >> 4), idesc_f16(D), j != 0 || b != 0 || k != 0);
+                if (b) umma_commit(&v_empty[st]);
+                umma_commit(&o_done[2 * t + b]);   // (last: the CTA may end once it has come)
+              }
+              __syncwarp();
+              if (j + 1 < live) {
+                wait(&o_done[2 * t + b], ju, 70);   // P, which lies over S, has been read
+                scores(unit + 1, b);
+              }
+            }
+            ++ju;
+          } else if (lane == 0) {
+            mbar_arrive(&v_empty[st]);
+          }
+          // units past this row tile's: their keys are not read either
+          if (lane == 0) {
+            if (j == 0 && live == 0) mbar_arrive(&k_empty[st]);
+            if (j + 1 < units && j + 1 >= live) mbar_arrive(&k_empty[st ^ 1]);
+          }
+          __syncwarp();
+        }
+        i += units;
       }
     } else if (warp == kProd) {
       // ---------------- pages: lane i has page i of a batch of 32
@@ -840,7 +831,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(kPromptRows) k_kv8_join(const AttnParams p, int ctas) {
   const int c = blockIdx.x + 1;
-  const Start start = find_start<kPromptRows>(p.seqs.B, c, ctas, kPromptLeast, [&](int b) {
+  __shared__ long long scratch[kPromptRows / 32 + 2];
+  const Start start = find_start<kPromptRows>(scratch, p.seqs.B, c, ctas, kPromptLeast, [&](int b) {
     return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
   pdl_wait();   // every block: the kernels after this one must find the one before it done
