@@ -9,7 +9,9 @@ Function names match the C entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 from . import _build
 
@@ -94,12 +96,11 @@ SIGNATURES = {
     "fl_rmsnorm": (_i, [_vp, _l, _vp, _l, _vp, ctypes.c_float, _i, _i, _i, _vp, _l, _vp, _l, _vp, _vp, _i, _vp]),
     "fl_rope": (_i, [_vp, _l, _i, _vp, _l, _i, _i, _i, _i, _i, _vp, _i, ctypes.POINTER(ctypes.c_int32), _vp,
                      _vp, _l, _vp, _l, _vp]),
-    "fl_kv8_append": (_i, [_vp, _l, _vp, _l, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), _vp, _vp]),
+    "fl_kv8_append": (_i, [_vp, _l, _vp, _l, _vp, _vp, _vp, _vp]),
     "fl_kv8_test_pages": (_i, [ctypes.POINTER(FlKv8Seqs), _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_test_units": (_i, [_i, _i, _i, _i, _i, ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_attention_workspace": (_i, [_i, _i, _i, _i, _i, _c_size_p]),
-    "fl_kv8_attention": (_i, [_vp, _l, _i, ctypes.POINTER(FlKv8Cache), ctypes.POINTER(FlKv8Seqs), ctypes.c_float, _i,
-                              _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fl_kv8_attention": (_i, [_vp, _l, _i, _vp, _vp, ctypes.c_float, _i, _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _LIB = None
@@ -127,9 +128,15 @@ def lib():
     return _LIB
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _check(where, rc):
@@ -163,7 +170,9 @@ _WS = {}
 def _workspace(nbytes, device):
     """A zero-filled workspace per (device, stream), grown on demand."""
     torch = _torch()
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    key = (device.index, raw(device.index) if raw is not None and device.index is not None
+           else torch.cuda.current_stream(device).cuda_stream)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -416,25 +425,40 @@ def fl_moe_router_logits(x, w_router, logits=None, ws=None):
 
 
 # ------------------------------------------------- decoder-layer operators
+# These calls sit between the linears of a decode step, where the host's time
+# for a call counts: pointers go as plain integers, and the two structures of a
+# cache call as packed bytes.
+
+_KV8_CACHE = struct.Struct("PPPPiiiii")   # struct fl_kv8_cache
+_KV8_SEQS = struct.Struct("PPPiiii")      # struct fl_kv8_seqs
+
+
+def _raise(name, what):
+    raise ValueError(f"{name}: {what}")
+
+
+def _ptr(t, dtype, name):
+    """Address of a contiguous CUDA tensor of the given type."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _raise(name, f"expected a contiguous {dtype} CUDA tensor, got {t.dtype}, strides {t.stride()}, on {t.device}")
+    return t.data_ptr()
+
 
 def _tokens(t, name):
-    """(pointer, token stride) of bf16 [tokens, heads, width] whose heads are
-    packed; the tokens may be rows of a wider projection."""
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dtype is not _torch().bfloat16:
-        raise ValueError(f"{name}: expected bfloat16, got {t.dtype}")
-    n, h, w = t.shape
-    st = t.stride()
-    if (w > 1 and st[2] != 1) or (h > 1 and st[1] != w):
-        raise ValueError(f"{name}: the heads of a token must be packed")
-    return t.data_ptr(), st[0] if n > 1 else h * w   # (the stride of a single token means nothing)
-
-
-def _typed(t, dtype, name):
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    return _p(t)
+    """(address, token stride) of bf16 [tokens, heads, width], or [tokens,
+    width], whose heads are packed; tokens may be rows of a wider projection."""
+    st, sh = t.stride(), t.shape
+    if t.dtype is not _TORCH.bfloat16 or not t.is_cuda:
+        _raise(name, f"expected a bfloat16 CUDA tensor, got {t.dtype} on {t.device}")
+    if len(sh) == 3:
+        n, h, w = sh
+        if (st[2] != 1 and w > 1) or (st[1] != w and h > 1):
+            _raise(name, "the heads of a token must be packed")
+        return t.data_ptr(), st[0] if n > 1 else h * w   # (the stride of a single token means nothing)
+    n, w = sh
+    if st[1] != 1 and w > 1:
+        _raise(name, "the columns of a row must be packed")
+    return t.data_ptr(), st[0] if n > 1 else w
 
 
 def fl_rmsnorm(x, weight=None, eps=1e-6, residual=None, y=None, residual_out=None, out8=False, group=0, need_y=True):
@@ -445,39 +469,51 @@ def fl_rmsnorm(x, weight=None, eps=1e-6, residual=None, y=None, residual_out=Non
     for group 0).  y and residual_out may be given, and may be x or residual."""
     torch = _torch()
     shape = x.shape
-    if len(shape) not in (2, 3):
-        raise ValueError("fl_rmsnorm: x is [M, H] or [M, heads, H]")
-
-    def rows(t, name):
-        if t.shape != shape:
-            raise ValueError(f"fl_rmsnorm: {name} and x differ in shape")
-        return _tokens(t if len(shape) == 3 else t.unsqueeze(1), name)
-
-    M, heads, H = shape if len(shape) == 3 else (shape[0], 1, shape[1])
-    xp, xs = rows(x, "x")
-    rp, rs = rows(residual, "residual") if residual is not None else (None, 0)
+    if len(shape) == 2:
+        M, H = shape
+        heads = 1
+    elif len(shape) == 3:
+        M, heads, H = shape
+    else:
+        _raise("fl_rmsnorm", "x is [M, H] or [M, heads, H]")
+    xp, xs = _tokens(x, "x")
     out = {}
+    rp, rs, op, os_, yp, ys, cp, sp, wp = None, 0, None, 0, None, 0, None, None, None
+    if residual is not None:
+        if residual.shape != shape:
+            _raise("fl_rmsnorm", "residual and x differ in shape")
+        rp, rs = _tokens(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     if y is None and need_y:
         y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    yp, ys = rows(y, "y") if y is not None else (None, 0)
-    op, os_ = rows(residual_out, "residual_out") if residual_out is not None else (None, 0)
     if y is not None:
+        if y.shape != shape:
+            _raise("fl_rmsnorm", "y and x differ in shape")
+        yp, ys = _tokens(y, "y")
         out["y"] = y
     if residual_out is not None:
+        if residual_out.shape != shape:
+            _raise("fl_rmsnorm", "residual_out and x differ in shape")
+        op, os_ = _tokens(residual_out, "residual_out")
         out["residual"] = residual_out
-    cp = sp = None
     if out8:
-        out["codes"] = torch.empty(shape, dtype=torch.uint8, device=x.device)
-        out["scales"] = torch.empty((*shape[:-1], H // group if group else 1), dtype=torch.float32, device=x.device)
-        cp, sp = out["codes"].data_ptr(), out["scales"].data_ptr()
-    if weight is not None and weight.numel() != H:
-        raise ValueError("fl_rmsnorm: weight is [H]")
-    wp = _typed(weight, torch.bfloat16, "weight") if weight is not None else None
+        codes = out["codes"] = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        scales = out["scales"] = torch.empty((*shape[:-1], H // group if group else 1), dtype=torch.float32,
+                                             device=x.device)
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    if weight is not None:
+        if weight.numel() != H:
+            _raise("fl_rmsnorm", "weight is [H]")
+        wp = _ptr(weight, torch.bfloat16, "weight")
     _check("fl_rmsnorm", lib().fl_rmsnorm(xp, xs, rp, rs, wp, eps, M, heads, H, yp, ys, op, os_, cp, sp,
                                           group if out8 else 0, _stream()))
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _sections(sections):
+    return (ctypes.c_int32 * len(sections))(*sections)
 
 
 def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k_out=None):
@@ -491,51 +527,52 @@ def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k
     qp, qs = _tokens(q, "q")
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    elif q_out.shape != q.shape:
+        _raise("fl_rope", "q_out and q differ in shape")
     qop, qos = _tokens(q_out, "q_out")
     kp, ks, kop, kos, Hk = None, 0, None, 0, 0
     if k is not None:
-        Hk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D:
-            raise ValueError("fl_rope: q and k differ in tokens or width")
+        Tk, Hk, Dk = k.shape
+        if Tk != T or Dk != D:
+            _raise("fl_rope", "q and k differ in tokens or width")
         kp, ks = _tokens(k, "k")
         if k_out is None:
             k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
-        if k_out.shape != k.shape:
-            raise ValueError("fl_rope: k_out and k differ in shape")
+        elif k_out.shape != k.shape:
+            _raise("fl_rope", "k_out and k differ in shape")
         kop, kos = _tokens(k_out, "k_out")
-    if q_out.shape != q.shape:
-        raise ValueError("fl_rope: q_out and q differ in shape")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if positions.shape[-1] != T or (sections is not None and len(sections) != axes):
-        raise ValueError("fl_rope: positions are [n_axes, T], sections [n_axes]")
-    sec = (ctypes.c_int32 * axes)(*sections) if sections is not None else None
+    psh = positions.shape
+    axes = psh[0] if len(psh) == 2 else 1
+    if psh[-1] != T or (sections is not None and len(sections) != axes):
+        _raise("fl_rope", "positions are [n_axes, T], sections [n_axes]")
     _check("fl_rope", lib().fl_rope(qp, qs, Hq, kp, ks, Hk, T, D, 2 * inv_freq.numel(),
                                     FL_ROPE_HALVES if halves else FL_ROPE_PAIRS,
-                                    _typed(positions, torch.int32, "positions"), axes, sec,
-                                    _typed(inv_freq, torch.float64, "inv_freq"), qop, qos, kop, kos, _stream()))
+                                    _ptr(positions, torch.int32, "positions"), axes,
+                                    _sections(tuple(sections)) if sections is not None else None,
+                                    _ptr(inv_freq, torch.float64, "inv_freq"), qop, qos, kop, kos, _stream()))
     return q_out, k_out
 
 
 def _kv8(where, T, heads, dim, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt):
-    """The two structures of a cache call, from its tensors."""
-    torch = _torch()
-    nb, hk, block, d = k_cache.shape
-    B = kv_lens.shape[0]
-    if v_cache.shape != k_cache.shape or k_scale.shape != (nb, hk) or v_scale.shape != (nb, hk):
-        raise ValueError(f"{where}: the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
+    """The two structures of a cache call, from its tensors, and B and kv_heads."""
+    torch = _TORCH
+    shape = k_cache.shape
+    nb, hk, block, d = shape
+    if v_cache.shape != shape or k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        _raise(where, "the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
     if d != dim or (heads is not None and heads != hk):
-        raise ValueError(f"{where}: the tokens and the cache differ in heads or width")
-    if block_table.dim() != 2 or block_table.shape[0] != B or (cu_q is not None and cu_q.shape != (B + 1,)):
-        raise ValueError(f"{where}: block_table is [B, max_blocks], kv_lens [B], cu_q [B + 1]")
+        _raise(where, "the tokens and the cache differ in heads or width")
+    B = kv_lens.numel()
+    rows, most = block_table.shape
+    if rows != B or (cu_q is not None and cu_q.numel() != B + 1):
+        _raise(where, "block_table is [B, max_blocks], kv_lens [B], cu_q [B + 1]")
     if max_q is None:
         max_q = T // B if cu_q is None else T
-    c = FlKv8Cache(_typed(k_cache, torch.uint8, "k_cache"), _typed(v_cache, torch.uint8, "v_cache"),
-                   _typed(k_scale, torch.float32, "k_scale"), _typed(v_scale, torch.float32, "v_scale"),
-                   nb, block, hk, d, fmt)
-    s = FlKv8Seqs(_typed(cu_q, torch.int32, "cu_q") if cu_q is not None else None,
-                  _typed(kv_lens, torch.int32, "kv_lens"), _typed(block_table, torch.int32, "block_table"),
-                  T, B, max_q, block_table.shape[1])
-    return c, s
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    return (_KV8_CACHE.pack(_ptr(k_cache, u8, "k_cache"), _ptr(v_cache, u8, "v_cache"), _ptr(k_scale, f32, "k_scale"),
+                            _ptr(v_scale, f32, "v_scale"), nb, block, hk, d, fmt),
+            _KV8_SEQS.pack(_ptr(cu_q, i32, "cu_q") if cu_q is not None else 0, _ptr(kv_lens, i32, "kv_lens"),
+                           _ptr(block_table, i32, "block_table"), T, B, max_q, most), B, hk)
 
 
 def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q=None, max_q=None,
@@ -546,15 +583,16 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     its kv_lens[b] tokens; token j lives in block block_table[b][j // block].
     status: the status block to record device-side errors in (an int32 or uint8
     CUDA tensor of 16 bytes or a workspace; None: this stream's workspace)."""
+    _torch()
     T, h, d = k.shape
     if v.shape != k.shape:
-        raise ValueError("fl_kv8_append: k and v differ in shape")
+        _raise("fl_kv8_append", "k and v differ in shape")
     kp, ks = _tokens(k, "k")
     vp, vs = _tokens(v, "v")
-    c, s = _kv8("fl_kv8_append", T, h, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
+    c, s, _, _ = _kv8("fl_kv8_append", T, h, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
     if status is None:
         status = _workspace(256, k.device)
-    _check("fl_kv8_append", lib().fl_kv8_append(kp, ks, vp, vs, ctypes.byref(c), ctypes.byref(s), _p(status), _stream()))
+    _check("fl_kv8_append", lib().fl_kv8_append(kp, ks, vp, vs, c, s, _p(status), _stream()))
 
 
 def fl_kv8_test_pages(kv_lens, table, T, num_blocks, block, b, cu_q=None, max_q=None, window=0):
@@ -589,26 +627,35 @@ def fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim):
     return out.value
 
 
+@functools.lru_cache(maxsize=4096)
+def _kv8_workspace(device_index, T, B, Hq, kv_heads, head_dim):
+    return fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim)
+
+
 def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q=None, max_q=None,
                      fmt=FL_KV8_E4M3, scale=None, window=0, out=None, return_lse=False, ws=None):
     """Attention of bf16 q [T, Hq, head_dim] over the 8-bit cache (tensors as
     for fl_kv8_append; kv_lens count the tokens already written, the rows of q
     among them).  Row i of a sequence sees the tokens up to its own position,
     with window > 0 only the last `window`.  scale: 1 / sqrt(head_dim) by
-    default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32)."""
+    default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32).
+    ws: a workspace of the caller's, zero-filled before its first use; give one
+    to calls that are captured in a graph."""
     torch = _torch()
     T, Hq, d = q.shape
     qp, qs = _tokens(q, "q")
-    c, s = _kv8("fl_kv8_attention", T, None, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
+    c, s, B, hk = _kv8("fl_kv8_attention", T, None, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q,
+                       max_q, fmt)
+    device = q.device
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
     elif out.shape != q.shape:
-        raise ValueError("fl_kv8_attention: out and q differ in shape")
+        _raise("fl_kv8_attention", "out and q differ in shape")
     op, os_ = _tokens(out, "out")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=device) if return_lse else None
     if ws is None:
-        ws = _workspace(fl_kv8_attention_workspace(T, s.B, Hq, c.kv_heads, d), q.device)
+        ws = _workspace(_kv8_workspace(device.index, T, B, Hq, hk, d), device)
     _check("fl_kv8_attention",
-           lib().fl_kv8_attention(qp, qs, Hq, ctypes.byref(c), ctypes.byref(s), d ** -0.5 if scale is None else scale,
-                                  window, op, os_, lse.data_ptr() if return_lse else None, _p(ws), ws.numel(), _stream()))
+           lib().fl_kv8_attention(qp, qs, Hq, c, s, d ** -0.5 if scale is None else scale, window, op, os_,
+                                  lse.data_ptr() if return_lse else None, _p(ws), ws.numel(), _stream()))
     return (out, lse) if return_lse else out
