@@ -10,10 +10,13 @@
 // equal run of them, whatever the sequences' lengths.  A tile of rows that
 // several CTAs share is joined by the last of them, in CTA order.
 //
-// Inside a CTA a producer warp copies the units' pages by TMA (swizzled, so
-// that both operand reads below are free of bank conflicts) into a ring, and
-// eight warps take 16 tokens of each unit with a softmax state of their own,
-// joined once a segment.  A warp's products are transposed, so that tokens
+// Inside a CTA each of eight warps takes 16 tokens of every unit, with a softmax
+// state of its own, joined once a segment.  A warp copies its slices by TMA
+// (swizzled, so that both operand reads below are free of bank conflicts) into
+// a ring of its own and waits for nobody else; two CTAs fit an SM with 8 rows.
+// (With one CTA, a producer warp and a ring that all warps share, reading was
+// held to 3.3 TB/s by the latency of the warps' chains of work.)
+// A warp's products are transposed, so that tokens
 // fill the 16 rows of mma.sync and query rows its 8 columns:
 //   S^T [16 tokens x 8 rows] = K q^T,   O^T [D x 8 rows] += V^T p^T.
 // Codes become f16 in registers, exactly; the contraction index of either
@@ -22,9 +25,10 @@
 // 4 x 4 bytes it transposes with byte permutes.
 // Scales stay out of the operands.  q is brought to [1, 2) by a power of two a
 // row (then f16 holds it with no loss that matters: 2^-25 of the row's largest
-// value).  x is scaled in fp32.  p is rounded to f16 (2^-11, against the
-// output's 2^-9) after a factor 2^14 v_scale / v_ref, v_ref the largest value
-// scale so far, so that it keeps its 11 bits down to 2^-28 of the largest
+// value).  x is scaled in fp32.  A row's reference m moves only when a maximum
+// has passed it by 2^8, so p reaches 2^8.  p is rounded to f16 (2^-11, against
+// the output's 2^-9) after a factor 2^6 v_scale / v_ref, v_ref the largest value
+// scale so far, so that it keeps its 11 bits down to 2^-20 of the largest
 // weight; the accumulators are in units of v_ref.  Sums are fp32.
 #include "fl_kv8_prompt.cuh"
 #include "fl_tc.cuh"
@@ -34,9 +38,10 @@ using namespace flkv;
 namespace {
 
 constexpr int kTile = 128;              // tokens of a unit
-constexpr int kWarps = 8;               // consumer warps
-constexpr int kRowsThreads = 32 * (kWarps + 1);
-constexpr float kPScale = 16384.f;      // 2^14
+constexpr int kWarps = 8;
+constexpr int kRowsThreads = 32 * kWarps;
+constexpr float kPScale = 64.f;         // 2^6
+constexpr float kSlack = 8.f;           // a reference may lag its maximum by 2^kSlack
 // Most rows of a sequence (query heads of a kv head x tokens) that this kernel
 // takes; sequences with more go to the tcgen05 kernel, in the same call.
 constexpr int kFewRows = 64;
@@ -44,17 +49,18 @@ constexpr int kFewRows = 64;
 template <int D, int NT>
 struct RowsCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kHalf = kTile * D;            // keys (or values) of a stage
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = D == 128 ? (NT == 1 ? 5 : 4) : 8;
+  static constexpr int kCtas = NT == 1 ? 2 : 1;      // on an SM
+  static constexpr int kHalf = 16 * D;               // a warp's keys (or values) of a unit
+  static constexpr int kSlots = (NT == 1 ? 3 : 6) * (128 / D);
+  static constexpr int kRing = kSlots * 2 * kHalf;   // of one warp
   static constexpr int kCombLd = D + 4;              // joined rows: conflict-free float2 writes
-  static constexpr int kCombOff = kStages * kStage;
-  static constexpr int kMlOff = kCombOff + kWarps * kRows * kCombLd * 4;
-  static constexpr int kMetaOff = kMlOff + kWarps * kRows * 2 * 4;
-  static constexpr int kBarOff = kMetaOff + kStages * kTile / 16 * 2 * 4;
-  static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 1024;
-  static_assert(kSmem <= 232448, "shared memory");
-  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O, m, l
+  static constexpr int kComb = kWarps * kRows * kCombLd * 4;   // over the rings, which are empty then
+  static constexpr int kMlOff = kWarps * kRing;
+  static constexpr int kBarOff = kMlOff + kWarps * kRows * 2 * 4;
+  static constexpr int kLastOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kSmem = kLastOff + 16;
+  static_assert(kComb <= kWarps * kRing && kSmem <= (232448 - 1024 * kCtas) / kCtas, "shared memory");
+  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O, then m, l of each row
 };
 
 // The units of one sequence.
@@ -117,33 +123,36 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return d;
 }
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kRowsThreads, 1)
+__global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     k_kv8_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnParams p) {
   using C = RowsCfg<D, NT>;
-  constexpr int ROWS = C::kRows, NS = C::kStages, KS = D / 16, WB = D / 16;   // WB: words of a lane's keys, m tiles of O^T
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* comb = reinterpret_cast<float*>(smem + C::kCombOff);
+  constexpr int ROWS = C::kRows, NS = C::kSlots, KS = D / 16, WB = D / 16;   // WB: m tiles of O^T
+  // No static shared memory: the dynamic part begins the CTA's window, on the
+  // 1024-byte boundary that the swizzled tiles need (checked below).
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* comb = reinterpret_cast<float*>(smem);
   float* ml = reinterpret_cast<float*>(smem + C::kMlOff);          // [warp][row][m, l]
-  float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff);    // [stage][16 tokens]: key, value scale
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-  uint64_t* empty = full + NS;
-  __shared__ int s_last;
+  int* s_last = reinterpret_cast<int*>(smem + C::kLastOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], kWarps);
-    }
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NS;
+  uint8_t* ring = smem + warp * C::kRing;
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 57);
+    return;
+  }
+  if (lane == 0) {
+    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
-
-  __shared__ long long scratch[kRowsThreads / 32 + 2];
-  const Start start = find_start<kRowsThreads>(scratch, p.seqs.B, blockIdx.x, gridDim.x, 1, [&](int b) { return seq_work<ROWS>(p, b).units; });
+  const Start start =
+      find_start<kRowsThreads>(reinterpret_cast<long long*>(smem), p.seqs.B, blockIdx.x, gridDim.x, 1,
+                               [&](int b) { return seq_work<ROWS>(p, b).units; });
   const long long U = start.U;
   const int P = start.P, c = blockIdx.x;
   if (c >= P) return;
+  fence_proxy_async();   // the scan's scratch lies in a ring
+  __syncthreads();
   Walk<ROWS> walk;
   walk.u = unit_begin(c, U, P);
   walk.end = unit_begin(c + 1, U, P);
@@ -152,84 +161,58 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   walk.w = seq_work<ROWS>(p, walk.b);
   const long long ubeg = walk.u;
 
-  if (warp == kWarps) {
-    // ---------------- producer: lane i has page i of a batch of 32 pages
-    const int ppt = kTile / p.block, tiles = 32 / ppt, pbytes = p.block * D;
-    int j = 0;
-    bool ok = true;
-    Segment s;
-    while (ok && walk.next(p, s)) {
-      const PageRun run = read_pages(walk.w.q, p.block, p.window);
-      const int pg0 = (walk.w.t0 + s.t) * ppt;
-      auto page_at = [&](int i) {   // page i of the segment, -1 for none
-        const int pg = pg0 + i;
-        if (i >= s.n * ppt || pg < run.first || pg >= run.first + run.n) return -1;
-        const int id = page_block(p.seqs, s.b, pg, p.num_blocks);
-        if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 52);
-        return id;
-      };
-      auto scales_of = [&](int id) {
-        if (id < 0) return make_float2(1.f, 1.f);
-        const int64_t at = static_cast<int64_t>(id) * p.heads + s.h;
-        return make_float2(p.ks[at], p.vs[at]);
-      };
-      // page numbers are read two batches ahead, scales one
-      int id0 = -1, id1 = page_at(lane), id2 = page_at(32 + lane);
-      float2 sc0 = make_float2(1.f, 1.f), sc1 = sc0;
-      bool have1 = false;
-      for (int i = 0; i < s.n; ++i, ++j) {
-        const int k = i % tiles;
-        if (k == 0) {
-          id0 = id1;
-          id1 = id2;
-          id2 = page_at((i / tiles + 2) * 32 + lane);
-        }
-        const int st = j % NS;
-        if (j >= NS && !mbar_wait(&empty[st], static_cast<uint32_t>(j / NS - 1) & 1u)) {
-          if (lane == 0) set_status(p.status, FL_ERR_TIMEOUT, 53);
-          ok = false;
-          break;
-        }
-        const bool mine = lane >= k * ppt && lane < (k + 1) * ppt;   // lanes with a page of this tile
-        const uint32_t valid = __ballot_sync(0xffffffffu, mine && id0 >= 0);
-        if (lane == 0 && valid) mbar_expect_tx(&full[st], 2u * pbytes * __popc(valid));
-        __syncwarp();
-        if (mine && id0 >= 0) {
-          const int row = static_cast<int>((static_cast<int64_t>(id0) * p.heads + s.h) * p.block);
-          uint8_t* dst = smem + st * C::kStage + (lane - k * ppt) * pbytes;
-          tma_load_2d(dst, &kmap, 0, row, &full[st]);
-          tma_load_2d(dst + C::kHalf, &vmap, 0, row, &full[st]);
-        }
-        if (k == 0) {
-          sc0 = have1 ? sc1 : scales_of(id0);
-          sc1 = scales_of(id1);
-          have1 = true;
-        }
-        // slice l (16 tokens) takes the scales of the page that it lies in
-        const int from = k * ppt + (lane & 7) * 16 / p.block;
-        const float a = __shfl_sync(0xffffffffu, sc0.x, from), v = __shfl_sync(0xffffffffu, sc0.y, from);
-        if (lane < kTile / 16) meta[st * (kTile / 16) + lane] = make_float2(a, v);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
-      }
-    }
-    if (!ok)   // let the copies in flight land before the CTA can exit
-      for (int jj = j > NS ? j - NS : 0; jj < j; ++jj) mbar_wait(&full[jj % NS], static_cast<uint32_t>(jj / NS) & 1u);
-    return;
-  }
-
-  // ------------------ consumers
   const int g = lane >> 2, t = lane & 3;
   bool ok = true;
-  int j = 0;
+  int slot = 0;         // of the next slice to take
+  uint32_t phase = 0;
   Segment s;
   while (walk.next(p, s)) {
     const SeqWork& w = walk.w;
     const int past = w.q.kv - w.q.n;   // position of the sequence's first row
+    const int pos0 = (w.t0 + s.t) * kTile + 16 * warp;   // the warp's first token
+    // ---------------- the warp's slices: lane i knows the pages of 32 of them
+    const PageRun run = read_pages(w.q, p.block, p.window);
+    auto page_at = [&](int i) {   // the page of slice i, -1 for none
+      const int pg = (pos0 + i * kTile) / p.block;
+      if (i >= s.n || pg < run.first || pg >= run.first + run.n) return -1;
+      const int id = page_block(p.seqs, s.b, pg, p.num_blocks);
+      if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 52);
+      return id;
+    };
+    auto scales_of = [&](int id) {
+      if (id < 0) return make_float2(1.f, 1.f);
+      const int64_t at = static_cast<int64_t>(id) * p.heads + s.h;
+      return make_float2(p.ks[at], p.vs[at]);
+    };
+    int ids = page_at(lane), next_ids = page_at(32 + lane);   // of the slices being copied, and the 32 after them
+    int issued = 0, to = slot;                                // slices copied so far, the slot of the next
+    auto copy = [&]() {
+      if (issued >= s.n || !ok) return;
+      if (issued > 0 && (issued & 31) == 0) {
+        ids = next_ids;
+        next_ids = page_at(issued + 32 + lane);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
+      if (lane == 0) {
+        if (id >= 0) {
+          const int row = static_cast<int>((static_cast<int64_t>(id) * p.heads + s.h) * p.block) + (pos0 + issued * kTile) % p.block;
+          mbar_arrive_expect_tx(&full[to], 2 * C::kHalf);
+          tma_load_2d(ring + to * 2 * C::kHalf, &kmap, 0, row, &full[to]);
+          tma_load_2d(ring + to * 2 * C::kHalf + C::kHalf, &vmap, 0, row, &full[to]);
+        } else {
+          mbar_arrive(&full[to]);
+        }
+      }
+      ++issued;
+      if (++to == NS) to = 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < NS - 1; ++i) copy();
+    float2 scales = scales_of(ids), next_scales = scales;     // of 32 slices being taken, and of the 32 being copied
+
     // query rows as the B operand: lane (g, t) has row g's elements [t D/4, (t+1) D/4)
     uint32_t qf[NT][KS][2];
     float fac[NT][2];
-    int lim[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = s.r * ROWS + 8 * nt + g;
@@ -242,28 +225,27 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
       }
-      const uint32_t* a = &raw[0].x;
       uint32_t top = 0;   // the largest magnitude's bits
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) top = max(top, max(a[i] & 0x7fffu, (a[i] >> 16) & 0x7fffu));
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t a[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, max(a[k] & 0x7fffu, (a[k] >> 16) & 0x7fffu));
+      }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = row_exponent(top);
       const float down = pow2i(-e);
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t a[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t v = a[2 * i + h];
-          qf[nt][i][h] = pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
-        }
+        for (int k = 0; k < 4; ++k)
+          qf[nt][2 * i + (k >> 1)][k & 1] = pack_f16(__uint_as_float(a[k] << 16) * down, __uint_as_float(a[k] & 0xffff0000u) * down);
+      }
       const float f = p.scale2 * pow2i(e);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        fac[nt][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + h));
-        const int rr = min(s.r * ROWS + 8 * nt + 2 * t + h, w.rows - 1);
-        lim[nt][h] = past + rr / p.group + 1;
-      }
+      for (int h = 0; h < 2; ++h) fac[nt][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + h));
     }
     // tokens that any, and that every row of the tile sees
     const int lim_lo = past + s.r * ROWS / p.group + 1;
@@ -283,23 +265,33 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
       for (int h = 0; h < 2; ++h) m[nt][h] = -INFINITY, l[nt][h] = 0.f;
 
-    for (int i = 0; i < s.n; ++i, ++j) {
-      const int st = j % NS;
-      if (ok && !mbar_wait(&full[st], static_cast<uint32_t>(j / NS) & 1u)) {
+#pragma unroll 1
+    for (int i = 0; i < s.n; ++i) {
+      if (issued > 32 && (issued & 31) == 1 && issued - i <= NS) next_scales = scales_of(ids);   // copies have begun on 32 more
+      if (i > 0 && (i & 31) == 0) scales = next_scales;
+      copy();
+      if (ok && !mbar_wait_many(&full[slot], phase)) {
         if (lane == 0) set_status(p.status, FL_ERR_TIMEOUT, 54);
-        ok = false;   // no more waits: the rest is walked through without data
+        ok = false;   // nothing more is copied: the rest is walked through without data
+        int sl = slot;
+        uint32_t ph = phase;
+        for (int k = i; k < issued; ++k) {   // (what is in flight may still land)
+          mbar_wait_many(&full[sl], ph);
+          if (++sl == NS) sl = 0, ph ^= 1u;
+        }
       }
-      const int pos = (w.t0 + s.t + i) * kTile + 16 * warp;   // the warp's first token
+      ok = __all_sync(0xffffffffu, ok);
+      const int pos = pos0 + i * kTile;
+      const float2 sc = make_float2(__shfl_sync(0xffffffffu, scales.x, i & 31), __shfl_sync(0xffffffffu, scales.y, i & 31));
       if (ok && pos < lim_hi && pos + 16 > low_lo) {
-        const uint8_t* kt = smem + st * C::kStage + warp * 16 * D;
+        const uint8_t* kt = ring + slot * 2 * C::kHalf;
         const uint8_t* vt = kt + C::kHalf;
-        const float2 sc = meta[st * (kTile / 16) + warp];
-        // S^T = K q^T
-        float x[NT][4];
+        // S^T = K q^T, in two chains
+        float x[NT][4], x2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[nt][k] = 0.f;
+          for (int k = 0; k < 4; ++k) x[nt][k] = 0.f, x2[nt][k] = 0.f;
         {
           uint32_t ka[2][KS];
 #pragma unroll
@@ -315,7 +307,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             const uint32_t a0 = code_pair_f16<FMT, false>(ka[0][k]), a2 = code_pair_f16<FMT, true>(ka[0][k]);
             const uint32_t a1 = code_pair_f16<FMT, false>(ka[1][k]), a3 = code_pair_f16<FMT, true>(ka[1][k]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(x[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(k & 1 ? x2[nt] : x[nt], a0, a1, a2, a3, qf[nt][k][0], qf[nt][k][1]);
           }
         }
         const bool mask = pos + 16 > lim_lo || pos < low_hi;
@@ -323,17 +315,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[nt][k] *= sc.x * fac[nt][k & 1];
-            if (mask) {
+          for (int k = 0; k < 4; ++k) x[nt][k] = (x[nt][k] + x2[nt][k]) * (sc.x * fac[nt][k & 1]);
+        if (mask) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
               const int tok = pos + g + (k >> 1) * 8;
-              const int lm = lim[nt][k & 1];
+              const int lm = past + min(s.r * ROWS + 8 * nt + 2 * t + (k & 1), w.rows - 1) / p.group + 1;
               if (tok >= lm || (p.window && tok < lm - p.window)) x[nt][k] = -INFINITY;
             }
-            grow |= x[nt][k] > m[nt][k & 1];
-          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) grow |= fmaxf(x[nt][h], x[nt][h + 2]) > m[nt][h] + kSlack;
         if (__any_sync(0xffffffffu, grow) || sc.y > vref) {
-          // a larger maximum of some row, or a larger value scale
+          // a maximum has outgrown its reference, or the value scale is the largest so far
           const float vnew = fmaxf(vref, sc.y), vr = vref / vnew;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -343,7 +341,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float f = mx == -INFINITY ? 1.f : exp2_approx(m[nt][h] - mx);
+              const float f = mx == m[nt][h] ? 1.f : exp2_approx(m[nt][h] - mx);
               m[nt][h] = mx;
               l[nt][h] *= f;
 #pragma unroll
@@ -410,12 +408,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      __syncwarp();   // the slot has been read
+      if (++slot == NS) slot = 0, phase ^= 1u;
     }
 
     // ---------------- join the eight warps
     const float back = vref / kPScale;
+    __syncthreads();   // every ring is empty: the rows go over them
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -431,93 +430,121 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         for (int i = 0; i < WB; ++i)
           *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[i][nt][h] * back, o[i][nt][h + 2] * back);
       }
-    named_bar(1, 32 * kWarps);
-    const bool whole = s.n == w.nt;
-    float* slot = p.part + static_cast<size_t>(2 * c + (s.first < ubeg ? 0 : 1)) * C::kSlot;
-    for (int i = tid; i < ROWS * D / 2; i += 32 * kWarps) {
-      const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
+    __syncthreads();
+    // the sum of eight partial rows in shared memory, element pair d of row
+    struct Joined {
+      float mx, sum, ox, oy;
+    };
+    auto joined = [&](int row, int d) {
       const int at = d % (D / 8) / 2 * 16 + d / (D / 8) * 2;
-      float mx = -INFINITY;
+      Joined r = {-INFINITY, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, ml[2 * (k * ROWS + row)]);
-      float sum = 0.f, ox = 0.f, oy = 0.f;
+      for (int k = 0; k < kWarps; ++k) r.mx = fmaxf(r.mx, ml[2 * (k * ROWS + row)]);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float mk = ml[2 * (k * ROWS + row)];
-        const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - mx);
+        const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - r.mx);
         const float2 v = *reinterpret_cast<const float2*>(comb + (k * ROWS + row) * C::kCombLd + at);
-        sum = fmaf(f, ml[2 * (k * ROWS + row) + 1], sum);
-        ox = fmaf(f, v.x, ox), oy = fmaf(f, v.y, oy);
+        r.sum = fmaf(f, ml[2 * (k * ROWS + row) + 1], r.sum);
+        r.ox = fmaf(f, v.x, r.ox), r.oy = fmaf(f, v.y, r.oy);
       }
-      if (!whole) {
-        __stcg(reinterpret_cast<float2*>(slot + row * D + d), make_float2(ox, oy));
-        if (d == 0) __stcg(reinterpret_cast<float2*>(slot + ROWS * D + 2 * row), make_float2(mx, sum));
-        continue;
-      }
+      return r;
+    };
+    auto finish = [&](const Joined& v, int row, int d) {   // the output of element pair d of a row
       const int r = s.r * ROWS + row;
-      if (r < w.rows) {
-        const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
-        const int64_t tk = w.q.start + tok;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no token (a NaN is not)
-        *reinterpret_cast<__nv_bfloat162*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + d) =
-            __floats2bfloat162_rn(ox * inv, oy * inv);
-        if (d == 0 && p.lse) p.lse[tk * p.Hq + hd] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      if (r >= w.rows) return;
+      const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
+      const int64_t tk = w.q.start + tok;
+      const float inv = v.sum == 0.f ? 0.f : 1.f / v.sum;   // 0: no token (a NaN is not)
+      *reinterpret_cast<__nv_bfloat162*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + d) =
+          __floats2bfloat162_rn(v.ox * inv, v.oy * inv);
+      if (d == 0 && p.lse) p.lse[tk * p.Hq + hd] = v.sum == 0.f ? -INFINITY : (v.mx + log2f(v.sum)) * kLn2;
+    };
+    const bool whole = s.n == w.nt;
+    float* part = p.part + static_cast<size_t>(2 * c + (s.first < ubeg ? 0 : 1)) * C::kSlot;
+    for (int i = tid; i < ROWS * D / 2; i += kRowsThreads) {
+      const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
+      const Joined v = joined(row, d);
+      if (whole) {
+        finish(v, row, d);
+      } else {
+        __stcg(reinterpret_cast<float2*>(part + row * D + d), make_float2(v.ox, v.oy));
+        if (d == 0) __stcg(reinterpret_cast<float2*>(part + ROWS * D + 2 * row), make_float2(v.mx, v.sum));
       }
     }
     if (!whole) {
-      // the last of the CTAs that share the row tile adds them up, in CTA order
+      // The last of the CTAs that share the row tile adds them up, in CTA order:
+      // warp k takes every eighth of them, then the warps are joined as above.
       const int cf = cta_of_unit(s.first, U, P), cl = cta_of_unit(s.first + w.nt - 1, U, P);
-      named_bar(1, 32 * kWarps);
+      __syncthreads();
       if (tid == 0) {
         fence_acq_rel_gpu();
         const int done = atomicAdd(&p.cnt[cf], 1);
-        s_last = done == cl - cf;
-        if (s_last) {
+        *s_last = done == cl - cf;
+        if (*s_last) {
           fence_acq_rel_gpu();
           p.cnt[cf] = 0;
         }
       }
-      named_bar(1, 32 * kWarps);
-      if (s_last) {
-        auto slot_of = [&](int cc) {
-          return p.part + static_cast<size_t>(2 * cc + (s.first < unit_begin(cc, U, P) ? 0 : 1)) * C::kSlot;
-        };
-        for (int i = tid; i < ROWS * D / 2; i += 32 * kWarps) {
-          const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
-          const int r = s.r * ROWS + row;
-          if (r >= w.rows) continue;
-          float mx = -INFINITY;
-          for (int cc = cf; cc <= cl; ++cc) mx = fmaxf(mx, __ldcg(slot_of(cc) + ROWS * D + 2 * row));
-          float sum = 0.f, ox = 0.f, oy = 0.f;
-          for (int cc = cf; cc <= cl; ++cc) {
-            const float2 a = __ldcg(reinterpret_cast<const float2*>(slot_of(cc) + ROWS * D + 2 * row));
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(slot_of(cc) + row * D + d));
-            const float f = a.x == -INFINITY ? 0.f : exp2_approx(a.x - mx);
-            sum = fmaf(f, a.y, sum);
-            ox = fmaf(f, v.x, ox), oy = fmaf(f, v.y, oy);
+      __syncthreads();
+      if (*s_last) {
+        constexpr int kPer = ROWS * D / 128;   // float4 of O a lane
+        constexpr int kLanes = D / 4;          // lanes of a row's float4 (a row is a whole number of passes, or two rows a pass)
+        float4 acc[kPer];
+        float am[kPer], al[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), am[k] = -INFINITY, al[k] = 0.f;
+#pragma unroll 1
+        for (int cc = cf + warp; cc <= cl; cc += kWarps) {
+          const float* sl = p.part + static_cast<size_t>(2 * cc + (s.first < unit_begin(cc, U, P) ? 0 : 1)) * C::kSlot;
+          float4 v[kPer];
+          float2 a[kPer];
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            v[k] = __ldcg(reinterpret_cast<const float4*>(sl) + k * 32 + lane);
+            a[k] = __ldcg(reinterpret_cast<const float2*>(sl + ROWS * D) + (k * 32 + lane) / kLanes);
           }
-          const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
-          const int64_t tk = w.q.start + tok;
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no token (a NaN is not)
-          *reinterpret_cast<__nv_bfloat162*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + d) =
-              __floats2bfloat162_rn(ox * inv, oy * inv);
-          if (d == 0 && p.lse) p.lse[tk * p.Hq + hd] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const float nm = fmaxf(am[k], a[k].x);
+            const float f = am[k] == nm ? 1.f : exp2_approx(am[k] - nm);
+            const float h = a[k].x == -INFINITY ? 0.f : exp2_approx(a[k].x - nm);
+            acc[k].x = fmaf(acc[k].x, f, h * v[k].x), acc[k].y = fmaf(acc[k].y, f, h * v[k].y);
+            acc[k].z = fmaf(acc[k].z, f, h * v[k].z), acc[k].w = fmaf(acc[k].w, f, h * v[k].w);
+            al[k] = fmaf(al[k], f, h * a[k].y);
+            am[k] = nm;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          const int row = (k * 32 + lane) / kLanes, d = (k * 32 + lane) % kLanes * 4;
+          float* dst = comb + (warp * ROWS + row) * C::kCombLd;
+          // (the order of `joined`: pair d of a row lies at d % (D/8) / 2 * 16 + d / (D/8) * 2)
+          *reinterpret_cast<float2*>(dst + d % (D / 8) / 2 * 16 + d / (D / 8) * 2) = make_float2(acc[k].x, acc[k].y);
+          *reinterpret_cast<float2*>(dst + (d + 2) % (D / 8) / 2 * 16 + (d + 2) / (D / 8) * 2) = make_float2(acc[k].z, acc[k].w);
+          if (d == 0) reinterpret_cast<float2*>(ml)[warp * ROWS + row] = make_float2(am[k], al[k]);
+        }
+        __syncthreads();
+        for (int i = tid; i < ROWS * D / 2; i += kRowsThreads) {
+          const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
+          finish(joined(row, d), row, d);
         }
       }
     }
-    named_bar(1, 32 * kWarps);   // the joined rows and s_last are read before the next segment writes them
+    fence_proxy_async();   // what lay over the rings, before copies into them
+    __syncthreads();
   }
 }
 
 // ------------------------------------------------------------------ host
-// The codes as rows of head_dim bytes, one page of one head a box.
-bool code_map(CUtensorMap* map, void* base, const fl_kv8_cache& c) {
+// The codes as rows of head_dim bytes, `rows` tokens of a page of one head a box.
+bool code_map(CUtensorMap* map, void* base, const fl_kv8_cache& c, int rows) {
   auto enc = flh::encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim),
                               static_cast<cuuint64_t>(c.num_blocks) * c.kv_heads * c.block};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(c.block)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(c.head_dim), static_cast<cuuint32_t>(rows)};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
              c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -535,7 +562,7 @@ int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& 
       return FL_ERR_CUDA;
     if (dev < 64) attr_done[dev] = true;
   }
-  k_kv8_rows<FMT, D, NT><<<flh::sm_count(), kRowsThreads, C::kSmem, s>>>(km, vm, p);
+  k_kv8_rows<FMT, D, NT><<<C::kCtas * flh::sm_count(), kRowsThreads, C::kSmem, s>>>(km, vm, p);
   return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
 }
 
@@ -551,7 +578,8 @@ extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, in
   if (head_dim != 64 && head_dim != 128) return FL_ERR_UNSUPPORTED;
   // two partials a CTA: the rows that it shares with the CTAs before and after
   const bool prompt = static_cast<long long>(T) * (Hq / kv_heads) > kFewRows;
-  const size_t slot = prompt ? prompt_slot_floats(head_dim) : 16 * (head_dim + 2);
+  const size_t few = 16 * (head_dim + 2);   // two CTAs an SM with 8 rows, or one with 16
+  const size_t slot = prompt ? prompt_slot_floats(head_dim) : few;
   *out = kScratchOff + 2ull * flh::sm_count() * slot * 4;
   return FL_OK;
 }
@@ -574,7 +602,6 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   const long long rows = static_cast<long long>(seqs->max_q) * (Hq / cache->kv_heads);
   if (rows > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
   CUtensorMap km, vm;
-  if (!code_map(&km, cache->k, *cache) || !code_map(&vm, cache->v, *cache)) return FL_ERR_CUDA;
   AttnParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -590,11 +617,13 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   p.scale2 = scale * 1.44269504088896340736f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (rows > kFewRows) {
+    if (!code_map(&km, cache->k, *cache, cache->block) || !code_map(&vm, cache->v, *cache, cache->block)) return FL_ERR_CUDA;
     // one sequence goes to the one kernel; a batch may hold both kinds
     p.rows_lo = seqs->B > 1 ? kFewRows : 0, p.rows_hi = 0x7fffffff;
     const int e = launch_prompt(km, vm, p, cache->format, cache->head_dim, s);
     if (e != FL_OK || seqs->B == 1) return e;
   }
+  if (!code_map(&km, cache->k, *cache, 16) || !code_map(&vm, cache->v, *cache, 16)) return FL_ERR_CUDA;
   p.rows_lo = 0, p.rows_hi = kFewRows;
   if (cache->format == FL_KV8_E4M3)
     return cache->head_dim == 64 ? pick_rows<FL_KV8_E4M3, 64>(km, vm, p, rows, s)
