@@ -42,6 +42,7 @@ constexpr int kWarps = 8;
 constexpr int kRowsThreads = 32 * kWarps;
 constexpr float kPScale = 64.f;         // 2^6
 constexpr float kSlack = 8.f;           // a reference may lag its maximum by 2^kSlack
+constexpr float kNone = -1e30f;         // the reference of a row without a token so far
 // Most rows of a sequence (query heads of a kv head x tokens) that this kernel
 // takes; sequences with more go to the tcgen05 kernel, in the same call.
 constexpr int kFewRows = 64;
@@ -162,6 +163,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
   const long long ubeg = walk.u;
 
   const int g = lane >> 2, t = lane & 3;
+  const int lb = 31 - __clz(p.block);   // block = 2^lb
   bool ok = true;
   int slot = 0;         // of the next slice to take
   uint32_t phase = 0;
@@ -172,30 +174,22 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     const int pos0 = (w.t0 + s.t) * kTile + 16 * warp;   // the warp's first token
     // ---------------- the warp's slices: lane i knows the pages of 32 of them
     const PageRun run = read_pages(w.q, p.block, p.window);
-    auto page_at = [&](int i) {   // the page of slice i, -1 for none
-      const int pg = (pos0 + i * kTile) / p.block;
+    auto page_at = [&](int i) {   // the (page, head) of slice i, -1 for none
+      const int pg = (pos0 + i * kTile) >> lb;
       if (i >= s.n || pg < run.first || pg >= run.first + run.n) return -1;
       const int id = page_block(p.seqs, s.b, pg, p.num_blocks);
       if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 52);
-      return id;
+      return id < 0 ? -1 : id * p.heads + s.h;   // (blocks x heads x tokens fit 31 bits)
     };
-    auto scales_of = [&](int id) {
-      if (id < 0) return make_float2(1.f, 1.f);
-      const int64_t at = static_cast<int64_t>(id) * p.heads + s.h;
-      return make_float2(p.ks[at], p.vs[at]);
-    };
+    auto scales_of = [&](int at) { return at < 0 ? make_float2(1.f, 1.f) : make_float2(p.ks[at], p.vs[at]); };
     int ids = page_at(lane), next_ids = page_at(32 + lane);   // of the slices being copied, and the 32 after them
     int issued = 0, to = slot;                                // slices copied so far, the slot of the next
     auto copy = [&]() {
       if (issued >= s.n || !ok) return;
-      if (issued > 0 && (issued & 31) == 0) {
-        ids = next_ids;
-        next_ids = page_at(issued + 32 + lane);
-      }
-      const int id = __shfl_sync(0xffffffffu, ids, issued & 31);
+      const int at = __shfl_sync(0xffffffffu, ids, issued & 31);
       if (lane == 0) {
-        if (id >= 0) {
-          const int row = static_cast<int>((static_cast<int64_t>(id) * p.heads + s.h) * p.block) + (pos0 + issued * kTile) % p.block;
+        if (at >= 0) {
+          const int row = (at << lb) + ((pos0 + issued * kTile) & (p.block - 1));
           mbar_arrive_expect_tx(&full[to], 2 * C::kHalf);
           tma_load_2d(ring + to * 2 * C::kHalf, &kmap, 0, row, &full[to]);
           tma_load_2d(ring + to * 2 * C::kHalf + C::kHalf, &vmap, 0, row, &full[to]);
@@ -208,7 +202,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     };
 #pragma unroll 1
     for (int i = 0; i < NS - 1; ++i) copy();
-    float2 scales = scales_of(ids), next_scales = scales;     // of 32 slices being taken, and of the 32 being copied
+    float2 next_scales = scales_of(ids);   // of the 32 slices being copied
 
     // query rows as the B operand: lane (g, t) has row g's elements [t D/4, (t+1) D/4)
     uint32_t qf[NT][KS][2];
@@ -247,13 +241,13 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll
       for (int h = 0; h < 2; ++h) fac[nt][h] = __shfl_sync(0xffffffffu, f, 4 * (2 * t + h));
     }
-    // tokens that any, and that every row of the tile sees
+    // tokens that any row of the tile sees are [low_lo, lim_hi), that every row sees [low_hi, lim_lo)
     const int lim_lo = past + s.r * ROWS / p.group + 1;
     const int lim_hi = past + min(s.r * ROWS + ROWS - 1, w.rows - 1) / p.group + 1;
     const int low_lo = p.window ? lim_lo - p.window : 0, low_hi = p.window ? lim_hi - p.window : 0;
 
     float o[WB][NT][4];
-    float m[NT][2], l[NT][2], vref = 0.f;
+    float m[NT][2], l[NT][2], vref = 0.f, rv = 0.f;   // rv: 1 / vref
 #pragma unroll
     for (int i = 0; i < WB; ++i)
 #pragma unroll
@@ -263,24 +257,32 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) m[nt][h] = -INFINITY, l[nt][h] = 0.f;
+      for (int h = 0; h < 2; ++h) m[nt][h] = kNone, l[nt][h] = 0.f;
 
+    float2 scales = next_scales;
 #pragma unroll 1
     for (int i = 0; i < s.n; ++i) {
-      if (issued > 32 && (issued & 31) == 1 && issued - i <= NS) next_scales = scales_of(ids);   // copies have begun on 32 more
-      if (i > 0 && (i & 31) == 0) scales = next_scales;
-      copy();
-      if (ok && !mbar_wait_many(&full[slot], phase)) {
-        if (lane == 0) set_status(p.status, FL_ERR_TIMEOUT, 54);
-        ok = false;   // nothing more is copied: the rest is walked through without data
-        int sl = slot;
-        uint32_t ph = phase;
-        for (int k = i; k < issued; ++k) {   // (what is in flight may still land)
-          mbar_wait_many(&full[sl], ph);
-          if (++sl == NS) sl = 0, ph ^= 1u;
-        }
+      if ((i & 31) == 0 && i > 0) {
+        scales = next_scales;
+      } else if ((i & 31) == 33 - NS && i + NS < s.n + 1) {
+        // the next copy is the first of 32 more slices
+        ids = next_ids;
+        next_ids = page_at((i & ~31) + 64 + lane);
+        next_scales = scales_of(ids);
       }
-      ok = __all_sync(0xffffffffu, ok);
+      copy();
+      if (!__all_sync(0xffffffffu, ok && mbar_wait_many(&full[slot], phase))) {
+        if (ok) {   // a wait ran out: nothing more is copied, the rest is walked through without data
+          if (lane == 0) set_status(p.status, FL_ERR_TIMEOUT, 54);
+          int sl = slot;
+          uint32_t ph = phase;
+          for (int k = i; k < issued; ++k) {   // (what is in flight may still land)
+            mbar_wait_many(&full[sl], ph);
+            if (++sl == NS) sl = 0, ph ^= 1u;
+          }
+        }
+        ok = false;
+      }
       const int pos = pos0 + i * kTile;
       const float2 sc = make_float2(__shfl_sync(0xffffffffu, scales.x, i & 31), __shfl_sync(0xffffffffu, scales.y, i & 31));
       if (ok && pos < lim_hi && pos + 16 > low_lo) {
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float f = mx == m[nt][h] ? 1.f : exp2_approx(m[nt][h] - mx);
+              const float f = exp2_approx(m[nt][h] - mx);
               m[nt][h] = mx;
               l[nt][h] *= f;
 #pragma unroll
@@ -350,17 +352,16 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
                 o[q][nt][h + 2] *= f * vr;
               }
             }
-          vref = vnew;
+          vref = vnew, rv = 1.f / vnew;
         }
-        const float pv = kPScale * (sc.y / vref);
+        const float pv = kPScale * sc.y * rv;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float e[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float mm = m[nt][k & 1];
-            e[k] = exp2_approx(x[nt][k] - (mm == -INFINITY ? 0.f : mm));
+            e[k] = exp2_approx(x[nt][k] - m[nt][k & 1]);
             l[nt][k & 1] += e[k];
           }
           pb[nt][0] = transpose8x8(pack_f16(e[0] * pv, e[1] * pv));
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = 8 * nt + 2 * t + h;
-        if (g == 0) reinterpret_cast<float2*>(ml)[warp * ROWS + row] = make_float2(m[nt][h], sum);
+        if (g == 0) reinterpret_cast<float2*>(ml)[warp * ROWS + row] = make_float2(m[nt][h] == kNone ? -INFINITY : m[nt][h], sum);
         float* dst = comb + (warp * ROWS + row) * C::kCombLd + 2 * g;
 #pragma unroll
         for (int i = 0; i < WB; ++i)
