@@ -14,6 +14,8 @@
 // state of its own, joined once a segment.  A warp copies its slices by TMA
 // (swizzled, so that both operand reads below are free of bank conflicts) into
 // a ring of its own and waits for nobody else; two CTAs fit an SM with 8 rows.
+// The copies run on into the CTA's next segment while this one is joined: the
+// segments lie in shared memory one ahead.
 // (With one CTA, a producer warp and a ring that all warps share, reading was
 // held to 3.3 TB/s by the latency of the warps' chains of work.)
 // A warp's products are transposed, so that tokens
@@ -54,14 +56,16 @@ struct RowsCfg {
   static constexpr int kHalf = 16 * D;               // a warp's keys (or values) of a unit
   static constexpr int kSlots = (NT == 1 ? 3 : 6) * (128 / D);
   static constexpr int kRing = kSlots * 2 * kHalf;   // of one warp
-  static constexpr int kCombLd = D + 4;              // joined rows: conflict-free float2 writes
-  static constexpr int kComb = kWarps * kRows * kCombLd * 4;   // over the rings, which are empty then
-  static constexpr int kMlOff = kWarps * kRing;
-  static constexpr int kBarOff = kMlOff + kWarps * kRows * 2 * 4;
-  static constexpr int kLastOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kVals = kRows * D / 32;       // accumulators of a lane
+  static constexpr int kJoinOff = kWarps * kRing;    // four warps' accumulators, [warp][value][lane]
+  static constexpr int kMlOff = kJoinOff + kWarps / 2 * kVals * 32 * 4;   // and references and sums, [warp][row]
+  static constexpr int kBarOff = kMlOff + kWarps / 2 * kRows * 2 * 4;
+  static constexpr int kDescOff = kBarOff + kWarps * kSlots * 8;
+  static constexpr int kWalkOff = kDescOff + 3 * 64;
+  static constexpr int kLastOff = kWalkOff + 96;
   static constexpr int kSmem = kLastOff + 16;
-  static_assert(kComb <= kWarps * kRing && kSmem <= (232448 - 1024 * kCtas) / kCtas, "shared memory");
-  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O, then m, l of each row
+  static_assert(kSmem <= (232448 + 1024) / kCtas - 1024, "shared memory");
+  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O [value][lane], then m, l of each row
 };
 
 // The units of one sequence.
@@ -83,31 +87,44 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
 }
 
 // A run of tiles of one (sequence, head, row tile) inside the CTA's units.
-struct Segment {
-  int b, h, r, t, n;          // tiles [t, t + n) of the sequence's nt
-  long long first;            // unit of the row tile's first tile
+struct __align__(16) Segment {
+  int n;                  // tiles, 0: no more segments
+  int b, h, r;            // sequence, kv head, row tile
+  int pos;                // first token of the first tile
+  int start, past, rows;  // the sequence's first query row, its position, its rows
+  int page0, pages;       // pages that a row sees
+  int slot;               // the partial to write, or -1: the row tile is whole, write its output
+  int cf, cl;             // CTAs that share the row tile
+  int pad[3];
 };
+static_assert(sizeof(Segment) == 64, "segments");
 template <int ROWS>
 struct Walk {
-  long long u, end, base;
-  int b;
+  long long u, end, base, beg, U;
+  int b, P;
   SeqWork w;
-  __device__ bool next(const AttnParams& p, Segment& s) {
-    if (u >= end) return false;
+  __device__ void next(const AttnParams& p, Segment& s) {
+    s.n = 0;
+    if (u >= end) return;
     while (u >= base + w.units) {
       base += w.units;
-      if (++b >= p.seqs.B) return false;
+      if (++b >= p.seqs.B) return;
       w = seq_work<ROWS>(p, b);
     }
     const long long local = u - base, seg = local / w.nt;
+    const int t = static_cast<int>(local - seg * w.nt);
+    s.n = static_cast<int>(min(static_cast<long long>(w.nt - t), end - u));
     s.b = b;
-    s.t = static_cast<int>(local - seg * w.nt);
     s.h = static_cast<int>(seg / w.rt);
     s.r = static_cast<int>(seg - static_cast<long long>(s.h) * w.rt);
-    s.n = static_cast<int>(min(static_cast<long long>(w.nt - s.t), end - u));
-    s.first = u - s.t;
+    s.pos = (w.t0 + t) * kTile;
+    s.start = w.q.start, s.past = w.q.kv - w.q.n, s.rows = w.rows;
+    const PageRun run = read_pages(w.q, p.block, p.window);
+    s.page0 = run.first, s.pages = run.n;
+    const long long first = u - t;
+    s.slot = s.n == w.nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (first < beg ? 0 : 1);
+    s.cf = cta_of_unit(first, U, P), s.cl = cta_of_unit(first + w.nt - 1, U, P);
     u += s.n;
-    return true;
   }
 };
 
@@ -131,8 +148,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
   // No static shared memory: the dynamic part begins the CTA's window, on the
   // 1024-byte boundary that the swizzled tiles need (checked below).
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* comb = reinterpret_cast<float*>(smem);
-  float* ml = reinterpret_cast<float*>(smem + C::kMlOff);          // [warp][row][m, l]
+  float* jv = reinterpret_cast<float*>(smem + C::kJoinOff);
+  float2* jm = reinterpret_cast<float2*>(smem + C::kMlOff);
+  Segment* segs = reinterpret_cast<Segment*>(smem + C::kDescOff);
+  Walk<ROWS>* plan = reinterpret_cast<Walk<ROWS>*>(smem + C::kWalkOff);
+  static_assert(sizeof(Walk<ROWS>) <= 96, "plan");
   int* s_last = reinterpret_cast<int*>(smem + C::kLastOff);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -146,64 +166,75 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
-  const Start start =
-      find_start<kRowsThreads>(reinterpret_cast<long long*>(smem), p.seqs.B, blockIdx.x, gridDim.x, 1,
-                               [&](int b) { return seq_work<ROWS>(p, b).units; });
-  const long long U = start.U;
-  const int P = start.P, c = blockIdx.x;
-  if (c >= P) return;
-  fence_proxy_async();   // the scan's scratch lies in a ring
-  __syncthreads();
-  Walk<ROWS> walk;
-  walk.u = unit_begin(c, U, P);
-  walk.end = unit_begin(c + 1, U, P);
-  walk.b = start.b;
-  walk.base = start.base;
-  walk.w = seq_work<ROWS>(p, walk.b);
-  const long long ubeg = walk.u;
+  {
+    const Start start =
+        find_start<kRowsThreads>(reinterpret_cast<long long*>(smem + C::kJoinOff), p.seqs.B, blockIdx.x, gridDim.x, 1,
+                                 [&](int b) { return seq_work<ROWS>(p, b).units; });
+    if (static_cast<int>(blockIdx.x) >= start.P) return;
+    if (tid == 0) {
+      Walk<ROWS> walk;
+      walk.U = start.U, walk.P = start.P;
+      walk.u = walk.beg = unit_begin(blockIdx.x, start.U, start.P);
+      walk.end = unit_begin(blockIdx.x + 1, start.U, start.P);
+      walk.b = start.b;
+      walk.base = start.base;
+      walk.w = seq_work<ROWS>(p, walk.b);
+      walk.next(p, segs[0]);
+      walk.next(p, segs[1]);
+      *plan = walk;
+    }
+    __syncthreads();
+  }
 
   const int g = lane >> 2, t = lane & 3;
   const int lb = 31 - __clz(p.block);   // block = 2^lb
   bool ok = true;
   int slot = 0;         // of the next slice to take
   uint32_t phase = 0;
-  Segment s;
-  while (walk.next(p, s)) {
-    const SeqWork& w = walk.w;
-    const int past = w.q.kv - w.q.n;   // position of the sequence's first row
-    const int pos0 = (w.t0 + s.t) * kTile + 16 * warp;   // the warp's first token
-    // ---------------- the warp's slices: lane i knows the pages of 32 of them
-    const PageRun run = read_pages(w.q, p.block, p.window);
-    auto page_at = [&](int i) {   // the (page, head) of slice i, -1 for none
-      const int pg = (pos0 + i * kTile) >> lb;
-      if (i >= s.n || pg < run.first || pg >= run.first + run.n) return -1;
-      const int id = page_block(p.seqs, s.b, pg, p.num_blocks);
-      if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 52);
-      return id < 0 ? -1 : id * p.heads + s.h;   // (blocks x heads x tokens fit 31 bits)
-    };
-    auto scales_of = [&](int at) { return at < 0 ? make_float2(1.f, 1.f) : make_float2(p.ks[at], p.vs[at]); };
-    int ids = page_at(lane), next_ids = page_at(32 + lane);   // of the slices being copied, and the 32 after them
-    int issued = 0, to = slot;                                // slices copied so far, the slot of the next
-    auto copy = [&]() {
-      if (issued >= s.n || !ok) return;
-      const int at = __shfl_sync(0xffffffffu, ids, issued & 31);
-      if (lane == 0) {
-        if (at >= 0) {
-          const int row = (at << lb) + ((pos0 + issued * kTile) & (p.block - 1));
-          mbar_arrive_expect_tx(&full[to], 2 * C::kHalf);
-          tma_load_2d(ring + to * 2 * C::kHalf, &kmap, 0, row, &full[to]);
-          tma_load_2d(ring + to * 2 * C::kHalf + C::kHalf, &vmap, 0, row, &full[to]);
-        } else {
-          mbar_arrive(&full[to]);
-        }
+  // ---------------- the warp's slices: lane i knows the pages of 32 of them
+  auto page_at = [&](const Segment& s, int i) {   // the (page, head) of slice i, -1 for none
+    const int pg = (s.pos + 16 * warp + i * kTile) >> lb;
+    if (i >= s.n || pg < s.page0 || pg >= s.page0 + s.pages) return -1;
+    const int id = page_block(p.seqs, s.b, pg, p.num_blocks);
+    if (id < 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 52);
+    return id < 0 ? -1 : id * p.heads + s.h;   // (blocks x heads x tokens fit 31 bits)
+  };
+  auto scales_of = [&](int at) { return at < 0 ? make_float2(1.f, 1.f) : make_float2(p.ks[at], p.vs[at]); };
+  // Copies: of segment `on`, its `todo` slices from `from`, `issued` of them so
+  // far; the pages of 32 of them and of the 32 after; the slot of the next.
+  int on = 0, todo = segs[0].n, from = segs[0].pos + 16 * warp, issued = 0, to = 0;
+  int ids = page_at(segs[0], lane), next_ids = page_at(segs[0], 32 + lane);
+  int seg_ids = page_at(segs[1], lane);                       // the first pages of the segment after
+  float2 next_scales = scales_of(ids), seg_scales;            // of the 32 slices being copied; of the next segment's first
+  auto copy = [&]() {
+    if (!ok || issued >= todo) return;
+    const int at = __shfl_sync(0xffffffffu, ids, issued & 31);
+    if (lane == 0) {
+      if (at >= 0) {
+        const int row = (at << lb) + ((from + issued * kTile) & (p.block - 1));
+        mbar_arrive_expect_tx(&full[to], 2 * C::kHalf);
+        tma_load_2d(ring + to * 2 * C::kHalf, &kmap, 0, row, &full[to]);
+        tma_load_2d(ring + to * 2 * C::kHalf + C::kHalf, &vmap, 0, row, &full[to]);
+      } else {
+        mbar_arrive(&full[to]);
       }
-      ++issued;
-      if (++to == NS) to = 0;
-    };
+    }
+    ++issued;
+    if (++to == NS) to = 0;
+  };
 #pragma unroll 1
-    for (int i = 0; i < NS - 1; ++i) copy();
-    float2 next_scales = scales_of(ids);   // of the 32 slices being copied
+  for (int i = 0; i < NS - 1; ++i) copy();
 
+#pragma unroll 1
+  for (int seg = 0; segs[seg % 3].n > 0; ++seg) {
+    const Segment& s = segs[seg % 3];
+    const int n = s.n, rows = s.rows, past = s.past;
+    const int pos0 = s.pos + 16 * warp;   // the warp's first token
+    if (tid == 0) {   // the segment after the next
+      Walk<ROWS> walk = *plan;
+      walk.next(p, segs[(seg + 2) % 3]);
+      *plan = walk;
+    }
     // query rows as the B operand: lane (g, t) has row g's elements [t D/4, (t+1) D/4)
     uint32_t qf[NT][KS][2];
     float fac[NT][2];
@@ -213,9 +244,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
       uint4 raw[D / 32];
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-      if (r < w.rows) {
+      if (r < rows) {
         const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (w.q.start + tok) * p.qs + static_cast<int64_t>(hd) * D + t * (D / 4));
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(s.start + tok) * p.qs + static_cast<int64_t>(hd) * D + t * (D / 4));
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) raw[i] = src[i];
       }
@@ -243,7 +274,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     }
     // tokens that any row of the tile sees are [low_lo, lim_hi), that every row sees [low_hi, lim_lo)
     const int lim_lo = past + s.r * ROWS / p.group + 1;
-    const int lim_hi = past + min(s.r * ROWS + ROWS - 1, w.rows - 1) / p.group + 1;
+    const int lim_hi = past + min(s.r * ROWS + ROWS - 1, rows - 1) / p.group + 1;
     const int low_lo = p.window ? lim_lo - p.window : 0, low_hi = p.window ? lim_hi - p.window : 0;
 
     float o[WB][NT][4];
@@ -259,15 +290,21 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll
       for (int h = 0; h < 2; ++h) m[nt][h] = kNone, l[nt][h] = 0.f;
 
-    float2 scales = next_scales;
+    float2 scales = seg == 0 ? next_scales : seg_scales;
 #pragma unroll 1
-    for (int i = 0; i < s.n; ++i) {
-      if ((i & 31) == 0 && i > 0) {
-        scales = next_scales;
-      } else if ((i & 31) == 33 - NS && i + NS < s.n + 1) {
+    for (int i = 0; i < n; ++i) {
+      if ((i & 31) == 0 && i > 0) scales = next_scales;
+      if (on == seg && issued == todo) {
+        // on to the next segment (its last slice has been issued at least an iteration ago)
+        ++on;
+        const Segment& x = segs[on % 3];
+        todo = x.n, from = x.pos + 16 * warp, issued = 0;
+        ids = seg_ids, next_ids = page_at(x, 32 + lane);
+        seg_scales = scales_of(ids);
+      } else if (issued > 0 && (issued & 31) == 0) {
         // the next copy is the first of 32 more slices
         ids = next_ids;
-        next_ids = page_at((i & ~31) + 64 + lane);
+        next_ids = page_at(segs[on % 3], issued + 32 + lane);
         next_scales = scales_of(ids);
       }
       copy();
@@ -276,10 +313,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
           if (lane == 0) set_status(p.status, FL_ERR_TIMEOUT, 54);
           int sl = slot;
           uint32_t ph = phase;
-          for (int k = i; k < issued; ++k) {   // (what is in flight may still land)
+          do {   // (what is in flight may still land)
             mbar_wait_many(&full[sl], ph);
             if (++sl == NS) sl = 0, ph ^= 1u;
-          }
+          } while (sl != to);
         }
         ok = false;
       }
@@ -324,7 +361,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int tok = pos + g + (k >> 1) * 8;
-              const int lm = past + min(s.r * ROWS + 8 * nt + 2 * t + (k & 1), w.rows - 1) / p.group + 1;
+              const int lm = past + min(s.r * ROWS + 8 * nt + 2 * t + (k & 1), rows - 1) / p.group + 1;
               if (tok >= lm || (p.window && tok < lm - p.window)) x[nt][k] = -INFINITY;
             }
         }
@@ -413,127 +450,160 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
       if (++slot == NS) slot = 0, phase ^= 1u;
     }
 
-    // ---------------- join the eight warps
+    // ---------------- join the eight warps: in three rounds, half of them hand
+    // their accumulators to the others
     const float back = vref / kPScale;
-    __syncthreads();   // every ring is empty: the rows go over them
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float sum = l[nt][h];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int row = 8 * nt + 2 * t + h;
-        if (g == 0) reinterpret_cast<float2*>(ml)[warp * ROWS + row] = make_float2(m[nt][h] == kNone ? -INFINITY : m[nt][h], sum);
-        float* dst = comb + (warp * ROWS + row) * C::kCombLd + 2 * g;
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 4);
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 8);
+        l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 16);
 #pragma unroll
-        for (int i = 0; i < WB; ++i)
-          *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[i][nt][h] * back, o[i][nt][h + 2] * back);
+        for (int q = 0; q < WB; ++q) o[q][nt][h] *= back, o[q][nt][h + 2] *= back;
       }
-    __syncthreads();
-    // the sum of eight partial rows in shared memory, element pair d of row
-    struct Joined {
-      float mx, sum, ox, oy;
-    };
-    auto joined = [&](int row, int d) {
-      const int at = d % (D / 8) / 2 * 16 + d / (D / 8) * 2;
-      Joined r = {-INFINITY, 0.f, 0.f, 0.f};
+    auto merge = [&](float (&f)[NT][2], float (&fo)[NT][2], const float2 (&other)[NT][2]) {   // factors of ours and theirs
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) r.mx = fmaxf(r.mx, ml[2 * (k * ROWS + row)]);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float mk = ml[2 * (k * ROWS + row)];
-        const float f = mk == -INFINITY ? 0.f : exp2_approx(mk - r.mx);
-        const float2 v = *reinterpret_cast<const float2*>(comb + (k * ROWS + row) * C::kCombLd + at);
-        r.sum = fmaf(f, ml[2 * (k * ROWS + row) + 1], r.sum);
-        r.ox = fmaf(f, v.x, r.ox), r.oy = fmaf(f, v.y, r.oy);
-      }
-      return r;
+        for (int h = 0; h < 2; ++h) {
+          const float mx = fmaxf(m[nt][h], other[nt][h].x);
+          f[nt][h] = exp2_approx(m[nt][h] - mx), fo[nt][h] = exp2_approx(other[nt][h].x - mx);
+          m[nt][h] = mx;
+          l[nt][h] = fmaf(l[nt][h], f[nt][h], other[nt][h].y * fo[nt][h]);
+        }
     };
-    auto finish = [&](const Joined& v, int row, int d) {   // the output of element pair d of a row
-      const int r = s.r * ROWS + row;
-      if (r >= w.rows) return;
-      const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
-      const int64_t tk = w.q.start + tok;
-      const float inv = v.sum == 0.f ? 0.f : 1.f / v.sum;   // 0: no token (a NaN is not)
-      *reinterpret_cast<__nv_bfloat162*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + d) =
-          __floats2bfloat162_rn(v.ox * inv, v.oy * inv);
-      if (d == 0 && p.lse) p.lse[tk * p.Hq + hd] = v.sum == 0.f ? -INFINITY : (v.mx + log2f(v.sum)) * kLn2;
-    };
-    const bool whole = s.n == w.nt;
-    float* part = p.part + static_cast<size_t>(2 * c + (s.first < ubeg ? 0 : 1)) * C::kSlot;
-    for (int i = tid; i < ROWS * D / 2; i += kRowsThreads) {
-      const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
-      const Joined v = joined(row, d);
-      if (whole) {
-        finish(v, row, d);
-      } else {
-        __stcg(reinterpret_cast<float2*>(part + row * D + d), make_float2(v.ox, v.oy));
-        if (d == 0) __stcg(reinterpret_cast<float2*>(part + ROWS * D + 2 * row), make_float2(v.mx, v.sum));
+    auto join = [&]() {   // leaves the sum in warp 0
+#pragma unroll 1
+      for (int half = kWarps / 2; half > 0; half >>= 1) {
+        __syncthreads();   // the places have been read
+        if (warp >= half && warp < 2 * half) {
+          float* dst = jv + (warp - half) * C::kVals * 32 + lane;
+#pragma unroll
+          for (int q = 0; q < WB; ++q)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) dst[((q * NT + nt) * 4 + k) * 32] = o[q][nt][k];
+          if (g == 0)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) jm[(warp - half) * ROWS + 8 * nt + 2 * t + h] = make_float2(m[nt][h], l[nt][h]);
+        }
+        __syncthreads();
+        if (warp < half) {
+          float2 other[NT][2];
+          float f[NT][2], fo[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) other[nt][h] = jm[warp * ROWS + 8 * nt + 2 * t + h];
+          merge(f, fo, other);
+          const float* src = jv + warp * C::kVals * 32 + lane;
+#pragma unroll
+          for (int q = 0; q < WB; ++q)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[q][nt][k] = fmaf(o[q][nt][k], f[nt][k & 1], src[((q * NT + nt) * 4 + k) * 32] * fo[nt][k & 1]);
+        }
       }
-    }
-    if (!whole) {
+    };
+    auto output = [&]() {   // warp 0: the rows' output
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = s.r * ROWS + 8 * nt + 2 * t + h;
+          if (r >= rows) continue;
+          const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
+          const int64_t tk = s.start + tok;
+          const float sum = l[nt][h], inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no token (a NaN is not)
+          uint32_t v[WB];
+#pragma unroll
+          for (int q = 0; q < WB; ++q) {   // elements g D/8 + 2 q and the next
+            const __nv_bfloat162 z = __floats2bfloat162_rn(o[q][nt][h] * inv, o[q][nt][h + 2] * inv);
+            v[q] = *reinterpret_cast<const uint32_t*>(&z);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + g * (D / 8));
+#pragma unroll
+          for (int q = 0; q < WB / 4; ++q) dst[q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          if (g == 0 && p.lse) p.lse[tk * p.Hq + hd] = sum == 0.f ? -INFINITY : (m[nt][h] + log2f(sum)) * kLn2;
+        }
+    };
+    join();
+    if (s.slot < 0) {
+      if (warp == 0) output();
+    } else {
       // The last of the CTAs that share the row tile adds them up, in CTA order:
       // warp k takes every eighth of them, then the warps are joined as above.
-      const int cf = cta_of_unit(s.first, U, P), cl = cta_of_unit(s.first + w.nt - 1, U, P);
-      __syncthreads();
-      if (tid == 0) {
-        fence_acq_rel_gpu();
-        const int done = atomicAdd(&p.cnt[cf], 1);
-        *s_last = done == cl - cf;
-        if (*s_last) {
+      if (warp == 0) {
+        float* dst = p.part + static_cast<size_t>(s.slot) * C::kSlot + lane;
+#pragma unroll
+        for (int q = 0; q < WB; ++q)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) __stcg(dst + ((q * NT + nt) * 4 + k) * 32, o[q][nt][k]);
+        float2* dm = reinterpret_cast<float2*>(p.part + static_cast<size_t>(s.slot) * C::kSlot + ROWS * D);
+        if (g == 0)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) __stcg(dm + 8 * nt + 2 * t + h, make_float2(m[nt][h], l[nt][h]));
+        __syncwarp();
+        if (lane == 0) {
           fence_acq_rel_gpu();
-          p.cnt[cf] = 0;
+          const int done = atomicAdd(&p.cnt[s.cf], 1);
+          *s_last = done == s.cl - s.cf;
+          if (*s_last) {
+            fence_acq_rel_gpu();
+            p.cnt[s.cf] = 0;
+          }
         }
       }
       __syncthreads();
       if (*s_last) {
-        constexpr int kPer = ROWS * D / 128;   // float4 of O a lane
-        constexpr int kLanes = D / 4;          // lanes of a row's float4 (a row is a whole number of passes, or two rows a pass)
-        float4 acc[kPer];
-        float am[kPer], al[kPer];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f), am[k] = -INFINITY, al[k] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            m[nt][h] = kNone, l[nt][h] = 0.f;
+#pragma unroll
+            for (int q = 0; q < WB; ++q) o[q][nt][h] = 0.f, o[q][nt][h + 2] = 0.f;
+          }
 #pragma unroll 1
-        for (int cc = cf + warp; cc <= cl; cc += kWarps) {
-          const float* sl = p.part + static_cast<size_t>(2 * cc + (s.first < unit_begin(cc, U, P) ? 0 : 1)) * C::kSlot;
-          float4 v[kPer];
-          float2 a[kPer];
+        for (int cc = s.cf + warp; cc <= s.cl; cc += kWarps) {
+          const float* src = p.part + static_cast<size_t>(2 * cc + (cc == s.cf ? 1 : 0)) * C::kSlot;
+          float v[C::kVals];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            v[k] = __ldcg(reinterpret_cast<const float4*>(sl) + k * 32 + lane);
-            a[k] = __ldcg(reinterpret_cast<const float2*>(sl + ROWS * D) + (k * 32 + lane) / kLanes);
-          }
+          for (int k = 0; k < C::kVals; ++k) v[k] = __ldcg(src + k * 32 + lane);
+          float2 other[NT][2];
+          float f[NT][2], fo[NT][2];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const float nm = fmaxf(am[k], a[k].x);
-            const float f = am[k] == nm ? 1.f : exp2_approx(am[k] - nm);
-            const float h = a[k].x == -INFINITY ? 0.f : exp2_approx(a[k].x - nm);
-            acc[k].x = fmaf(acc[k].x, f, h * v[k].x), acc[k].y = fmaf(acc[k].y, f, h * v[k].y);
-            acc[k].z = fmaf(acc[k].z, f, h * v[k].z), acc[k].w = fmaf(acc[k].w, f, h * v[k].w);
-            al[k] = fmaf(al[k], f, h * a[k].y);
-            am[k] = nm;
-          }
-        }
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int row = (k * 32 + lane) / kLanes, d = (k * 32 + lane) % kLanes * 4;
-          float* dst = comb + (warp * ROWS + row) * C::kCombLd;
-          // (the order of `joined`: pair d of a row lies at d % (D/8) / 2 * 16 + d / (D/8) * 2)
-          *reinterpret_cast<float2*>(dst + d % (D / 8) / 2 * 16 + d / (D / 8) * 2) = make_float2(acc[k].x, acc[k].y);
-          *reinterpret_cast<float2*>(dst + (d + 2) % (D / 8) / 2 * 16 + (d + 2) / (D / 8) * 2) = make_float2(acc[k].z, acc[k].w);
-          if (d == 0) reinterpret_cast<float2*>(ml)[warp * ROWS + row] = make_float2(am[k], al[k]);
+            for (int h = 0; h < 2; ++h)
+              other[nt][h] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * D) + 8 * nt + 2 * t + h);
+          merge(f, fo, other);
+#pragma unroll
+          for (int q = 0; q < WB; ++q)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                o[q][nt][k] = fmaf(o[q][nt][k], f[nt][k & 1], v[(q * NT + nt) * 4 + k] * fo[nt][k & 1]);
         }
-        __syncthreads();
-        for (int i = tid; i < ROWS * D / 2; i += kRowsThreads) {
-          const int row = i / (D / 2), d = 2 * (i - row * (D / 2));
-          finish(joined(row, d), row, d);
-        }
+        join();
+        if (warp == 0) output();
       }
     }
-    fence_proxy_async();   // what lay over the rings, before copies into them
-    __syncthreads();
+    __syncthreads();   // the segment after the next is known, and nobody reads this one any more
+    seg_ids = page_at(segs[(seg + 2) % 3], lane);
+    if (on == seg) ++on;   // (after a wait that ran out)
   }
 }
 
