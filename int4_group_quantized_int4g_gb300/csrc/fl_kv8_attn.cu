@@ -13,7 +13,7 @@
 // Inside a CTA each of eight warps takes 16 tokens of every unit, with a softmax
 // state of its own, joined once a segment.  A warp copies its slices by TMA
 // (swizzled, so that both operand reads below are free of bank conflicts) into
-// a ring of its own and waits for nobody else; two CTAs fit an SM with 8 rows.
+// a ring of its own and waits for nobody else; two CTAs fit an SM.
 // The copies run on into the CTA's next segment while this one is joined: the
 // segments lie in shared memory one ahead.
 // (With one CTA, a producer warp and a ring that all warps share, reading was
@@ -46,15 +46,17 @@ constexpr float kPScale = 64.f;         // 2^6
 constexpr float kSlack = 8.f;           // a reference may lag its maximum by 2^kSlack
 constexpr float kNone = -1e30f;         // the reference of a row without a token so far
 // Most rows of a sequence (query heads of a kv head x tokens) that this kernel
-// takes; sequences with more go to the tcgen05 kernel, in the same call.
-constexpr int kFewRows = 64;
+// takes; sequences with more go to the tcgen05 kernel, in the same call.  (16
+// sequences of 4096 tokens, 8 heads of 128: with 24 rows 79 us here and 103 us
+// there, with 64 rows 158 us here and 105 us there.)
+constexpr int kFewRows = 32;
 
 template <int D, int NT>
 struct RowsCfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = NT == 1 ? 2 : 1;      // on an SM
+  static constexpr int kCtas = 2;                    // on an SM
   static constexpr int kHalf = 16 * D;               // a warp's keys (or values) of a unit
-  static constexpr int kSlots = (NT == 1 ? 3 : 6) * (128 / D);
+  static constexpr int kSlots = D == 128 ? 3 : NT == 1 ? 6 : 5;
   static constexpr int kRing = kSlots * 2 * kHalf;   // of one warp
   static constexpr int kVals = kRows * D / 32;       // accumulators of a lane
   static constexpr int kJoinOff = kWarps * kRing;    // four warps' accumulators, [warp][value][lane]
@@ -68,7 +70,11 @@ struct RowsCfg {
   static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O [value][lane], then m, l of each row
 };
 
-// The units of one sequence.
+// The units of one sequence.  A row tile counts kEnd more than it has tiles:
+// its start and its join take a CTA about that long, and runs of short
+// sequences would take longer than others otherwise (48 sequences of 130 to
+// 8100 tokens, sorted by length: 128 us without, 97 us with).
+constexpr int kEnd = 2;
 struct SeqWork {
   SeqInfo q;
   int rows, rt, t0, nt;   // row tiles; first tile, tiles
@@ -82,7 +88,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttnParams& p, int b) {
   w.rt = w.rows > p.rows_lo && w.rows <= p.rows_hi ? (w.rows + ROWS - 1) / ROWS : 0;
   w.t0 = first_seen(w.q, p.window) / kTile;
   w.nt = max(1, (w.q.kv + kTile - 1) / kTile - w.t0);   // one even without tokens: it stores the zeros
-  w.units = static_cast<long long>(p.heads) * w.rt * w.nt;
+  w.units = static_cast<long long>(p.heads) * w.rt * (w.nt + kEnd);
   return w;
 }
 
@@ -105,14 +111,21 @@ struct Walk {
   SeqWork w;
   __device__ void next(const AttnParams& p, Segment& s) {
     s.n = 0;
-    if (u >= end) return;
-    while (u >= base + w.units) {
-      base += w.units;
-      if (++b >= p.seqs.B) return;
-      w = seq_work<ROWS>(p, b);
+    long long seg;
+    int t;
+    for (;;) {
+      if (u >= end) return;
+      while (u >= base + w.units) {
+        base += w.units;
+        if (++b >= p.seqs.B) return;
+        w = seq_work<ROWS>(p, b);
+      }
+      const long long local = u - base;
+      seg = local / (w.nt + kEnd);
+      t = static_cast<int>(local - seg * (w.nt + kEnd));
+      if (t < w.nt) break;
+      u += w.nt + kEnd - t;   // what is left of a row tile's last units
     }
-    const long long local = u - base, seg = local / w.nt;
-    const int t = static_cast<int>(local - seg * w.nt);
     s.n = static_cast<int>(min(static_cast<long long>(w.nt - t), end - u));
     s.b = b;
     s.h = static_cast<int>(seg / w.rt);
@@ -639,7 +652,15 @@ int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& 
 
 template <int FMT, int D>
 int pick_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, long long rows, cudaStream_t s) {
-  return rows <= 8 ? launch_rows<FMT, D, 1>(km, vm, p, s) : launch_rows<FMT, D, 2>(km, vm, p, s);
+  // Heads of 64 with more than 8 rows take tiles of 16 (16 sequences of 2 to 5
+  // rows x 3 heads, 37 to 4001 tokens: 29 us against 31 us with tiles of 8; 64
+  // rows over 4096 tokens: 87 against 117).  Heads of 128 always take tiles of 8:
+  // the accumulators of 16 rows leave one CTA on an SM (12 rows: 44 us against
+  // 36 us; 16 rows over 4096 tokens: 52 against 54).
+  if constexpr (D == 64) {
+    if (rows > 8) return launch_rows<FMT, D, 2>(km, vm, p, s);
+  }
+  return launch_rows<FMT, D, 1>(km, vm, p, s);
 }
 
 }  // namespace
@@ -649,7 +670,7 @@ extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, in
   if (head_dim != 64 && head_dim != 128) return FL_ERR_UNSUPPORTED;
   // two partials a CTA: the rows that it shares with the CTAs before and after
   const bool prompt = static_cast<long long>(T) * (Hq / kv_heads) > kFewRows;
-  const size_t few = 16 * (head_dim + 2);   // two CTAs an SM with 8 rows, or one with 16
+  const size_t few = 2 * 16 * (head_dim + 2);   // (two CTAs an SM)
   const size_t slot = prompt ? prompt_slot_floats(head_dim) : few;
   *out = kScratchOff + 2ull * flh::sm_count() * slot * 4;
   return FL_OK;
