@@ -7,181 +7,218 @@
 // If the block holds earlier tokens whose scale was larger it keeps that one;
 // if it was smaller, their codes are moved to the new scale.  Then the new
 // codes are written.  Division by a power of two is exact, so a code is one
-// rounding of its bf16 input.  Bound by HBM: 3 bytes an element.
+// rounding of its bf16 input.  Bound by HBM: 3 bytes an element.  The kernel is
+// built for each block size, so that a thread keeps no more registers than it
+// has vectors and more CTAs fit an SM.
 #include "fl_kv8.cuh"
 
 using namespace flkv;
 
 namespace {
 
-constexpr int kApThreads = 256;
-
+struct Half {   // keys, or values
+  const __nv_bfloat16* src;
+  int64_t stride;
+  uint8_t* dst;
+  float* scale;
+};
 struct AppendParams {
-  const __nv_bfloat16* src[2];
-  int64_t stride[2];
-  uint8_t* dst[2];
-  float* scale[2];
+  Half k, v;
   Seqs seqs;
-  int num_blocks, block, heads;
+  int num_blocks, heads;
   int32_t* status;
 };
 
-__device__ __forceinline__ uint32_t quant_byte(float x, int fmt) {
-  if (fmt == FL_KV8_E4M3) return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-  return static_cast<uint32_t>(static_cast<int>(rintf(x))) & 0xffu;
+// Four values to four codes.  Integers: adding 1.5 * 2^23 leaves the nearest
+// even integer in the sum's low bits.
+template <int FMT>
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
+  if constexpr (FMT == FL_KV8_E4M3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+  } else {
+    constexpr float kMagic = 12582912.f;
+    const uint32_t ab = __byte_perm(__float_as_uint(a + kMagic), __float_as_uint(b + kMagic), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(c + kMagic), __float_as_uint(d + kMagic), 0x0040);
+    return __byte_perm(ab, cd, 0x5410);
+  }
 }
-__device__ __forceinline__ float code_value(uint32_t c, int fmt) {
-  if (fmt == FL_KV8_E4M3) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E4M3);
+template <int FMT>
+__device__ __forceinline__ float code_value(uint32_t c) {
+  if constexpr (FMT == FL_KV8_E4M3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c & 0xffu), __NV_E4M3);
     return __half2float(*reinterpret_cast<const __half*>(&h));
   }
   return static_cast<float>(static_cast<int8_t>(c));
 }
 
-template <int FMT, int D>
-__global__ void __launch_bounds__(kApThreads) k_kv8_append(const AppendParams p) {
-  constexpr int kVecs = 128 * D / 8 / kApThreads;   // vectors of 8 elements a thread, at most
-  __shared__ int s_scan[kApThreads / 32];
-  __shared__ int s_hit[2];
-  __shared__ float s_red[kApThreads / 32];
+// The CTA's sequence and block of it: the x-th written block of the batch.
+template <int THREADS>
+__device__ __forceinline__ bool find_block(const Seqs& s, int block, int x, int& b, int& j) {
+  b = 0, j = x;
+  if (s.B == 1) return true;
+  __shared__ int scan[THREADS / 32 + 2];
+  int* hit = scan + THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the CTA's sequence and block: the blockIdx.x-th touched block of the batch
-  int b = 0, j = blockIdx.x;
-  if (p.seqs.B > 1) {
-    if (tid == 0) s_hit[0] = -1;
-    int base = 0;
-    bool found = false;
-    for (int c = 0; c < p.seqs.B && !found; c += kApThreads) {
-      const int n = c + tid < p.seqs.B ? written_pages(seq_info(p.seqs, c + tid, p.block), p.block).n : 0;
-      int inc = n;
+  if (tid == 0) hit[0] = -1;
+  int base = 0;
+  for (int c = 0; c < s.B && x >= base; c += THREADS) {
+    const int n = c + tid < s.B ? written_pages(seq_info(s, c + tid, block), block).n : 0;
+    int inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
-      __syncthreads();
-      int before = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kApThreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        all += s_scan[w];
-      }
-      const int mine = base + before + inc - n;
-      if (static_cast<int>(blockIdx.x) >= mine && static_cast<int>(blockIdx.x) < mine + n) {
-        s_hit[0] = c + tid;
-        s_hit[1] = blockIdx.x - mine;
-      }
-      base += all;
-      found = static_cast<int>(blockIdx.x) < base;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
     }
     __syncthreads();
-    b = s_hit[0];
-    j = s_hit[1];
-    if (b < 0) return;
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+    const int mine = base + before + inc - n;
+    if (x >= mine && x < mine + n) {
+      hit[0] = c + tid;
+      hit[1] = x - mine;
+    }
+    base += all;
   }
-  const SeqInfo q = seq_info(p.seqs, b, p.block);
-  const PageRun run = written_pages(q, p.block);
+  __syncthreads();
+  b = hit[0];
+  j = hit[1];
+  return b >= 0;
+}
+
+template <int FMT, int D, int BLK>
+struct ApCfg {
+  static constexpr int kAll = BLK * D / 8;                    // vectors of 8 elements of a block
+  static constexpr int kThreads = kAll < 256 ? kAll : 256;
+  static constexpr int kVecs = kAll / kThreads;               // of a thread, at most
+};
+
+template <int FMT, int D, int BLK>
+__global__ void __launch_bounds__(ApCfg<FMT, D, BLK>::kThreads) k_kv8_append(const AppendParams p) {
+  using C = ApCfg<FMT, D, BLK>;
+  constexpr int kThreads = C::kThreads, kVecs = C::kVecs, kWarps = kThreads / 32;
+  __shared__ float s_red[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int b, j;
+  if (!find_block<kThreads>(p.seqs, BLK, blockIdx.x, b, j)) return;
+  const SeqInfo q = seq_info(p.seqs, b, BLK);
+  const PageRun run = written_pages(q, BLK);
   if (j >= run.n) return;
   const int p0 = max(q.kv - q.n, 0);           // first position written
   const int jb = run.first + j;
-  const int lo = max(p0 - jb * p.block, 0);    // slots [lo, hi) of the block are written
-  const int hi = min(q.kv - jb * p.block, p.block);
-  const int head = blockIdx.y, kv = blockIdx.z;
+  const int lo = max(p0 - jb * BLK, 0);        // slots [lo, hi) of the block are written
+  const int hi = min(q.kv - jb * BLK, BLK);
+  const int head = blockIdx.y;
+  const bool vals = blockIdx.z != 0;
+  const Half h = {vals ? p.v.src : p.k.src, vals ? p.v.stride : p.k.stride, vals ? p.v.dst : p.k.dst,
+                  vals ? p.v.scale : p.k.scale};
   const int page = page_block(p.seqs, b, jb, p.num_blocks);
+  // row of the first written token in the call's tokens
+  const int64_t row0 = static_cast<int64_t>(q.start) + (jb * BLK + lo - (q.kv - q.n));
+  const __nv_bfloat16* src = h.src + row0 * h.stride + head * D;
+  const int nv = (hi - lo) * (D / 8);
+  uint4 x[kVecs];
+  uint32_t top2 = 0;   // the largest magnitudes' bits, of either half of a word
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int v = i * kThreads + tid;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (v < nv) x[i] = __ldcs(reinterpret_cast<const uint4*>(src + static_cast<int64_t>(v / (D / 8)) * h.stride + v % (D / 8) * 8));
+  }
   if (page < 0) {
     if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 50);
     return;
   }
   const int64_t tile = static_cast<int64_t>(page) * p.heads + head;
-  uint8_t* codes = p.dst[kv] + tile * p.block * D;
-  // row of the first written token in the call's tokens
-  const int64_t row0 = static_cast<int64_t>(q.start) + (jb * p.block + lo - (q.kv - q.n));
-  const __nv_bfloat16* src = p.src[kv] + row0 * p.stride[kv] + head * D;
-  const int nv = (hi - lo) * (D / 8);
-  uint4 x[kVecs];
-  float top = 0.f;
-  bool odd = false;   // an infinity or NaN
+  uint8_t* codes = h.dst + tile * BLK * D;
+  const float old = lo > 0 ? h.scale[tile] : 0.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int v = i * kApThreads + tid;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (v < nv) x[i] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(v / (D / 8)) * p.stride[kv] + v % (D / 8) * 8);
+    top2 = __vmaxu2(top2, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu));
+    top2 = __vmaxu2(top2, __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
   }
+  uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+  if (top >= 0x7f80u) {
+    // infinities become the largest finite bf16, NaN 0
+    set_status(p.status, FL_ERR_RANGE, 51);
+    top = 0;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    uint32_t* a = &x[i].x;
+    for (int i = 0; i < kVecs; ++i) {
+      auto mend = [&](uint32_t a) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      // an infinity becomes the largest finite bf16, a NaN 0
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t e = (a[t] >> (16 * h)) & 0x7fffu;
-        if (e >= 0x7f80u) {
-          odd = true;
-          const uint32_t keep = e == 0x7f80u ? ((a[t] >> (16 * h)) & 0x8000u) | 0x7f7fu : 0u;
-          a[t] = (a[t] & ~(0xffffu << (16 * h))) | (keep << (16 * h));
+        for (int h = 0; h < 32; h += 16) {
+          const uint32_t e = (a >> h) & 0x7fffu;
+          if (e >= 0x7f80u) a = (a & ~(0xffffu << h)) | (e == 0x7f80u ? ((a >> h) & 0x8000u) | 0x7f7fu : 0u) << h;
+          top = max(top, (a >> h) & 0x7fffu);
         }
-      }
-      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(a[t] << 16)), fabsf(__uint_as_float(a[t] & 0xffff0000u))));
+        return a;
+      };
+      x[i] = make_uint4(mend(x[i].x), mend(x[i].y), mend(x[i].z), mend(x[i].w));
     }
   }
-  if (odd) set_status(p.status, FL_ERR_RANGE, 51);
-  const float old = lo > 0 ? p.scale[kv][tile] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_red[warp] = top;
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (lane == 0) s_red[warp] = __uint_as_float(top);
   __syncthreads();   // (also: every thread has read the old scale)
 #pragma unroll
-  for (int w = 0; w < kApThreads / 32; ++w) top = fmaxf(top, s_red[w]);
+  for (int w = 0; w < kWarps; ++w) top = max(top, __float_as_uint(s_red[w]));
   // top = m 2^e with 1 <= m < 2; the range's end is 1.75 * 2^8 or 1.984375 * 2^6
-  const uint32_t bits = __float_as_uint(top);
-  int e = static_cast<int>(bits >> 23) - 127 - (FMT == FL_KV8_E4M3 ? 8 : 6);
-  if ((bits & 0x7fffffu) > (FMT == FL_KV8_E4M3 ? 0x600000u : 0x7e0000u)) ++e;
+  int e = static_cast<int>(top >> 7) - 127 - (FMT == FL_KV8_E4M3 ? 8 : 6);
+  if ((top & 0x7fu) > (FMT == FL_KV8_E4M3 ? 0x60u : 0x7eu)) ++e;
   const float need = pow2i(max(e, -126));
   const bool keep = lo > 0 && old >= need;
   const float scale = keep ? old : need;
   if (lo > 0 && !keep) {
     // earlier tokens move to the larger scale, rounded once more
     const float ratio = old / scale;
-    for (int v = tid; v < lo * (D / 16); v += kApThreads) {
-      uint4 c = reinterpret_cast<const uint4*>(codes)[v];
-      uint32_t* a = &c.x;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t o = 0;
-#pragma unroll
-        for (int h = 0; h < 4; ++h) o |= quant_byte(code_value((a[t] >> (8 * h)) & 0xffu, FMT) * ratio, FMT) << (8 * h);
-        a[t] = o;
-      }
-      reinterpret_cast<uint4*>(codes)[v] = c;
+    for (int v = tid; v < lo * (D / 16); v += kThreads) {
+      const uint4 c = reinterpret_cast<const uint4*>(codes)[v];
+      auto move = [&](uint32_t a) {
+        return quant4<FMT>(code_value<FMT>(a) * ratio, code_value<FMT>(a >> 8) * ratio, code_value<FMT>(a >> 16) * ratio,
+                           code_value<FMT>(a >> 24) * ratio);
+      };
+      reinterpret_cast<uint4*>(codes)[v] = make_uint4(move(c.x), move(c.y), move(c.z), move(c.w));
     }
   }
   // 1 / scale: exact for a power of two; a scale that a caller chose is divided by
   const bool pow2 = (__float_as_uint(scale) & 0x7fffffu) == 0;
   const float inv = 1.f / scale;
-  const float most = FMT == FL_KV8_E4M3 ? 448.f : 127.f;
+  constexpr float kTop = FMT == FL_KV8_E4M3 ? 448.f : 127.f;
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int v = i * kApThreads + tid;
+    const int v = i * kThreads + tid;
     if (v >= nv) continue;
     const uint32_t a[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t o[2] = {0, 0};
+    float f[8];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const float f = __uint_as_float((t & 1) ? a[t >> 1] & 0xffff0000u : a[t >> 1] << 16);
-      const float u = fminf(fmaxf(pow2 ? f * inv : f / scale, -most), most);
-      o[t >> 2] |= quant_byte(u, FMT) << (8 * (t & 3));
+    for (int t = 0; t < 4; ++t) f[2 * t] = __uint_as_float(a[t] << 16), f[2 * t + 1] = __uint_as_float(a[t] & 0xffff0000u);
+    if (pow2) {   // (of the largest value's own making, or larger: nothing is outside the range)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) f[t] *= inv;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) f[t] = fminf(fmaxf(f[t] / scale, -kTop), kTop);
     }
-    reinterpret_cast<uint2*>(codes + static_cast<int64_t>(lo) * D)[v] = make_uint2(o[0], o[1]);
+    reinterpret_cast<uint2*>(codes + static_cast<int64_t>(lo) * D)[v] =
+        make_uint2(quant4<FMT>(f[0], f[1], f[2], f[3]), quant4<FMT>(f[4], f[5], f[6], f[7]));
   }
-  if (tid == 0) p.scale[kv][tile] = scale;
+  if (tid == 0) h.scale[tile] = scale;
 }
 
 template <int FMT, int D>
-void launch_append(const AppendParams& p, dim3 grid, cudaStream_t s) {
-  k_kv8_append<FMT, D><<<grid, kApThreads, 0, s>>>(p);
+void launch_append(const AppendParams& p, int block, dim3 grid, cudaStream_t s) {
+  switch (block) {
+    case 16: k_kv8_append<FMT, D, 16><<<grid, ApCfg<FMT, D, 16>::kThreads, 0, s>>>(p); break;
+    case 32: k_kv8_append<FMT, D, 32><<<grid, ApCfg<FMT, D, 32>::kThreads, 0, s>>>(p); break;
+    case 64: k_kv8_append<FMT, D, 64><<<grid, ApCfg<FMT, D, 64>::kThreads, 0, s>>>(p); break;
+    default: k_kv8_append<FMT, D, 128><<<grid, ApCfg<FMT, D, 128>::kThreads, 0, s>>>(p); break;
+  }
 }
 
 }  // namespace
@@ -195,12 +232,10 @@ extern "C" int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int
   if (k_stride < width || v_stride < width || k_stride % 8 || v_stride % 8) return FL_ERR_ARG;
   if (cache->kv_heads > 65535) return FL_ERR_UNSUPPORTED;
   AppendParams p;
-  p.src[0] = static_cast<const __nv_bfloat16*>(k), p.src[1] = static_cast<const __nv_bfloat16*>(v);
-  p.stride[0] = k_stride, p.stride[1] = v_stride;
-  p.dst[0] = static_cast<uint8_t*>(cache->k), p.dst[1] = static_cast<uint8_t*>(cache->v);
-  p.scale[0] = cache->k_scale, p.scale[1] = cache->v_scale;
+  p.k = {static_cast<const __nv_bfloat16*>(k), k_stride, static_cast<uint8_t*>(cache->k), cache->k_scale};
+  p.v = {static_cast<const __nv_bfloat16*>(v), v_stride, static_cast<uint8_t*>(cache->v), cache->v_scale};
   p.seqs = {seqs->cu_q, seqs->kv_lens, seqs->block_table, seqs->T, seqs->B, seqs->max_q, seqs->max_blocks};
-  p.num_blocks = cache->num_blocks, p.block = cache->block, p.heads = cache->kv_heads;
+  p.num_blocks = cache->num_blocks, p.heads = cache->kv_heads;
   p.status = static_cast<int32_t*>(status);
   // n new tokens touch at most (n - 1) / block + 2 blocks, and never more than
   // n; so the batch at most the sum of either over its sequences
@@ -210,9 +245,11 @@ extern "C" int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int
   const dim3 grid(static_cast<unsigned>(most), cache->kv_heads, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->format == FL_KV8_E4M3)
-    cache->head_dim == 64 ? launch_append<FL_KV8_E4M3, 64>(p, grid, s) : launch_append<FL_KV8_E4M3, 128>(p, grid, s);
+    cache->head_dim == 64 ? launch_append<FL_KV8_E4M3, 64>(p, cache->block, grid, s)
+                          : launch_append<FL_KV8_E4M3, 128>(p, cache->block, grid, s);
   else
-    cache->head_dim == 64 ? launch_append<FL_KV8_INT8, 64>(p, grid, s) : launch_append<FL_KV8_INT8, 128>(p, grid, s);
+    cache->head_dim == 64 ? launch_append<FL_KV8_INT8, 64>(p, cache->block, grid, s)
+                          : launch_append<FL_KV8_INT8, 128>(p, cache->block, grid, s);
   return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
 }
 
