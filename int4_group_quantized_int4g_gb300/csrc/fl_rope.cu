@@ -6,9 +6,11 @@
 // * 2^64 and pos * step_i mod 2^64 is the angle's fraction of a turn, exact
 // but for the rounding of step_i (2^-53 of f_i; at position 2^20 that is
 // 2^-33 of a turn), with no table and no fp64 in the loop.  Its top 32 bits go
-// through sincospif.  The sines of one token's pairs are computed once, into
-// shared memory, for all of its heads, so the kernel is bound by HBM: 4 bytes
-// an element.
+// through sincospif.  The sines of a token's pairs are computed once, into
+// shared memory, for all of its heads, in the order in which neighbouring
+// threads read them (pair by pair they met four-way bank conflicts: 64 us for
+// 16381 tokens of 36 heads of 128 instead of 54).  Bound by HBM, 4 bytes an
+// element: 302 MB there, 5.6 TB/s, what a plain copy reaches.
 #include "fl_common.cuh"
 
 using namespace fl;
@@ -28,7 +30,7 @@ struct RopeParams {
   const double* freq;
   int64_t qs, ks, qos, kos;
   int T, Hq, Hk, D, rot, style, axes, tt;   // tt: tokens of a pass
-  int end[FL_ROPE_MAX_AXES];                // first pair past each axis's section
+  int end0, end1, end2;                     // first pair past the first, second, third axis's section
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -38,79 +40,128 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// What one thread moves: 8 pairs of either half (halves), 4 pairs (pairs), 8
+// copied elements; or, element by element, one pair or one copied element.
 template <bool VEC>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeParams p) {
+struct Unit {
+  uint4 a, b;
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;
+  int tok;
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(kRopeThreads, 5) k_rope(const RopeParams p) {
   __shared__ unsigned long long step[kRopePairs];
   __shared__ __align__(16) float2 sc[kRopeTable];   // (cos, sin)
   const int pairs = p.rot / 2, heads = p.Hq + p.Hk;
+  const bool halves = p.style == FL_ROPE_HALVES;
+  const int turned = VEC ? (halves ? pairs / 8 : p.rot / 8) : pairs;   // units of a head that turn
+  const int units = turned + (VEC ? (p.D - p.rot) / 8 : p.D - p.rot);
+  // A thread keeps its unit of a head and steps through the heads of the CTA's
+  // tokens; `lanes` threads have a head, `step_h` heads go at a time.
+  const int lanes = min(units, kRopeThreads), step_h = kRopeThreads / lanes;
+  const int h0 = threadIdx.x / lanes;
+  const int t0 = blockIdx.x * p.tt, nt = min(p.tt, p.T - t0);
+  int u = threadIdx.x - h0 * lanes;
+  int at = 0, t = 0, h = 0, left = 0;   // the unit's first element, the next head, heads left
+  auto begin = [&]() {
+    at = u < turned ? (VEC ? 8 * u : 0) : p.rot + (u - turned) * (VEC ? 8 : 1);
+    t = h0 / heads, h = h0 - t * heads;
+    left = h0 < step_h ? (nt * heads - h0 + step_h - 1) / step_h : 0;
+  };
+  auto load = [&](Unit<VEC>& x) {   // of the thread's next head
+    x.tok = t;
+    const int64_t tok = t0 + t;
+    x.src = h < p.Hq ? p.q + tok * p.qs + h * p.D : p.k + tok * p.ks + (h - p.Hq) * p.D;
+    x.dst = h < p.Hq ? p.qo + tok * p.qos + h * p.D : p.ko + tok * p.kos + (h - p.Hq) * p.D;
+    if constexpr (VEC) {
+      x.a = *reinterpret_cast<const uint4*>(x.src + at);
+      if (u < turned && halves) x.b = *reinterpret_cast<const uint4*>(x.src + pairs + at);
+    }
+    h += step_h;
+    while (h >= heads) h -= heads, ++t;
+  };
+  // the first loads go out before the sines are computed
+  Unit<VEC> x, y;
+  begin();
+  if (left > 0) load(x);
+  if (left > 1) load(y);
+
   for (int i = threadIdx.x; i < pairs; i += kRopeThreads) {
     const double turns = p.freq[i] * 0.15915494309189533576888376337251436;   // 1 / (2 pi)
     step[i] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
   }
-  // units of work of a head: 8 elements of either half (halves) or 8 adjacent
-  // elements (pairs), or one pair or one copied element
-  const int turn_units = VEC ? (p.style == FL_ROPE_HALVES ? pairs / 8 : p.rot / 8) : pairs;
-  const int units = turn_units + (VEC ? (p.D - p.rot) / 8 : p.D - p.rot);
-  for (int t0 = blockIdx.x * p.tt; t0 < p.T; t0 += gridDim.x * p.tt) {
-    const int nt = min(p.tt, p.T - t0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-      const int t = i / pairs, pr = i - t * pairs;
-      int a = 0;
-      while (a + 1 < p.axes && pr >= p.end[a]) ++a;
-      const long long at = p.pos[static_cast<int64_t>(a) * p.T + t0 + t];
-      const unsigned long long ph = static_cast<unsigned long long>(at) * step[pr];
-      const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077392578125e-10f;
-      float s, c;
-      sincospif(half_turns, &s, &c);
-      sc[i] = make_float2(c, s);
-    }
-    __syncthreads();
-    const int n = nt * heads * units;
-    for (int i = threadIdx.x; i < n; i += kRopeThreads) {
-      const int hh = i / units, u = i - hh * units;
-      const int t = hh / heads, h = hh - t * heads;
-      const int64_t tok = t0 + t;
-      const __nv_bfloat16* src = h < p.Hq ? p.q + tok * p.qs + h * p.D : p.k + tok * p.ks + (h - p.Hq) * p.D;
-      __nv_bfloat16* dst = h < p.Hq ? p.qo + tok * p.qos + h * p.D : p.ko + tok * p.kos + (h - p.Hq) * p.D;
-      const float2* cs = sc + t * pairs;
-      if (u >= turn_units) {   // past the rotated part
-        const int c = p.rot + (u - turn_units) * (VEC ? 8 : 1);
-        if constexpr (VEC)
-          *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-        else
-          dst[c] = src[c];
-      } else if constexpr (!VEC) {
-        const int a = p.style == FL_ROPE_HALVES ? u : 2 * u, b = p.style == FL_ROPE_HALVES ? u + pairs : 2 * u + 1;
-        const float x = __bfloat162float(src[a]), y = __bfloat162float(src[b]);
-        dst[a] = __float2bfloat16_rn(x * cs[u].x - y * cs[u].y);
-        dst[b] = __float2bfloat16_rn(y * cs[u].x + x * cs[u].y);
-      } else if (p.style == FL_ROPE_HALVES) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(src + 8 * u);
-        const uint4 yv = *reinterpret_cast<const uint4*>(src + pairs + 8 * u);
-        const uint32_t xa[4] = {xv.x, xv.y, xv.z, xv.w}, ya[4] = {yv.x, yv.y, yv.z, yv.w};
+  __syncthreads();
+  // Where a token's pair lies: the unit's pairs two by two, all units' first two,
+  // then their next, so that neighbouring lanes read neighbouring 16 bytes.
+  auto place = [&](int pr) {
+    if (!VEC) return pr;
+    const int per = halves ? 8 : 4, unit = pr / per, k = pr - unit * per;
+    return ((k >> 1) * turned + unit) * 2 + (k & 1);
+  };
+  for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
+    const int tok = i / pairs, pr = i - tok * pairs;
+    const int a = (pr >= p.end0) + (pr >= p.end1) + (pr >= p.end2);
+    const long long pos = p.pos[static_cast<int64_t>(a) * p.T + t0 + tok];
+    const unsigned long long ph = static_cast<unsigned long long>(pos) * step[pr];
+    const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077392578125e-10f;
+    float sn, c;
+    sincospif(half_turns, &sn, &c);
+    sc[tok * pairs + place(pr)] = make_float2(c, sn);
+  }
+  __syncthreads();
+  {
+    auto store = [&](const Unit<VEC>& x) {
+      const float2* cs = sc + x.tok * pairs;
+      if constexpr (!VEC) {
+        if (u >= turned) {
+          x.dst[at] = x.src[at];
+        } else {
+          const int a = halves ? u : 2 * u, b = halves ? u + pairs : 2 * u + 1;
+          const float v = __bfloat162float(x.src[a]), w = __bfloat162float(x.src[b]);
+          x.dst[a] = __float2bfloat16_rn(v * cs[u].x - w * cs[u].y);
+          x.dst[b] = __float2bfloat16_rn(w * cs[u].x + v * cs[u].y);
+        }
+      } else if (u >= turned) {   // past the rotated part
+        *reinterpret_cast<uint4*>(x.dst + at) = x.a;
+      } else if (halves) {
+        const uint32_t xa[4] = {x.a.x, x.a.y, x.a.z, x.a.w}, ya[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
         uint32_t xo[4], yo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float4 w = *reinterpret_cast<const float4*>(cs + 8 * u + 2 * j);
+          const float4 w = *reinterpret_cast<const float4*>(cs + (j * turned + u) * 2);
           const float x0 = lo_f(xa[j]), x1 = hi_f(xa[j]), y0 = lo_f(ya[j]), y1 = hi_f(ya[j]);
           xo[j] = pack_bf16(x0 * w.x - y0 * w.y, x1 * w.z - y1 * w.w);
           yo[j] = pack_bf16(y0 * w.x + x0 * w.y, y1 * w.z + x1 * w.w);
         }
-        *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-        *reinterpret_cast<uint4*>(dst + pairs + 8 * u) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+        *reinterpret_cast<uint4*>(x.dst + at) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+        *reinterpret_cast<uint4*>(x.dst + pairs + at) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
       } else {
-        const uint4 xv = *reinterpret_cast<const uint4*>(src + 8 * u);
-        const uint32_t xa[4] = {xv.x, xv.y, xv.z, xv.w};
+        const uint32_t xa[4] = {x.a.x, x.a.y, x.a.z, x.a.w};
         uint32_t xo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 w = cs[4 * u + j];
-          const float x = lo_f(xa[j]), y = hi_f(xa[j]);
-          xo[j] = pack_bf16(x * w.x - y * w.y, y * w.x + x * w.y);
+          const float2 w = cs[((j >> 1) * turned + u) * 2 + (j & 1)];
+          const float v = lo_f(xa[j]), z = hi_f(xa[j]);
+          xo[j] = pack_bf16(v * w.x - z * w.y, z * w.x + v * w.y);
         }
-        *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+        *reinterpret_cast<uint4*>(x.dst + at) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
       }
+    };
+    for (;;) {
+      while (left > 0) {   // two heads at a time
+        store(x);
+        if (left > 1) store(y);
+        left -= 2;
+        if (left > 0) load(x);
+        if (left > 1) load(y);
+      }
+      u += lanes;   // (a head of more units than the CTA has threads)
+      if (u >= units || h0 >= step_h) break;
+      begin();
+      if (left > 0) load(x);
+      if (left > 1) load(y);
     }
   }
 }
@@ -134,14 +185,15 @@ extern "C" int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, i
       !aligned_to(positions, 4) || !aligned_to(inv_freq, 8))
     return FL_ERR_ARG;
   RopeParams p;
-  int sum = 0;
+  int sum = 0, end[FL_ROPE_MAX_AXES];
   for (int a = 0; a < FL_ROPE_MAX_AXES; ++a) {
     const int n = a >= n_axes ? 0 : sections ? sections[a] : rot / 2;
     if (n < 0 || n > rot / 2) return FL_ERR_ARG;
     sum += n;
-    p.end[a] = sum;
+    end[a] = sum;
   }
   if (sum != rot / 2) return FL_ERR_ARG;
+  p.end0 = end[0], p.end1 = end[1], p.end2 = end[2];
   p.q = static_cast<const __nv_bfloat16*>(q), p.k = static_cast<const __nv_bfloat16*>(k);
   p.qo = static_cast<__nv_bfloat16*>(q_out), p.ko = static_cast<__nv_bfloat16*>(k_out);
   p.pos = positions, p.freq = inv_freq;
@@ -152,15 +204,15 @@ extern "C" int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, i
              q_out_stride % 8 == 0;
   if (Hk > 0)
     vec = vec && aligned_to(k, 16) && aligned_to(k_out, 16) && k_stride % 8 == 0 && k_out_stride % 8 == 0;
-  // tokens of a pass: as many as give every thread of a CTA a unit, within the table
-  const int per = (Hq + Hk) * (vec ? (style == FL_ROPE_HALVES ? D / 16 : D / 8) : pairs);
-  int tt = kRopeThreads / (per > 0 ? per : 1);
-  if (tt > kRopeTable / pairs) tt = kRopeTable / pairs;
+  // Tokens of a CTA: as many as fit the table, up to 8, but with few tokens one
+  // each, so that every SM gets some.  (16381 tokens of 36 heads: 54 us with 8,
+  // 56 with 4, 58 with 16; a plain copy of the same bytes takes 54.)
+  int tt = kRopeTable / pairs < 8 ? kRopeTable / pairs : 8;
+  const int even = static_cast<int>(T / (4ll * flh::sm_count()));
+  if (tt > even) tt = even;
   if (tt < 1) tt = 1;
   p.tt = tt;
-  const int64_t passes = (static_cast<int64_t>(T) + tt - 1) / tt;
-  const int64_t most = 8ll * flh::sm_count();   // resident CTAs: 8 of 256 threads on an SM
-  const unsigned grid = static_cast<unsigned>(passes < most ? passes : most);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + tt - 1) / tt);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (vec)
     k_rope<true><<<grid, kRopeThreads, 0, s>>>(p);
