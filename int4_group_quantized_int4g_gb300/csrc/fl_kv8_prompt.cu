@@ -119,13 +119,6 @@ __device__ __forceinline__ void tmem_ld8_wait(uint32_t (&r)[8]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld16f(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  tmem_ld16_issue(taddr, r);
-  tmem_ld_wait(r);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
 // 64 columns, and the wait for them, in one: the registers need no tie to a wait
 // of its own (which cost a move for each).
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&a)[32], float (&b)[32]) {
@@ -149,13 +142,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
-}
-
-__device__ __forceinline__ void tmem_st16f(uint32_t taddr, const float (&v)[16]) {
-  uint32_t r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
-  tmem_st16(taddr, r);
 }
 
 template <int N>
@@ -191,28 +177,45 @@ struct PromptWalk {
   long long u, end, base;
   int b;
   PromptWork w;
+  // the item that unit u lies in: of head h, `nt` units from the head's `at` on
+  int h, item, nt;
+  long long at;
   __device__ void load(const AttnParams& p) {
     w = prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi);
   }
-  // Moves to the sequence that unit u lies in; false past the last.
-  __device__ bool seek(const AttnParams& p) {
-    while (u >= base + w.per_head * p.heads) {
-      base += w.per_head * p.heads;
-      if (++b >= p.seqs.B) return false;
-      load(p);
+  // Finds unit u's item; u lies in sequence b, which is loaded.
+  __device__ void find() {
+    const long long local = u - base;
+    h = static_cast<int>(local / w.per_head);
+    const long long in_head = local - h * w.per_head;
+    item = w.item_of(in_head);
+    at = w.before(item);
+    nt = static_cast<int>(w.before(item + 1) - at);
+  }
+  // Moves to the next item; false past the last.
+  __device__ bool step(const AttnParams& p) {
+    at += nt;
+    if (++item == w.items) {
+      item = 0, at = 0;
+      if (++h == p.heads) {
+        h = 0;
+        base += w.per_head * p.heads;
+        do {
+          if (++b >= p.seqs.B) return false;
+          load(p);
+        } while (w.items == 0);
+      }
     }
+    nt = static_cast<int>(w.before(item + 1) - at);
     return true;
   }
   __device__ bool next(const AttnParams& p, Segment& s, long long ubeg) {
     s.units = -1;
-    if (u >= end || !seek(p)) return false;
-    const long long local = u - base;
-    s.b = b;
-    s.h = static_cast<int>(local / w.per_head);
-    const long long in_head = local - s.h * w.per_head;
-    const int item = w.item_of(in_head), nt = w.tiles(item);
-    const int t = static_cast<int>(in_head - w.before(item));
+    if (u >= end) return false;
+    const int t = static_cast<int>(u - base - h * w.per_head - at);
     const int n = static_cast<int>(min(static_cast<long long>(nt - t), end - u));
+    s.b = b;
+    s.h = h;
     s.row0 = item * kPromptRows;
     s.rows = w.rows;
     s.tile = w.first_tile(item) + t;
@@ -225,6 +228,7 @@ struct PromptWalk {
     // a CTA's partials: 0 for an item begun by the CTAs before, 1 for one begun here
     s.slot = n == nt ? -1 : 2 * static_cast<int>(blockIdx.x) + (u - t < ubeg ? 0 : 1);
     u += n;
+    if (u < end && t + n == nt) step(p);
     return true;
   }
 };
@@ -345,38 +349,46 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const bool general = s.general != 0;
       float a = 0.f;
       if (live > 0) {
-        // the row of q, times a power of two and the sign of the scale, as f16
-        uint4 x[D / 8];
+        // The warp's 32 rows of q, times a power of two a row and the sign of the
+        // scale, as f16: kL lanes read a row together (one lane a row met 32 lines
+        // a load), kR rows a load.
+        constexpr int kL = D / 8, kR = 32 / kL, kN = 32 / kR;
+        const int own = s.row0 + 128 * t + r, tok = own / p.group;
+        const unsigned long long from =
+            own < s.rows ? reinterpret_cast<unsigned long long>(p.q + (static_cast<int64_t>(s.start) + tok) * p.qs +
+                                                                static_cast<int64_t>(s.h * p.group + own - tok * p.group) * D)
+                         : 0ull;
+        uint4 x[kN];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0, 0, 0, 0);
-        const int row = s.row0 + 128 * t + r, tok = row / p.group;
-        if (row < s.rows) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(s.start) + tok) * p.qs +
-                                                            static_cast<int64_t>(s.h * p.group + row - tok * p.group) * D);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) x[i] = src[i];
+        for (int i = 0; i < kN; ++i) {
+          const unsigned long long row = __shfl_sync(0xffffffffu, from, kR * i + lane / kL);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (row) x[i] = reinterpret_cast<const uint4*>(row)[lane % kL];
         }
-        uint32_t top = 0;
+        uint32_t mine = 0;   // the largest magnitude's bits of the own row
+        const uint32_t sign = p.scale2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
+        for (int i = 0; i < kN; ++i) {
           const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7fffu, (v[k] >> 16) & 0x7fffu));
-        }
-        const int e = row_exponent(top);
-        const float down = copysignf(pow2i(-e), p.scale2);
-        a = fabsf(p.scale2) * pow2i(e) * pow2i(max(s.ke - code_shift<FMT>(), -126));
-        a = fmaxf(a, 1.1754943508222875e-38f);   // (not 0: -inf of a masked column stays -inf)
-        uint8_t* q = smem + t * C::kQ + r * 128;
+          for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+          top = max(top & 0xffffu, top >> 16);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          for (int q = 1; q < kL; q <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, q));
+          const uint32_t other = __shfl_sync(0xffffffffu, top, lane % kR * kL);
+          if (lane / kR == i) mine = other;
+          const float down = pow2i(-row_exponent(top));
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            o[k] = pack_f16(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xffff0000u) * down);
-          *reinterpret_cast<uint4*>(q + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            o[k] = pack_f16(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xffff0000u) * down) ^ sign;
+          const int rr = (warp & 3) * 32 + kR * i + lane / kL, ch = lane % kL;
+          *reinterpret_cast<uint4*>(smem + t * C::kQ + rr * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rr & 7)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
+        a = fabsf(p.scale2) * pow2i(row_exponent(mine)) * pow2i(max(s.ke - code_shift<FMT>(), -126));
+        a = fmaxf(a, 1.1754943508222875e-38f);   // (not 0: -inf of a masked column stays -inf)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
@@ -397,25 +409,22 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // fit the instruction cache together, and a unit took twice as long.  And
         // they spill no register: little of the L1 is left beside the tiles, so
         // that a spilled value comes back from L2.
-        if (j >= plain_end || j < plain_begin || general) {
-          // S as it is meant, back to its columns: the keys' mantissas, -inf
-          // where this row does not see the token
-          const int pos = s.tile * kPromptTile + 64 * j;
-          const int hi = s.past + min(s.row0 + 128 * t + r, s.rows - 1) / p.group + 1 - pos;   // columns [lo, hi) are seen
-          const int lo = p.window ? hi - p.window : -0x40000000;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            float v[16];
-            tmem_ld16f(ts + 16 * k, v);
-            const float mk = general ? meta[((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1) + k].x : 1.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = 16 * k + i >= hi || 16 * k + i < lo ? -INFINITY : v[i] * mk;
-            tmem_st16f(ts + 16 * k, v);
-          }
-          tmem_wait_st();
-        }
         float x[2][32];
         tmem_ld64(ts, x[0], x[1]);
+        if (general) {   // the keys' mantissas
+          const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] *= mt[i >> 4].x;
+        }
+        if (j >= plain_end || j < plain_begin) {
+          // -inf where this row does not see the token: columns [lo, hi) are seen
+          const int pos = s.tile * kPromptTile + 64 * j;
+          const int hi = s.past + min(s.row0 + 128 * t + r, s.rows - 1) / p.group + 1 - pos;
+          const int lo = p.window ? hi - p.window : -0x40000000;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= hi || i < lo) x[i >> 5][i & 31] = -INFINITY;
+        }
         float mx4[4] = {x[0][0], x[0][1], x[1][0], x[1][1]};
 #pragma unroll
         for (int i = 1; i < 16; ++i) {
@@ -479,12 +488,16 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       }
       const float back = pow2i(max(s.ve - code_shift<FMT>(), -126));
       if (s.slot < 0) {
+        // The warp's rows as bf16 over its rows of q, which is not needed any more,
+        // then out, kL lanes a row.
         const int row = s.row0 + 128 * t + r, tok = min(row, s.rows - 1) / p.group;
-        const bool real = row < s.rows;
         const float inv = l == 0.f ? 0.f : back / l;   // 0: no token (a NaN is not)
         const int64_t tk = static_cast<int64_t>(s.start) + tok;
         const int hd = s.h * p.group + row - tok * p.group;
-        __nv_bfloat16* dst = p.out + tk * p.os + static_cast<int64_t>(hd) * D;
+        const unsigned long long into =
+            row < s.rows ? reinterpret_cast<unsigned long long>(p.out + tk * p.os + static_cast<int64_t>(hd) * D) : 0ull;
+        if (row < s.rows && p.lse) p.lse[tk * p.Hq + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        uint8_t* tile = smem + t * C::kQ;
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           // elements 32 i .. 32 i + 31: columns 8 i .. 8 i + 7 of each quarter
@@ -499,21 +512,31 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld8_wait(o[q]);
           }
-          if (real) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t v[4];
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(o[2 * (q & 1)][2 * k + (q >> 1)]) * inv,
-                                                               __uint_as_float(o[2 * (q & 1) + 1][2 * k + (q >> 1)]) * inv);
-                v[q] = *reinterpret_cast<const uint32_t*>(&z);
-              }
-              *reinterpret_cast<uint4*>(dst + 32 * i + 8 * k) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int q = 0; q < 4; ++q) {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(__uint_as_float(o[2 * (q & 1)][2 * k + (q >> 1)]) * inv,
+                                                             __uint_as_float(o[2 * (q & 1) + 1][2 * k + (q >> 1)]) * inv);
+              v[q] = *reinterpret_cast<const uint32_t*>(&z);
             }
+            const int ch = 4 * i + k;
+            *reinterpret_cast<uint4*>(tile + r * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (r & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-        if (real && p.lse) p.lse[tk * p.Hq + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        __syncwarp();
+        constexpr int kL = D / 8, kR = 32 / kL, kN = 32 / kR;
+#pragma unroll 4
+        for (int i = 0; i < kN; ++i) {
+          const unsigned long long dst = __shfl_sync(0xffffffffu, into, kR * i + lane / kL);
+          const int rr = (warp & 3) * 32 + kR * i + lane / kL, ch = lane % kL;
+          if (dst)
+            reinterpret_cast<uint4*>(dst)[ch] = *reinterpret_cast<const uint4*>(
+                tile + rr * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rr & 7)) << 4));
+        }
+        __syncwarp();
       } else {
         float* slot = p.part + static_cast<size_t>(s.slot) * C::kSlot + 128 * t + r;
 #pragma unroll 1
@@ -789,6 +812,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       walk.b = start.b;
       walk.base = start.base;
       walk.load(p);
+      walk.find();
       const long long ubeg = walk.u;
       int i = 0;
       bool more = true;
