@@ -75,9 +75,6 @@ struct PfParams {
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_all() {
-  asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-}
 
 template <int NC, typename Rel, typename Use>
 __device__ __forceinline__ void pf_drain(uint32_t taddr, Rel&& release, Use&& use) {

@@ -183,12 +183,23 @@ struct PromptWalk {
   __device__ void load(const AttnParams& p) {
     w = prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi);
   }
-  // Finds unit u's item; u lies in sequence b, which is loaded.
+  // Finds unit u's item; u lies in sequence b, which is loaded.  A warp's 32
+  // lanes look at 32 items at a time.
   __device__ void find() {
     const long long local = u - base;
-    h = static_cast<int>(local / w.per_head);
+    h = local < (1ll << 31) && w.per_head < (1ll << 31)
+            ? static_cast<int>(static_cast<unsigned>(local) / static_cast<unsigned>(w.per_head))
+            : static_cast<int>(local / w.per_head);
     const long long in_head = local - h * w.per_head;
-    item = w.item_of(in_head);
+    int lo = 0, n = w.items;   // the item is one of [lo, lo + n)
+    while (n > 1) {
+      const int step = (n + 31) / 32, at_lane = lo + min(static_cast<int>(threadIdx.x & 31) * step, n);
+      const uint32_t begun = __ballot_sync(0xffffffffu, at_lane < lo + n && w.before(at_lane) <= in_head);
+      const int k = 31 - __clz(begun);   // (lane 0's always has)
+      n = min(step, n - k * step);
+      lo += k * step;
+    }
+    item = lo;
     at = w.before(item);
     nt = static_cast<int>(w.before(item + 1) - at);
   }
@@ -349,43 +360,44 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const bool general = s.general != 0;
       float a = 0.f;
       if (live > 0) {
-        // The warp's 32 rows of q, times a power of two a row and the sign of the
-        // scale, as f16: kL lanes read a row together (one lane a row met 32 lines
-        // a load), kR rows a load.
+        // The warp's 32 rows of q, kL lanes a row: copied to their places in the
+        // tile, then there, in rolled loops (code that runs once a segment is
+        // fetched at some 7 cycles an instruction: unrolled, this took 8000),
+        // times a power of two a row and the sign of the scale, as f16.
         constexpr int kL = D / 8, kR = 32 / kL, kN = 32 / kR;
         const int own = s.row0 + 128 * t + r, tok = own / p.group;
         const unsigned long long from =
             own < s.rows ? reinterpret_cast<unsigned long long>(p.q + (static_cast<int64_t>(s.start) + tok) * p.qs +
                                                                 static_cast<int64_t>(s.h * p.group + own - tok * p.group) * D)
                          : 0ull;
-        uint4 x[kN];
-#pragma unroll
+        const int ch = lane % kL;
+        uint8_t* tile = smem + t * C::kQ + (ch >> 3) * (128 * 128);
+        auto place = [&](int i) {   // this lane's 16 bytes of its row of pass i
+          const int rr = (warp & 3) * 32 + kR * i + lane / kL;
+          return reinterpret_cast<uint4*>(tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+        };
+#pragma unroll 1
         for (int i = 0; i < kN; ++i) {
           const unsigned long long row = __shfl_sync(0xffffffffu, from, kR * i + lane / kL);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (row) x[i] = reinterpret_cast<const uint4*>(row)[lane % kL];
+          cp_async16(place(i), reinterpret_cast<const uint4*>(row ? row : reinterpret_cast<unsigned long long>(p.q)) + ch, row != 0);
         }
+        cp_async_wait_all();
         uint32_t mine = 0;   // the largest magnitude's bits of the own row
         const uint32_t sign = p.scale2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < kN; ++i) {
-          const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-          uint32_t top = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) top = __vmaxu2(top, v[k] & 0x7fff7fffu);
+          const uint4 x = *place(i);
+          uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
           top = max(top & 0xffffu, top >> 16);
 #pragma unroll
           for (int q = 1; q < kL; q <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, q));
           const uint32_t other = __shfl_sync(0xffffffffu, top, lane % kR * kL);
           if (lane / kR == i) mine = other;
           const float down = pow2i(-row_exponent(top));
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = pack_f16(__uint_as_float(v[k] << 16) * down, __uint_as_float(v[k] & 0xffff0000u) * down) ^ sign;
-          const int rr = (warp & 3) * 32 + kR * i + lane / kL, ch = lane % kL;
-          *reinterpret_cast<uint4*>(smem + t * C::kQ + rr * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rr & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
+          auto pair = [&](uint32_t v) {
+            return pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down) ^ sign;
+          };
+          *place(i) = make_uint4(pair(x.x), pair(x.y), pair(x.z), pair(x.w));
         }
         a = fabsf(p.scale2) * pow2i(row_exponent(mine)) * pow2i(max(s.ke - code_shift<FMT>(), -126));
         a = fmaxf(a, 1.1754943508222875e-38f);   // (not 0: -inf of a masked column stays -inf)
@@ -528,7 +540,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         __syncwarp();
         constexpr int kL = D / 8, kR = 32 / kL, kN = 32 / kR;
-#pragma unroll 4
+#pragma unroll 1
         for (int i = 0; i < kN; ++i) {
           const unsigned long long dst = __shfl_sync(0xffffffffu, into, kR * i + lane / kL);
           const int rr = (warp & 3) * 32 + kR * i + lane / kL, ch = lane % kL;

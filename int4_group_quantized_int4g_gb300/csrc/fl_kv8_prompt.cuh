@@ -10,20 +10,20 @@ namespace flkv {
 constexpr int kPromptRows = 256;   // rows of an item: two row tiles of 128
 constexpr int kPromptTile = 128;   // tokens of a unit
 
-// sum over i < n of floor((a i + b) / m), for n >= 0, m >= 1, a, b >= 0.  T: a
-// type that the sum fits (64-bit divisions are slow on the device).
-template <typename T>
-__host__ __device__ __forceinline__ T floor_sum(T n, T m, T a, T b) {
-  T sum = 0;
+// sum over i < n of floor((a i + b) / m), for n >= 0, m >= 1, a, b >= 0 and
+// sums, on the way too, within 32 bits
+__host__ __device__ __forceinline__ unsigned floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  unsigned sum = 0;
   while (n > 0) {
-    sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const T y = a * n + b;
+    const unsigned qa = a / m, qb = b / m;
+    sum += n * (n - 1) / 2 * qa + n * qb;
+    a -= qa * m;
+    b -= qb * m;
+    const unsigned y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const T t = m;
+    b = y - n * m;
+    const unsigned t = m;
     m = a;
     a = t;
   }
@@ -36,20 +36,18 @@ __host__ __device__ __forceinline__ T floor_sum(T n, T m, T a, T b) {
 // last row's own position, so that its tiles are those that some row sees:
 //   tiles(i) = floor((past g + 256 (i + 1) - 1) / (128 g)) + 1,
 // summed in closed form (the division by 128 g is one by 128, then one by g).
-// With a window, or with rows before the first token, every item gets the
-// same number of units, some of them without work.
+// With a window, with rows before the first token, or with sums past 32 bits,
+// every item gets the same number of units, some of them without work.
 struct PromptWork {
   SeqInfo q;
   int rows, items, g, past, window, nc;   // nc: units of each item, 0 for the causal form
-  bool small;                             // the sums of `before` fit 32 bits, on the way too
   long long per_head;
 
   __host__ __device__ long long before(int i) const {   // units of a head's items before item i
     if (nc) return static_cast<long long>(i) * nc;
     const int k = min(i, items - 1);
-    const long long b = (static_cast<long long>(past) * g + 255) >> 7;
-    const long long n = k + (small ? static_cast<long long>(floor_sum<unsigned>(k, g, 2, static_cast<unsigned>(b)))
-                                   : floor_sum<long long>(k, g, 2, b));
+    const unsigned b = static_cast<unsigned>((static_cast<long long>(past) * g + 255) >> 7);
+    const long long n = k + static_cast<long long>(floor_sum(k, g, 2, b));
     return i < items ? n : n + (q.kv + kPromptTile - 1) / kPromptTile;
   }
   __host__ __device__ int tiles(int i) const { return static_cast<int>(before(i + 1) - before(i)); }
@@ -80,11 +78,11 @@ __host__ __device__ __forceinline__ PromptWork prompt_work(const SeqInfo& q, int
   w.past = q.kv - q.n;
   w.window = window < q.kv ? window : 0;
   w.nc = 0;
-  // (terms: items^2 at most 2^31, items times a quotient of at most kv / 128 + 2,
-  // 2 items + b with b at most kv g / 128 + 2)
-  w.small = w.items < 32768 && static_cast<long long>(w.items) * (q.kv / kPromptTile + 3) < (1ll << 30) &&
-            static_cast<long long>(q.kv) * group < (1ll << 36);
-  if (w.past < 0 || w.window) {
+  // The sums of the causal form have to fit 32 bits: items^2 is below 2^30,
+  // items times a quotient of at most kv / 128 + 3 too, 2 items + b below 2^31.
+  const bool fits = w.items < 32768 && static_cast<long long>(w.items) * (q.kv / kPromptTile + 3) < (1ll << 30) &&
+                    static_cast<long long>(q.kv) * group < (1ll << 36);
+  if (w.past < 0 || w.window || !fits) {
     const int all = max(1, (q.kv + kPromptTile - 1) / kPromptTile);
     // a window's first tile starts up to 127 tokens early, and an item's rows
     // span up to 256 / g + 1 tokens
