@@ -360,44 +360,44 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       const bool general = s.general != 0;
       float a = 0.f;
       if (live > 0) {
-        // The warp's 32 rows of q, kL lanes a row: copied to their places in the
-        // tile, then there, in rolled loops (code that runs once a segment is
-        // fetched at some 7 cycles an instruction: unrolled, this took 8000),
-        // times a power of two a row and the sign of the scale, as f16.
+        // The warp's 32 rows of q: copied to their places in the tile, kL lanes a
+        // row, then there times a power of two a row and the sign of the scale, as
+        // f16.  In short loops: code that runs once a segment is fetched at some 7
+        // cycles an instruction.
         constexpr int kL = D / 8, kR = 32 / kL, kN = 32 / kR;
         const int own = s.row0 + 128 * t + r, tok = own / p.group;
         const unsigned long long from =
             own < s.rows ? reinterpret_cast<unsigned long long>(p.q + (static_cast<int64_t>(s.start) + tok) * p.qs +
                                                                 static_cast<int64_t>(s.h * p.group + own - tok * p.group) * D)
                          : 0ull;
-        const int ch = lane % kL;
-        uint8_t* tile = smem + t * C::kQ + (ch >> 3) * (128 * 128);
-        auto place = [&](int i) {   // this lane's 16 bytes of its row of pass i
-          const int rr = (warp & 3) * 32 + kR * i + lane / kL;
-          return reinterpret_cast<uint4*>(tile + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+        uint8_t* tile = smem + t * C::kQ;
+        auto place = [&](int rr, int ch) {   // 16 bytes of a row of the tile
+          return reinterpret_cast<uint4*>(tile + rr * 128 + (ch >> 3) * (128 * 128) + (((ch & 7) ^ (rr & 7)) << 4));
         };
 #pragma unroll 1
         for (int i = 0; i < kN; ++i) {
           const unsigned long long row = __shfl_sync(0xffffffffu, from, kR * i + lane / kL);
-          cp_async16(place(i), reinterpret_cast<const uint4*>(row ? row : reinterpret_cast<unsigned long long>(p.q)) + ch, row != 0);
+          cp_async16(place((warp & 3) * 32 + kR * i + lane / kL, lane % kL),
+                     reinterpret_cast<const uint4*>(row ? row : reinterpret_cast<unsigned long long>(p.q)) + lane % kL, row != 0);
         }
         cp_async_wait_all();
-        uint32_t mine = 0;   // the largest magnitude's bits of the own row
-        const uint32_t sign = p.scale2 < 0.f ? 0x80008000u : 0u;
-#pragma unroll 2
-        for (int i = 0; i < kN; ++i) {
-          const uint4 x = *place(i);
-          uint32_t top = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
-          top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-          for (int q = 1; q < kL; q <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, q));
-          const uint32_t other = __shfl_sync(0xffffffffu, top, lane % kR * kL);
-          if (lane / kR == i) mine = other;
-          const float down = pow2i(-row_exponent(top));
+        __syncwarp();
+        // from here a lane has its own row (in place, without bank conflicts)
+        uint32_t mine = 0;   // the largest magnitude's bits
+#pragma unroll 4
+        for (int i = 0; i < kL; ++i) {
+          const uint4 x = *place(r, i);
+          mine = __vmaxu2(mine, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+        }
+        mine = max(mine & 0xffffu, mine >> 16);
+        const float down = copysignf(pow2i(-row_exponent(mine)), p.scale2);
+#pragma unroll 4
+        for (int i = 0; i < kL; ++i) {
+          const uint4 x = *place(r, i);
           auto pair = [&](uint32_t v) {
-            return pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down) ^ sign;
+            return pack_f16(__uint_as_float(v << 16) * down, __uint_as_float(v & 0xffff0000u) * down);
           };
-          *place(i) = make_uint4(pair(x.x), pair(x.y), pair(x.z), pair(x.w));
+          *place(r, i) = make_uint4(pair(x.x), pair(x.y), pair(x.z), pair(x.w));
         }
         a = fabsf(p.scale2) * pow2i(row_exponent(mine)) * pow2i(max(s.ke - code_shift<FMT>(), -126));
         a = fmaxf(a, 1.1754943508222875e-38f);   // (not 0: -inf of a masked column stays -inf)
