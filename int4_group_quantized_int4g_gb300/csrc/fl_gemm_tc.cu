@@ -67,15 +67,14 @@ struct PfParams {
 };
 
 // ------------------------------------------------------------ tcgen05 helpers
-// Read NC chunks of 16 columns starting at taddr, keeping the next chunk's
-// load in flight while the current one is consumed; `release` runs as soon as
-// the last load has completed (the accumulator may then be overwritten).
-// 4-byte asynchronous copy global -> shared (generic proxy), and the wait for
-// all of this thread's copies.
+// 4-byte asynchronous copy global -> shared (generic proxy).
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
+// Read NC chunks of 16 columns starting at taddr, keeping the next chunk's
+// load in flight while the current one is consumed; `release` runs as soon as
+// the last load has completed (the accumulator may then be overwritten).
 template <int NC, typename Rel, typename Use>
 __device__ __forceinline__ void pf_drain(uint32_t taddr, Rel&& release, Use&& use) {
   static_assert(NC % 2 == 0, "chunks come in pairs");

@@ -833,7 +833,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         Segment s;
         more = walk.next(p, s, ubeg);
         if (more) {
-          const PageRun run = read_pages(walk.w.q, p.block, p.window);
+          // (the walk may be at the next sequence already)
+          const PageRun run = read_pages(SeqInfo{s.start, s.kv - s.past, s.kv}, p.block, p.window);
           const int from = max(run.first, s.tile * ppt), to = min(run.first + run.n, (s.tile + s.units) * ppt);
           int ke = -126, ve = -126;
           bool mantissas = false;

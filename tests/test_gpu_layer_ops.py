@@ -449,6 +449,19 @@ def test_attention_mixed_rows():
     _close(*_attend([(1, 700), (130, 130), (1, 1), (70, 333), (3, 90), (1, 2000)], 4, 1, 128, 32, "e4m3", seed=14))
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("mantissas", [False, True])
+def test_attention_sequences_of_falling_length(fmt, mantissas):
+    """A CTA's run goes from a long sequence's last tokens to a shorter one,
+    and every page has a scale of its own."""
+    def scales(rng, shape):
+        return [(2.0 ** rng.integers(-11, -5, shape) * (rng.uniform(1, 2, shape) if mantissas else 1)).astype(np.float32)
+                for _ in range(2)]
+    _close(*_attend([(58, 226), (43, 126), (26, 240)], 4, 1, 128, 32, fmt, seed=17, scales=scales))
+    _close(*_attend([(90, 2000), (70, 1500), (90, 1100), (40, 300), (33, 33)], 4, 2, 64, 16, fmt, seed=18, scales=scales))
+    _close(*_attend([(300, 1900), (150, 700), (70, 100)], 3, 1, 64, 64, fmt, window=300, seed=19, scales=scales))
+
+
 def test_attention_far_blocks():
     """Blocks whose codes lie more than 2^32 bytes into the cache."""
     rng = np.random.default_rng(4)
