@@ -881,24 +881,24 @@ __global__ void __launch_bounds__(kPromptRows) k_kv8_join(const AttnParams p, in
   const Start start = find_start<kPromptRows>(scratch, p.seqs.B, c, ctas, kPromptLeast, [&](int b) {
     return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
-  pdl_wait();   // every block: the kernels after this one must find the one before it done
   const long long U = start.U;
   const int P = start.P;
-  if (c >= P) return;
   PromptWalk walk;
-  walk.u = unit_begin(c, U, P);
-  walk.b = start.b;
-  walk.base = start.base;
-  walk.load(p);
+  int cf = -1, cl = -1;   // the CTAs that share the item
+  if (c < P) {
+    walk.u = unit_begin(c, U, P);
+    walk.b = start.b;
+    walk.base = start.base;
+    walk.load(p);
+    walk.find();
+    const long long first = walk.base + walk.h * walk.w.per_head + walk.at;
+    if (first < walk.u) cf = cta_of_unit(first, U, P), cl = cta_of_unit(first + walk.nt - 1, U, P);
+  }
+  // Every block waits: the kernels after this one must find the one before it done.
+  pdl_wait();
+  if (cf != c - 1) return;   // past the units, a boundary between two items, or an item that an earlier block joins
   const PromptWork& w = walk.w;
-  const long long local = walk.u - walk.base;
-  const int h = static_cast<int>(local / w.per_head);
-  const long long in_head = local - h * w.per_head;
-  const int item = w.item_of(in_head);
-  const long long first = walk.u - (in_head - w.before(item));
-  if (first == walk.u) return;                       // the boundary is between two items
-  const int cf = cta_of_unit(first, U, P), cl = cta_of_unit(first + w.tiles(item) - 1, U, P);
-  if (cf != c - 1) return;                           // an earlier boundary's
+  const int h = walk.h, item = walk.item;
   const int r = threadIdx.x, row = item * kPromptRows + r;
   if (row >= w.rows) return;
   const int tok = row / p.group, hd = h * p.group + row - tok * p.group;
