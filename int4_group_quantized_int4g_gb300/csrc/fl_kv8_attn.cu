@@ -670,9 +670,8 @@ extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, in
   if (head_dim != 64 && head_dim != 128) return FL_ERR_UNSUPPORTED;
   // two partials a CTA: the rows that it shares with the CTAs before and after
   const bool prompt = static_cast<long long>(T) * (Hq / kv_heads) > kFewRows;
-  const size_t few = 2 * 16 * (head_dim + 2);   // (two CTAs an SM)
-  const size_t slot = prompt ? prompt_slot_floats(head_dim) : few;
-  *out = kScratchOff + 2ull * flh::sm_count() * slot * 4;
+  const size_t few = 2ull * flh::sm_count() * 2 * 16 * (head_dim + 2) * 4;   // (two CTAs an SM)
+  *out = kScratchOff + (prompt ? prompt_scratch(head_dim) : few);
   return FL_OK;
 }
 

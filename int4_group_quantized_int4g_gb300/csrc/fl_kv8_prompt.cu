@@ -173,6 +173,14 @@ struct __align__(16) Segment {
 };
 static_assert(sizeof(Segment) == 64, "segment ring");
 
+// What the joining kernel needs of the item that CTA c begins and others go on
+// with: CTA c writes entry c, with last = -1 if there is none.
+struct __align__(16) JoinItem {
+  int last;                  // the last CTA of the item
+  int start, rows, row0, h;  // as in the segment
+  int pad[3];
+};
+
 struct PromptWalk {
   long long u, end, base;
   int b;
@@ -244,6 +252,12 @@ struct PromptWalk {
   }
 };
 
+// (behind the partials)
+template <int D>
+__device__ __forceinline__ JoinItem* join_items(const AttnParams& p, int ctas) {
+  return reinterpret_cast<JoinItem*>(p.part + 2 * static_cast<size_t>(ctas) * PrCfg<D>::kSlot);
+}
+
 // A scale's power of two and what is left of it.
 __device__ __forceinline__ int scale_exponent(float s) {
   return min(max(static_cast<int>((__float_as_uint(s) >> 23) & 255u) - 127, -126), 126);
@@ -298,10 +312,14 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {
-    if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 56);
+    if (tid == 0) {
+      set_status(p.status, FL_ERR_DEVICE_CHECK, 56);
+      join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;
+    }
     return;
   }
   pdl_launch_dependents();   // (the joining kernel waits for the end of this one itself)
+  if (warp == kPlan && lane == 0) join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;   // until the plan says more
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&stg_full[i], 1);
@@ -853,6 +871,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           s.general = __any_sync(0xffffffffu, mantissas);
           s.meta = i & 7;
           i += s.units;
+          if (lane == 0 && s.slot >= 0 && (s.slot & 1)) {   // the CTA's last item, which others go on with
+            const long long last = walk.base + walk.h * walk.w.per_head + walk.at + walk.nt - 1;
+            join_items<D>(p, gridDim.x)[blockIdx.x] = {cta_of_unit(last, start.U, start.P), s.start, s.rows, s.row0, s.h, {}};
+          }
         }
         if (lane == 0) {
           segs[seg & 3] = s;
@@ -870,67 +892,66 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   if (warp == kIssue0) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partials of the items that several CTAs share.  Block x looks at
-// the boundary between the units of CTAs x and x + 1, and joins the item there
-// if x is the first CTA of it; block y has 16 elements of its rows, a thread a
-// row.
+constexpr int kEl = 16;
+// Joins the partials of the items that several CTAs share.  Block x has the
+// item that CTA x begins, and CTAs up to `last` go on with, in their order;
+// block y has kEl elements of its rows, a thread a row.  It runs while nothing
+// else does, so its time is latency: it finds its item written down, and the
+// loads of kWide partials are under way together.
 template <int D>
 __global__ void __launch_bounds__(kPromptRows) k_kv8_join(const AttnParams p, int ctas) {
-  const int c = blockIdx.x + 1;
-  __shared__ long long scratch[kPromptRows / 32 + 2];
-  const Start start = find_start<kPromptRows>(scratch, p.seqs.B, c, ctas, kPromptLeast, [&](int b) {
-    return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
-  });
-  const long long U = start.U;
-  const int P = start.P;
-  PromptWalk walk;
-  int cf = -1, cl = -1;   // the CTAs that share the item
-  if (c < P) {
-    walk.u = unit_begin(c, U, P);
-    walk.b = start.b;
-    walk.base = start.base;
-    walk.load(p);
-    walk.find();
-    const long long first = walk.base + walk.h * walk.w.per_head + walk.at;
-    if (first < walk.u) cf = cta_of_unit(first, U, P), cl = cta_of_unit(first + walk.nt - 1, U, P);
-  }
-  // Every block waits: the kernels after this one must find the one before it done.
-  pdl_wait();
-  if (cf != c - 1) return;   // past the units, a boundary between two items, or an item that an earlier block joins
-  const PromptWork& w = walk.w;
-  const int h = walk.h, item = walk.item;
-  const int r = threadIdx.x, row = item * kPromptRows + r;
-  if (row >= w.rows) return;
+  constexpr int kWide = 2;
+  pdl_wait();   // every block: the kernels after this one must find the one before it done
+  const int c = blockIdx.x;
+  const JoinItem* at = join_items<D>(p, ctas) + c;
+  const int4 it = __ldcg(reinterpret_cast<const int4*>(at));   // last, start, rows, row0
+  const int h = __ldcg(&at->h);
+  const int r = threadIdx.x, row = it.w + r;
+  if (it.x < 0 || row >= it.z) return;
   const int tok = row / p.group, hd = h * p.group + row - tok * p.group;
-  const int64_t tk = static_cast<int64_t>(w.q.start) + tok;
+  const int64_t tk = static_cast<int64_t>(it.y) + tok;
   constexpr size_t kSlot = PrCfg<D>::kSlot;
-  auto slot_of = [&](int cc) { return p.part + static_cast<size_t>(2 * cc + (cc == cf ? 1 : 0)) * kSlot + r; };
-  float mx = -INFINITY;
-#pragma unroll 8
-  for (int cc = cf; cc <= cl; ++cc) mx = fmaxf(mx, __ldcg(slot_of(cc) + D * kPromptRows));
-  float sum = 0.f, o[16];
+  float mx = -INFINITY, sum = 0.f, o[kEl];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-#pragma unroll 4
-  for (int cc = cf; cc <= cl; ++cc) {
-    const float* sl = slot_of(cc);
-    const float m = __ldcg(sl + D * kPromptRows), l = __ldcg(sl + (D + 1) * kPromptRows);
-    const float f = m == -INFINITY ? 0.f : exp2_approx(m - mx);
-    sum = fmaf(f, l, sum);
+  for (int k = 0; k < kEl; ++k) o[k] = 0.f;
+#pragma unroll 1
+  for (int cc = c; cc <= it.x; cc += kWide) {
+    float m[kWide], l[kWide], v[kWide][kEl];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)   // element e lies in column e % 4 D/4 + e / 4
-      o[k] = fmaf(f, __ldcg(sl + ((k & 3) * (D / 4) + 4 * blockIdx.y + (k >> 2)) * kPromptRows), o[k]);
+    for (int j = 0; j < kWide; ++j) {
+      const float* sl = p.part + static_cast<size_t>(2 * min(cc + j, it.x) + (cc + j == c ? 1 : 0)) * kSlot + r;
+      m[j] = cc + j <= it.x ? __ldcg(sl + D * kPromptRows) : -INFINITY;
+      l[j] = __ldcg(sl + (D + 1) * kPromptRows);
+#pragma unroll
+      for (int k = 0; k < kEl; ++k)   // element e lies in column e % 4 D/4 + e / 4
+        v[j][k] = __ldcg(sl + ((k & 3) * (D / 4) + kEl / 4 * blockIdx.y + (k >> 2)) * kPromptRows);
+    }
+    float top = mx;
+#pragma unroll
+    for (int j = 0; j < kWide; ++j) top = fmaxf(top, m[j]);
+    const float ref = top == -INFINITY ? 0.f : top, f = exp2_approx(mx - ref);
+    mx = top;
+    sum *= f;
+#pragma unroll
+    for (int k = 0; k < kEl; ++k) o[k] *= f;
+#pragma unroll
+    for (int j = 0; j < kWide; ++j) {
+      const float g = exp2_approx(m[j] - ref);
+      sum = fmaf(g, l[j], sum);
+#pragma unroll
+      for (int k = 0; k < kEl; ++k) o[k] = fmaf(g, v[j][k], o[k]);
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint32_t v[8];
+  uint32_t v[kEl / 2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kEl / 2; ++k) {
     const __nv_bfloat162 z = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
     v[k] = *reinterpret_cast<const uint32_t*>(&z);
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + 16 * blockIdx.y);
-  dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-  dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + kEl * blockIdx.y);
+#pragma unroll
+  for (int k = 0; k < kEl / 8; ++k) dst[k] = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
   if (blockIdx.y == 0 && p.lse) p.lse[tk * p.Hq + hd] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
@@ -952,7 +973,7 @@ int launch(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, cu
   if (cudaGetLastError() != cudaSuccess) return FL_ERR_CUDA;
   if (ctas < 2) return FL_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1, D / 16);
+  cfg.gridDim = dim3(ctas - 1, D / kEl);
   cfg.blockDim = dim3(kPromptRows);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -967,7 +988,9 @@ int launch(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, cu
 
 namespace flkv {
 
-size_t prompt_slot_floats(int head_dim) { return static_cast<size_t>(kPromptRows) * (head_dim + 2); }
+size_t prompt_scratch(int head_dim) {
+  return flh::sm_count() * (2 * static_cast<size_t>(kPromptRows) * (head_dim + 2) * 4 + sizeof(JoinItem));
+}
 
 int launch_prompt(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int format, int head_dim, cudaStream_t s) {
   if (format == FL_KV8_E4M3)

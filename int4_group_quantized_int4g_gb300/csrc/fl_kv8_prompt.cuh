@@ -94,6 +94,6 @@ __host__ __device__ __forceinline__ PromptWork prompt_work(const SeqInfo& q, int
 }
 
 int launch_prompt(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, int format, int head_dim, cudaStream_t s);
-size_t prompt_slot_floats(int head_dim);
+size_t prompt_scratch(int head_dim);   // bytes of partials
 
 }  // namespace flkv
