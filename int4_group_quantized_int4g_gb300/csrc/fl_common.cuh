@@ -273,4 +273,23 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 int sm_count();  // cached per device (fl_abi.cu)
 
+// Launches a kernel whose CTAs may start while the kernel before it in the
+// stream ends.  The kernel calls pdl_wait in every CTA before it touches memory.
+template <typename... P, typename... A>
+inline int launch_early(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return FL_OK;
+  cudaGetLastError();
+  return FL_ERR_CUDA;
+}
+
 }  // namespace flh

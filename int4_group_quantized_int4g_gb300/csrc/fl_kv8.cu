@@ -105,6 +105,8 @@ __global__ void __launch_bounds__(ApCfg<FMT, D, BLK>::kThreads) k_kv8_append(con
   using C = ApCfg<FMT, D, BLK>;
   constexpr int kThreads = C::kThreads, kVecs = C::kVecs, kWarps = kThreads / 32;
   __shared__ float s_red[kWarps];
+  pdl_launch_dependents();
+  pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int b, j;
   if (!find_block<kThreads>(p.seqs, BLK, blockIdx.x, b, j)) return;
@@ -212,12 +214,12 @@ __global__ void __launch_bounds__(ApCfg<FMT, D, BLK>::kThreads) k_kv8_append(con
 }
 
 template <int FMT, int D>
-void launch_append(const AppendParams& p, int block, dim3 grid, cudaStream_t s) {
+int launch_append(const AppendParams& p, int block, dim3 grid, cudaStream_t s) {
   switch (block) {
-    case 16: k_kv8_append<FMT, D, 16><<<grid, ApCfg<FMT, D, 16>::kThreads, 0, s>>>(p); break;
-    case 32: k_kv8_append<FMT, D, 32><<<grid, ApCfg<FMT, D, 32>::kThreads, 0, s>>>(p); break;
-    case 64: k_kv8_append<FMT, D, 64><<<grid, ApCfg<FMT, D, 64>::kThreads, 0, s>>>(p); break;
-    default: k_kv8_append<FMT, D, 128><<<grid, ApCfg<FMT, D, 128>::kThreads, 0, s>>>(p); break;
+    case 16: return flh::launch_early(k_kv8_append<FMT, D, 16>, grid, ApCfg<FMT, D, 16>::kThreads, 0, s, p);
+    case 32: return flh::launch_early(k_kv8_append<FMT, D, 32>, grid, ApCfg<FMT, D, 32>::kThreads, 0, s, p);
+    case 64: return flh::launch_early(k_kv8_append<FMT, D, 64>, grid, ApCfg<FMT, D, 64>::kThreads, 0, s, p);
+    default: return flh::launch_early(k_kv8_append<FMT, D, 128>, grid, ApCfg<FMT, D, 128>::kThreads, 0, s, p);
   }
 }
 
@@ -245,12 +247,10 @@ extern "C" int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int
   const dim3 grid(static_cast<unsigned>(most), cache->kv_heads, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->format == FL_KV8_E4M3)
-    cache->head_dim == 64 ? launch_append<FL_KV8_E4M3, 64>(p, cache->block, grid, s)
-                          : launch_append<FL_KV8_E4M3, 128>(p, cache->block, grid, s);
-  else
-    cache->head_dim == 64 ? launch_append<FL_KV8_INT8, 64>(p, cache->block, grid, s)
-                          : launch_append<FL_KV8_INT8, 128>(p, cache->block, grid, s);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+    return cache->head_dim == 64 ? launch_append<FL_KV8_E4M3, 64>(p, cache->block, grid, s)
+                                 : launch_append<FL_KV8_E4M3, 128>(p, cache->block, grid, s);
+  return cache->head_dim == 64 ? launch_append<FL_KV8_INT8, 64>(p, cache->block, grid, s)
+                               : launch_append<FL_KV8_INT8, 128>(p, cache->block, grid, s);
 }
 
 extern "C" int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int block, int window, int b, long long* out) {

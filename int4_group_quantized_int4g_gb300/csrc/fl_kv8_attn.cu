@@ -171,13 +171,16 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NS;
   uint8_t* ring = smem + warp * C::kRing;
-  if (smem_u32(smem) & 1023u) {
-    if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 57);
-    return;
-  }
+  pdl_launch_dependents();
+  if (tid == 0) prefetch_map(&kmap), prefetch_map(&vmap);
   if (lane == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
+  }
+  pdl_wait();
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 57);
+    return;
   }
   {
     const Start start =
@@ -646,8 +649,7 @@ int launch_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& 
       return FL_ERR_CUDA;
     if (dev < 64) attr_done[dev] = true;
   }
-  k_kv8_rows<FMT, D, NT><<<C::kCtas * flh::sm_count(), kRowsThreads, C::kSmem, s>>>(km, vm, p);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+  return flh::launch_early(k_kv8_rows<FMT, D, NT>, C::kCtas * flh::sm_count(), kRowsThreads, C::kSmem, s, km, vm, p);
 }
 
 template <int FMT, int D>

@@ -311,15 +311,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + 4);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (smem_u32(smem) & 1023u) {
-    if (tid == 0) {
-      set_status(p.status, FL_ERR_DEVICE_CHECK, 56);
-      join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;
-    }
-    return;
-  }
-  pdl_launch_dependents();   // (the joining kernel waits for the end of this one itself)
-  if (warp == kPlan && lane == 0) join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;   // until the plan says more
+  pdl_launch_dependents();
+  if (warp == kProd && lane == 0) prefetch_map(&kmap), prefetch_map(&vmap);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&stg_full[i], 1);
@@ -339,6 +332,15 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
     fence_mbar_init();
   }
+  pdl_wait();
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) {
+      set_status(p.status, FL_ERR_DEVICE_CHECK, 56);
+      join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;
+    }
+    return;
+  }
+  if (warp == kPlan && lane == 0) join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;   // until the plan says more
   const Start start = find_start<kPrThreads>(reinterpret_cast<long long*>(smem + C::kStgOff), p.seqs.B, blockIdx.x, gridDim.x, kPromptLeast, [&](int b) {
     return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
@@ -969,19 +971,9 @@ int launch(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p, cu
     if (dev < 64) attr_done[dev] = true;
   }
   const int ctas = flh::sm_count();
-  k_kv8_prompt<FMT, D><<<ctas, kPrThreads, C::kSmem, s>>>(km, vm, p);
-  if (cudaGetLastError() != cudaSuccess) return FL_ERR_CUDA;
-  if (ctas < 2) return FL_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1, D / kEl);
-  cfg.blockDim = dim3(kPromptRows);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv8_join<D>, p, ctas) == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+  const int e = flh::launch_early(k_kv8_prompt<FMT, D>, ctas, kPrThreads, C::kSmem, s, km, vm, p);
+  if (e != FL_OK || ctas < 2) return e;
+  return flh::launch_early(k_kv8_join<D>, dim3(ctas - 1, D / kEl), kPromptRows, 0, s, p, ctas);
 }
 
 }  // namespace

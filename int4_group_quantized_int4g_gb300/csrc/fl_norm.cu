@@ -94,6 +94,8 @@ __device__ __forceinline__ float team_reduce(float v, float* red) {
 template <int TPR, int V, bool VEC>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_rmsnorm(const NormParams p) {
   __shared__ float red[2][TPR / 32];
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int kTeams = TPR == 32 ? 4 : 1;
   const int t = threadIdx.x % TPR;
   const long long row = static_cast<long long>(blockIdx.x) * kTeams + threadIdx.x / TPR;
@@ -195,11 +197,7 @@ int launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
   const long long grid = (p.rows + kTeams - 1) / kTeams;
   if (grid > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
   const dim3 g(static_cast<unsigned>(grid)), b(TPR == 32 ? 128 : TPR);
-  if (vec)
-    k_rmsnorm<TPR, V, true><<<g, b, 0, s>>>(p);
-  else
-    k_rmsnorm<TPR, V, false><<<g, b, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+  return vec ? flh::launch_early(k_rmsnorm<TPR, V, true>, g, b, 0, s, p) : flh::launch_early(k_rmsnorm<TPR, V, false>, g, b, 0, s, p);
 }
 
 template <int V>

@@ -54,6 +54,8 @@ template <bool VEC>
 __global__ void __launch_bounds__(kRopeThreads, 5) k_rope(const RopeParams p) {
   __shared__ unsigned long long step[kRopePairs];
   __shared__ __align__(16) float2 sc[kRopeTable];   // (cos, sin)
+  pdl_launch_dependents();
+  pdl_wait();
   const int pairs = p.rot / 2, heads = p.Hq + p.Hk;
   const bool halves = p.style == FL_ROPE_HALVES;
   const int turned = VEC ? (halves ? pairs / 8 : p.rot / 8) : pairs;   // units of a head that turn
@@ -214,9 +216,5 @@ extern "C" int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, i
   p.tt = tt;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + tt - 1) / tt);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (vec)
-    k_rope<true><<<grid, kRopeThreads, 0, s>>>(p);
-  else
-    k_rope<false><<<grid, kRopeThreads, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FL_OK : FL_ERR_CUDA;
+  return flh::launch_early(vec ? k_rope<true> : k_rope<false>, grid, kRopeThreads, 0, s, p);
 }
