@@ -31,8 +31,7 @@
 // the segment's, codes are multiplied by 2^(e_b - e_ref + k) as they
 // become f16 (exact down to 2^-24 of f16: blocks whose scales are 2^20 apart)
 // and the reference goes into the row's factor or the output.  Mantissas of
-// scales other than powers of two multiply S and P, for the sequences that have
-// them.  q as in the kernel for few rows.  P is f16 (2^-11, the output's
+// scales other than powers of two go into S, for the sequences that have them.  q as in the kernel for few rows.  P is f16 (2^-11, the output's
 // rounding is 2^-9) times 2^6, and up to 2^14; its fp32 sum is taken before.
 #include "fl_kv8_prompt.cuh"
 #include "fl_tc.cuh"
@@ -441,13 +440,26 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // fit the instruction cache together, and a unit took twice as long.  And
         // they spill no register: little of the L1 is left beside the tiles, so
         // that a spilled value comes back from L2.
+        // Mantissas of scales: the keys' multiply S, the values' add their log2 to
+        // the exponent of the weight and leave its sum below.  This is done in
+        // tensor memory, so that no register of the loop is touched: as a branch on
+        // the values themselves it cost every prompt a sixth.
+        const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);   // of 16 tokens each
+        if (general) {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            const float mul = mt[k >> 1].x, add = log2f(mt[k >> 1].y) / a;
+            uint32_t o[8];
+            tmem_ld8_issue(ts + 8 * k, o);
+            tmem_ld8_wait(o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), mul, add));
+            tmem_st8(ts + 8 * k, o);
+          }
+          tmem_wait_st();
+        }
         float x[2][32];
         tmem_ld64(ts, x[0], x[1]);
-        if (general) {   // the keys' mantissas
-          const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);
-#pragma unroll
-          for (int i = 0; i < 64; ++i) x[i >> 5][i & 31] *= mt[i >> 4].x;
-        }
         if (j >= plain_end || j < plain_begin) {
           // -inf where this row does not see the token: columns [lo, hi) are seen
           const int pos = s.tile * kPromptTile + 64 * j;
@@ -485,27 +497,28 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           }
         }
         const float mm = m == -INFINITY ? 0.f : -m;
-        float2 lsum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 lsum[4];   // of 16 tokens each
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 e = __ffma2_rn(make_float2(x[k][2 * i], x[k][2 * i + 1]), make_float2(a, a), make_float2(mm, mm));
             x[k][2 * i] = exp2_approx(e.x), x[k][2 * i + 1] = exp2_approx(e.y);
-            lsum[i & 1] = __fadd2_rn(lsum[i & 1], make_float2(x[k][2 * i], x[k][2 * i + 1]));
-          }
-          if (general) {   // the values' mantissas
-            const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1) + 2 * k;
-            const float m0 = mt[0].y, m1 = mt[1].y;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[k][i] *= i < 16 ? m0 : m1;
+            const float2 w = make_float2(x[k][2 * i], x[k][2 * i + 1]);
+            lsum[2 * k + (i >> 3)] = (i & 7) == 0 ? w : __fadd2_rn(lsum[2 * k + (i >> 3)], w);
           }
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_f16(x[k][2 * i], x[k][2 * i + 1]);
           tmem_st16(ts + 16 * k, pk);   // over columns of S that have been read
         }
-        l += (lsum[0].x + lsum[1].x) + (lsum[0].y + lsum[1].y);
+        float part[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) part[k] = lsum[k].x + lsum[k].y;
+        if (general)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) part[k] /= mt[k].y;
+        l += (part[0] + part[1]) + (part[2] + part[3]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
