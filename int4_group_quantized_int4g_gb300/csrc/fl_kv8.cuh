@@ -92,6 +92,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Arguments of the attention kernels.  A launch serves the sequences whose
 // rows (query heads of a kv head x tokens) number in (rows_lo, rows_hi].
 struct AttnParams {

@@ -58,8 +58,8 @@ struct PrCfg {
   static constexpr int kKOff = 2 * kQ;         // two stages
   static constexpr int kVOff = kKOff + 2 * kKv;
   static constexpr int kStgOff = kVOff + 2 * kKv;
-  static constexpr int kMetaOff = kStgOff + 2 * kStg;      // [8 units][8 slices of 16 tokens]: mantissas of the key, value scale
-  static constexpr int kRatioOff = kMetaOff + 8 * 8 * 8;   // [8][8]: the codes' multipliers, f16 pairs
+  static constexpr int kMetaOff = kStgOff + 2 * kStg;      // [8 units][8 slices of 16 tokens]: mantissas of scales
+  static constexpr int kRatioOff = kMetaOff + 8 * 8 * 16;   // [8][8]: the codes' multipliers, f16 pairs
   static constexpr int kSegOff = kRatioOff + 8 * 8 * 8;    // [4] segments
   static constexpr int kBarOff = kSegOff + 4 * 64;
   static constexpr int kBars = 4 + 8 + 2 + 4 + 4 + 4 + 8;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   // No static shared memory: the dynamic part begins the CTA's window, on the
   // 1024-byte boundary that the swizzled tiles need (checked below).
   extern __shared__ __align__(1024) uint8_t smem[];
-  float2* meta = reinterpret_cast<float2*>(smem + C::kMetaOff);
+  float4* meta = reinterpret_cast<float4*>(smem + C::kMetaOff);   // the key's, log2 of the value's, one over the value's
   uint2* ratios = reinterpret_cast<uint2*>(smem + C::kRatioOff);
   Segment* segs = reinterpret_cast<Segment*>(smem + C::kSegOff);
   uint64_t* stg_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);   // [keys, values]
@@ -444,11 +444,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // the exponent of the weight and leave its sum below.  This is done in
         // tensor memory, so that no register of the loop is touched: as a branch on
         // the values themselves it cost every prompt a sixth.
-        const float2* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);   // of 16 tokens each
+        const float4* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);   // of 16 tokens each
         if (general) {
+          const float down = rcp_approx(a);
 #pragma unroll 1
           for (int k = 0; k < 8; ++k) {
-            const float mul = mt[k >> 1].x, add = log2f(mt[k >> 1].y) / a;
+            const float mul = mt[k >> 1].x, add = mt[k >> 1].y * down;
             uint32_t o[8];
             tmem_ld8_issue(ts + 8 * k, o);
             tmem_ld8_wait(o);
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (int k = 0; k < 4; ++k) part[k] = lsum[k].x + lsum[k].y;
         if (general)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) part[k] /= mt[k].y;
+          for (int k = 0; k < 4; ++k) part[k] *= mt[k].z;
         l += (part[0] + part[1]) + (part[2] + part[3]);
         tmem_wait_st();
         tc_fence_before();
@@ -788,6 +789,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         wait(&seg_full[seg & 3], seg >> 2, 59);
         const Segment& s = segs[seg & 3];
         const int units = s.units, b = s.b, h = s.h, ke = s.ke, ve = s.ve;
+        const bool general = s.general != 0;
         if (!ok || units < 0) break;
         SeqInfo q;
         q.kv = s.kv, q.n = s.kv - s.past, q.start = 0;
@@ -833,7 +835,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
               if (hh == 0 && lane < 8) {
                 const __half2 rk = ratio(a, ke), rv = ratio(v, ve);
                 ratios[(i & 7) * 8 + lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&rk), *reinterpret_cast<const uint32_t*>(&rv));
-                meta[(i & 7) * 8 + lane] = make_float2(scale_mantissa(a), scale_mantissa(v));
+                if (general) {
+                  const float vm = v > 0.f ? scale_mantissa(v) : 1.f;   // (0: the codes' multiplier is as good as 0)
+                  meta[(i & 7) * 8 + lane] = make_float4(scale_mantissa(a), log2f(vm), 1.f / vm, 0.f);
+                }
               }
               __syncwarp();
               if (mine)
