@@ -394,8 +394,9 @@ int fl_moe_int4g_ptrs(const void* x, const float* logits, int M, int H, int E, i
  *   n_i = s_i / sqrt(mean_j s_j^2 + eps) * weight_i   (fp32),
  *   y = bf16(n),
  *   codes, scales: for each run of `group` columns (group 0: the whole row)
- *   scale = max|n| / 448 and code_i = e4m3(n_i / scale), nearest even (a run
- *   of zeros: scale 0, codes 0).
+ *   scale = max|n| / 448 and code_i = e4m3(n_i / scale), nearest even (n_i
+ *   times fp32's 1 / scale: the quotient to 2^-23; a run of zeros: scale 0,
+ *   codes 0).
  *   x, residual, y, residual_out  bf16; row (m, h) starts at
  *           m * stride + h * H elements, stride >= heads * H
  *   weight  bf16 [H], or NULL for ones
@@ -449,7 +450,8 @@ int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, int64_t k_st
  *   k, v              uint8 [num_blocks, kv_heads, block, head_dim] device
  *   k_scale, v_scale  fp32  [num_blocks, kv_heads] device, positive
  * block is 16, 32, 64 or 128; head_dim 64 or 128; num_blocks * kv_heads *
- * block < 2^31; at most 2^30 tokens a sequence and 2^29 rows a call.  A block need not be initialised before its first write. */
+ * block < 2^31; at most 2^30 tokens a sequence and 2^29 rows a call.  A block
+ * need not be initialised before its first write. */
 typedef struct fl_kv8_cache {
   void* k;
   void* v;
@@ -514,7 +516,9 @@ int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int block, int wi
  * some row of the item sees. */
 int fl_kv8_test_units(int n, int kv, int group, int heads, int window, long long u, long long* out);
 
-/* Workspace bytes needed by fl_kv8_attention. */
+/* Workspace bytes needed by fl_kv8_attention: the status block and counters of
+ * every workspace, then two partials a CTA.  The layout is that of the other
+ * entry points, so one workspace serves them all in turn. */
 int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out);
 
 /* Attention of the T query rows over the cache.  Row i of sequence b and
