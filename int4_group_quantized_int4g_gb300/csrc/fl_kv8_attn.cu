@@ -58,6 +58,12 @@ constexpr float kNone = -1e30f;         // the reference of a row without a toke
 // heads, 32 rows: 23 and 37; one of 32768 tokens, 8 heads, 32 rows: 50 and 60.)
 constexpr int kFewRows = 32;
 
+// Up to so many CTAs of a row tile are added up by a thread for each four
+// elements, more of them warp by warp and then across the warps (one sequence of
+// 517 tokens, five CTAs: 9.1 us against 10.0; 12 row tiles of 25 CTAs: 65.4 us
+// against 63.4).
+constexpr int kDirect = 8;
+
 template <int D, int NT>
 struct RowsCfg {
   static constexpr int kRows = 8 * NT;
@@ -74,7 +80,7 @@ struct RowsCfg {
   static constexpr int kLastOff = kWalkOff + 96;
   static constexpr int kSmem = kLastOff + 16;
   static_assert(kSmem <= (232448 + 1024) / kCtas - 1024, "shared memory");
-  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O [value][lane], then m, l of each row
+  static constexpr int kSlot = kRows * (D + 2);      // floats of a partial: O [4 values][lane], then m, l of each row
 };
 
 // The units of one sequence.  A row tile counts kEnd more than it has tiles:
@@ -561,22 +567,20 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
     if (s.slot < 0) {
       if (warp == 0) output();
     } else {
-      // The last of the CTAs that share the row tile adds them up, in CTA order:
-      // warp k takes every eighth of them, then the warps are joined as above.
+      // The last of the CTAs that share the row tile adds them up, in CTA order.
       if (warp == 0) {
-        float* dst = p.part + static_cast<size_t>(s.slot) * C::kSlot + lane;
+        float* dst = p.part + static_cast<size_t>(s.slot) * C::kSlot;
 #pragma unroll
-        for (int q = 0; q < WB; ++q)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int h = 0; h < 2; ++h) {
+            const int r = 8 * nt + 2 * t + h;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) __stcg(dst + ((q * NT + nt) * 4 + k) * 32, o[q][nt][k]);
-        float2* dm = reinterpret_cast<float2*>(p.part + static_cast<size_t>(s.slot) * C::kSlot + ROWS * D);
-        if (g == 0)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) __stcg(dm + 8 * nt + 2 * t + h, make_float2(m[nt][h], l[nt][h]));
+            for (int q = 0; q < WB; q += 2)
+              __stcg(reinterpret_cast<float4*>(dst) + ((nt * 2 + h) * (WB / 2) + q / 2) * 32 + lane,
+                     make_float4(o[q][nt][h], o[q][nt][h + 2], o[q + 1][nt][h], o[q + 1][nt][h + 2]));
+            if (g == 0) __stcg(reinterpret_cast<float2*>(dst + ROWS * D) + r, make_float2(m[nt][h], l[nt][h]));
+          }
         __syncwarp();
         if (lane == 0) {
           fence_acq_rel_gpu();
@@ -589,7 +593,45 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
         }
       }
       __syncthreads();
-      if (*s_last) {
+      if (*s_last && s.cl - s.cf < kDirect) {
+        // A thread has four elements of a row and loads all partials at once: their
+        // latency is all that is left of the call by then.
+        const int at = tid / 32, h = at / (WB / 2);   // (warp `at` has vector at % (WB / 2) of row 2t + (h & 1) of tile h / 2)
+        const int jr = 8 * (h >> 1) + 2 * t + (h & 1), jc = g * (D / 8) + 4 * (at % (WB / 2)), r = s.r * ROWS + jr;
+        if (jr < ROWS && r < rows) {
+          float2 ml[kDirect];
+          float4 v[kDirect];
+#pragma unroll
+          for (int i = 0; i < kDirect; ++i) {
+            const int c = s.cf + i;
+            if (c <= s.cl) {
+              const float* src = p.part + static_cast<size_t>(2 * c + (i == 0 ? 1 : 0)) * C::kSlot;
+              ml[i] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * D) + jr);
+              v[i] = __ldcg(reinterpret_cast<const float4*>(src) + tid);
+            } else {
+              ml[i] = make_float2(kNone, 0.f), v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          float mx = kNone, sum = 0.f, a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kDirect; ++i) mx = fmaxf(mx, ml[i].x);
+#pragma unroll
+          for (int i = 0; i < kDirect; ++i) {
+            const float w = exp2_approx(ml[i].x - mx);
+            sum = fmaf(ml[i].y, w, sum);
+            a[0] = fmaf(v[i].x, w, a[0]), a[1] = fmaf(v[i].y, w, a[1]);
+            a[2] = fmaf(v[i].z, w, a[2]), a[3] = fmaf(v[i].w, w, a[3]);
+          }
+          const int tok = r / p.group, hd = s.h * p.group + (r - tok * p.group);
+          const int64_t tk = s.start + tok;
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;   // 0: no token (a NaN is not)
+          const __nv_bfloat162 z0 = __floats2bfloat162_rn(a[0] * inv, a[1] * inv), z1 = __floats2bfloat162_rn(a[2] * inv, a[3] * inv);
+          *reinterpret_cast<uint2*>(p.out + tk * p.os + static_cast<int64_t>(hd) * D + jc) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&z0), *reinterpret_cast<const uint32_t*>(&z1));
+          if (jc == 0 && p.lse) p.lse[tk * p.Hq + hd] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        }
+      } else if (*s_last) {
+        // warp k takes every eighth partial, then the warps are joined as above
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -601,24 +643,31 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll 1
         for (int cc = s.cf + warp; cc <= s.cl; cc += kWarps) {
           const float* src = p.part + static_cast<size_t>(2 * cc + (cc == s.cf ? 1 : 0)) * C::kSlot;
-          float v[C::kVals];
-#pragma unroll
-          for (int k = 0; k < C::kVals; ++k) v[k] = __ldcg(src + k * 32 + lane);
+          float4 v[NT][2][WB / 2];
           float2 other[NT][2];
           float f[NT][2], fo[NT][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              other[nt][h] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * D) + 8 * nt + 2 * t + h);
+            for (int h = 0; h < 2; ++h) {
+              const int r = 8 * nt + 2 * t + h;
+#pragma unroll
+              for (int q = 0; q < WB / 2; ++q) v[nt][h][q] = __ldcg(reinterpret_cast<const float4*>(src) + ((nt * 2 + h) * (WB / 2) + q) * 32 + lane);
+              other[nt][h] = __ldcg(reinterpret_cast<const float2*>(src + ROWS * D) + r);
+            }
           merge(f, fo, other);
 #pragma unroll
-          for (int q = 0; q < WB; ++q)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                o[q][nt][k] = fmaf(o[q][nt][k], f[nt][k & 1], v[(q * NT + nt) * 4 + k] * fo[nt][k & 1]);
+              for (int q = 0; q < WB / 2; ++q) {
+                const float4 x = v[nt][h][q];
+                o[2 * q][nt][h] = fmaf(o[2 * q][nt][h], f[nt][h], x.x * fo[nt][h]);
+                o[2 * q][nt][h + 2] = fmaf(o[2 * q][nt][h + 2], f[nt][h], x.y * fo[nt][h]);
+                o[2 * q + 1][nt][h] = fmaf(o[2 * q + 1][nt][h], f[nt][h], x.z * fo[nt][h]);
+                o[2 * q + 1][nt][h + 2] = fmaf(o[2 * q + 1][nt][h + 2], f[nt][h], x.w * fo[nt][h]);
+              }
         }
         join();
         if (warp == 0) output();
