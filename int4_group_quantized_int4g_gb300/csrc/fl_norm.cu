@@ -191,6 +191,53 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
   }
 }
 
+// Rows of at most 8 LPR columns (heads of 64 or 128) without codes: LPR lanes
+// hold one, a vector each.  (8191 tokens of 32 heads of 128, 134 MB: 25 us, 5.3
+// TB/s; a warp a row as above, half of it idle, 68 us; two rows a team 24, four 25.)
+constexpr int kNarrowThreads = 256;
+template <int LPR>
+__global__ void __launch_bounds__(kNarrowThreads, 8) k_rmsnorm_narrow(const NormParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const unsigned row = blockIdx.x * (kNarrowThreads / LPR) + threadIdx.x / LPR;
+  const unsigned m = row / static_cast<unsigned>(p.heads);
+  const int c = threadIdx.x % LPR * 8;
+  const int off = static_cast<int>(row - m * p.heads) * p.H;
+  const int H = row < p.rows ? p.H : 0;   // (past the last row: zeros, for the shuffles)
+  float s[8], w[8];
+  load8<true>(p.x + (H ? m * p.xs + off : 0), c, H, s);
+  if (p.r) {
+    float u[8];
+    load8<true>(p.r + (H ? m * p.rs + off : 0), c, H, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += u[j];
+  }
+  if (p.w) {
+    load8<true>(p.w, c, H, w);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 1.f;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum = fmaf(s[j], s[j], sum);
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+  if (!H) return;
+  if (p.ro) store8<true>(p.ro + m * p.ros + off, c, H, s);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = s[j] * rstd * w[j];
+  store8<true>(p.y + m * p.ys + off, c, H, s);
+}
+
+template <int LPR>
+int launch_narrow(const NormParams& p, cudaStream_t s) {
+  constexpr int kRows = kNarrowThreads / LPR;
+  return flh::launch_early(k_rmsnorm_narrow<LPR>, dim3(static_cast<unsigned>((p.rows + kRows - 1) / kRows)),
+                           dim3(kNarrowThreads), 0, s, p);
+}
+
 template <int TPR, int V>
 int launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
   constexpr int kTeams = TPR == 32 ? 4 : 1;
@@ -250,6 +297,7 @@ extern "C" int fl_rmsnorm(const void* x, int64_t x_stride, const void* residual,
   p.rows = static_cast<long long>(M) * heads;
   p.heads = heads, p.H = H, p.group = group, p.eps = eps;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (vec && !codes && H <= 128 && w < (1ll << 31) && p.rows < 0x7fffffffll) return H <= 64 ? launch_narrow<8>(p, s) : launch_narrow<16>(p, s);
   int tpr = 32;
   while (tpr < 1024 && tpr * 32 < H) tpr = tpr == 32 ? 128 : 2 * tpr;   // at most 4 vectors a thread
   if (tpr * 8 >= H) return pick_team<1>(p, tpr, vec, s);

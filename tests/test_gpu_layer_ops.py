@@ -97,6 +97,20 @@ def test_rmsnorm_heads_in_place(D):
     assert torch.equal(qkv[:, :2], before[:, :2]) and torch.equal(qkv[:, 6:], before[:, 6:])
 
 
+@pytest.mark.parametrize("H", [8, 24, 64, 72, 128])
+@pytest.mark.parametrize("M,heads", [(1, 1), (5, 3), (37, 7), (600, 5)])
+def test_rmsnorm_narrow_rows(M, heads, H):
+    """Several rows a warp, with and without residual and weight; the last CTA
+    partly filled, rows of a wider projection."""
+    rng = np.random.default_rng(M + H)
+    wide = _bf16(rng.standard_normal((M, heads + 2, H))).to(DEV)
+    r = _bf16(3 * rng.standard_normal((M, heads, H))).to(DEV)
+    w = _bf16(1 + 0.1 * rng.standard_normal(H)).to(DEV)
+    x = wide[:, 1:1 + heads]
+    _norm_check(x, w, r, fl.fl_rmsnorm(x, w, 1e-6, residual=r), 0, 1e-6)
+    _norm_check(x, None, None, fl.fl_rmsnorm(x, None, 1e-5), 0, 1e-5)
+
+
 def test_rmsnorm_residual_in_place_and_misaligned():
     rng = np.random.default_rng(3)
     buf = _bf16(rng.standard_normal((5, 264))).to(DEV)
