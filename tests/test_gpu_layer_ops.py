@@ -68,6 +68,18 @@ def test_rmsnorm_widths(H, M):
     _norm_check(x, None, None, out, 0, 1e-5)
 
 
+@pytest.mark.parametrize("H", [33, 300, 511, 700, 1030, 2046, 2816, 5001, 6144, 11003, 20001])
+def test_rmsnorm_odd_widths(H):
+    """Every number of vectors a thread, 16 bytes at a time and one by one."""
+    rng = np.random.default_rng(H)
+    x, r = _bf16(rng.standard_normal((5, H))).to(DEV), _bf16(2 * rng.standard_normal((5, H))).to(DEV)
+    w = _bf16(1 + 0.2 * rng.standard_normal(H)).to(DEV)
+    _norm_check(x, w, r, fl.fl_rmsnorm(x, w, 1e-6, residual=r, out8=True), 0, 1e-6)
+    shifted = torch.zeros(5 * H + 1, dtype=torch.bfloat16, device=DEV)[1:].view(5, H)
+    shifted.copy_(x)
+    _norm_check(shifted, w, None, fl.fl_rmsnorm(shifted, w, 1e-6), 0, 1e-6)
+
+
 @pytest.mark.parametrize("M", [2, 33, 700])
 @pytest.mark.parametrize("group", [0, 64, 128, 256])
 def test_rmsnorm_groups_and_rows(M, group):
