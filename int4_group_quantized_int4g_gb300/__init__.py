@@ -144,13 +144,19 @@ def _check(where, rc):
         raise Int4gError(where, rc)
 
 
+def _device():
+    """The current device's index (CUDA is up: the caller has a tensor on it)."""
+    get = getattr(_TORCH._C, "_cuda_getDevice", None)
+    return get() if get is not None else _TORCH.cuda.current_device()
+
+
 def _stream(stream=None):
     torch = _torch()
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is not None:   # the current stream's handle without building a Stream object
-        return ctypes.c_void_p(raw(torch.cuda.current_device()))
+        return ctypes.c_void_p(raw(_device()))
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
@@ -484,15 +490,18 @@ def fl_rmsnorm(x, weight=None, eps=1e-6, residual=None, y=None, residual_out=Non
             _raise("fl_rmsnorm", "residual and x differ in shape")
         rp, rs = _tokens(residual, "residual")
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    if y is None and need_y:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    if y is not None:
+            residual_out = out["residual"] = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            op, os_ = residual_out.data_ptr(), heads * H
+    if y is None:
+        if need_y:
+            y = out["y"] = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            yp, ys = y.data_ptr(), heads * H
+    else:
         if y.shape != shape:
             _raise("fl_rmsnorm", "y and x differ in shape")
         yp, ys = _tokens(y, "y")
         out["y"] = y
-    if residual_out is not None:
+    if residual_out is not None and op is None:
         if residual_out.shape != shape:
             _raise("fl_rmsnorm", "residual_out and x differ in shape")
         op, os_ = _tokens(residual_out, "residual_out")
@@ -527,9 +536,11 @@ def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k
     qp, qs = _tokens(q, "q")
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        qop, qos = q_out.data_ptr(), Hq * D
     elif q_out.shape != q.shape:
         _raise("fl_rope", "q_out and q differ in shape")
-    qop, qos = _tokens(q_out, "q_out")
+    else:
+        qop, qos = _tokens(q_out, "q_out")
     kp, ks, kop, kos, Hk = None, 0, None, 0, 0
     if k is not None:
         Tk, Hk, Dk = k.shape
@@ -538,9 +549,11 @@ def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k
         kp, ks = _tokens(k, "k")
         if k_out is None:
             k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+            kop, kos = k_out.data_ptr(), Hk * D
         elif k_out.shape != k.shape:
             _raise("fl_rope", "k_out and k differ in shape")
-        kop, kos = _tokens(k_out, "k_out")
+        else:
+            kop, kos = _tokens(k_out, "k_out")
     psh = positions.shape
     axes = psh[0] if len(psh) == 2 else 1
     if psh[-1] != T or (sections is not None and len(sections) != axes):
@@ -649,9 +662,11 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     device = q.device
     if out is None:
         out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=device)
+        op, os_ = out.data_ptr(), Hq * d
     elif out.shape != q.shape:
         _raise("fl_kv8_attention", "out and q differ in shape")
-    op, os_ = _tokens(out, "out")
+    else:
+        op, os_ = _tokens(out, "out")
     lse = torch.empty((T, Hq), dtype=torch.float32, device=device) if return_lse else None
     if ws is None:
         ws = _workspace(_kv8_workspace(device.index, T, B, Hq, hk, d), device)

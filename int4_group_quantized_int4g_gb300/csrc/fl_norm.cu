@@ -249,15 +249,19 @@ int launch_norm(const NormParams& p, bool vec, cudaStream_t s) {
   return vec ? flh::launch_early(k_rmsnorm<TPR, V, true>, g, b, 0, s, p) : flh::launch_early(k_rmsnorm<TPR, V, false>, g, b, 0, s, p);
 }
 
+// Teams grow before they would need more than 4 vectors a thread, so one vector
+// happens in teams of 32 only, two in teams of 32 and 128.
 template <int V>
 int pick_team(const NormParams& p, int tpr, bool vec, cudaStream_t s) {
-  switch (tpr) {
-    case 32: return launch_norm<32, V>(p, vec, s);
-    case 128: return launch_norm<128, V>(p, vec, s);
-    case 256: return launch_norm<256, V>(p, vec, s);
-    case 512: return launch_norm<512, V>(p, vec, s);
-    default: return launch_norm<1024, V>(p, vec, s);
+  if constexpr (V >= 2) {
+    if (tpr == 128) return launch_norm<128, V>(p, vec, s);
   }
+  if constexpr (V >= 3) {
+    if (tpr == 256) return launch_norm<256, V>(p, vec, s);
+    if (tpr == 512) return launch_norm<512, V>(p, vec, s);
+    if (tpr == 1024) return launch_norm<1024, V>(p, vec, s);
+  }
+  return launch_norm<32, V>(p, vec, s);
 }
 
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
