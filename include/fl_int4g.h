@@ -470,7 +470,8 @@ typedef struct fl_kv8_cache {
  *   cu_q        int32 [B+1] device, or NULL: every sequence has T / B rows
  *   kv_lens     int32 [B] device, lengths with the new tokens
  *   block_table int32 [B, max_blocks] device
- *   max_q       the largest number of rows of a sequence (an upper bound)
+ *   max_q       the largest number of rows of a sequence: an upper bound, which
+ *             may be loose, and larger than T
  * A sequence may have no rows; kv_lens[b] below its number of rows is allowed:
  * the first rows then have negative positions (they are not written and see
  * no key). */
@@ -516,8 +517,15 @@ int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int block, int wi
  * some row of the item sees. */
 int fl_kv8_test_units(int n, int kv, int group, int heads, int window, long long u, long long* out);
 
-/* Workspace bytes needed by fl_kv8_attention: the status block and counters of
- * every workspace, then two partials a CTA.  The layout is that of the other
+/* Test hook: what fl_kv8_attention launches for T rows in B sequences, at most
+ * max_q of one sequence (host code only).  out[0..3] receives the bound on a
+ * sequence's rows (query heads of a kv head x tokens) that it goes by, whether
+ * the kernels for many and for few rows are launched, and the workspace bytes
+ * that those kernels reach. */
+int fl_kv8_test_plan(int T, int B, int max_q, int Hq, int kv_heads, int head_dim, long long* out);
+
+/* Workspace bytes needed by fl_kv8_attention, whatever its max_q: the status
+ * block and counters of every workspace, then two partials a CTA.  The layout is that of the other
  * entry points, so one workspace serves them all in turn. */
 int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out);
 

@@ -27,7 +27,7 @@ __all__ = [
     "fl_int4g_mlp", "fl_int4g_mlp_fused",
     "FL_KV8_E4M3", "FL_KV8_INT8", "FlKv8Cache", "FlKv8Seqs",
     "fl_rmsnorm", "fl_rope", "fl_kv8_append", "fl_kv8_attention_workspace", "fl_kv8_attention",
-    "fl_kv8_test_pages", "fl_kv8_test_units",
+    "fl_kv8_test_pages", "fl_kv8_test_units", "fl_kv8_test_plan",
 ]
 
 GROUP = 128
@@ -99,6 +99,7 @@ SIGNATURES = {
     "fl_kv8_append": (_i, [_vp, _l, _vp, _l, _vp, _vp, _vp, _vp]),
     "fl_kv8_test_pages": (_i, [ctypes.POINTER(FlKv8Seqs), _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_test_units": (_i, [_i, _i, _i, _i, _i, ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)]),
+    "fl_kv8_test_plan": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_attention_workspace": (_i, [_i, _i, _i, _i, _i, _c_size_p]),
     "fl_kv8_attention": (_i, [_vp, _l, _i, _vp, _vp, ctypes.c_float, _i, _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
 }
@@ -594,6 +595,7 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     [blocks, kv_heads, block, head_dim], scales fp32 [blocks, kv_heads]).
     Sequence b's rows cu_q[b] .. cu_q[b+1]-1 (None: T / B each) are the last of
     its kv_lens[b] tokens; token j lives in block block_table[b][j // block].
+    max_q: at least the rows of every sequence; it may be larger.
     status: the status block to record device-side errors in (an int32 or uint8
     CUDA tensor of 16 bytes or a workspace; None: this stream's workspace)."""
     _torch()
@@ -631,6 +633,14 @@ def fl_kv8_test_units(n, kv, group, u=-1, window=0):
     out = (ctypes.c_longlong * 8)()
     _check("fl_kv8_test_units", lib().fl_kv8_test_units(n, kv, group, 1, window, u, out))
     return tuple(out[:2]) if u < 0 else tuple(out[2:])
+
+
+def fl_kv8_test_plan(T, B, max_q, Hq, kv_heads, head_dim):
+    """Test hook: (rows, many, few, bytes): the bound on a sequence's rows, the
+    attention kernels launched for it and the workspace bytes they reach."""
+    out = (ctypes.c_longlong * 4)()
+    _check("fl_kv8_test_plan", lib().fl_kv8_test_plan(T, B, max_q, Hq, kv_heads, head_dim, out))
+    return tuple(out)
 
 
 def fl_kv8_attention_workspace(T, B, Hq, kv_heads, head_dim):

@@ -254,7 +254,7 @@ extern "C" int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int
   AppendParams p;
   p.k = {static_cast<const __nv_bfloat16*>(k), k_stride, static_cast<uint8_t*>(cache->k), cache->k_scale};
   p.v = {static_cast<const __nv_bfloat16*>(v), v_stride, static_cast<uint8_t*>(cache->v), cache->v_scale};
-  p.seqs = {seqs->cu_q, seqs->kv_lens, seqs->block_table, seqs->T, seqs->B, seqs->max_q, seqs->max_blocks};
+  p.seqs = flh::seqs_of(*seqs);
   p.num_blocks = cache->num_blocks, p.heads = cache->kv_heads;
   p.status = static_cast<int32_t*>(status);
   // n new tokens touch at most (n - 1) / block + 2 blocks, and never more than
@@ -276,7 +276,7 @@ extern "C" int fl_kv8_test_pages(const fl_kv8_seqs* seqs, int num_blocks, int bl
       b >= seqs->B || seqs->T > (1 << 29) || seqs->max_blocks > (1 << 30) / block)
     return FL_ERR_ARG;
   if (window >= seqs->max_blocks * block) window = 0;
-  const Seqs s = {seqs->cu_q, seqs->kv_lens, seqs->block_table, seqs->T, seqs->B, seqs->max_q, seqs->max_blocks};
+  const Seqs s = flh::seqs_of(*seqs);
   const SeqInfo q = seq_info(s, b, block);
   const PageRun runs[2] = {written_pages(q, block), read_pages(q, block, window)};
   out[0] = q.start, out[1] = q.n, out[2] = q.kv;

@@ -207,6 +207,12 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 
 namespace flh {
 
+// The device's view of the sequences.  max_q is a bound that may be loose; no
+// sequence has more than T rows.
+inline flkv::Seqs seqs_of(const fl_kv8_seqs& s) {
+  return {s.cu_q, s.kv_lens, s.block_table, s.T, s.B, s.max_q < s.T ? s.max_q : s.T, s.max_blocks};
+}
+
 // Arguments that fl_kv8_append and fl_kv8_attention share.
 inline int kv8_check(const fl_kv8_cache* c, const fl_kv8_seqs* s) {
   if (!c || !s || !c->k || !c->v || !c->k_scale || !c->v_scale || !s->kv_lens || !s->block_table) return FL_ERR_ARG;

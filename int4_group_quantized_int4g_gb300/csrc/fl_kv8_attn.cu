@@ -721,15 +721,41 @@ int pick_rows(const CUtensorMap& km, const CUtensorMap& vm, const AttnParams& p,
   return launch_rows<FMT, D, 1>(km, vm, p, s);
 }
 
+// What a call of T rows in B sequences, at most max_q of one sequence, launches,
+// and the scratch of those kernels.  max_q may be loose: no sequence has more
+// rows than T.  The size query, which knows no max_q, asks for T: the scratch
+// does not fall with max_q, so its answer covers every call of these T and B.
+struct AttnPlan {
+  long long rows;      // most rows of a sequence, query heads of a kv head x tokens
+  bool prompt, few;    // the kernels for many rows and for few
+  size_t scratch;
+};
+AttnPlan attn_plan(int T, int B, int max_q, int group, int head_dim) {
+  AttnPlan a;
+  a.rows = static_cast<long long>(max_q < T ? max_q : T) * group;
+  a.prompt = a.rows > kFewRows;
+  a.few = !a.prompt || B > 1;   // one sequence goes to the one kernel; a batch may hold both kinds
+  // two partials a CTA: the rows that it shares with the CTAs before and after
+  const size_t few = 2ull * flh::sm_count() * 2 * 16 * (head_dim + 2) * 4;   // (two CTAs an SM)
+  const size_t many = prompt_scratch(head_dim);
+  a.scratch = a.prompt && many > few ? many : few;
+  return a;
+}
+
 }  // namespace
 
 extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out) {
   if (!out || T < 1 || B < 1 || Hq < 1 || kv_heads < 1 || Hq % kv_heads) return FL_ERR_ARG;
   if (head_dim != 64 && head_dim != 128) return FL_ERR_UNSUPPORTED;
-  // two partials a CTA: the rows that it shares with the CTAs before and after
-  const bool prompt = static_cast<long long>(T) * (Hq / kv_heads) > kFewRows;
-  const size_t few = 2ull * flh::sm_count() * 2 * 16 * (head_dim + 2) * 4;   // (two CTAs an SM)
-  *out = kScratchOff + (prompt ? prompt_scratch(head_dim) : few);
+  *out = kScratchOff + attn_plan(T, B, T, Hq / kv_heads, head_dim).scratch;
+  return FL_OK;
+}
+
+extern "C" int fl_kv8_test_plan(int T, int B, int max_q, int Hq, int kv_heads, int head_dim, long long* out) {
+  if (!out || T < 1 || B < 1 || max_q < 1 || Hq < 1 || kv_heads < 1 || Hq % kv_heads || (head_dim != 64 && head_dim != 128))
+    return FL_ERR_ARG;
+  const AttnPlan a = attn_plan(T, B, max_q, Hq / kv_heads, head_dim);
+  out[0] = a.rows, out[1] = a.prompt, out[2] = a.few, out[3] = static_cast<long long>(kScratchOff + a.scratch);
   return FL_OK;
 }
 
@@ -748,8 +774,8 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   size_t need = 0;
   fl_kv8_attention_workspace(seqs->T, seqs->B, Hq, cache->kv_heads, cache->head_dim, &need);
   if (ws_bytes < need) return FL_ERR_WORKSPACE;
-  const long long rows = static_cast<long long>(seqs->max_q) * (Hq / cache->kv_heads);
-  if (rows > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
+  const AttnPlan plan = attn_plan(seqs->T, seqs->B, seqs->max_q, Hq / cache->kv_heads, cache->head_dim);
+  if (plan.rows > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
   CUtensorMap km, vm;
   AttnParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -760,23 +786,22 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   p.cnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kTicketOff);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kScratchOff);
   p.qs = q_stride, p.os = out_stride;
-  p.seqs = {seqs->cu_q, seqs->kv_lens, seqs->block_table, seqs->T, seqs->B, seqs->max_q, seqs->max_blocks};
+  p.seqs = flh::seqs_of(*seqs);
   p.num_blocks = cache->num_blocks, p.block = cache->block, p.heads = cache->kv_heads;
   p.group = Hq / cache->kv_heads, p.Hq = Hq, p.window = window;
   p.scale2 = scale * 1.44269504088896340736f;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (rows > kFewRows) {
+  if (plan.prompt) {
     if (!code_map(&km, cache->k, *cache, cache->block) || !code_map(&vm, cache->v, *cache, cache->block)) return FL_ERR_CUDA;
-    // one sequence goes to the one kernel; a batch may hold both kinds
-    p.rows_lo = seqs->B > 1 ? kFewRows : 0, p.rows_hi = 0x7fffffff;
+    p.rows_lo = plan.few ? kFewRows : 0, p.rows_hi = 0x7fffffff;
     const int e = launch_prompt(km, vm, p, cache->format, cache->head_dim, s);
-    if (e != FL_OK || seqs->B == 1) return e;
+    if (e != FL_OK || !plan.few) return e;
   }
   if (!code_map(&km, cache->k, *cache, 16) || !code_map(&vm, cache->v, *cache, 16)) return FL_ERR_CUDA;
   p.rows_lo = 0, p.rows_hi = kFewRows;
   if (cache->format == FL_KV8_E4M3)
-    return cache->head_dim == 64 ? pick_rows<FL_KV8_E4M3, 64>(km, vm, p, rows, s)
-                                 : pick_rows<FL_KV8_E4M3, 128>(km, vm, p, rows, s);
-  return cache->head_dim == 64 ? pick_rows<FL_KV8_INT8, 64>(km, vm, p, rows, s)
-                               : pick_rows<FL_KV8_INT8, 128>(km, vm, p, rows, s);
+    return cache->head_dim == 64 ? pick_rows<FL_KV8_E4M3, 64>(km, vm, p, plan.rows, s)
+                                 : pick_rows<FL_KV8_E4M3, 128>(km, vm, p, plan.rows, s);
+  return cache->head_dim == 64 ? pick_rows<FL_KV8_INT8, 64>(km, vm, p, plan.rows, s)
+                               : pick_rows<FL_KV8_INT8, 128>(km, vm, p, plan.rows, s);
 }
