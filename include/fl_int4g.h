@@ -395,8 +395,8 @@ int fl_moe_int4g_ptrs(const void* x, const float* logits, int M, int H, int E, i
  *   y = bf16(n),
  *   codes, scales: for each run of `group` columns (group 0: the whole row)
  *   scale = max|n| / 448 and code_i = e4m3(n_i / scale), nearest even (n_i
- *   times fp32's 1 / scale: the quotient to 2^-23; a run of zeros: scale 0,
- *   codes 0).
+ *   times fp32's 1 / scale: the quotient to 2^-23; a run of zeros, or whose
+ *   scale fp32 rounds to 0: scale 0, codes 0).
  *   x, residual, y, residual_out  bf16; row (m, h) starts at
  *           m * stride + h * H elements, stride >= heads * H
  *   weight  bf16 [H], or NULL for ones

@@ -167,6 +167,18 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
 #pragma unroll
       for (int i = 0; i < V; ++i) top[i] = a;
     }
+    // 1 / scale of a scale below fp32's normal numbers may be infinite: such a run
+    // and its scale are taken times 2^64.
+    constexpr float kTiny = 448.f * 1.1754943508222875e-38f, kLift = 18446744073709551616.f;
+    bool tiny = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) tiny |= top[i] < kTiny;
+    if (tiny) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] *= top[i] < kTiny ? kLift : 1.f;
+    }
     const int ng = p.group ? p.H / p.group : 1;
     uint8_t* cr = p.codes + row * p.H;
 #pragma unroll
@@ -174,7 +186,8 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
       const int c = (i * TPR + t) * 8;
       if (c >= p.H) continue;
       const float scale = __fdiv_rn(top[i], 448.f);
-      const float inv = scale > 0.f ? __frcp_rn(scale) : 1.f;   // (n times it: n / scale within 2^-23)
+      const float up = top[i] < kTiny ? scale * kLift : scale;
+      const float inv = scale > 0.f ? __frcp_rn(up) : 0.f;   // (n times it: n / scale within 2^-23)
       if (p.group ? c % p.group == 0 : c == 0) p.scales[row * ng + (p.group ? c / p.group : 0)] = scale;
       uint32_t o[2] = {0, 0};
 #pragma unroll

@@ -60,3 +60,46 @@ def test_append_loose_max_q(fmt):
         for i in range(2):
             O.append(_np(x) * (1 - 2 * i), c.codes[i], c.scale[i], table, lens, _cu(q_len), FMT[fmt])
         assert c.equal_host() and fl.fl_int4g_status(st) == 0
+
+
+# ------------------------------------------------------------------ norm
+
+def _small_runs_check(n, out, group):
+    """Codes of runs down to fp32's last numbers: n to 2^-18 and a last place,
+    the scale rounded to a last place (half of one, 2^-150, moves the 448
+    steps of the largest code), half a step of e4m3 then."""
+    g = group or n.shape[-1]
+    parts = n.reshape(*n.shape[:-1], -1, g)
+    top, rel, last = np.abs(parts).max(-1), 2.0 ** -18, 2.0 ** -149
+    scale = _np(out["scales"])
+    assert np.all(np.abs(scale - top / 448) <= rel * top / 448 + last)
+    got = O.values(out["codes"].cpu().numpy(), O.E4M3).reshape(parts.shape)
+    assert not np.isnan(got).any()
+    assert not got[parts == 0].any()
+    err = np.abs(got * scale[..., None] - parts)
+    assert np.all(err <= (2.0 ** -4 + rel) * np.abs(parts) + (2.0 ** -10 + rel) * scale[..., None] + 449 * last)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("group", [0, 64, 128, 256])
+def test_rmsnorm_codes_of_tiny_runs(group, aligned):
+    """Runs of 1e-35 to 1e-40, with zeros among them: as columns of an otherwise
+    normal row, by tiny weights, and as whole rows."""
+    rng = np.random.default_rng(group + aligned)
+    H, sizes = 1024, 10.0 ** -np.array([0.0, 36, 40, 35.5, 37, 38, 39, 36.3])
+    x = rng.standard_normal((9, H))
+    x[:, ::7] = 0
+    gain = np.repeat(sizes, H // 8)                      # runs of 128 columns, of 256 with a larger half
+    x[:4] *= gain
+    x[4:6] *= 10.0 ** -np.array([[39.0], [40.0]])        # a whole row: n is 1000 times as large
+    x[6, :] *= np.repeat(sizes[[1, 2]], H // 2)
+    w = np.ones(H)
+    w[256:512] = 1e-37
+    buf = torch.zeros(9 * H + 8, dtype=torch.bfloat16, device=DEV)
+    xd = (buf[:9 * H] if aligned else buf[1:9 * H + 1]).view(9, H)
+    xd.copy_(_bf16(x))
+    wd = _bf16(w).to(DEV)
+    for weight in (None, wd):
+        out = fl.fl_rmsnorm(xd, weight, 1e-6, out8=True, group=group)
+        _, n = O.rmsnorm(_np(xd), None, _np(weight) if weight is not None else None, 1e-6)
+        _small_runs_check(n, out, group)
