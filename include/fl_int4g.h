@@ -408,7 +408,9 @@ int fl_moe_int4g_ptrs(const void* x, const float* logits, int M, int H, int E, i
  * group is 0, 64, 128 or 256 (H % group == 0); 1 <= H <= 32768.  Rows whose
  * pointers are 16-byte aligned with H and the strides multiples of 8 are read
  * 16 bytes at a time, others element by element.  Pointers need only their
- * elements' alignment.  A row with infinities or NaN gives NaN. */
+ * elements' alignment.  A row with infinities or NaN gives NaN (codes NaN, with
+ * scale 0); finite rows of any size, and rows of tiny values with eps 0, are
+ * normed as the formula says. */
 int fl_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride, const void* weight,
                float eps, int M, int heads, int H, void* y, int64_t y_stride, void* residual_out,
                int64_t residual_out_stride, void* codes, float* scales, int group, fl_stream_t stream);

@@ -87,6 +87,22 @@ __device__ __forceinline__ float team_reduce(float v, float* red) {
   return v;
 }
 
+// A row whose mean square is not among these, for which its squares are summed
+// once more with the values times a power of two: above, fp32 has no number for
+// the sum (values beyond 1e19 / sqrt(H), infinities, NaN); below, with next to no
+// eps, the squares are rounded to its last numbers or to 0.
+constexpr float kMeanMin = 7.888609052210118e-31f, kMeanMax = 3.4028234663852886e38f;   // 2^-100, the largest
+__device__ __forceinline__ bool odd_mean(float ms) { return !(ms >= kMeanMin && ms <= kMeanMax); }
+// 2^90 or 2^-72: the squares of all fp32 numbers that can lead here, and their sum, are normal numbers.
+__device__ __forceinline__ float odd_factor(float ms) { return ms < 1.f ? 1.2379400392853803e27f : 2.117582368135751e-22f; }
+// 1 / sqrt(mean + eps) from the sum with the values times f, and what the
+// values have to be multiplied by before (x: tiny values' reciprocal may pass
+// fp32).  A row with an infinity or a NaN: NaN.
+__device__ __forceinline__ float2 odd_rstd(float sum, float f, int H, float eps) {
+  const float ms = sum / static_cast<float>(H) + eps * f * f, r = rsqrtf(ms);
+  return f > 1.f ? make_float2(f, r) : make_float2(1.f, ms <= kMeanMax ? r * f : __int_as_float(0x7fffffff));
+}
+
 // TPR threads hold one row, V vectors of 8 columns each: thread i has the
 // vectors i, i + TPR, ...  A CTA is one team, or four when a team is a warp.
 // V is what the row needs: 8191 rows of 5120 columns take 33 us with 3 vectors a
@@ -95,7 +111,7 @@ __device__ __forceinline__ float team_reduce(float v, float* red) {
 // with residual and codes: 56 us; 7 of them 64, 9 of them, which spill, 66).
 template <int TPR, int V, bool VEC>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_rmsnorm(const NormParams p) {
-  __shared__ float red[2][TPR / 32];
+  __shared__ float red[3][TPR / 32];
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kTeams = TPR == 32 ? 4 : 1;
@@ -124,11 +140,26 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum = fmaf(s[i][j], s[i][j], sum);
   sum = team_reduce<TPR, false>(sum, red[0]);
-  const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+  const float ms = sum / static_cast<float>(p.H) + p.eps;
+  float rstd = rsqrtf(ms);
   if (p.ro) {
     __nv_bfloat16* ro = p.ro + m * p.ros + off;
 #pragma unroll
     for (int i = 0; i < V; ++i) store8<VEC>(ro, (i * TPR + t) * 8, p.H, s[i]);
+  }
+  if (odd_mean(ms)) {   // (the same in the whole team)
+    const float f = odd_factor(ms);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(s[i][j] * f, s[i][j] * f, sum);
+    const float2 by = odd_rstd(team_reduce<TPR, false>(sum, red[2]), f, p.H, p.eps);
+    rstd = by.y;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] *= by.x;
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -206,12 +237,51 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
   }
 }
 
+// The rows of a warp of the kernel below, once one of them has an odd mean: all
+// from the start, in a function of its own, so that the kernel's common path
+// keeps its registers (as a branch in it: heads of 128 27.9 us, not 25.1).
+template <int LPR>
+__device__ __noinline__ void odd_narrow(const NormParams& p, unsigned row) {
+  const unsigned m = row / static_cast<unsigned>(p.heads);
+  const int c = threadIdx.x % LPR * 8, H = row < p.rows ? p.H : 0;
+  const int off = static_cast<int>(row - m * p.heads) * p.H;
+  float s[8], w[8];
+  load8<true>(p.x + (H ? m * p.xs + off : 0), c, H, s);
+  if (p.r) {
+    load8<true>(p.r + (H ? m * p.rs + off : 0), c, H, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += w[j];
+  }
+  float f = 1.f;   // for an ordinary row
+  float2 rstd;
+  for (int pass = 0; pass < 2; ++pass) {
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(s[j] * f, s[j] * f, sum);
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float ms = sum / static_cast<float>(p.H) + p.eps;
+    if (pass == 1) {
+      if (f != 1.f) rstd = odd_rstd(sum, f, p.H, p.eps);
+    } else {
+      rstd = make_float2(1.f, rsqrtf(ms));
+      if (odd_mean(ms)) f = odd_factor(ms);
+    }
+  }
+  if (!H) return;
+  if (p.ro) store8<true>(p.ro + m * p.ros + off, c, H, s);
+  if (p.w) load8<true>(p.w, c, H, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = s[j] * rstd.x * rstd.y * (p.w ? w[j] : 1.f);
+  store8<true>(p.y + m * p.ys + off, c, H, s);
+}
+
 // Rows of at most 8 LPR columns (heads of 64 or 128) without codes: LPR lanes
 // hold one, a vector each.  (8191 tokens of 32 heads of 128, 134 MB: 25 us, 5.3
 // TB/s; a warp a row as above, half of it idle, 68 us; two rows a team 24, four 25.)
 constexpr int kNarrowThreads = 256;
 template <int LPR>
-__global__ void __launch_bounds__(kNarrowThreads, 8) k_rmsnorm_narrow(const NormParams p) {
+__global__ void __launch_bounds__(kNarrowThreads, 8) k_rmsnorm_narrow(const __grid_constant__ NormParams p) {
   pdl_launch_dependents();
   pdl_wait();
   const unsigned row = blockIdx.x * (kNarrowThreads / LPR) + threadIdx.x / LPR;
@@ -238,7 +308,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 8) k_rmsnorm_narrow(const Norm
   for (int j = 0; j < 8; ++j) sum = fmaf(s[j], s[j], sum);
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float rstd = rsqrtf(sum / static_cast<float>(p.H) + p.eps);
+  const float ms = sum / static_cast<float>(p.H) + p.eps;
+  if (__any_sync(0xffffffffu, odd_mean(ms))) {
+    odd_narrow<LPR>(p, row);   // (nothing of the warp's rows has been stored)
+    return;
+  }
+  const float rstd = rsqrtf(ms);
   if (!H) return;
   if (p.ro) store8<true>(p.ro + m * p.ros + off, c, H, s);
 #pragma unroll

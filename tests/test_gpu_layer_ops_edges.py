@@ -103,3 +103,58 @@ def test_rmsnorm_codes_of_tiny_runs(group, aligned):
         out = fl.fl_rmsnorm(xd, weight, 1e-6, out8=True, group=group)
         _, n = O.rmsnorm(_np(xd), None, _np(weight) if weight is not None else None, 1e-6)
         _small_runs_check(n, out, group)
+
+
+def _shifted(x, aligned):
+    """x on the device, on the 16-byte grid or one element off it."""
+    buf = torch.zeros(x.numel() + 8, dtype=torch.bfloat16, device=DEV)
+    d = buf[0 if aligned else 1:][:x.numel()].view(x.shape)
+    d.copy_(x)
+    return d
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("H", [8, 64, 128, 256, 1000, 1024, 3000, 4096, 8192, 16384, 32768])
+def test_rmsnorm_rows_of_any_size(H, aligned):
+    """Finite rows whose squares pass fp32, rows of tiny values without eps, and
+    ordinary rows between them (neighbours of one warp in narrow rows)."""
+    rng = np.random.default_rng(H + aligned)
+    for sizes, eps in (([1.0, 1e19, 1e30, 1e38, 1e18, 1.0, 3e38, 1e25], 1e-6), ([1.0, 1e-16, 1e-20, 1e-30, 1e-39, 1.0, 1e-25, 1e38], 0.0),
+                       ([1e-22, 1.0, 1e-18, 1e25], 1e-38)):
+        x = rng.uniform(0.5, 1.0, (len(sizes), H)) * rng.choice([-1, 1], (len(sizes), H)) * np.array(sizes)[:, None]
+        x = _shifted(_bf16(x), aligned)
+        w = _shifted(_bf16(1 + 0.2 * rng.standard_normal(H)), aligned)
+        r = _shifted(_bf16(0.1 * x.double().cpu().numpy() * rng.uniform(-1, 1, x.shape)), aligned)
+        for weight, res in ((None, None), (w, r)):
+            for out8 in (False, True):
+                out = fl.fl_rmsnorm(x, weight, eps, residual=res, out8=out8)
+                s = _np(x) + (_np(res) if res is not None else 0)
+                n = s / np.sqrt(np.mean(s * s, -1, keepdims=True) + eps) * (_np(w) if weight is not None else 1)
+                assert np.all(np.abs(_np(out["y"]) - n) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(n) + 2.0 ** -133)
+                if res is not None:   # (fp32 adds, then bf16: 2^-8 and 2^-24, subnormals to half their step)
+                    assert np.all(np.abs(_np(out["residual"]) - s) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(s) + 2.0 ** -134)
+                if out8:
+                    _small_runs_check(n, out, 0)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("H", [8, 64, 128, 256, 1024, 4096, 16384])
+def test_rmsnorm_infinities_and_nan(H, aligned):
+    """A row with an infinity or a NaN gives NaN, all of it; the rows beside it
+    are not touched by it."""
+    rng = np.random.default_rng(H)
+    x = rng.standard_normal((6, H))
+    x[1, H // 2], x[2, 0], x[4, H - 1] = np.inf, -np.inf, np.nan
+    xd, r = _shifted(_bf16(x), aligned), _shifted(_bf16(np.zeros((6, H))), aligned)
+    for out8 in (False, True):
+        out = fl.fl_rmsnorm(xd, None, 1e-6, residual=r, out8=out8, group=64 if H % 64 == 0 and out8 else 0)
+        good = torch.tensor([True, False, False, True, False, True], device=DEV)
+        assert bool(out["y"][~good].isnan().all())
+        assert torch.equal(out["residual"].view(torch.int16), xd.view(torch.int16)) or bool(out["residual"][4, H - 1].isnan())
+        _, n = O.rmsnorm(_np(xd[good]), None, None, 1e-6)
+        assert np.all(np.abs(_np(out["y"][good]) - n) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(n))
+        if out8:
+            codes = O.values(out["codes"].cpu().numpy(), O.E4M3)
+            g = good.cpu().numpy()
+            assert np.isnan(codes[~g]).all() and not np.isnan(codes[g]).any()
+            assert not out["scales"][~good].any()
