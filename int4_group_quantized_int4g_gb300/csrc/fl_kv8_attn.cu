@@ -50,7 +50,7 @@ constexpr int kWarps = 8;
 constexpr int kRowsThreads = 32 * kWarps;
 constexpr float kPScale = 64.f;         // 2^6
 constexpr float kSlack = 8.f;           // a reference may lag its maximum by 2^kSlack
-constexpr float kNone = -1e30f;         // the reference of a row without a token so far
+constexpr float kNone = -3.4028234663852886e38f;   // the reference of a row without a token so far: below every finite score
 // Most rows of a sequence (query heads of a kv head x tokens) that this kernel
 // takes; sequences with more go to the tcgen05 kernel, in the same call.  (16
 // sequences of 4096 tokens, 8 heads of 128: with 24 rows 78 us here and 89 us
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) grow |= fmaxf(x[nt][h], x[nt][h + 2]) > m[nt][h] + kSlack;
+          for (int h = 0; h < 2; ++h) grow |= fmaxf(x[nt][h], x[nt][h + 2]) - m[nt][h] > kSlack;   // (the difference is exact where it counts)
         if (__any_sync(0xffffffffu, grow) || sc.y > vref) {
           // a maximum has outgrown its reference, or the value scale is the largest so far
           const float vnew = fmaxf(vref, sc.y), vr = vref / vnew;

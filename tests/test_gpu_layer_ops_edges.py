@@ -6,7 +6,7 @@ import torch
 
 import int4_group_quantized_int4g_gb300 as fl
 from oracle import layer_oracle as O
-from test_gpu_layer_ops import DEV, FMT, Cache, _bf16, _close, _cu, _i32, _np, _table
+from test_gpu_layer_ops import DEV, FMT, Cache, _attend, _bf16, _close, _cu, _i32, _np, _table
 
 pytestmark = pytest.mark.gpu
 
@@ -158,3 +158,54 @@ def test_rmsnorm_infinities_and_nan(H, aligned):
             g = good.cpu().numpy()
             assert np.isnan(codes[~g]).all() and not np.isnan(codes[g]).any()
             assert not out["scales"][~good].any()
+
+
+# ------------------------------------------------------------------ attention, scores of any size
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("rows,kv", [(1, 300), (1, 9000), (6, 700)])
+@pytest.mark.parametrize("size", [-1e33, -1e31, -3e29, -2.0 ** 27, 2.0 ** 27, 2.0 ** 29, 1e31])
+def test_attention_equal_scores_of_any_size(size, rows, kv, fmt):
+    """Equal keys: whatever the size of their score, the weights are equal.  (In
+    log2 units scores reach 1e33 * 64 * 2.)"""
+    rng = np.random.default_rng(rows + kv)
+    block, dim, heads = 64, 64, 4
+    blocks = -(-kv // block)
+    c = Cache(blocks, 1, block, dim, FMT[fmt], rng)
+    one = O.codes(np.full(dim, 96.0) + np.arange(dim) % 8, FMT[fmt])      # 1.5 and a little more, at 2^-6
+    c.codes[0][:] = one
+    c.scale[0][:] = 2.0 ** -6
+    c.scale[1][:] = 2.0 ** -7
+    for i in range(2):
+        c.dev[2 * i].copy_(torch.from_numpy(c.codes[i]))
+        c.dev[2 * i + 1].copy_(torch.from_numpy(c.scale[i]))
+    q = _bf16(rng.uniform(0.9, 1.1, (rows, heads, dim)))
+    s = size * (_np(q) @ (O.values(one, FMT[fmt]) * 2.0 ** -6))             # [rows, heads]
+    ws = torch.zeros(fl.fl_kv8_attention_workspace(rows, 1, heads, 1, dim), dtype=torch.uint8, device=DEV)
+    out, lse = fl.fl_kv8_attention(q.to(DEV), *c.args(), _i32(np.arange(blocks)[None]), _i32([kv]), fmt=FMT[fmt], scale=size,
+                                   return_lse=True, ws=ws)
+    v = O.gather(c.codes[1], c.scale[1], np.arange(blocks), kv, FMT[fmt])[0]
+    got, gl = _np(out), _np(lse)
+    for i in range(rows):
+        n = kv - rows + 1 + i
+        mean, av = v[:n].mean(0), np.abs(v[:n]).mean(0)
+        # the output's rounding, the weights' to f16, the sums' (as in the oracle's tolerance, with exact scores)
+        assert np.all(np.abs(got[i] - mean) <= 2.0 ** -8 * np.abs(mean) + (2.0 ** -11 + 2.0 ** -18) * av), (i, got[i, 0, :4], mean[:4])
+        assert np.all(np.abs(gl[i] - s[i] - np.log(n)) <= (dim + 4) * 2.0 ** -23 * np.abs(s[i]) + 2.0 ** -20)
+    assert fl.fl_int4g_status(ws) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 7])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("log2", [16, 20, 22, 23, 24, 25, 26, 27, 28, 30, 40])
+def test_attention_large_scores(log2, fmt, rows):
+    """Scores that fp32 holds to whole numbers and coarser: outputs stay within
+    what that rounding allows, mantissas in the scales or not."""
+    for i, mantissas in enumerate((False, True)):
+        def scales(rng, shape):
+            return [(2.0 ** rng.integers(-9, -7, shape) * (rng.uniform(1, 2, shape) if mantissas else 1)).astype(np.float32)
+                    for _ in range(2)]
+        out, lse, ref = _attend([(rows, 400), (rows, 131)], 4, 2, 128, 32, fmt, seed=log2 + i, scales=scales,
+                                scale=2.0 ** log2 * (1.3 if i else 1.0))
+        assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+        _close(out, lse, ref)
