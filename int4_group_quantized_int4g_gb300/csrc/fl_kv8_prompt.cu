@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
       if (!ok || s.units < 0) break;
       const int live = s.live[t];
       const bool general = s.general != 0;
-      float a = 0.f;
+      float a = 0.f, far = 1.f;   // what S is times to be a score, as far * a with a <= 1
       if (live > 0) {
         // The warp's 32 rows of q: copied to their places in the tile, kL lanes a
         // row, then there times a power of two a row and the sign of the scale, as
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         }
         a = fabsf(p.scale2) * pow2i(row_exponent(mine)) * pow2i(max(s.ke - code_shift<FMT>(), -126));
         a = fmaxf(a, 1.1754943508222875e-38f);   // (not 0: -inf of a masked column stays -inf)
+        far = fmaxf(a, 1.f), a = fminf(a, 1.f);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[t]);
@@ -440,6 +441,13 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         plain_end = (s.past + r0 / p.group + 1 - pos) >> 6;
         if (p.window) plain_begin = (s.past + min(r0 + 127, s.rows - 1) / p.group + 1 - p.window - pos + 63) >> 6;
       }
+      // S is below 2^24 (2^25 with mantissas).  With a factor of at most 1 a score is
+      // too, and the rounding of its reference, an integer, leaves P within f16.
+      // Scores beyond have lost their fractions in fp32; for them S takes what the
+      // factor has above 1 first, so that all are rounded alike (in one rounding with
+      // the subtraction of the reference, weights of equal scores of 2^26 came out
+      // infinite or 0).
+      const bool any_far = __any_sync(0xffffffffu, far > 1.f);
       float m = -INFINITY, l = 0.f;   // weights are 2^(x - m); the reference m is an integer, about kBias below a maximum
       for (int j = 0; j < 2 * live; ++j, ++js) {
         const uint32_t ts = tmem + lanes + 128 * t + 64 * (js & 1);
@@ -454,11 +462,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // tensor memory, so that no register of the loop is touched: as a branch on
         // the values themselves it cost a sixth (4095-token prompt 220 us, not 184).
         const float4* mt = meta + ((s.meta + (j >> 1)) & 7) * 8 + 4 * (j & 1);   // of 16 tokens each
-        if (general) {
+        if (general || any_far) {
           const float down = rcp_approx(a);
 #pragma unroll 1
           for (int k = 0; k < 8; ++k) {
-            const float mul = mt[k >> 1].x, add = mt[k >> 1].y * down;
+            const float mul = general ? mt[k >> 1].x * far : far, add = general ? mt[k >> 1].y * down : 0.f;
             uint32_t o[8];
             tmem_ld8_issue(ts + 8 * k, o);
             tmem_ld8_wait(o);
@@ -485,10 +493,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
           mx4[i & 1] = max3(mx4[i & 1], x[0][2 * i], x[0][2 * i + 1]);
           mx4[2 + (i & 1)] = max3(mx4[2 + (i & 1)], x[1][2 * i], x[1][2 * i + 1]);
         }
-        const float top = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * a - kBias;
-        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+        const float top = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * a;
+        if (__any_sync(0xffffffffu, top - m > kBias + kSlack)) {
           // a maximum has outgrown its reference: the rows of O and the sum move
-          const float nm = top > m + kSlack ? ceilf(top) : m;
+          const float nm = top - m > kBias + kSlack ? ceilf(top - kBias) : m;
           const float f = nm == m ? 1.f : exp2_approx(m - nm);
           m = nm;
           l *= f;

@@ -163,7 +163,7 @@ def test_rmsnorm_infinities_and_nan(H, aligned):
 # ------------------------------------------------------------------ attention, scores of any size
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("rows,kv", [(1, 300), (1, 9000), (6, 700)])
+@pytest.mark.parametrize("rows,kv", [(1, 300), (1, 9000), (6, 700), (70, 300), (70, 9000)])
 @pytest.mark.parametrize("size", [-1e33, -1e31, -3e29, -2.0 ** 27, 2.0 ** 27, 2.0 ** 29, 1e31])
 def test_attention_equal_scores_of_any_size(size, rows, kv, fmt):
     """Equal keys: whatever the size of their score, the weights are equal.  (In
@@ -195,7 +195,7 @@ def test_attention_equal_scores_of_any_size(size, rows, kv, fmt):
     assert fl.fl_int4g_status(ws) == 0
 
 
-@pytest.mark.parametrize("rows", [1, 7])
+@pytest.mark.parametrize("rows", [1, 7, 90])
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("log2", [16, 20, 22, 23, 24, 25, 26, 27, 28, 30, 40])
 def test_attention_large_scores(log2, fmt, rows):
