@@ -474,9 +474,16 @@ typedef struct fl_kv8_cache {
  *   block_table int32 [B, max_blocks] device
  *   max_q       the largest number of rows of a sequence: an upper bound, which
  *             may be loose, and larger than T
- * A sequence may have no rows; kv_lens[b] below its number of rows is allowed:
- * the first rows then have negative positions (they are not written and see
- * no key). */
+ * A sequence may have no rows; kv_lens[b] below its number of rows is allowed
+ * (a negative one counts as 0): the first rows then have negative positions
+ * (they are not written and see no key).  Rows of no sequence, before cu_q[0] or
+ * from cu_q[B] on, are neither written nor read.
+ * A sequence whose lists name what is not there is left out by the kernels:
+ * cu_q falls, or leaves 0 .. T; more rows than max_q; rows, and a length
+ * past the max_blocks * block tokens of its table.  Nothing is written for it, neither
+ * into the cache nor to its output rows, and FL_ERR_DEVICE_CHECK is recorded in
+ * the status block.  With cu_q NULL, T / B rows a sequence above max_q are an
+ * FL_ERR_ARG of the call. */
 typedef struct fl_kv8_seqs {
   const int32_t* cu_q;
   const int32_t* kv_lens;

@@ -72,18 +72,29 @@ __device__ __forceinline__ float code_value(uint32_t c) {
   return static_cast<float>(static_cast<int8_t>(c));
 }
 
-// The CTA's sequence and block of it: the x-th written block of the batch.
+// A CTA's work: slots [lo, hi) of page `page` of sequence b, from the call's
+// token `row` on.  b is -1 without work.
+struct Block {
+  int b, page, lo, hi, row;
+};
+__device__ __forceinline__ Block block_of(const SeqInfo& q, int block, int b, int j) {
+  const PageRun run = written_pages(q, block);
+  const int page = run.first + j, lo = max(max(q.kv - q.n, 0) - page * block, 0);   // (from the first position written)
+  return {j < run.n ? b : -1, page, lo, min(q.kv - page * block, block), q.start + (page * block + lo - (q.kv - q.n))};
+}
+// The x-th written block of the batch.
 template <int THREADS>
-__device__ __forceinline__ bool find_block(const Seqs& s, int block, int x, int& b, int& j) {
-  b = 0, j = x;
-  if (s.B == 1) return true;
-  __shared__ int scan[THREADS / 32 + 2];
-  int* hit = scan + THREADS / 32;
+__device__ __forceinline__ Block find_block(const Seqs& s, int block, int x) {
+  if (s.B == 1) return block_of(seq_info(s, 0, block), block, 0, x);
+  __shared__ int scan[THREADS / 32];
+  __shared__ Block hit;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) hit[0] = -1;
+  if (tid == 0) hit.b = -1;
   int base = 0;
   for (int c = 0; c < s.B && x >= base; c += THREADS) {
-    const int n = c + tid < s.B ? written_pages(seq_info(s, c + tid, block), block).n : 0;
+    SeqInfo q = {0, 0, 0, false};
+    if (c + tid < s.B) q = seq_info(s, c + tid, block);
+    const int n = written_pages(q, block).n;
     int inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -100,16 +111,11 @@ __device__ __forceinline__ bool find_block(const Seqs& s, int block, int x, int&
       all += scan[w];
     }
     const int mine = base + before + inc - n;
-    if (x >= mine && x < mine + n) {
-      hit[0] = c + tid;
-      hit[1] = x - mine;
-    }
+    if (x >= mine && x < mine + n) hit = block_of(q, block, c + tid, x - mine);
     base += all;
   }
   __syncthreads();
-  b = hit[0];
-  j = hit[1];
-  return b >= 0;
+  return hit;
 }
 
 template <int FMT, int D, int BLK>
@@ -128,22 +134,21 @@ __global__ void __launch_bounds__(ApCfg<FMT, D, BLK>::kThreads) k_kv8_append(con
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int b, j;
-  if (!find_block<kThreads>(p.seqs, BLK, blockIdx.x, b, j)) return;
-  const SeqInfo q = seq_info(p.seqs, b, BLK);
-  const PageRun run = written_pages(q, BLK);
-  if (j >= run.n) return;
-  const int p0 = max(q.kv - q.n, 0);           // first position written
-  const int jb = run.first + j;
-  const int lo = max(p0 - jb * BLK, 0);        // slots [lo, hi) of the block are written
-  const int hi = min(q.kv - jb * BLK, BLK);
+  if (blockIdx.x == gridDim.x - 1) {   // past the last block: records the sequences that are left out
+    if (blockIdx.y == 0 && blockIdx.z == 0)
+      for (int i = tid; i < p.seqs.B; i += kThreads)
+        if (seq_info(p.seqs, i, BLK).bad) set_status(p.status, FL_ERR_DEVICE_CHECK, 53);
+    return;
+  }
+  const Block at = find_block<kThreads>(p.seqs, BLK, blockIdx.x);
+  if (at.b < 0) return;
+  const int lo = at.lo, hi = at.hi;
   const int head = blockIdx.y;
   const bool vals = blockIdx.z != 0;
   const Half h = {vals ? p.v.src : p.k.src, vals ? p.v.stride : p.k.stride, vals ? p.v.dst : p.k.dst,
                   vals ? p.v.scale : p.k.scale};
-  const int page = page_block(p.seqs, b, jb, p.num_blocks);
-  // row of the first written token in the call's tokens
-  const int64_t row0 = static_cast<int64_t>(q.start) + (jb * BLK + lo - (q.kv - q.n));
-  const __nv_bfloat16* src = h.src + row0 * h.stride + head * D;
+  const int page = page_block(p.seqs, at.b, at.page, p.num_blocks);
+  const __nv_bfloat16* src = h.src + at.row * h.stride + head * D;
   const int nv = (hi - lo) * (D / 8);
   uint4 x[kVecs];
   uint32_t top2 = 0;   // the largest magnitudes' bits, of either half of a word
@@ -261,8 +266,8 @@ extern "C" int fl_kv8_append(const void* k, int64_t k_stride, const void* v, int
   // n; so the batch at most the sum of either over its sequences
   long long most = seqs->T / cache->block + 2ll * seqs->B;
   if (most > seqs->T) most = seqs->T;
-  if (most > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(most), cache->kv_heads, 2);
+  if (most > 0x7ffffffell) return FL_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(most) + 1, cache->kv_heads, 2);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->format == FL_KV8_E4M3)
     return cache->head_dim == 64 ? launch_append<FL_KV8_E4M3, 64>(p, cache->block, grid, s)

@@ -19,22 +19,26 @@ struct Seqs {
   int T, B, max_q, max_blocks;
 };
 
-// Query rows [start, start + n) of sequence b and its cache length, clamped
-// to the arrays.
+// Query rows [start, start + n) of sequence b and its cache length.  bad: the
+// lists name rows or tokens that the arrays have not; the sequence is left out
+// (cut to the arrays, its rows would stand at other positions than their own).
 struct SeqInfo {
   int start, n, kv;
+  bool bad;
 };
 __host__ __device__ __forceinline__ SeqInfo seq_info(const Seqs& s, int b, int block) {
   SeqInfo r;
+  int end;
   if (s.cu_q) {
-    r.start = min(max(s.cu_q[b], 0), s.T);
-    r.n = min(max(s.cu_q[b + 1], r.start), s.T) - r.start;
+    r.start = s.cu_q[b], end = s.cu_q[b + 1];
   } else {
-    r.n = s.T / s.B;
-    r.start = b * r.n;
+    r.start = b * (s.T / s.B), end = r.start + s.T / s.B;
   }
-  r.n = min(r.n, s.max_q);
-  r.kv = min(max(s.kv_lens[b], 0), s.max_blocks * block);
+  r.kv = max(s.kv_lens[b], 0);
+  r.bad = r.start < 0 || end < r.start || end > s.T || end - r.start > s.max_q ||
+          (end > r.start && r.kv > s.max_blocks * block);
+  r.n = r.bad ? 0 : end - r.start;
+  if (r.n == 0) r.start = r.kv = 0;
   return r;
 }
 
@@ -222,7 +226,7 @@ inline int kv8_check(const fl_kv8_cache* c, const fl_kv8_seqs* s) {
     return FL_ERR_ARG;
   if (c->num_blocks < 1 || c->kv_heads < 1 || s->T < 1 || s->B < 1 || s->max_q < 1 || s->max_blocks < 1) return FL_ERR_ARG;
   if (c->format != FL_KV8_E4M3 && c->format != FL_KV8_INT8) return FL_ERR_ARG;
-  if (!s->cu_q && s->T % s->B) return FL_ERR_ARG;
+  if (!s->cu_q && (s->T % s->B || s->T / s->B > s->max_q)) return FL_ERR_ARG;
   if ((c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) ||
       (c->head_dim != 64 && c->head_dim != 128))
     return FL_ERR_UNSUPPORTED;

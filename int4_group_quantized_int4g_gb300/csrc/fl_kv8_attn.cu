@@ -198,7 +198,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsCfg<D, NT>::kCtas)
   {
     const Start start =
         find_start<kRowsThreads>(reinterpret_cast<long long*>(smem + C::kJoinOff), p.seqs.B, blockIdx.x, gridDim.x, 1,
-                                 [&](int b) { return seq_work<ROWS>(p, b).units; });
+                                 [&](int b) {
+                                   const SeqWork w = seq_work<ROWS>(p, b);
+                                   if (w.q.bad && blockIdx.x == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 58);
+                                   return w.units;
+                                 });
     if (static_cast<int>(blockIdx.x) >= start.P) return;
     if (tid == 0) {
       Walk<ROWS> walk;

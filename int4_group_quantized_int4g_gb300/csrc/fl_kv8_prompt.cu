@@ -350,7 +350,9 @@ __global__ void __launch_bounds__(kPrThreads, 1)
   }
   if (warp == kPlan && lane == 0) join_items<D>(p, gridDim.x)[blockIdx.x].last = -1;   // until the plan says more
   const Start start = find_start<kPrThreads>(reinterpret_cast<long long*>(smem + C::kStgOff), p.seqs.B, blockIdx.x, gridDim.x, kPromptLeast, [&](int b) {
-    return prompt_work(seq_info(p.seqs, b, p.block), p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
+    const SeqInfo q = seq_info(p.seqs, b, p.block);
+    if (q.bad && blockIdx.x == 0) set_status(p.status, FL_ERR_DEVICE_CHECK, 58);
+    return prompt_work(q, p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
   if (static_cast<int>(blockIdx.x) >= start.P) return;
   if (warp == kIssue0) {

@@ -209,3 +209,73 @@ def test_attention_large_scores(log2, fmt, rows):
                                 scale=2.0 ** log2 * (1.3 if i else 1.0))
         assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
         _close(out, lse, ref)
+
+
+# ------------------------------------------------------------------ lists
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bad", ["length", "falls", "rows", "past"])
+def test_sequences_that_are_left_out_are_reported(bad, many):
+    """A sequence whose lists name what is not there: an error in the status
+    block, nothing written for it, the others right.  (What the kernels take from
+    such lists is checked on the host.)"""
+    rng = np.random.default_rng(7)
+    n = 40 if many else 2                                              # rows: either attention kernel
+    B, block = 300 if bad == "length" and not many else 3, 16
+    q_len, kv = [n] * B, [int(k) for k in rng.integers(n, 60, B)]
+    at = B - 1                                                         # the sequence that is left out
+    table, blocks = _table(rng, kv, block)
+    lens, cu, T, max_q = list(kv), _cu(q_len), B * n, n
+    if bad == "length":
+        lens[at] = table.shape[1] * block + 1
+    elif bad == "falls":
+        cu[at + 1] = cu[at] - 1
+    elif bad == "past":
+        cu[at + 1] = T + 1
+    else:
+        q_len[0], max_q = n - 1, n - 1                                 # (the others have as many rows as allowed)
+        q_len[1], cu = n - 1, _cu([n - 1, n - 1, n])
+    good = [b for b in range(B) if b != at]
+    x = _bf16(rng.standard_normal((T, 2, 64)))
+    c = Cache(blocks, 1, block, 64, O.E4M3, rng)
+    st = torch.zeros(4, dtype=torch.int32, device=DEV)
+    fl.fl_kv8_append(x[:, :1].contiguous().to(DEV), x[:, 1:].contiguous().to(DEV), *c.args(), _i32(table), _i32(lens), cu_q=_i32(cu),
+                     max_q=max_q, status=st)
+    assert fl.fl_int4g_status(st) == 6
+    for i in range(2):
+        for b in good:
+            O.append(_np(x[cu[b]:cu[b + 1], i:i + 1]), c.codes[i], c.scale[i], table[b:b + 1], [lens[b]], [0, cu[b + 1] - cu[b]], O.E4M3)
+    assert c.equal_host()
+    ws = torch.zeros(fl.fl_kv8_attention_workspace(T, B, 2, 1, 64), dtype=torch.uint8, device=DEV)
+    out = torch.full((T, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    _, lse = fl.fl_kv8_attention(x.to(DEV), *c.args(), _i32(table), _i32(lens), cu_q=_i32(cu), max_q=max_q, out=out, return_lse=True, ws=ws)
+    assert fl.fl_int4g_status(ws) == 6
+    for b in good:
+        rows = slice(cu[b], cu[b + 1])
+        _close(out[rows], lse[rows], O.attention(_np(x[rows]), *c.codes, *c.scale, table[b:b + 1], [lens[b]], [0, cu[b + 1] - cu[b]], O.E4M3, 0.125))
+    assert bool((out[cu[at - 1 if bad == "falls" else at] + (n if bad == "falls" else 0):] == 7.0).all())
+
+
+def test_rows_of_no_sequence_are_left_alone():
+    """Rows before the first sequence's and past the last's, as a padded batch
+    has them, without an error; sequences without rows may have any length."""
+    rng = np.random.default_rng(9)
+    cu, kv = [2, 3, 3, 5], [40, 1 << 20, 17]
+    table = np.array([[0, 1, 2], [-1, -1, -1], [3, 4, -1]], np.int32)
+    c = Cache(5, 1, 16, 64, O.INT8, rng)
+    x = _bf16(rng.standard_normal((8, 2, 64)))
+    ws = torch.zeros(fl.fl_kv8_attention_workspace(8, 3, 2, 1, 64), dtype=torch.uint8, device=DEV)
+    out = torch.full((8, 2, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    fl.fl_kv8_append(x[:, :1].contiguous().to(DEV), x[:, 1:].contiguous().to(DEV), *c.args(), _i32(table), _i32(kv), cu_q=_i32(cu),
+                     max_q=4, fmt=O.INT8, status=ws)
+    for i in range(2):
+        for b in (0, 2):
+            O.append(_np(x[cu[b]:cu[b + 1], i:i + 1]), c.codes[i], c.scale[i], table[b:b + 1], [kv[b]], [0, cu[b + 1] - cu[b]], O.INT8)
+    assert c.equal_host()
+    _, lse = fl.fl_kv8_attention(x.to(DEV), *c.args(), _i32(table), _i32(kv), cu_q=_i32(cu), max_q=4, fmt=O.INT8, out=out,
+                                 return_lse=True, ws=ws)
+    assert fl.fl_int4g_status(ws) == 0
+    for b in (0, 2):
+        rows = slice(cu[b], cu[b + 1])
+        _close(out[rows], lse[rows], O.attention(_np(x[rows]), *c.codes, *c.scale, table[b:b + 1], [kv[b]], [0, cu[b + 1] - cu[b]], O.INT8, 0.125))
+    assert bool((out[:2] == 7.0).all()) and bool((out[5:] == 7.0).all())

@@ -45,3 +45,37 @@ def test_pages_of_a_loose_max_q():
     for max_q in (3, 5, 6, 1000, 2 ** 31 - 1):
         r = fl.fl_kv8_test_pages([50, 33], [[3, 1, 4, 0], [7, 2, 5, 6]], 5, 8, 16, 0, cu_q=[0, 3, 5], max_q=max_q)
         assert (r["start"], r["rows"], r["kv"]) == (0, 3, 50) and r["write"] == (2, 2, 0) and r["read"] == (0, 4, 0)
+
+
+# ---------------------------------------------------------------- lists
+
+def test_sequences_that_name_what_is_not_there_are_left_out():
+    """A length past the table, more rows than max_q, lists that fall or leave
+    the call's rows: no row and no page, instead of rows at other positions."""
+    table = [[3, 1], [7, 2], [0, 4]]                                  # room for 32 tokens each
+
+    def seen(lens, cu, b, max_q=None):
+        r = fl.fl_kv8_test_pages(lens, table, 9, 8, 16, b, cu_q=cu, max_q=max_q)
+        return r["rows"], r["kv"], r["write"][1], r["read"][1]
+    good = [20, 32, 5], [0, 3, 7, 9]
+    assert [seen(*good, b) for b in range(3)] == [(3, 20, 1, 2), (4, 32, 1, 2), (2, 5, 1, 1)]
+    left_out = (0, 0, 0, 0)
+    for n in (33, 34, 48, 2 ** 31 - 1):
+        lens = [20, n, 5]
+        assert seen(lens, good[1], 1) == left_out and seen(lens, good[1], 0) == (3, 20, 1, 2) and seen(lens, good[1], 2) == (2, 5, 1, 1)
+    for max_q in (1, 3):
+        assert seen(*good, 1, max_q) == left_out
+    assert seen(*good, 0, 3) == (3, 20, 1, 2) and seen(*good, 1, 4) == (4, 32, 1, 2)
+    for cu in ([0, 3, 2, 9], [0, 3, 10, 10], [0, 3, -1, 9], [0, 3, 2 ** 31 - 1, 9], [0, 3, -2 ** 31, 9]):
+        assert seen(good[0], cu, 1) == left_out and seen(good[0], cu, 0) == (3, 20, 1, 2)
+    assert seen(good[0], [-1, 3, 7, 9], 0) == left_out
+    assert seen([20, -5, 5], good[1], 1) == (4, 0, 0, 0)              # a negative length is no token
+    assert seen([20, 99, 5], [0, 3, 3, 9], 1) == left_out             # (without rows nothing is read anyway)
+
+
+def test_more_rows_a_sequence_than_max_q_is_refused(L):
+    A = ctypes.c_void_p(0x10000)
+    c = fl.FlKv8Cache(k=A, v=A, k_scale=A, v_scale=A, num_blocks=8, block=16, kv_heads=2, head_dim=64, format=0)
+    s = fl.FlKv8Seqs(cu_q=None, kv_lens=A, block_table=A, T=8, B=2, max_q=3, max_blocks=4)
+    assert L.fl_kv8_append(A, 128, A, 128, ctypes.byref(c), ctypes.byref(s), A, None) == 1
+    assert L.fl_kv8_attention(A, 256, 4, ctypes.byref(c), ctypes.byref(s), 0.1, 0, A, 256, None, A, 1 << 30, None) == 1
