@@ -607,6 +607,8 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     c, s, _, _ = _kv8("fl_kv8_append", T, h, d, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_q, max_q, fmt)
     if status is None:
         status = _workspace(256, k.device)
+    elif status.numel() * status.element_size() < 16:
+        _raise("fl_kv8_append", "the status block has 16 bytes")
     _check("fl_kv8_append", lib().fl_kv8_append(kp, ks, vp, vs, c, s, _p(status), _stream()))
 
 

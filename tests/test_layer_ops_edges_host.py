@@ -79,3 +79,59 @@ def test_more_rows_a_sequence_than_max_q_is_refused(L):
     s = fl.FlKv8Seqs(cu_q=None, kv_lens=A, block_table=A, T=8, B=2, max_q=3, max_blocks=4)
     assert L.fl_kv8_append(A, 128, A, 128, ctypes.byref(c), ctypes.byref(s), A, None) == 1
     assert L.fl_kv8_attention(A, 256, 4, ctypes.byref(c), ctypes.byref(s), 0.1, 0, A, 256, None, A, 1 << 30, None) == 1
+
+
+# ---------------------------------------------------------------- binding
+
+class Fake:
+    """A tensor on a GPU, as far as the binding looks at it; nothing is launched."""
+
+    def __init__(self, shape, dtype):
+        import torch
+        self.shape, self.dtype, self.is_cuda, self.device = torch.Size(shape), dtype, True, torch.device("cuda", 0)
+
+    def stride(self):
+        st, n = [], 1
+        for d in reversed(self.shape):
+            st.insert(0, n)
+            n *= d
+        return tuple(st)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library's calls by name, none of them made."""
+    made = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: made.append(name) or 0
+    monkeypatch.setattr(fl, "lib", lambda: Lib())
+    monkeypatch.setattr(fl, "_stream", lambda stream=None: None)
+    return made
+
+
+def test_append_refuses_a_status_that_is_too_small(calls):
+    import torch
+    bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    args = [Fake((2, 1, 64), bf), Fake((2, 1, 64), bf), Fake((4, 1, 16, 64), u8), Fake((4, 1, 16, 64), u8), Fake((4, 1), f32),
+            Fake((4, 1), f32), Fake((2, 2), i32), Fake((2,), i32)]
+    for status in (Fake((1,), i32), Fake((3,), i32), Fake((15,), u8), Fake((0,), u8)):
+        with pytest.raises(ValueError):
+            fl.fl_kv8_append(*args, status=status)
+    assert calls == []
+    for status in (Fake((4,), i32), Fake((16,), u8), Fake((1 << 20,), u8)):
+        fl.fl_kv8_append(*args, status=status)
+    assert calls == ["fl_kv8_append"] * 3
