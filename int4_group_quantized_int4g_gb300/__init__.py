@@ -557,7 +557,7 @@ def fl_rope(q, k, positions, inv_freq, sections=None, halves=True, q_out=None, k
             kop, kos = _tokens(k_out, "k_out")
     psh = positions.shape
     axes = psh[0] if len(psh) == 2 else 1
-    if psh[-1] != T or (sections is not None and len(sections) != axes):
+    if len(psh) not in (1, 2) or psh[-1] != T or (sections is not None and len(sections) != axes):
         _raise("fl_rope", "positions are [n_axes, T], sections [n_axes]")
     _check("fl_rope", lib().fl_rope(qp, qs, Hq, kp, ks, Hk, T, D, 2 * inv_freq.numel(),
                                     FL_ROPE_HALVES if halves else FL_ROPE_PAIRS,

@@ -135,3 +135,23 @@ def test_append_refuses_a_status_that_is_too_small(calls):
     for status in (Fake((4,), i32), Fake((16,), u8), Fake((1 << 20,), u8)):
         fl.fl_kv8_append(*args, status=status)
     assert calls == ["fl_kv8_append"] * 3
+
+
+def test_rope_refuses_positions_of_another_shape(calls):
+    """Positions of three axes of dimensions, or of as many tokens in another
+    order, are not read as if they were one list."""
+    import torch
+    q, f = Fake((6, 2, 64), torch.bfloat16), Fake((32,), torch.float64)
+
+    def turn(shape, **kw):
+        return fl.fl_rope(q, None, Fake(shape, torch.int32), f, q_out=q, **kw)
+    for shape in ((1, 1, 6), (2, 3, 6), (), (5,), (6, 1), (3, 5)):
+        with pytest.raises(ValueError):
+            turn(shape)
+    with pytest.raises(ValueError):
+        turn((2, 6), sections=[10, 10, 12])
+    assert calls == []
+    turn((6,))
+    turn((1, 6))
+    turn((3, 6), sections=[10, 10, 12])
+    assert calls == ["fl_rope"] * 3
