@@ -172,18 +172,25 @@ def _p(t):
 
 
 _WS = {}
+_OUTGROWN = []   # workspaces that a larger one has replaced: a captured graph may hold them
 
 
 def _workspace(nbytes, device):
-    """A zero-filled workspace per (device, stream), grown on demand."""
+    """A zero-filled workspace per (device, stream), grown on demand.  One that
+    is made while the stream is captured is zero-filled by the graph's replay
+    alone, so it serves that one call."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     key = (device.index, raw(device.index) if raw is not None and device.index is not None
            else torch.cuda.current_stream(device).cuda_stream)
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        _WS[key] = buf
+        if torch.cuda.is_current_stream_capturing():
+            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if buf is not None:
+            _OUTGROWN.append(buf)
+            nbytes = max(nbytes, 2 * buf.numel())   # (so that those kept are smaller together than the last)
+        buf = _WS[key] = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
     return buf
 
 
@@ -597,7 +604,8 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     its kv_lens[b] tokens; token j lives in block block_table[b][j // block].
     max_q: at least the rows of every sequence; it may be larger.
     status: the status block to record device-side errors in (an int32 or uint8
-    CUDA tensor of 16 bytes or a workspace; None: this stream's workspace)."""
+    CUDA tensor of 16 bytes or a workspace; None: this stream's workspace, whose
+    status nobody reads)."""
     _torch()
     T, h, d = k.shape
     if v.shape != k.shape:
@@ -665,7 +673,8 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     with window > 0 only the last `window`.  scale: 1 / sqrt(head_dim) by
     default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32).
     ws: a workspace of the caller's, zero-filled before its first use; give one
-    to calls that are captured in a graph."""
+    to calls that are captured in a graph (without one each captured call whose
+    stream has none yet fills its own with zeros at every replay)."""
     torch = _torch()
     T, Hq, d = q.shape
     qp, qs = _tokens(q, "q")

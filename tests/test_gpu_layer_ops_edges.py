@@ -279,3 +279,42 @@ def test_rows_of_no_sequence_are_left_alone():
         rows = slice(cu[b], cu[b + 1])
         _close(out[rows], lse[rows], O.attention(_np(x[rows]), *c.codes, *c.scale, table[b:b + 1], [kv[b]], [0, cu[b + 1] - cu[b]], O.INT8, 0.125))
     assert bool((out[:2] == 7.0).all()) and bool((out[5:] == 7.0).all())
+
+
+# ------------------------------------------------------------------ workspaces of captured calls
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_captured_calls_without_a_workspace(rows):
+    """Two graphs captured on one stream, the second replayed alone; then a larger
+    call on that stream, and the first graph: partials are counted from zero in
+    all of them."""
+    rng = np.random.default_rng(12)
+    kv = 3000
+    c = Cache(-(-kv // 32), 1, 32, 128, O.E4M3, rng)
+    table, lens = _i32(np.arange(-(-kv // 32))[None]), _i32([kv])
+    q = _bf16(rng.standard_normal((rows, 4, 128))).to(DEV)
+    big = torch.zeros((2 * rows + 300, 8, 128), dtype=torch.bfloat16, device=DEV)
+    ref = O.attention(_np(q), *c.codes, *c.scale, [np.arange(-(-kv // 32))], [kv], [0, rows], O.E4M3, 128 ** -0.5)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for warm in (False, True):
+        graphs = []
+        for _ in range(2):
+            if warm:
+                with torch.cuda.stream(s):
+                    fl.fl_kv8_attention(q, *c.args(), table, lens)
+                s.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                out, lse = fl.fl_kv8_attention(q, *c.args(), table, lens, return_lse=True)
+            graphs.append((g, out, lse))
+        for i in (1, 0, 1):
+            graphs[i][1].zero_()
+            graphs[i][0].replay()
+            torch.cuda.synchronize()
+            _close(graphs[i][1], graphs[i][2], ref)
+            with torch.cuda.stream(s):   # outgrows the stream's workspace, and takes what is free
+                fl.fl_kv8_attention(big, *c.args(), table, lens)
+                junk = [torch.full((1 << 22,), 0x5a, dtype=torch.uint8, device=DEV) for _ in range(8)]
+            torch.cuda.synchronize()
+        del junk

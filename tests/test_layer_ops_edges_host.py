@@ -155,3 +155,50 @@ def test_rope_refuses_positions_of_another_shape(calls):
     turn((1, 6))
     turn((3, 6), sections=[10, 10, 12])
     assert calls == ["fl_rope"] * 3
+
+
+def test_workspaces_under_capture_and_outgrown(monkeypatch):
+    """A workspace made while a stream is captured belongs to that call alone
+    (its zeros are written when the graph is replayed, not before); one that a
+    larger replaces stays, for the graphs that were captured with it."""
+    import gc
+    import types
+    import weakref
+
+    import torch
+    made, state = [], {"capturing": False}
+
+    class Buffer:
+        def __init__(self, n):
+            self.n = n
+
+        def numel(self):
+            return self.n
+
+    def zeros(n, **kw):
+        b = Buffer(n)
+        made.append(weakref.ref(b))
+        return b
+    fake = types.SimpleNamespace(zeros=zeros, uint8=torch.uint8, _C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: 77),
+                                 cuda=types.SimpleNamespace(is_current_stream_capturing=lambda: state["capturing"]))
+    monkeypatch.setattr(fl, "_torch", lambda: fake)
+    monkeypatch.setattr(fl, "_WS", {})
+    monkeypatch.setattr(fl, "_OUTGROWN", [])
+    dev = torch.device("cuda", 0)
+    state["capturing"] = True
+    a, b = fl._workspace(1000, dev), fl._workspace(1000, dev)
+    assert a is not b and not fl._WS                       # each has zeros of its own in the graph
+    state["capturing"] = False
+    small = fl._workspace(1000, dev)
+    assert small is not a and fl._workspace(900, dev) is small
+    state["capturing"] = True
+    assert fl._workspace(1000, dev) is small               # zero already: a captured call may use it
+    large = fl._workspace(5000, dev)
+    assert large is not fl._workspace(5000, dev)
+    state["capturing"] = False
+    ref = weakref.ref(small)
+    del small
+    grown = fl._workspace(1001, dev)
+    gc.collect()
+    assert ref() is not None and grown.numel() >= 2000     # (at least twice as large: what stays is bounded)
+    assert fl._workspace(2000, dev) is grown
