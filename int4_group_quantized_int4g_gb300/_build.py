@@ -9,6 +9,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import shutil
 import subprocess
 
@@ -20,6 +21,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfl_int4g.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+# Kernels that split the registers of their launch among their warps, and the
+# count a thread that the split adds up to.  They refuse to be launched with
+# another one, so a compiler that chooses one is found here, when it builds.
+REGISTERS = {"fl_kv8_prompt.cu": ("k_kv8_prompt", 96)}
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
 
@@ -48,6 +53,18 @@ def up_to_date():
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def check_registers(log, kernel, count):
+    """Raises unless every build of `kernel` in a ptxas -v log has `count` registers."""
+    used = {}
+    for name, regs in re.findall(r"Compiling entry function '(\w+)'.*?Used (\d+) registers", log, flags=re.S):
+        if kernel in name:
+            used[name] = int(regs)
+    wrong = {n: r for n, r in used.items() if r != count}
+    if wrong or not used:
+        raise RuntimeError(f"{kernel} has to be compiled to {count} registers a thread, got {wrong or 'no such kernel'}: "
+                           "its split of them among the warps has to be changed with the compiler")
+
+
 def build(force=False, verbose=False):
     if not force and up_to_date():
         return LIB
@@ -56,10 +73,13 @@ def build(force=False, verbose=False):
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        cmd = [nvcc, *ARCH, *FLAGS, "-I", INCLUDE, "-c", src, "-o", obj]
+        split = REGISTERS.get(os.path.basename(src))
+        cmd = [nvcc, *ARCH, *FLAGS, *(["-Xptxas", "-v"] if split else []), "-I", INCLUDE, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        if split:
+            check_registers(r.stdout + r.stderr, *split)
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr)
         return obj

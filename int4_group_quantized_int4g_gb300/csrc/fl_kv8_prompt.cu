@@ -52,7 +52,8 @@ namespace {
 constexpr int kPrThreads = 640;
 constexpr int kConv0 = 8, kIssue0 = 16, kProd = 18, kPlan = 19;   // first warps of the roles
 constexpr int kConvWarps = 4;                         // for keys, and for values
-// Registers a thread: all at launch, then by role (warps 16..19 share one count)
+// Registers a thread: all at launch (the build fails where the compiler takes
+// another count), then by role (warps 16..19 share one count)
 constexpr int kRegs = 96, kRegsSoftmax = 136, kRegsConv = 64, kRegsRest = 80;
 static_assert(256 * kRegsSoftmax + 64 * kConvWarps * kRegsConv + 128 * kRegsRest <= kPrThreads * kRegs, "register pool");
 constexpr int kPromptLeast = 2;                       // fewest units of a CTA

@@ -202,3 +202,22 @@ def test_workspaces_under_capture_and_outgrown(monkeypatch):
     gc.collect()
     assert ref() is not None and grown.numel() >= 2000     # (at least twice as large: what stays is bounded)
     assert fl._workspace(2000, dev) is grown
+
+
+# ---------------------------------------------------------------- build
+
+def test_build_checks_the_registers_of_split_kernels():
+    """A compiler that gives the prompt kernel another register count fails the
+    build, not the calls."""
+    def log(*regs):
+        return "".join(f"ptxas info    : Compiling entry function '_Z{i}k_kv8_promptILi{i}EE' for 'sm_103a'\n"
+                       "ptxas info    : Function properties for x\n    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads\n"
+                       f"ptxas info    : Used {r} registers, used 1 barriers\n" for i, r in enumerate(regs)) + (
+            "ptxas info    : Compiling entry function '_Z9k_kv8_joinILi64EE' for 'sm_103a'\nptxas info    : Used 46 registers\n")
+    _build.check_registers(log(96, 96, 96, 96), "k_kv8_prompt", 96)
+    for bad in (log(96, 88), log(104), log()):
+        with pytest.raises(RuntimeError, match="96 registers"):
+            _build.check_registers(bad, "k_kv8_prompt", 96)
+    for name, (kernel, count) in _build.REGISTERS.items():
+        text = open(_build.CSRC + "/" + name).read()
+        assert f"kRegs = {count}," in text and f"{kernel}(" in text
