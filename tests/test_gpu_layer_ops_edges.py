@@ -318,3 +318,66 @@ def test_captured_calls_without_a_workspace(rows):
                 junk = [torch.full((1 << 22,), 0x5a, dtype=torch.uint8, device=DEV) for _ in range(8)]
             torch.cuda.synchronize()
         del junk
+
+
+# ------------------------------------------------------------------ write, then read
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dim,block", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("signs", [True, False])
+def test_append_then_attend_every_row(signs, dim, block, fmt):
+    """Prompts, chunks and single tokens through the write and the attention,
+    every row of every step against attention over the unrounded keys and
+    values.  Each query points at one token of its own choice, so that a token
+    out of place or a wrong scale shows; with keys of signs alone, which either
+    format holds as they are, to the rounding of a value.  Bounds: a code is off by half a step
+    (e4m3 2^-4 of it, 2^-10 of the scale below; int8 1/2 of the scale) and by as
+    much again of every smaller scale that its block had, which at least
+    double: twice that part in all."""
+    rng = np.random.default_rng(dim)
+    heads, B = 4, 2
+    steps = [([70, 33], 1.0), ([1, 1], 4.0), ([9, 40], 0.3), ([1, 1], 1.0), ([50, 2], 6.0), ([1, 1], 0.1)]
+    total = np.sum([a for a, _ in steps], 0)
+    table, blocks = _table(rng, total, block)
+    c = Cache(blocks, 2, block, dim, FMT[fmt])
+    lens, ks, vs = np.zeros(B, int), [np.zeros((0, 2, dim))] * B, [np.zeros((0, 2, dim))] * B
+
+    def off(x):   # bound of a code's error, [tokens, heads, dim]
+        e = np.zeros_like(x)
+        for j in range(0, len(x), block):
+            for h in range(2):
+                s = O.least_scale(np.abs(x[j:j + block, h]).max(), FMT[fmt])
+                e[j:j + block, h] = 2.0 ** -4 * np.abs(x[j:j + block, h]) + 2 * 2.0 ** -10 * s if fmt == "e4m3" else s
+        return e
+    for q_len, size in steps:
+        new = [[_bf16(rng.choice([-1.0, 1.0], (n, 2, dim)) if signs and not i else
+                      rng.standard_normal((n, 2, dim)) * (1 + rng.random((n, 1, 1))) * (size if i else 1)) for i in range(2)] for n in q_len]
+        lens = lens + q_len
+        for b in range(B):
+            ks[b], vs[b] = np.concatenate([ks[b], _np(new[b][0])]), np.concatenate([vs[b], _np(new[b][1])])
+        q = []
+        for b in range(B):
+            n = q_len[b]
+            aim = [int(rng.integers(0, lens[b] - n + i + 1)) if i % 3 else lens[b] - n + i for i in range(n)]
+            q.append(np.stack([3.0 * 64 / dim * ks[b][a][[0, 0, 1, 1]] for a in aim]))
+        q = _bf16(np.concatenate(q))
+        fl.fl_kv8_append(torch.cat([x[0] for x in new]).to(DEV), torch.cat([x[1] for x in new]).to(DEV), *c.args(), _i32(table),
+                         _i32(lens), cu_q=_i32(_cu(q_len)), max_q=max(q_len), fmt=FMT[fmt])
+        got = _np(fl.fl_kv8_attention(q.to(DEV), *c.args(), _i32(table), _i32(lens), cu_q=_i32(_cu(q_len)), max_q=max(q_len), fmt=FMT[fmt]))
+        at = 0
+        for b in range(B):
+            dk, dv = off(ks[b]) * (not signs), off(vs[b])
+            for i in range(q_len[b]):
+                n = lens[b] - q_len[b] + i + 1
+                for h in range(heads):
+                    x, g = _np(q[at, h]), h // 2
+                    s = ks[b][:n, g] @ x / dim ** 0.5
+                    p = np.exp(s - s.max())
+                    p /= p.sum()
+                    v = vs[b][:n, g]
+                    out = p @ v
+                    more = np.exp(2 * (dk[:n, g] @ np.abs(x)).max() / dim ** 0.5)      # a weight's factor, at most
+                    tol = (more * (p @ dv[:n, g]) + (more - 1) * (p @ np.abs(v - out)) + 2.0 ** -8 * np.abs(out)
+                           + 2.0 ** -10 * (p @ np.abs(v)))
+                    assert np.all(np.abs(got[at, h] - out) <= tol), (b, i, h, np.max(np.abs(got[at, h] - out) / tol))
+                at += 1
