@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     return prompt_work(q, p.group, p.heads, p.window, p.rows_lo, p.rows_hi).per_head * p.heads;
   });
   if (static_cast<int>(blockIdx.x) >= start.P) return;
+  fence_proxy_async();   // the scan's numbers lay where pages are copied to
   if (warp == kIssue0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
