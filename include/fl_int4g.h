@@ -544,7 +544,8 @@ int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim,
  *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum exp s_j
  * fp32 softmax and accumulation; a row with no token gives out 0, lse -inf.
  *   q    bf16 [T, Hq, head_dim], out likewise (token strides in elements,
- *        multiples of 8; out must not overlap q)
+ *        multiples of 8; out must not overlap q: FL_ERR_ARG for the same rows,
+ *        and with equal strides for any row over another)
  *   lse  fp32 [T, Hq] natural logarithm, or NULL
  * Hq % kv_heads == 0.  Results do not depend on timing: partial sums are
  * joined in a fixed order.  A block number outside the cache is not read:

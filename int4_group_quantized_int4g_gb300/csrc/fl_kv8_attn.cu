@@ -746,6 +746,16 @@ AttnPlan attn_plan(int T, int B, int max_q, int group, int head_dim) {
   return a;
 }
 
+// Whether a row of `width` elements of `out` lies over one of q: CTAs read q's
+// rows at any time of the call.  Rows of the two may alternate in one buffer.
+bool rows_overlap(const void* q, int64_t qs, const void* out, int64_t os, int64_t width, int T) {
+  const int64_t d = (reinterpret_cast<intptr_t>(out) - reinterpret_cast<intptr_t>(q)) / 2;   // elements; both are aligned
+  if (d > -width && d < width) return true;
+  if (qs != os || T == 1) return false;
+  const int64_t rest = (d % qs + qs) % qs;   // from the row of q at or before a row of out
+  return (rest < width || qs - rest < width) && d > -(T - 1) * qs - width && d < (T - 1) * qs + width;
+}
+
 }  // namespace
 
 extern "C" int fl_kv8_attention_workspace(int T, int B, int Hq, int kv_heads, int head_dim, size_t* out) {
@@ -778,6 +788,7 @@ extern "C" int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const f
   size_t need = 0;
   fl_kv8_attention_workspace(seqs->T, seqs->B, Hq, cache->kv_heads, cache->head_dim, &need);
   if (ws_bytes < need) return FL_ERR_WORKSPACE;
+  if (rows_overlap(q, q_stride, out, out_stride, width, seqs->T)) return FL_ERR_ARG;
   const AttnPlan plan = attn_plan(seqs->T, seqs->B, seqs->max_q, Hq / cache->kv_heads, cache->head_dim);
   if (plan.rows > 0x7fffffffll) return FL_ERR_UNSUPPORTED;
   CUtensorMap km, vm;

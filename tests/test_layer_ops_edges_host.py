@@ -81,6 +81,31 @@ def test_more_rows_a_sequence_than_max_q_is_refused(L):
     assert L.fl_kv8_attention(A, 256, 4, ctypes.byref(c), ctypes.byref(s), 0.1, 0, A, 256, None, A, 1 << 30, None) == 1
 
 
+def test_attention_refuses_an_output_over_its_queries(L):
+    """q is read at any time of the call.  Rows that alternate in one buffer are
+    not refused (here they fail later: there is no GPU)."""
+    c = fl.FlKv8Cache(k=1 << 20, v=1 << 20, k_scale=1 << 20, v_scale=1 << 20, num_blocks=8, block=16, kv_heads=2, head_dim=64, format=0)
+    base = 1 << 24
+
+    def call(at, qs=256, os=256, T=4):   # the output starts `at` elements behind q; rows of 256
+        s = fl.FlKv8Seqs(cu_q=None, kv_lens=1 << 20, block_table=1 << 20, T=T, B=1, max_q=T, max_blocks=4)
+        return L.fl_kv8_attention(ctypes.c_void_p(base), qs, 4, ctypes.byref(c), ctypes.byref(s), 0.1, 0, ctypes.c_void_p(base + 2 * at), os,
+                                  None, ctypes.c_void_p(1 << 20), 1 << 30, None)
+    for T in (1, 4):
+        for at in (0, 8, -8, 248, -248):
+            assert call(at, T=T) == 1 and call(at, 512, 512, T) == 1 and call(at, 512, 256, T) == 1
+    assert call(256) == 1 and call(3 * 256 + 248) == 1 and call(-3 * 256 - 248) == 1      # over another row
+    assert call(512 + 8, 512, 512) == 1 and call(-512 - 8, 512, 512) == 1 and call(512 + 256 + 8, 512, 512) == 1
+    assert call(1 << 20, T=1 << 15) == 1
+
+    def free(*a, **kw):   # right as far as overlap goes
+        import torch
+        return torch.cuda.is_available() or call(*a, **kw) == 4
+    assert free(4 * 256) and free(-4 * 256) and free(256, T=1)
+    assert free(256, 512, 512) and free(-256, 512, 512) and free(512 + 256, 512, 512) and free(256, 1024, 1024)
+    assert free(1 << 20, 512, 512, T=1 << 11)
+
+
 # ---------------------------------------------------------------- binding
 
 class Fake:
