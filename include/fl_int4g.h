@@ -402,7 +402,8 @@ int fl_moe_int4g_ptrs(const void* x, const float* logits, int M, int H, int E, i
  *   weight  bf16 [H], or NULL for ones
  *   codes   uint8 [M, heads, H] e4m3 bits, or NULL
  *   scales  fp32 [M, heads, H / group] (group 0: [M, heads])
- * y and codes may each be NULL, not both; residual_out NULL: not stored.
+ * y and codes may each be NULL, not both; residual_out NULL: not stored.  y and
+ * residual_out are two places.
  * In place is allowed: y or residual_out may be x or residual (the same
  * pointer and stride).  heads > 1 norms each head of a projection by itself.
  * group is 0, 64, 128 or 256 (H % group == 0); 1 <= H <= 32768.  Rows whose

@@ -360,7 +360,7 @@ extern "C" int fl_rmsnorm(const void* x, int64_t x_stride, const void* residual,
                           const void* weight, float eps, int M, int heads, int H, void* y, int64_t y_stride,
                           void* residual_out, int64_t residual_out_stride, void* codes, float* scales, int group,
                           fl_stream_t stream) {
-  if (!x || (!y && !codes) || (codes != nullptr) != (scales != nullptr)) return FL_ERR_ARG;
+  if (!x || (!y && !codes) || (y && y == residual_out) || (codes != nullptr) != (scales != nullptr)) return FL_ERR_ARG;
   if (M < 1 || heads < 1 || H < 1 || !(eps >= 0.f) || eps > 3.0e38f) return FL_ERR_ARG;
   if (H > 32768) return FL_ERR_UNSUPPORTED;
   if (group != 0 && group != 64 && group != 128 && group != 256) return FL_ERR_UNSUPPORTED;

@@ -106,6 +106,17 @@ def test_attention_refuses_an_output_over_its_queries(L):
     assert free(1 << 20, 512, 512, T=1 << 11)
 
 
+def test_rmsnorm_refuses_one_place_for_both_outputs(L):
+    x, a, b = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21), ctypes.c_void_p(1 << 22)
+
+    def call(y, ro, H=256):
+        return L.fl_rmsnorm(x, H, x, H, None, 1e-6, 1, 1, H, y, H, ro, H, None, None, 0, None)
+    import torch
+    for H in (8, 64, 256):
+        assert call(a, a, H) == 1 and call(x, x, H) == 1
+        assert torch.cuda.is_available() or (call(a, b, H) == 4 and call(x, b, H) == 4 and call(a, None, H) == 4)
+
+
 # ---------------------------------------------------------------- binding
 
 class Fake:
