@@ -454,7 +454,8 @@ int fl_rope(const void* q, int64_t q_stride, int Hq, const void* k, int64_t k_st
  *   k_scale, v_scale  fp32  [num_blocks, kv_heads] device, positive
  * block is 16, 32, 64 or 128; head_dim 64 or 128; num_blocks * kv_heads *
  * block < 2^31; at most 2^30 tokens a sequence and 2^29 rows a call.  A block
- * need not be initialised before its first write. */
+ * need not be initialised before its first write.  Codes of tokens that a row of
+ * the call sees are finite, as the write's are. */
 typedef struct fl_kv8_cache {
   void* k;
   void* v;

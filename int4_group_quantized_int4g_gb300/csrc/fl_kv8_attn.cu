@@ -29,13 +29,13 @@
 // row (then f16 holds it with no loss that matters: 2^-25 of the row's largest
 // value).  x is scaled in fp32.  A row's reference m moves only when a maximum
 // has passed it by 2^8, so p reaches 2^8.  p is rounded to f16 (2^-11, against
-// the output's 2^-9) after a factor 2^6 v_scale / v_ref, v_ref the largest value
+// the output's 2^-8) after a factor 2^6 v_scale / v_ref, v_ref the largest value
 // scale so far, so that it keeps its 11 bits down to 2^-20 of the largest
 // weight; the accumulators are in units of v_ref.  Sums are fp32.
 //
 // Measured: 19 sequences of 65536 tokens, 8 kv heads of 128 (2.55 GB), 435 us,
-// 5.9 TB/s; 48 sequences of 130 to 8100 tokens (390 MB) 78 us in a chain of
-// calls, 5.0 TB/s.  What a call pays beside its bytes is the plan before the
+// 5.9 TB/s; 48 sequences of 130 to 8100 tokens (390 MB) 77 us in a chain of
+// calls, 5.1 TB/s.  What a call pays beside its bytes is the plan before the
 // first copy (5 us: lengths, the CTA's units, its pages) and the joins after the
 // last (4 us).
 #include "fl_kv8_prompt.cuh"

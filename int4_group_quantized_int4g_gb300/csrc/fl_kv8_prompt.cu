@@ -33,11 +33,11 @@
 // and the reference goes into the row's factor or the output.  Mantissas of
 // scales other than powers of two go into S, for the sequences that have them.
 // q as in the kernel for few rows.  P is f16 (2^-11, the output's rounding is
-// 2^-9) times 2^6, and up to 2^14; its fp32 sum is taken before.
+// 2^-8) times 2^6, and up to 2^15; its fp32 sum is taken before.
 //
 // Measured (heads of 128, e4m3): 2048 tokens after 14336, 32 query and 8 kv
-// heads, 398 us, 1.30 PFLOP/s; a prompt of 4095 tokens, 32 kv heads, 186 us, 0.74
-// PFLOP/s; 8192 tokens 621 us, 0.89.  A unit takes 3.3K cycles where its MMAs take
+// heads, 394 us, 1.31 PFLOP/s; a prompt of 4095 tokens, 32 kv heads, 181 us, 0.76
+// PFLOP/s; 8192 tokens 618 us, 0.89 (in a chain of calls).  A unit takes 3.3K cycles where its MMAs take
 // 2.0K: the softmax warps' latency (two a scheduler; more do not fit the
 // registers) is what bounds it.  A segment costs 15K cycles beside its units (q
 // in, the masked units, the output), 4 to 7 of them a CTA in the prompts, and a

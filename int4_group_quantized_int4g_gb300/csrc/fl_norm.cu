@@ -6,10 +6,11 @@
 // One pass over memory: a team of threads holds its row's s in registers
 // between the sum of squares and the scaling, so every input is read once and
 // every output written once (8 to 9 bytes an element with the residual and
-// the codes); the kernel is bound by HBM: 56 us for 8191 rows of 4096 with the
-// residual, bf16 and codes (303 MB, 5.4 TB/s; a plain copy of as many bytes
-// takes 54).  The sums and n stay in fp32 and each output is rounded once; the
-// norm uses s before its rounding to bf16.
+// the codes); the kernel is bound by HBM: 52 us in a chain of calls, 58 from cold
+// caches, for 8191 rows of 4096 with the residual, bf16 and codes (303 MB, 5.8 and
+// 5.2 TB/s; a plain copy of as many bytes from cold caches takes 54).  The sums
+// and n stay in fp32 and each output is rounded once; the norm uses s before its
+// rounding to bf16.
 #include <cuda_fp8.h>
 
 #include "fl_common.cuh"
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 ? 8 : 1) k_r
 
 // The rows of a warp of the kernel below, once one of them has an odd mean: all
 // from the start, in a function of its own, so that the kernel's common path
-// keeps its registers (as a branch in it: heads of 128 27.9 us, not 25.1).
+// keeps its registers (heads of 128: 26.2 us, as a branch in it 27.9).
 template <int LPR>
 __device__ __noinline__ void odd_narrow(const NormParams& p, unsigned row) {
   const unsigned m = row / static_cast<unsigned>(p.heads);
@@ -277,8 +278,9 @@ __device__ __noinline__ void odd_narrow(const NormParams& p, unsigned row) {
 }
 
 // Rows of at most 8 LPR columns (heads of 64 or 128) without codes: LPR lanes
-// hold one, a vector each.  (8191 tokens of 32 heads of 128, 134 MB: 25 us, 5.3
-// TB/s; a warp a row as above, half of it idle, 68 us; two rows a team 24, four 25.)
+// hold one, a vector each.  (8191 tokens of 32 heads of 128, 134 MB: 26 us, 5.2
+// TB/s; a warp a row as above, half of it idle, 68 us; before rows of odd means had
+// their path, two rows a team took 24 and four 25.)
 constexpr int kNarrowThreads = 256;
 template <int LPR>
 __global__ void __launch_bounds__(kNarrowThreads, 8) k_rmsnorm_narrow(const __grid_constant__ NormParams p) {
