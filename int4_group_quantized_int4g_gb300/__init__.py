@@ -602,7 +602,9 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     [blocks, kv_heads, block, head_dim], scales fp32 [blocks, kv_heads]).
     Sequence b's rows cu_q[b] .. cu_q[b+1]-1 (None: T / B each) are the last of
     its kv_lens[b] tokens; token j lives in block block_table[b][j // block].
-    max_q: at least the rows of every sequence; it may be larger.
+    max_q: at least the rows of every sequence; it may be larger.  A sequence
+    whose lists name rows, or tokens past its table, that are not there is left
+    out: nothing of it is written, and the status block says so.
     status: the status block to record device-side errors in (an int32 or uint8
     CUDA tensor of 16 bytes or a workspace; None: this stream's workspace, whose
     status nobody reads)."""
@@ -671,7 +673,9 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     for fl_kv8_append; kv_lens count the tokens already written, the rows of q
     among them).  Row i of a sequence sees the tokens up to its own position,
     with window > 0 only the last `window`.  scale: 1 / sqrt(head_dim) by
-    default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32).
+    default.  Returns out [T, Hq, head_dim], or (out, lse [T, Hq] fp32); out may
+    not lie over q.  Rows of no sequence, or of one that is left out as in
+    fl_kv8_append, are not written.
     ws: a workspace of the caller's, zero-filled before its first use; give one
     to calls that are captured in a graph (without one each captured call whose
     stream has none yet fills its own with zeros at every replay)."""
