@@ -556,6 +556,171 @@ int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const fl_kv8_cache
                      float scale, int window, void* out, int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
                      fl_stream_t stream);
 
+/* ------------------------------------------------- linear in 8-bit integers */
+
+/* Codes in 8 bits of the rows of x (bf16 [M, K], row stride in elements), one
+ * scale a row:
+ *   scale[m] = fp32(max_k |x[m, k]| / 127),
+ *   codes[m, k] = the nearest whole number to x[m, k] / scale[m], ties to even
+ * (of the quotient itself, not of a rounded one); a row of zeros: scale 0,
+ * codes 0; a row with an infinity or NaN: scale NaN, codes 0.
+ *   codes  int8 [M, K] device        scale  fp32 [M] device
+ * M >= 1, K >= 1.  Rows of x that start on 16 bytes are read 16 bytes at a
+ * time, others element by element; pointers need their elements' alignment. */
+int fl_int8_quantize(const void* x, int64_t x_stride, int M, int K, int8_t* codes, float* scale, fl_stream_t stream);
+
+#define FL_OUT_BF16 0
+#define FL_OUT_FP32 1
+
+/* Workspace bytes needed by fl_int8_linear, with x in bf16 or in codes. */
+int fl_int8_linear_workspace(int M, int N, int K, size_t* out);
+
+/* The linear layer with weights and tokens in 8-bit integers, a scale for each
+ * output channel and one for each token (fastllm's --dtype int8; the layers
+ * that do not stand 4 bits, the head above all):
+ *   y[m, n] = (sum_k q[m, k] * w[n, k]) * (s[m] * w_scale[n])
+ *   x        x_scale NULL: bf16 [M, K], rounded to codes q and scales s as
+ *            fl_int8_quantize does, within the call;
+ *            else the codes q, int8 [M, K], and x_scale fp32 [M] their scales
+ *   x_stride row stride of x in elements
+ *   w        int8 [N, K] device, row-major, any of the 256 codes, 16-byte
+ *            aligned         w_scale  fp32 [N] device
+ *   y        [M, N], row stride y_stride in elements; y_type FL_OUT_BF16 or
+ *            FL_OUT_FP32.  y may not lie over an input.
+ * K % 16 == 0, M, N >= 1.  Products and sums are those of the codes: f16
+ * operands hold them exactly, sums are fp32 (exact while they stay below
+ * 2^24), partial sums of a split K are added in a fixed order, so results do
+ * not depend on timing.  M <= 32 streams the weights through mma.sync, larger
+ * M runs on tcgen05.  A row whose scale is NaN gives NaN. */
+int fl_int8_linear(const void* x, int64_t x_stride, const float* x_scale, int M, int K, const int8_t* w,
+                   const float* w_scale, int N, void* y, int64_t y_stride, int y_type, void* ws, size_t ws_bytes,
+                   fl_stream_t stream);
+
+/* ------------------------------------------- from logits to the next token */
+
+/* What a row's logits go through before the choice of a token; every list is
+ * of device memory, one entry a row, and NULL leaves that step out:
+ *   history      int32 [B, history_stride]: the tokens of a row's prompt and
+ *                answer, history_lens int32 [B] of them, the first prompt_lens
+ *                int32 [B] (NULL: none) being the prompt.  Lengths are cut to
+ *                0 .. history_max, and tokens outside the vocabulary (a padding
+ *                of -1) count for nothing
+ *   repetition   fp32: of a token seen in prompt or answer, l > 0 becomes l / r,
+ *                any other l * r
+ *   frequency, presence  fp32: a token that stands c > 0 times in the answer
+ *                loses frequency * c, then presence
+ *   bias_offsets int32 [B+1], bias_ids int32 and bias fp32 [bias_count]: row b
+ *                adds bias[i] to token bias_ids[i], for i from bias_offsets[b]
+ *                to bias_offsets[b+1] - 1 in this order (offsets are cut to
+ *                0 .. bias_count; tokens outside the vocabulary are passed over)
+ *   temperature  fp32: multiplies by fp32(1 / t).  t that is not above 0 counts as 1
+ *                (the choice is the same: greedy)
+ *   allowed      int32 [B, allowed_stride]: token v stays if bit v % 32 of word
+ *                v / 32 is set, else it becomes -inf
+ * in this order, each step one fp32 rounding. */
+typedef struct fl_logits_rules {
+  const int32_t* history;
+  const int32_t* history_lens;
+  const int32_t* prompt_lens;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_offsets;
+  const int32_t* bias_ids;
+  const float* bias;
+  const int32_t* allowed;
+  const float* temperature;
+  int64_t history_stride;
+  int64_t allowed_stride;
+  int history_max;
+  int bias_count;
+} fl_logits_rules;
+
+/* Workspace bytes needed by fl_logits_process. */
+int fl_logits_process_workspace(int B, int V, size_t* out);
+
+/* Applies the rules to logits [B, V] and chooses each row's token:
+ *   logits  type FL_OUT_BF16 or FL_OUT_FP32, row stride in elements
+ *   out     fp32 [B, V], row stride out_stride, the logits after the rules; NULL:
+ *           not stored; may be the logits themselves (fp32, the same stride)
+ *   token   int32 [B]: the largest, the lowest index of equals; -1 where no token
+ *           is left (all -inf); a NaN is not chosen
+ *   lse     fp32 [B]: log sum exp of the row (-inf without a token), or NULL
+ *   logprob fp32 [B]: the token's logit less lse (-inf without a token), or NULL
+ * A row with NaN or +inf has NaN for lse and logprob.  Sums are fp32, in a fixed
+ * order.  1 <= V < 2^30, B >= 1.  Pointers need their elements' alignment; rows
+ * that start on 16 bytes are moved 16 bytes at a time. */
+int fl_logits_process(const void* logits, int64_t logits_stride, int type, int B, int V, const fl_logits_rules* rules,
+                      float* out, int64_t out_stride, int32_t* token, float* lse, float* logprob, void* ws,
+                      size_t ws_bytes, fl_stream_t stream);
+
+/* ------------------------------------------------- pages of the 8-bit cache */
+
+/* The book-keeping of a cache's blocks (pages), on the device: `slots`
+ * sequences, each with a row of the block table and a length, and for each
+ * block the number of sequences that hold it (0: free).
+ *   refs     int32 [num_blocks]     kv_lens  int32 [slots]
+ *   table    int32 [slots, max_blocks], entries behind a sequence's last page
+ *            are not read
+ * block: tokens of a page (16, 32, 64 or 128); slots * max_blocks < 2^31.  What
+ * the lists below name that is not there (a slot, a page) is left out, and
+ * FL_ERR_DEVICE_CHECK recorded in the 16-byte status block that each call takes
+ * (a workspace, where it takes one).  A slot named a second time in one list is left out in the same way. */
+typedef struct fl_kv8_pool {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* kv_lens;
+  int num_blocks;
+  int slots;
+  int max_blocks;
+  int block;
+} fl_kv8_pool;
+
+/* Cuts the sequences seqs[0 .. n) to keep[i] tokens (keep NULL: 0, the sequence
+ * ends): pages behind are given back, their entries become -1.  A sequence that
+ * is not longer stays as it is.  A slot may be named more than once here: the
+ * least keep counts. */
+int fl_kv8_pages_free(const fl_kv8_pool* pool, const int32_t* seqs, const int32_t* keep, int n, void* status,
+                      fl_stream_t stream);
+
+/* Slot children[i] becomes a sequence with the pages and the length of slot
+ * parents[i]; the pages are shared, the last one too.  A child that is not
+ * empty, or that is also a parent in the list, is left out. */
+int fl_kv8_pages_fork(const fl_kv8_pool* pool, const int32_t* parents, const int32_t* children, int n, void* status,
+                      fl_stream_t stream);
+
+/* Makes room for new_tokens[i] tokens at the end of the sequences seqs[0 .. n) and
+ * moves their lengths on.  A sequence takes new pages for tokens past its last
+ * page, and one more if it would write into a page that others hold too: that
+ * page is to be copied, and of the sequences of the list that share it, when
+ * nobody else does, the last keeps the page itself.  The lowest free pages are
+ * given first, in the order of the list, until a sequence's do not suffice: it
+ * and all after it get nothing (the ones left out take no part).
+ *   granted  int32 [n]: 1 with the room made, 0 without
+ *   pairs    int32 [n, 2]: pages to copy (from, to), in list order, before the new
+ *            tokens are written; -1 behind the last     count  int32 [1]
+ * ws: fl_kv8_pages_workspace bytes. */
+int fl_kv8_pages_workspace(const fl_kv8_pool* pool, size_t* out);
+int fl_kv8_pages_alloc(const fl_kv8_pool* pool, const int32_t* seqs, const int32_t* new_tokens, int n, int32_t* granted,
+                       int32_t* pairs, int32_t* count, void* ws, size_t ws_bytes, fl_stream_t stream);
+
+/* Moves the pages in use to the front of the pool: the k-th of those that lie at
+ * or behind their number, in ascending order, goes to the k-th free page before
+ * it.
+ *   table_out, refs_out  as table and refs, after the moves; may be those
+ *   moved    int32 [num_blocks]: where each page is now, -1 for free ones
+ *   pairs    int32 [num_blocks / 2, 2], count int32 [1]: the copies, as above (no
+ *            page is copied from and to, so their order does not matter) */
+int fl_kv8_pages_compact(const fl_kv8_pool* pool, int32_t* table_out, int32_t* refs_out, int32_t* moved, int32_t* pairs,
+                         int32_t* count, void* status, fl_stream_t stream);
+
+/* Copies the pages pairs[i] = (from, to), i < min(*count, max_pairs), codes and
+ * scales, keys and values, in each of `layers` caches (HOST array; all of one
+ * num_blocks, block, kv_heads and head_dim).  No page may be copied to twice or
+ * be both source and target.  Pairs that name no page are left out. */
+int fl_kv8_pages_copy(const fl_kv8_cache* caches, int layers, const int32_t* pairs, const int32_t* count, int max_pairs,
+                      void* status, fl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

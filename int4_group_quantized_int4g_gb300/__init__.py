@@ -28,6 +28,10 @@ __all__ = [
     "FL_KV8_E4M3", "FL_KV8_INT8", "FlKv8Cache", "FlKv8Seqs",
     "fl_rmsnorm", "fl_rope", "fl_kv8_append", "fl_kv8_attention_workspace", "fl_kv8_attention",
     "fl_kv8_test_pages", "fl_kv8_test_units", "fl_kv8_test_plan",
+    "FL_OUT_BF16", "FL_OUT_FP32", "FlLogitsRules", "FlKv8Pool",
+    "fl_int8_quantize", "fl_int8_linear_workspace", "fl_int8_linear", "fl_logits_process_workspace", "fl_logits_process",
+    "fl_kv8_pages_free", "fl_kv8_pages_fork", "fl_kv8_pages_workspace", "fl_kv8_pages_alloc", "fl_kv8_pages_compact",
+    "fl_kv8_pages_copy",
 ]
 
 GROUP = 128
@@ -37,6 +41,8 @@ FL_ROPE_HALVES = 0
 FL_ROPE_PAIRS = 1
 FL_KV8_E4M3 = 0
 FL_KV8_INT8 = 1
+FL_OUT_BF16 = 0
+FL_OUT_FP32 = 1
 
 _c_size_p = ctypes.POINTER(ctypes.c_size_t)
 _vp = ctypes.c_void_p
@@ -61,6 +67,20 @@ class FlKv8Seqs(ctypes.Structure):
     """struct fl_kv8_seqs (the sequences of one call)."""
     _fields_ = [("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("T", ctypes.c_int), ("B", ctypes.c_int), ("max_q", ctypes.c_int), ("max_blocks", ctypes.c_int)]
+
+
+class FlLogitsRules(ctypes.Structure):
+    """struct fl_logits_rules (what logits go through before the choice of a token)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("history", "history_lens", "prompt_lens", "repetition", "frequency", "presence",
+                                               "bias_offsets", "bias_ids", "bias", "allowed", "temperature")] + [
+        ("history_stride", ctypes.c_int64), ("allowed_stride", ctypes.c_int64), ("history_max", ctypes.c_int),
+        ("bias_count", ctypes.c_int)]
+
+
+class FlKv8Pool(ctypes.Structure):
+    """struct fl_kv8_pool (the book-keeping of the 8-bit cache's pages)."""
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_int), ("slots", ctypes.c_int), ("max_blocks", ctypes.c_int), ("block", ctypes.c_int)]
 
 
 # C signatures: name -> (restype, argtypes)
@@ -101,6 +121,17 @@ SIGNATURES = {
     "fl_kv8_test_units": (_i, [_i, _i, _i, _i, _i, ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_test_plan": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_kv8_attention_workspace": (_i, [_i, _i, _i, _i, _i, _c_size_p]),
+    "fl_int8_quantize": (_i, [_vp, _l, _i, _i, _vp, _vp, _vp]),
+    "fl_int8_linear_workspace": (_i, [_i, _i, _i, _c_size_p]),
+    "fl_int8_linear": (_i, [_vp, _l, _vp, _i, _i, _vp, _vp, _i, _vp, _l, _i, _vp, ctypes.c_size_t, _vp]),
+    "fl_logits_process_workspace": (_i, [_i, _i, _c_size_p]),
+    "fl_logits_process": (_i, [_vp, _l, _i, _i, _i, _vp, _vp, _l, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fl_kv8_pages_free": (_i, [_vp, _vp, _vp, _i, _vp, _vp]),
+    "fl_kv8_pages_fork": (_i, [_vp, _vp, _vp, _i, _vp, _vp]),
+    "fl_kv8_pages_workspace": (_i, [_vp, _c_size_p]),
+    "fl_kv8_pages_alloc": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fl_kv8_pages_compact": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fl_kv8_pages_copy": (_i, [_vp, _i, _vp, _vp, _i, _vp, _vp]),
     "fl_kv8_attention": (_i, [_vp, _l, _i, _vp, _vp, ctypes.c_float, _i, _vp, _l, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
@@ -699,3 +730,328 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
            lib().fl_kv8_attention(qp, qs, Hq, c, s, d ** -0.5 if scale is None else scale, window, op, os_,
                                   lse.data_ptr() if return_lse else None, _p(ws), ws.numel(), _stream()))
     return (out, lse) if return_lse else out
+
+
+# -------------------------------------------------- linear in 8-bit integers
+
+def _here(t, name):
+    """The tensor's device, which has to be the current one: its streams take the call."""
+    device = t.device
+    if not t.is_cuda or device.index != _device():
+        _raise(name, f"expected tensors of the current CUDA device, got one on {device}")
+    return device
+
+
+def _matrix(t, dtype, name):
+    """(address, row stride) of [rows, columns] whose columns are packed; the
+    rows may be those of a wider matrix."""
+    st, (n, w) = t.stride(), t.shape
+    if t.dtype is not dtype or not t.is_cuda or (st[1] != 1 and w > 1):
+        _raise(name, f"expected a {dtype} CUDA matrix with packed columns, got {t.dtype}, strides {st}, on {t.device}")
+    return t.data_ptr(), st[0] if n > 1 else w   # (the stride of a single row means nothing)
+
+
+def fl_int8_quantize(x):
+    """(codes int8 [M, K], scale fp32 [M]) of bf16 x [M, K]: scale = fp32(max |x| /
+    127) of the row, code = the nearest whole number to x / scale, ties to even.
+    Zeros: scale 0.  A row with an infinity or NaN: scale NaN, codes 0."""
+    torch = _torch()
+    if x.dim() != 2:
+        _raise("fl_int8_quantize", "x is [M, K]")
+    M, K = x.shape
+    device = _here(x, "fl_int8_quantize")
+    xp, xs = _matrix(x, torch.bfloat16, "x")
+    codes = torch.empty((M, K), dtype=torch.int8, device=device)
+    scale = torch.empty((M,), dtype=torch.float32, device=device)
+    _check("fl_int8_quantize", lib().fl_int8_quantize(xp, xs, M, K, codes.data_ptr(), scale.data_ptr(), _stream()))
+    return codes, scale
+
+
+def fl_int8_linear_workspace(M, N, K):
+    out = ctypes.c_size_t(0)
+    _check("fl_int8_linear_workspace", lib().fl_int8_linear_workspace(M, N, K, ctypes.byref(out)))
+    return out.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_workspace(device_index, M, N, K):
+    return fl_int8_linear_workspace(M, N, K)
+
+
+def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None):
+    """y [M, N] = x . w^T with int8 weights w [N, K], a scale w_scale fp32 [N] for
+    each output channel and one for each token.  x: bf16 [M, K], rounded to 8 bits
+    within the call as by fl_int8_quantize, or with x_scale (fp32 [M]) its codes,
+    int8.  y: bf16 or fp32, out_dtype when y is not given (bf16 by default).  Rows
+    of x and y may be those of wider matrices.  K is a multiple of 16.
+    ws: a workspace of the caller's, zero-filled before its first use (for calls
+    that are captured in a graph, as for fl_kv8_attention)."""
+    torch = _torch()
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        _raise("fl_int8_linear", "x is [M, K], w [N, K]")
+    M, K = x.shape
+    N = w.shape[0]
+    device = _here(x, "fl_int8_linear")
+    sp = None
+    if x_scale is None:
+        xp, xs = _matrix(x, torch.bfloat16, "x")
+    else:
+        xp, xs = _matrix(x, torch.int8, "x")
+        if x_scale.numel() != M:
+            _raise("fl_int8_linear", "x_scale is [M]")
+        sp = _ptr(x_scale, torch.float32, "x_scale")
+    if w_scale.numel() != N:
+        _raise("fl_int8_linear", "w_scale is [N]")
+    wp, tp = _ptr(w, torch.int8, "w"), _ptr(w_scale, torch.float32, "w_scale")
+    if y is None:
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        y = torch.empty((M, N), dtype=out_dtype, device=device)
+        yp, ys = y.data_ptr(), N
+    else:
+        if y.dim() != 2 or y.shape != (M, N) or out_dtype not in (None, y.dtype):
+            _raise("fl_int8_linear", "y is [M, N] of out_dtype")
+        out_dtype = y.dtype
+        yp, ys = _matrix(y, out_dtype, "y")
+    if out_dtype is torch.bfloat16:
+        kind = FL_OUT_BF16
+    elif out_dtype is torch.float32:
+        kind = FL_OUT_FP32
+    else:
+        _raise("fl_int8_linear", "y is bfloat16 or float32")
+    if ws is None:
+        ws = _workspace(_int8_workspace(device.index, M, N, K), device)
+    _check("fl_int8_linear", lib().fl_int8_linear(xp, xs, sp, M, K, wp, tp, N, yp, ys, kind, _p(ws), ws.numel(), _stream()))
+    return y
+
+
+# --------------------------------------------- from logits to the next token
+
+_LOGITS_RULES = struct.Struct("11Pqqii")   # struct fl_logits_rules
+
+
+def fl_logits_process_workspace(B, V):
+    out = ctypes.c_size_t(0)
+    _check("fl_logits_process_workspace", lib().fl_logits_process_workspace(B, V, ctypes.byref(out)))
+    return out.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _logits_workspace(device_index, B, V):
+    return fl_logits_process_workspace(B, V)
+
+
+def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, frequency=None,
+                      presence=None, bias_offsets=None, bias_ids=None, bias=None, allowed=None, temperature=None,
+                      out=None, need_logits=True, ws=None):
+    """Applies a row's rules to bf16 or fp32 logits [B, V] and chooses its token.
+    history int32 [B, longest], of which history_lens [B] count, the first
+    prompt_lens [B] the prompt: repetition [B] divides (or, not above 0,
+    multiplies) tokens of either, frequency [B] times the count and presence [B]
+    are taken off tokens of the answer.  bias_offsets int32 [B + 1], bias_ids
+    int32, bias: what row b adds to which tokens.  temperature [B] divides.  allowed
+    int32 [B, ceil(V / 32)]: tokens without a bit become -inf.  Any may be left out.
+    Returns a dict: "logits" (fp32 [B, V], unless need_logits is False; `out` if
+    given, which may be fp32 logits themselves), "token" (int32 [B], the first of
+    the largest, -1 where none is left), "lse" and "logprob" (fp32 [B]).
+    ws: as for fl_int8_linear."""
+    torch = _torch()
+    if logits.dim() != 2:
+        _raise("fl_logits_process", "logits are [B, V]")
+    B, V = logits.shape
+    device = _here(logits, "fl_logits_process")
+    i32, f32 = torch.int32, torch.float32
+    bf16 = logits.dtype is torch.bfloat16
+    lp, ls = _matrix(logits, torch.bfloat16 if bf16 else f32, "logits")
+
+    def rows(t, dtype, name, n=B):
+        if t is None:
+            return 0
+        if t.numel() != n:
+            _raise("fl_logits_process", f"{name} has {n} entries")
+        return _ptr(t, dtype, name)
+
+    hp, hs, most, ap, stride = 0, 0, 0, 0, 0
+    if (history is None) != (history_lens is None):
+        _raise("fl_logits_process", "history and history_lens go together")
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != B:
+            _raise("fl_logits_process", "history is [B, longest]")
+        hp, hs = _matrix(history, i32, "history")
+        most = history.shape[1]
+        hp = hp or history_lens.data_ptr()   # (an empty tensor has no address, and nothing is read)
+    elif prompt_lens is not None or repetition is not None or frequency is not None or presence is not None:
+        _raise("fl_logits_process", "penalties need a history")
+    if (bias is None) != (bias_ids is None) or (bias is None) != (bias_offsets is None):
+        _raise("fl_logits_process", "bias, bias_ids and bias_offsets go together")
+    count = 0
+    if bias is not None:
+        count = bias.numel()
+        if bias_ids.numel() != count:
+            _raise("fl_logits_process", "bias and bias_ids differ in length")
+        if count == 0:
+            bias = bias_ids = bias_offsets = None
+    if allowed is not None:
+        if allowed.dim() != 2 or allowed.shape[0] != B or allowed.shape[1] < (V + 31) // 32:
+            _raise("fl_logits_process", "allowed is [B, ceil(V / 32)]")
+        ap, stride = _matrix(allowed, i32, "allowed")
+    rules = _LOGITS_RULES.pack(
+        hp, rows(history_lens, i32, "history_lens"), rows(prompt_lens, i32, "prompt_lens"), rows(repetition, f32, "repetition"),
+        rows(frequency, f32, "frequency"), rows(presence, f32, "presence"), rows(bias_offsets, i32, "bias_offsets", B + 1),
+        _ptr(bias_ids, i32, "bias_ids") if bias_ids is not None else 0, _ptr(bias, f32, "bias") if bias is not None else 0,
+        ap, rows(temperature, f32, "temperature"), hs, stride, most, count)
+    got = {}
+    op, os_ = None, 0
+    if out is not None:
+        if out.shape != logits.shape:
+            _raise("fl_logits_process", "out and logits differ in shape")
+        got["logits"] = out
+        op, os_ = _matrix(out, f32, "out")
+    elif need_logits:
+        out = got["logits"] = torch.empty((B, V), dtype=f32, device=device)
+        op, os_ = out.data_ptr(), V
+    token = got["token"] = torch.empty((B,), dtype=i32, device=device)
+    lse, logprob = torch.empty((2, B), dtype=f32, device=device).unbind()
+    got["lse"], got["logprob"] = lse, logprob
+    if ws is None:
+        ws = _workspace(_logits_workspace(device.index, B, V), device)
+    _check("fl_logits_process",
+           lib().fl_logits_process(lp, ls, FL_OUT_BF16 if bf16 else FL_OUT_FP32, B, V, rules, op, os_, token.data_ptr(),
+                                   lse.data_ptr(), logprob.data_ptr(), _p(ws), ws.numel(), _stream()))
+    return got
+
+
+# ------------------------------------------------- pages of the 8-bit cache
+
+_KV8_POOL = struct.Struct("PPPiiii")            # struct fl_kv8_pool
+_KV8_CACHES = struct.Struct("PPPPiiiii4x")      # struct fl_kv8_cache in an array
+
+
+def _pool(where, refs, table, kv_lens, block):
+    i32 = _torch().int32
+    _here(refs, where)
+    if table.dim() != 2 or kv_lens.numel() != table.shape[0]:
+        _raise(where, "table is [slots, max_blocks], kv_lens [slots]")
+    slots, most = table.shape
+    return _KV8_POOL.pack(_ptr(refs, i32, "refs"), _ptr(table, i32, "table"), _ptr(kv_lens, i32, "kv_lens"), refs.numel(),
+                          slots, most, block)
+
+
+def _list(where, t, n, name):
+    if t.numel() != n:
+        _raise(where, f"{name} has {n} entries")
+    return _ptr(t, _TORCH.int32, name) if n else None
+
+
+def _status_block(where, status, device):
+    if status is None:
+        return _workspace(256, device).data_ptr()
+    if status.numel() * status.element_size() < 16:
+        _raise(where, "the status block has 16 bytes")
+    return _p(status)
+
+
+def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None):
+    """Cuts the sequences in slots seqs (int32) to keep (int32, None: 0) tokens and
+    gives their other pages back.  refs int32 [blocks]: the holders of each
+    page; table int32 [slots, max_blocks], kv_lens int32 [slots]: those of
+    fl_kv8_append and fl_kv8_attention; block: tokens of a page.  All three are
+    updated.  status: as for fl_kv8_append."""
+    pool = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
+    n = seqs.numel()
+    _check("fl_kv8_pages_free", lib().fl_kv8_pages_free(
+        pool, _list("fl_kv8_pages_free", seqs, n, "seqs"), _list("fl_kv8_pages_free", keep, n, "keep") if keep is not None else None,
+        n, _status_block("fl_kv8_pages_free", status, refs.device), _stream()))
+
+
+def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=None):
+    """Slot children[i], which is empty, becomes a sequence that shares all pages
+    of slot parents[i] (int32 lists; the rest as in fl_kv8_pages_free).  A child
+    that is not empty, that the list names again or that is a parent in it is left
+    out, and the status block says so."""
+    pool = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
+    n = parents.numel()
+    _check("fl_kv8_pages_fork", lib().fl_kv8_pages_fork(
+        pool, _list("fl_kv8_pages_fork", parents, n, "parents"), _list("fl_kv8_pages_fork", children, n, "children"), n,
+        _status_block("fl_kv8_pages_fork", status, refs.device), _stream()))
+
+
+def fl_kv8_pages_workspace(num_blocks, slots, max_blocks, block):
+    out = ctypes.c_size_t(0)
+    fake = 256   # (the query reads no list)
+    _check("fl_kv8_pages_workspace", lib().fl_kv8_pages_workspace(
+        _KV8_POOL.pack(fake, fake, fake, num_blocks, slots, max_blocks, block), ctypes.byref(out)))
+    return out.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _pages_workspace(num_blocks, slots, max_blocks, block):
+    return fl_kv8_pages_workspace(num_blocks, slots, max_blocks, block)
+
+
+def fl_kv8_pages_alloc(refs, table, kv_lens, seqs, new_tokens, block, ws=None):
+    """Makes room for new_tokens[i] tokens at the end of slot seqs[i] (int32 lists;
+    the rest as in fl_kv8_pages_free) and moves the lengths on.  Returns
+    (granted, pairs, count): granted int32 [n], 0 from the first sequence on for
+    which the free pages do not suffice; pairs int32 [n, 2] and count int32 [1],
+    the pages that fl_kv8_pages_copy has to copy before the new tokens are written:
+    pages that others hold too are not written into.  A slot that the list names
+    again, or whose table is too short, is left out, and the status block at the
+    start of ws says so.  ws: as for fl_int8_linear."""
+    torch = _torch()
+    pool = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
+    n, device = seqs.numel(), refs.device
+    granted = torch.empty((n,), dtype=torch.int32, device=device)
+    pairs = torch.empty((n, 2), dtype=torch.int32, device=device)
+    count = torch.empty((1,), dtype=torch.int32, device=device)
+    if ws is None:
+        ws = _workspace(_pages_workspace(refs.numel(), *table.shape, block), device)
+    _check("fl_kv8_pages_alloc", lib().fl_kv8_pages_alloc(
+        pool, _list("fl_kv8_pages_alloc", seqs, n, "seqs"), _list("fl_kv8_pages_alloc", new_tokens, n, "new_tokens"), n,
+        granted.data_ptr() or None, pairs.data_ptr() or None, count.data_ptr(), _p(ws), ws.numel(), _stream()))
+    return granted, pairs, count
+
+
+def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None):
+    """Moves the pages in use to the front of the pool: the k-th of those behind
+    goes to the k-th free page before.  Returns (table, refs, pairs, count, moved): the
+    table and counts after the moves (the given ones, updated, or with in_place
+    False new ones), the copies for fl_kv8_pages_copy, and int32 [blocks] where each
+    page is now, -1 for free ones."""
+    torch = _torch()
+    pool = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
+    device, blocks = refs.device, refs.numel()
+    if not in_place:
+        table, refs = torch.empty_like(table), torch.empty_like(refs)
+    pairs = torch.empty((blocks // 2, 2), dtype=torch.int32, device=device)
+    count = torch.empty((1,), dtype=torch.int32, device=device)
+    moved = torch.empty((blocks,), dtype=torch.int32, device=device)
+    _check("fl_kv8_pages_compact", lib().fl_kv8_pages_compact(
+        pool, table.data_ptr(), refs.data_ptr(), moved.data_ptr(), pairs.data_ptr() or None, count.data_ptr(),
+        _status_block("fl_kv8_pages_compact", status, device), _stream()))
+    return table, refs, pairs, count, moved
+
+
+def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, status=None):
+    """Copies the pages pairs[i] = (from, to), i < count[0] (int32 [n, 2], [1]; at
+    most n), in every layer's cache: lists of the tensors of fl_kv8_append, all of
+    one shape."""
+    torch = _torch()
+    where, layers = "fl_kv8_pages_copy", len(k_caches)
+    if layers < 1 or len(v_caches) != layers or len(k_scales) != layers or len(v_scales) != layers:
+        _raise(where, "the four lists have a tensor for each layer")
+    shape = k_caches[0].shape
+    if len(shape) != 4:
+        _raise(where, "the caches are [blocks, kv_heads, block, head_dim]")
+    nb, heads, block, dim = shape
+    device = _here(k_caches[0], where)
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    parts = []
+    for k, v, a, b in zip(k_caches, v_caches, k_scales, v_scales):
+        if k.shape != shape or v.shape != shape or a.shape != shape[:2] or b.shape != shape[:2]:
+            _raise(where, "the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
+        parts.append(_KV8_CACHES.pack(_ptr(k, u8, "k_cache"), _ptr(v, u8, "v_cache"), _ptr(a, f32, "k_scale"),
+                                      _ptr(b, f32, "v_scale"), nb, block, heads, dim, 0))
+    n = pairs.numel() // 2
+    _check(where, lib().fl_kv8_pages_copy(b"".join(parts), layers, _list(where, pairs, 2 * n, "pairs"),
+                                          _ptr(count, i32, "count"), n, _status_block(where, status, device), _stream()))
