@@ -177,7 +177,7 @@ Layout layout(int M, int N, int K) {
   l.scale = kScratch;
   l.x = up(l.scale + static_cast<size_t>(M) * 4);
   l.part = up(l.x + rows * width * 2);
-  l.bytes = l.part + up(rows_part_bytes(M <= kRowsMax ? M : kRowsMax));
+  l.bytes = l.part + up(M <= kRowsMax ? rows_part_bytes(M) : gemm_part_bytes(M));
   return l;
 }
 
@@ -221,19 +221,12 @@ extern "C" int fl_int8_linear(const void* x, int64_t x_stride, const float* x_sc
   c.y_stride = y_stride, c.K = K, c.N = N, c.fp32 = y_type == FL_OUT_FP32;
   CodesParams p = {x, x_stride, base + l.x, reinterpret_cast<float*>(base + l.scale), M, K, 0, 0};
   p.vec = x_scale ? aligned(x, 8) && x_stride % 8 == 0 : aligned(x, 16) && x_stride % 8 == 0;
-  const int step = c.fp32 ? 4 : 2;
-  for (int m = 0; m < M; m += kRowsMax) {
-    const int n = M - m < kRowsMax ? M - m : kRowsMax;
-    CodesParams q = p;
-    q.x = static_cast<const uint8_t*>(x) + static_cast<size_t>(m) * x_stride * (x_scale ? 1 : 2);
-    q.scale = p.scale + m, q.M = n, q.tiles = (n + 7) / 8;
-    const int rc = x_scale ? launch_codes<kInCodes, kOutFrags>(q, s) : launch_codes<kInBf16, kOutFrags>(q, s);
-    if (rc != FL_OK) return rc;
-    Call d = c;
-    d.x_scale = c.x_scale + m, d.M = n;
-    d.y = static_cast<uint8_t*>(y) + static_cast<size_t>(m) * y_stride * step;
-    const int rd = rows_launch(d, s);
-    if (rd != FL_OK) return rd;
+  c.M = M, c.y = y;
+  if (M <= kRowsMax) {
+    p.tiles = (M + 7) / 8;
+    const int rc = x_scale ? launch_codes<kInCodes, kOutFrags>(p, s) : launch_codes<kInBf16, kOutFrags>(p, s);
+    return rc != FL_OK ? rc : rows_launch(c, s);
   }
-  return FL_OK;
+  const int rc = x_scale ? launch_codes<kInCodes, kOutRows>(p, s) : launch_codes<kInBf16, kOutRows>(p, s);
+  return rc != FL_OK ? rc : gemm_launch(c, s);
 }

@@ -44,5 +44,7 @@ struct Call {
 
 int rows_launch(const Call& c, cudaStream_t s);
 size_t rows_part_bytes(int M);
+int gemm_launch(const Call& c, cudaStream_t s);
+size_t gemm_part_bytes(int M);
 
 }  // namespace fl8

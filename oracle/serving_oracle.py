@@ -21,8 +21,9 @@ def quantize8(x):
 
 
 def linear8(q, s, w, t):
-    """(y, scale of y): exact sums of the codes, times the scales."""
-    dot = q.astype(np.int64) @ w.astype(np.int64).T
+    """(sums, scales): the codes' sums, whole numbers that float64 holds, and what
+    each is multiplied with."""
+    dot = q.astype(np.float64) @ w.astype(np.float64).T
     return dot, s[:, None] * t[None, :].astype(np.float64)
 
 

@@ -107,7 +107,7 @@ def _linear_check(y, q, s, w, t, K):
     ref = dot * scale
     # sums of whole numbers are exact below 2^24; above, each of the K / 16 steps
     # of a sum (and of joining the parts) rounds by at most a step, 2^-23 of it
-    mag = np.abs(q.astype(np.int64)) @ np.abs(w.cpu().numpy().astype(np.int64)).T
+    mag = np.abs(q.astype(np.float64)) @ np.abs(w.cpu().numpy().astype(np.float64)).T
     tol = np.where(mag < 2 ** 24, 0.0, mag * (K / 16 + 20) * 2.0 ** -23) * np.abs(scale)
     tol += np.abs(ref) * (2.0 ** -8 if y.dtype == torch.bfloat16 else 0) + np.abs(ref) * 3 * 2.0 ** -24 + 1e-44
     assert np.all(np.abs(_np(y) - ref) <= tol), np.max(np.abs(_np(y) - ref) / tol)
@@ -116,7 +116,8 @@ def _linear_check(y, q, s, w, t, K):
 SIZES = [(1, 1, 16), (1, 100, 256), (3, 256, 128), (1, 4096, 1024), (7, 1000, 4096), (8, 300, 144), (9, 257, 1040), (16, 513, 272),
          (17, 128, 2064), (24, 5003, 512), (31, 255, 1024), (32, 700, 4096), (32, 40000, 256), (1, 300, 28672), (2, 40007, 896),
          (33, 127, 128), (40, 1000, 1040), (64, 4096, 512), (100, 129, 16), (128, 2500, 1008), (150, 300, 4096), (257, 777, 400),
-         (301, 1100, 2048), (512, 200, 6144), (700, 2049, 272), (1111, 130, 1024), (2050, 384, 528)]
+         (301, 1100, 2048), (512, 200, 6144), (700, 2049, 272), (1111, 130, 1024), (2050, 384, 528),
+         (2048, 4864, 144), (2304, 4870, 272), (3000, 5000, 256)]   # whole waves of tiles: without a rest, and with one
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
