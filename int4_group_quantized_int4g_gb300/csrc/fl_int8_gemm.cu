@@ -17,36 +17,37 @@
 // a run of weight tiles, for L2), as long as every pair gets a whole one; the
 // rest, from one to two tiles a pair, is cut into equal runs of units, and comes
 // first, so that joining its split tiles hides behind the whole ones.  A split
-// tile is finished warp by warp by the last to take its ticket, the parts added
-// in the pairs' order: results do not depend on timing.
+// tile is finished by the last pair to come, the parts added in the pairs'
+// order: results do not depend on timing.
 //
 // Roles in a CTA:
 //   warp 0        tokens: per unit two TMA boxes of BN / 2 tokens x 64 columns
 //   warp 1        tensor memory; in the pair's first CTA one thread issues the MMAs
 //   warp 2        weights: per unit a TMA box of 128 rows x 128 columns
-//   warps 4..11   codes to f16 into a ring of A tiles in tensor memory; they also wait for
-//                 the unit's tokens, so the issuer probes one barrier a unit,
-//                 the first CTA's, where both CTAs' warps arrive
-//   warps 12..19  accumulator times scales -> y, by TMA stores from a staging tile
-//                 where y's rows start on 16 bytes
+//   warps 3..10   codes to f16 into a ring of A tiles in tensor memory, four warps a
+//                 unit in turn (their arrivals, like the tokens' bytes, are counted on the
+//                 barriers of the first CTA, where the MMAs are issued)
+//   warps 11..18  accumulator times scales -> y, by TMA stores from a staging tile
+//                 where y's rows start and end on 16 bytes
 #include "fl_int8.cuh"
 
 using namespace fl8;
 
 namespace {
 
-constexpr int kThreads = 20 * 32;
-constexpr int kConv0 = 4, kEpi0 = 12;
-constexpr int kRing = 4;                       // stages of every ring
+constexpr int kThreads = 19 * 32;
+constexpr int kConv0 = 3, kEpi0 = 11;
+constexpr int kRing = 4;                       // stages of every ring (even: a slot has one group of converting warps)
 constexpr int kRows = 128;                     // weight rows of a CTA
 constexpr int kXStage = 128 * 64 * 2 * 2;      // 128 tokens x 128 columns f16, as two boxes
 constexpr int kWStage = kRows * kBlockK;
-constexpr int kStaging = 32768;
+constexpr int kStaging = 32768;                // y: 128 rows of 128 tokens in bf16, of 64 in fp32
 constexpr int kWOff = kRing * kXStage;
 constexpr int kStgOff = kWOff + kRing * kWStage;
 constexpr int kScOff = kStgOff + kStaging;     // 256 token scales
 constexpr int kBarOff = kScOff + 1024;
-constexpr int kBars = 6 * kRing + 4;
+constexpr int kBars = 5 * kRing + 4 + 8;
+constexpr int kJoin = kStgOff / 8;             // a warp's room for other pairs' parts, when the rings are done
 constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
 constexpr int kACols = 256;                    // tensor memory: accumulators [0, 256), A ring [256, 512)
@@ -58,7 +59,7 @@ struct Params {
   void* y;
   int64_t y_stride;
   float* part;       // [pair][2][rank] slots of [column][row]
-  int32_t* cnt;      // [pair][rank][warp]
+  int32_t* cnt;      // [pair][rank]
   int32_t* status;
   int M, N, fp32, tma_y;
   int BN, G, mtiles, ntiles;
@@ -117,28 +118,51 @@ __device__ __forceinline__ void commit_pair(uint64_t* bar) {
                "h"(static_cast<uint16_t>(3))
                : "memory");
 }
+// TMA load of a CTA of the pair into its own shared memory, counted on a barrier of
+// either (an address of the cluster's shared memory).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+// The first CTA's barrier at the same place.
+__device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+// Arrives on the first CTA's barrier.  What the arrival hands over lies in tensor
+// memory and is ordered by the fences of tcgen05, so the release need not reach
+// the other SM's threads: at cluster scope it costs 2000 cycles.
+__device__ __forceinline__ void arrive_first(const uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(first_cta(bar)) : "memory");
+}
+// Orders what this thread knows of global memory before its bulk copies from it.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity) { return mbar_wait_cluster(bar, parity); }
 
+template <bool FP32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_int8_gemm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                 const __grid_constant__ CUtensorMap ymap, const Params p) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + kBarOff);   // tokens landed
-  uint64_t* xempty = xfull + kRing;                                // the pair's MMAs have read them
-  uint64_t* wfull = xempty + kRing;                                // weights landed
-  uint64_t* wempty = wfull + kRing;                                // 8 converting warps have read them
-  uint64_t* afull = wempty + kRing;                                // first CTA: both CTAs' A tiles and tokens are there
-  uint64_t* aempty = afull + kRing;                                // the pair's MMAs have read the A tile
-  uint64_t* dfull = aempty + kRing;                                // [2] accumulator final
+  uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + kBarOff);   // first CTA: both CTAs' tokens landed
+  uint64_t* used = xfull + kRing;                                  // the pair's MMAs have read a unit's tokens and A tile
+  uint64_t* wfull = used + kRing;                                  // weights landed
+  uint64_t* wempty = wfull + kRing;                                // 4 converting warps have read them
+  uint64_t* afull = wempty + kRing;                                // first CTA: both CTAs' A tiles are there
+  uint64_t* dfull = afull + kRing;                                 // [2] accumulator final
   uint64_t* dempty = dfull + 2;                                    // [2] first CTA: both CTAs have read it out
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dempty + 2);
-  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  uint64_t* joined = dempty + 2;                                   // [8] other pairs' parts landed, for a warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 8);
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // the epilogue's: a wait ran out; parts to join
   float* sc = reinterpret_cast<float*>(smem + kScOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -148,17 +172,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&xfull[i], 1);
-      mbar_init(&xempty[i], 1);
+      mbar_init(&used[i], 1);
       mbar_init(&wfull[i], 1);
-      mbar_init(&wempty[i], 8);
-      mbar_init(&afull[i], 16);
-      mbar_init(&aempty[i], 1);
+      mbar_init(&wempty[i], 4);
+      mbar_init(&afull[i], 8);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&joined[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&dfull[i], 1);
       mbar_init(&dempty[i], 16);
     }
-    *abort_flag = 0;
+    flags[0] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -187,21 +211,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int m0 = mt * p.BN + rank * half;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
           const int s = i & (kRing - 1);
-          if (i >= kRing && !mbar_wait(&xempty[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
+          if (i >= kRing && !mbar_wait_many(&used[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
             set_status(p.status, FL_ERR_TIMEOUT, 90);
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&xfull[s], bytes);
-          tma_load_2d(smem + s * kXStage, &xmap, g * kBlockK, m0, &xfull[s]);
-          tma_load_2d(smem + s * kXStage + bytes / 2, &xmap, g * kBlockK + 64, m0, &xfull[s]);
+          if (rank == 0) mbar_arrive_expect_tx(&xfull[s], 2 * bytes);
+          const uint32_t bar = first_cta(&xfull[s]);
+          tma_load_pair(smem + s * kXStage, &xmap, g * kBlockK, m0, bar);
+          tma_load_pair(smem + s * kXStage + bytes / 2, &xmap, g * kBlockK + 64, m0, bar);
         }
       }
-      if (!ok) {
-        for (int j = i - kRing; j < i; ++j) mbar_wait(&xfull[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
-      } else {   // (the last arrivals from the pair's MMAs come in before the CTA can end)
-        for (int j = i > kRing ? i - kRing : 0; j < i; ++j) mbar_wait(&xempty[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
-      }
+      if (ok)   // (the last arrivals from the pair's MMAs come in before the CTA can end)
+        for (int j = i > kRing ? i - kRing : 0; j < i; ++j) mbar_wait(&used[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
     }
   } else if (warp == 2) {
     // ---------------- weights: older than the kernel before this one
@@ -215,7 +237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int n0 = nt * 2 * kRows + rank * kRows;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
           const int s = i & (kRing - 1);
-          if (i >= kRing && !mbar_wait(&wempty[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
+          if (i >= kRing && !mbar_wait_many(&wempty[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
             set_status(p.status, FL_ERR_TIMEOUT, 91);
             ok = false;
             break;
@@ -228,27 +250,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = i - kRing; j < i; ++j) mbar_wait(&wfull[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
     }
   } else if (warp == 1) {
-    // ---------------- MMAs of the pair
+    // ---------------- MMAs of the pair.  A probe of a barrier takes this thread 200
+    // cycles even if the phase is over, so the next unit's are asked for before the
+    // MMAs of this one and looked at after them (8190 x 4096 x 11008: 487 to 452 us)
     if (rank == 0 && lane == 0) {
       const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.BN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
       const uint32_t box = static_cast<uint32_t>(p.BN) * 64;   // bytes of 64 columns of this CTA's tokens
       Walk k(p, pair);
       int i = 0, j = 0;   // units, tiles
-      bool ok = true;
+      bool ok = true, there = false;
       while (ok && k.next(p)) {
         const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
-        if (use > 0 && !wait_cluster(&dempty[acc], static_cast<uint32_t>(use - 1) & 1u)) {
+        if (use > 0 && !mbar_wait_many(&dempty[acc], static_cast<uint32_t>(use - 1) & 1u)) {
           set_status(p.status, FL_ERR_TIMEOUT, 92);
           break;
         }
         const uint32_t d = tmem + acc * 128;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (kRing - 1);
-          if (!wait_cluster(&afull[s], static_cast<uint32_t>(i >> 2) & 1u)) {
+          const int s = i & (kRing - 1), s1 = (i + 1) & (kRing - 1);
+          const uint32_t ph = static_cast<uint32_t>(i >> 2) & 1u, ph1 = static_cast<uint32_t>((i + 1) >> 2) & 1u;
+          if (!there && (!mbar_wait_many(&xfull[s], ph) || !mbar_wait_many(&afull[s], ph))) {
             set_status(p.status, FL_ERR_TIMEOUT, 93);
             ok = false;
             break;
           }
+          const bool x1 = mbar_test(&xfull[s1], ph1), a1 = mbar_test(&afull[s1], ph1);
           tc_fence_after();
           const uint32_t b = smem_u32(smem + s * kXStage), a = tmem + kACols + s * 64;
 #pragma unroll
@@ -256,188 +282,262 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mma_pair(d, a + h * 32 + q * 8, sw128_desc(b + h * box + q * 32), idesc, g != k.g0 || h != 0 || q != 0);
-          commit_pair(&xempty[s]);
-          commit_pair(&aempty[s]);
+          commit_pair(&used[s]);
+          there = x1 && a1;
         }
         if (ok) commit_pair(&dfull[acc]);
         ++j;
       }
     }
   } else if (warp >= kConv0 && warp < kEpi0) {
-    // ---------------- codes to f16: thread = (weight row = tensor memory lane, half of the columns)
-    const int q = warp & 3, h = (warp - kConv0) >> 2, r = q * 32 + lane;
-    const uint32_t ta = tmem + kACols + (static_cast<uint32_t>(q * 32) << 16) + h * 32;
+    // ---------------- codes to f16: thread = weight row = tensor memory lane; every other unit
+    const int q = warp & 3, mine = (warp - kConv0) >> 2, r = q * 32 + lane;
+    const uint32_t ta = tmem + kACols + (static_cast<uint32_t>(q * 32) << 16);
+    const uint8_t* rows = smem + kWOff + r * 128;
     Walk k(p, pair);
     int i = 0;
     bool ok = true;
     while (ok && k.next(p)) {
       for (int g = k.g0; g < k.g1; ++g, ++i) {
+        if ((i & 1) != mine) continue;
         const int s = i & (kRing - 1);
         const uint32_t ph = static_cast<uint32_t>(i >> 2) & 1u;
-        if (!mbar_wait(&wfull[s], ph)) {
+        if (!mbar_wait_many(&wfull[s], ph)) {
           set_status(p.status, FL_ERR_TIMEOUT, 94);
           ok = false;
           break;
         }
-        const uint8_t* row = smem + kWOff + s * kWStage + r * 128;
-        uint4 c[4];
+        uint4 c[8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) c[t] = *reinterpret_cast<const uint4*>(row + (((4 * h + t) ^ (r & 7)) << 4));
+        for (int t = 0; t < 8; ++t) c[t] = *reinterpret_cast<const uint4*>(rows + s * kWStage + ((t ^ (r & 7)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[s]);
-        uint32_t o[32];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) codes_f16((&c[t >> 2].x)[t & 3], o[2 * t], o[2 * t + 1]);
-        if (i >= kRing && !mbar_wait(&aempty[s], ph ^ 1u)) {
+        if (i >= kRing && !mbar_wait_many(&used[s], ph ^ 1u)) {
           set_status(p.status, FL_ERR_TIMEOUT, 95);
           ok = false;
           break;
         }
         tc_fence_after();
-        tmem_st32(ta + s * 64, o);
-        tmem_wait_st();
-        if (!mbar_wait(&xfull[s], ph)) {
-          set_status(p.status, FL_ERR_TIMEOUT, 96);
-          ok = false;
-          break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t o[32];
+#pragma unroll
+          for (int t = 0; t < 16; ++t) codes_f16((&c[4 * h + (t >> 2)].x)[t & 3], o[2 * t], o[2 * t + 1]);
+          tmem_st32(ta + s * 64 + h * 32, o);
         }
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_rank0(&afull[s]);
+        if (lane == 0) arrive_first(&afull[s]);
       }
     }
-    if (ok)
-      for (int j = i > kRing ? i - kRing : 0; j < i; ++j) mbar_wait(&aempty[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
-  } else if (warp >= kEpi0) {
-    // ---------------- y: rows q * 32 + lane, one half of the tokens
+    if (ok)   // (both groups see the last arrivals in)
+      for (int j = i > kRing ? i - kRing : 0; j < i; ++j)
+        if ((j & 1) == mine) mbar_wait(&used[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
+  } else {
+    // ---------------- y: weight rows 32q .. 32q + 31, half of each round's tokens.  Tensor
+    // memory is read in mma's fragments (lane: rows g, g + 8, .. of 32, tokens 2c and
+    // 2c + 1), which stmatrix turns into rows of y; the staging tile has TMA's 128-byte
+    // swizzle, so both sides of it are free of bank conflicts.
+    constexpr int kRound = FP32 ? 64 : 128;          // tokens of a staging tile
+    constexpr int kChunks = kRound / 32;             // 16 tokens each, of a warp and round
     pdl_wait();
-    const int e = warp - kEpi0, q = warp & 3, h = e >> 2, r = q * 32 + lane, tid = threadIdx.x - kEpi0 * 32;
+    const int e = warp - kEpi0, q = warp & 3, h = e >> 2, tid = threadIdx.x - kEpi0 * 32;
+    const int g = lane >> 2, c2 = 2 * (lane & 3);
     const uint32_t quad = static_cast<uint32_t>(q * 32) << 16;
+    uint8_t* st = smem + kStgOff;
     Walk k(p, pair);
     for (int j = 0; k.next(p); ++j) {
       const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
       int nt, mt;
       place(p, k.tile, nt, mt);
-      const int n = nt * 2 * kRows + rank * kRows + r, m0 = mt * p.BN;
+      const int n0 = nt * 2 * kRows + rank * kRows, m0 = mt * p.BN;
+      const int T = k.tile - p.waves * p.P;          // of a split tile, whose pairs are cf .. cl
+      const int cf = k.split ? pair_of(T * p.G, p.U, p.P) : 0, cl = k.split ? pair_of((T + 1) * p.G - 1, p.U, p.P) : 0;
+      int32_t* cnt = p.cnt + cf * 2 + rank;
       named_bar(1, 256);   // (the scales of the tile before have been used)
       if (tid < p.BN) sc[tid] = m0 + tid < p.M ? p.x_scale[m0 + tid] : 0.f;
-      const float ts = n < p.N ? __ldg(p.w_scale + n) : 0.f;
-      if (!mbar_wait(&dfull[acc], static_cast<uint32_t>(use) & 1u)) *abort_flag = 1;
+      float ts[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + q * 32 + i * 8 + g;
+        ts[i] = n < p.N ? __ldg(p.w_scale + n) : 0.f;
+      }
+      if (!mbar_wait(&dfull[acc], static_cast<uint32_t>(use) & 1u)) flags[0] = 1;
+      if (tid == 0) flags[1] = k.split ? ld_acquire_gpu(cnt) == cl - cf : 1;   // the others of a split tile have all come
       named_bar(1, 256);
-      if (*reinterpret_cast<volatile int*>(abort_flag)) {
+      if (flags[0]) {
         set_status(p.status, FL_ERR_TIMEOUT, 97);
         break;
       }
+      const bool own = flags[1] != 0;
       tc_fence_after();
       const uint32_t d = tmem + acc * 128 + quad;
+      auto issue = [&](int col, uint32_t (&u)[16]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=r"(u[8 * i]), "=r"(u[8 * i + 1]), "=r"(u[8 * i + 2]), "=r"(u[8 * i + 3]), "=r"(u[8 * i + 4]), "=r"(u[8 * i + 5]),
+                         "=r"(u[8 * i + 6]), "=r"(u[8 * i + 7])
+                       : "r"(d + (static_cast<uint32_t>(16 * i) << 16) + col));
+      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_rank0(&dempty[acc]);
+        if (lane == 0) arrive_first(&dempty[acc]);
       };
-      auto store16 = [&](int col, const float (&v)[16]) {   // without staging
-        if (n >= p.N) return;
-#pragma unroll
-        for (int t = 0; t < 16; ++t) {
-          if (m0 + col + t >= p.M) break;
-          const float f = v[t] * __fmul_rn(sc[col + t], ts);
-          const size_t at = static_cast<size_t>(m0 + col + t) * p.y_stride + n;
-          if (p.fp32)
-            static_cast<float*>(p.y)[at] = f;
-          else
-            static_cast<__nv_bfloat16*>(p.y)[at] = __float2bfloat16_rn(f);
-        }
+      const int bytes = p.BN * 64;                   // of a warp's part of a split tile
+      auto slot = [&](int c) {                       // [chunk][4][lane] of 16 bytes
+        const int which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
+        return reinterpret_cast<float4*>(p.part) + ((static_cast<size_t>(2 * c + which) * 2 + rank) * 8 + e) * (bytes / 16) + lane;
       };
-      auto load16 = [&](int col, float (&v)[16]) {
-        uint32_t u[16];
-        tmem_ld16_issue(d + col, u);
-        tmem_ld_wait(u);
-#pragma unroll
-        for (int t = 0; t < 16; ++t) v[t] = __uint_as_float(u[t]);
-      };
-      const int mine = p.BN / 2, c0 = h * mine;   // this warp's columns, without staging
-      if (!k.split && p.tma_y) {
-        const int round = p.fp32 ? 64 : 128;      // tokens of a staging tile
-        for (int t0 = 0; t0 < p.BN; t0 += round) {
-          const int n_t = min(round, p.BN - t0), lt = h * (n_t / 2);
+      bool room = false;
+      if (!own) {
+        float4* dst = slot(pair);
+        for (int t0 = 0; t0 < p.BN; t0 += kRound) {
+          const int n_t = min(kRound, p.BN - t0), count = n_t / 2, from = t0 + h * count;
 #pragma unroll 1
-          for (int col = 0; col < n_t / 2; col += 16) {
-            float v[16];
-            load16(t0 + lt + col, v);
-            uint8_t* st = smem + kStgOff;
+          for (int ch = 0; 16 * ch < count; ++ch) {
+            uint32_t u[16];
+            issue(from + 16 * ch, u);
+            tmem_ld_wait(u);
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              const float f = v[t] * __fmul_rn(sc[t0 + lt + col + t], ts);
-              const int at = (lt + col + t) * kRows + r;
-              if (p.fp32)
-                reinterpret_cast<float*>(st)[at] = f;
-              else
-                reinterpret_cast<__nv_bfloat16*>(st)[at] = __float2bfloat16_rn(f);
+            for (int i = 0; i < 4; ++i)
+              __stcg(dst + ((t0 / 32 + ch) * 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                                                      __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
+          }
+        }
+        release();
+        named_bar(1, 256);
+        if (tid == 0) flags[1] = atom_add_acq_rel_gpu(cnt, 1) == cl - cf;
+        named_bar(1, 256);
+        if (!flags[1]) continue;
+      }
+      if (k.split) {
+        if (tid == 0) *cnt = 0;
+        // at the CTA's last tile the rings are empty and take the parts, all in flight at once
+        const int others = cl - cf + 1 - own;
+        room = k.u >= k.u1 && k.w >= p.waves && others * bytes <= kJoin;
+        if (room) {
+          if (lane == 0) {
+            fence_proxy_async_all();
+            mbar_arrive_expect_tx(&joined[e], static_cast<uint32_t>(others * bytes));
+            for (int c = cf, o = 0; c <= cl; ++c)
+              if (!(own && c == pair)) bulk_g2s(smem + e * kJoin + bytes * o++, slot(c) - lane, bytes, &joined[e]);
+          }
+          __syncwarp();
+          if (!mbar_wait(&joined[e], 0)) set_status(p.status, FL_ERR_TIMEOUT, 98);
+        }
+      }
+      for (int t0 = 0; t0 < p.BN; t0 += kRound) {
+        const int n_t = min(kRound, p.BN - t0), count = n_t / 2, from = t0 + h * count;
+        uint32_t held[32];
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (16 * ch < count) {
+            uint32_t u[16];
+            if (own) {
+              issue(from + 16 * ch, u);
+              tmem_ld_wait(u);
+            }
+            if (k.split) {
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0.f;
+              int o = 0;
+#pragma unroll 1
+              for (int c = cf; c <= cl; ++c) {   // (the pairs' order)
+                if (own && c == pair) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(u[i]);
+                  continue;
+                }
+                float4 f[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int at = ((t0 / 32 + ch) * 4 + i) * 32;
+                  f[i] = room ? *reinterpret_cast<const float4*>(smem + e * kJoin + bytes * o + (at + lane) * 16) : __ldcg(slot(c) + at);
+                }
+                ++o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * i] += f[i].x, v[4 * i + 1] += f[i].y, v[4 * i + 2] += f[i].z, v[4 * i + 3] += f[i].w;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
+            }
+            // u[8 i + 4 b + 2 r + k]: row 16 i + 8 r + g, token 8 b + c2 + k of the chunk
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const float2 s2 = *reinterpret_cast<const float2*>(sc + from + 16 * ch + 8 * b + c2);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = 8 * (i >> 1) + 4 * b + 2 * (i & 1);
+                const float f0 = __uint_as_float(u[at]) * __fmul_rn(s2.x, ts[i]), f1 = __uint_as_float(u[at + 1]) * __fmul_rn(s2.y, ts[i]);
+                if constexpr (FP32) {
+                  held[16 * ch + at] = __float_as_uint(f0), held[16 * ch + at + 1] = __float_as_uint(f1);
+                } else {
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(f0, f1);
+                  held[8 * ch + 4 * b + i] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+              }
             }
           }
-          if (t0 + round >= p.BN) release();
-          fence_proxy_async();
-          named_bar(1, 256);
-          if (e == 0 && lane == 0) {
-            for (int t = 0; t < n_t && m0 + t0 + t < p.M && n < p.N; t += 32)   // (n: the tile's first row here)
-              tma_store_2d(&ymap, smem + kStgOff + t * kRows * (p.fp32 ? 4 : 2), nt * 2 * kRows + rank * kRows, m0 + t0 + t);
-            bulk_commit();
-            bulk_wait_read0();
+        }
+        if (own && t0 + kRound >= p.BN) release();
+        if (tid == 0) bulk_wait_read0();   // the round before has left the staging tile
+        named_bar(1, 256);
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (16 * ch < count) {
+            const int lt = h * count + 16 * ch;   // token of the round
+            if constexpr (FP32) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int tok = lt + 8 * ((i >> 2) & 1) + c2 + (i & 1), n = 16 * (i >> 3) + 8 * ((i >> 1) & 1) + g;
+                *reinterpret_cast<uint32_t*>(st + q * 8192 + tok * 128 + (((n >> 2) ^ (tok & 7)) << 4) + (n & 3) * 4) = held[16 * ch + i];
+              }
+            } else {
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int tok = lt + 8 * b + (lane & 7), n8 = (q & 1) * 4 + (lane >> 3);
+                const uint32_t* r = held + 8 * ch + 4 * b;
+                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 smem_u32(st + (q >> 1) * 16384 + tok * 128 + ((n8 ^ (tok & 7)) << 4))),
+                             "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                             : "memory");
+              }
+            }
           }
+        }
+        fence_proxy_async();
+        named_bar(1, 256);
+        if (p.tma_y) {
+          if (tid == 0) {
+            constexpr int kWide = FP32 ? 32 : 64, kSlab = kRound * 128;   // rows and bytes of 128-byte columns of the tile
+            for (int t = 0; t < n_t && m0 + t0 + t < p.M; t += 32)
+#pragma unroll 1
+              for (int w = 0; w < kRows / kWide && n0 + w * kWide < p.N; ++w)
+                tma_store_2d(&ymap, st + w * kSlab + t * 128, n0 + w * kWide, m0 + t0 + t);
+            bulk_commit();
+          }
+        } else {   // rows of y that do not start on 16 bytes: element by element, a warp a token
+          for (int tok = e; tok < n_t && m0 + t0 + tok < p.M; tok += 8)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int n = 32 * w + lane;
+              const size_t at = static_cast<size_t>(m0 + t0 + tok) * p.y_stride + n0 + n;
+              if (n0 + n >= p.N) continue;
+              if constexpr (FP32)
+                static_cast<float*>(p.y)[at] = *reinterpret_cast<const float*>(st + w * 8192 + tok * 128 + (((lane >> 2) ^ (tok & 7)) << 4) + (lane & 3) * 4);
+              else
+                static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(
+                    st + (n >> 6) * 16384 + tok * 128 + ((((n & 63) >> 3) ^ (tok & 7)) << 4) + (n & 7) * 2);
+            }
           named_bar(1, 256);
         }
-        continue;
-      }
-      if (!k.split) {
-#pragma unroll 1
-        for (int col = c0; col < c0 + mine; col += 16) {
-          float v[16];
-          load16(col, v);
-          if (col + 16 >= c0 + mine) release();
-          store16(col, v);
-        }
-        continue;
-      }
-      // a part of a split tile: pairs cf .. cl, added in their order by the last
-      const int T = k.tile - p.waves * p.P;
-      const int cf = pair_of(T * p.G, p.U, p.P), cl = pair_of((T + 1) * p.G - 1, p.U, p.P);
-      auto slot = [&](int c) {
-        const int which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
-        return p.part + (static_cast<size_t>(2 * c + which) * 2 + rank) * kRows * p.BN + r;
-      };
-      {
-        float* dst = slot(pair);
-#pragma unroll 1
-        for (int col = c0; col < c0 + mine; col += 16) {
-          float v[16];
-          load16(col, v);
-          if (col + 16 >= c0 + mine) release();
-#pragma unroll
-          for (int t = 0; t < 16; ++t) __stcg(dst + static_cast<size_t>(col + t) * kRows, v[t]);
-        }
-      }
-      __syncwarp();
-      int last = 0;
-      int32_t* cnt = p.cnt + (cf * 2 + rank) * 8 + e;
-      if (lane == 0) last = atom_add_acq_rel_gpu(cnt, 1) == cl - cf;
-      last = __shfl_sync(0xffffffffu, last, 0);
-      if (!last) continue;
-      if (lane == 0) *cnt = 0;
-      __syncwarp();
-#pragma unroll 1
-      for (int col = c0; col < c0 + mine; col += 16) {
-        float v[16];
-#pragma unroll
-        for (int t = 0; t < 16; ++t) v[t] = 0.f;
-        for (int c = cf; c <= cl; ++c) {
-          const float* src = slot(c) + static_cast<size_t>(col) * kRows;
-#pragma unroll
-          for (int t = 0; t < 16; ++t) v[t] += __ldcg(src + t * kRows);
-        }
-        store16(col, v);
       }
     }
-    if (e == 0 && lane == 0) bulk_wait0();
+    if (tid == 0) bulk_wait0();
   }
   tc_fence_before();
   __syncwarp();
@@ -506,13 +606,14 @@ int gemm_launch(const Call& c, cudaStream_t s) {
       return FL_ERR_CUDA;
   }
   const size_t size = c.fp32 ? 4 : 2;
-  p.tma_y = flh::aligned16(c.y) && c.y_stride * size % 16 == 0;
+  // (a swizzled store ends at whole 16 bytes: past a ragged N it would write into what lies beside y)
+  p.tma_y = flh::aligned16(c.y) && c.y_stride * size % 16 == 0 && c.N * size % 16 == 0;
   memset(&ymap, 0, sizeof(ymap));
   if (p.tma_y) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.N), static_cast<cuuint64_t>(c.M)}, strides[1] = {static_cast<cuuint64_t>(c.y_stride) * size};
-    const cuuint32_t box[2] = {kRows, 32};
+    const cuuint32_t box[2] = {c.fp32 ? 32u : 64u, 32};
     if (enc(&ymap, c.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.y, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
         CUDA_SUCCESS)
       return FL_ERR_CUDA;
   }
@@ -520,13 +621,14 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !ready[dev]) {
-    if (cudaFuncSetAttribute(k_int8_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_int8_gemm<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaFuncSetAttribute(k_int8_gemm<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
       cudaGetLastError();
       return FL_ERR_CUDA;
     }
     ready[dev] = true;
   }
-  return flh::launch_early(k_int8_gemm, dim3(2 * p.P), dim3(kThreads), kSmem, s, wmap, xmap, ymap, p);
+  return flh::launch_early(c.fp32 ? k_int8_gemm<true> : k_int8_gemm<false>, dim3(2 * p.P), dim3(kThreads), kSmem, s, wmap, xmap, ymap, p);
 }
 
 }  // namespace fl8
