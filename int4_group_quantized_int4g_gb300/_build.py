@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # Kernels that split the registers of their launch among their warps, and the
 # count a thread that the split adds up to.  They refuse to be launched with
 # another one, so a compiler that chooses one is found here, when it builds.
-REGISTERS = {"fl_kv8_prompt.cu": ("k_kv8_prompt", 96)}
+REGISTERS = {"fl_kv8_prompt.cu": ("k_kv8_prompt", 96), "fl_int8_gemm.cu": ("k_int8_gemm", 96)}
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 
 

@@ -24,10 +24,10 @@
 //   warp 0        tokens: per unit two TMA boxes of BN / 2 tokens x 64 columns
 //   warp 1        tensor memory; in the pair's first CTA one thread issues the MMAs
 //   warp 2        weights: per unit a TMA box of 128 rows x 128 columns
-//   warps 3..10   codes to f16 into a ring of A tiles in tensor memory, four warps a
+//   warps 4..11   codes to f16 into a ring of A tiles in tensor memory, four warps a
 //                 unit in turn (their arrivals, like the tokens' bytes, are counted on the
 //                 barriers of the first CTA, where the MMAs are issued)
-//   warps 11..18  accumulator times scales -> y, by TMA stores from a staging tile
+//   warps 12..19  accumulator times scales -> y, by TMA stores from a staging tile
 //                 where y's rows start and end on 16 bytes
 #include "fl_int8.cuh"
 
@@ -35,18 +35,24 @@ using namespace fl8;
 
 namespace {
 
-constexpr int kThreads = 19 * 32;
-constexpr int kConv0 = 3, kEpi0 = 11;
-constexpr int kRing = 4;                       // stages of every ring (even: a slot has one group of converting warps)
+constexpr int kThreads = 20 * 32;
+constexpr int kConv0 = 4, kEpi0 = 12;
+// Registers a thread: of the launch, and of the producers and the issuer, the
+// converting warps and the epilogue (which spills its sums with 96).
+constexpr int kRegs = 96, kRegsIo = 64, kRegsConv = 80, kRegsEpi = 128;
+static_assert(4 * kRegsIo + 8 * kRegsConv + 8 * kRegsEpi <= 20 * kRegs, "the split draws on the launch's registers");
+constexpr int kRing = 4;                       // weight stages and A tiles (even: a slot has one group of converting warps)
+constexpr int kXRing = 8;                      // token stages, at most
 constexpr int kRows = 128;                     // weight rows of a CTA
-constexpr int kXStage = 128 * 64 * 2 * 2;      // 128 tokens x 128 columns f16, as two boxes
+constexpr int kXBytes = 131072;                // token stages: BN / 2 tokens x 128 columns f16 each, as two boxes
 constexpr int kWStage = kRows * kBlockK;
-constexpr int kStaging = 32768;                // y: 128 rows of 128 tokens in bf16, of 64 in fp32
-constexpr int kWOff = kRing * kXStage;
+constexpr int kStaging = 32768;                // y: 4 KB a warp of the epilogue
+constexpr int kWOff = kXBytes;
 constexpr int kStgOff = kWOff + kRing * kWStage;
 constexpr int kScOff = kStgOff + kStaging;     // 256 token scales
-constexpr int kBarOff = kScOff + 1024;
-constexpr int kBars = 5 * kRing + 4 + 8;
+constexpr int kSlotOff = kScOff + 1024;        // a split tile's parts
+constexpr int kBarOff = kSlotOff + 512;
+constexpr int kBars = 2 * kXRing + 4 * kRing + 4 + 8;
 constexpr int kJoin = kStgOff / 8;             // a warp's room for other pairs' parts, when the rings are done
 constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
@@ -63,6 +69,7 @@ struct Params {
   int32_t* status;
   int M, N, fp32, tma_y;
   int BN, G, mtiles, ntiles;
+  int xring;         // token stages
   int P, waves, U;   // pairs, whole tiles of each, units of the rest
 };
 
@@ -133,11 +140,23 @@ __device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
   return a;
 }
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Arrives on the first CTA's barrier.  What the arrival hands over lies in tensor
 // memory and is ordered by the fences of tcgen05, so the release need not reach
 // the other SM's threads: at cluster scope it costs 2000 cycles.
 __device__ __forceinline__ void arrive_first(const uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(first_cta(bar)) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 // Orders what this thread knows of global memory before its bulk copies from it.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
@@ -154,28 +173,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + kBarOff);   // first CTA: both CTAs' tokens landed
-  uint64_t* used = xfull + kRing;                                  // the pair's MMAs have read a unit's tokens and A tile
-  uint64_t* wfull = used + kRing;                                  // weights landed
+  uint64_t* xempty = xfull + kXRing;                               // the pair's MMAs have read them
+  uint64_t* wfull = xempty + kXRing;                                // weights landed
   uint64_t* wempty = wfull + kRing;                                // 4 converting warps have read them
   uint64_t* afull = wempty + kRing;                                // first CTA: both CTAs' A tiles are there
-  uint64_t* dfull = afull + kRing;                                 // [2] accumulator final
+  uint64_t* aempty = afull + kRing;                                // the pair's MMAs have read the A tile
+  uint64_t* dfull = aempty + kRing;                                // [2] accumulator final
   uint64_t* dempty = dfull + 2;                                    // [2] first CTA: both CTAs have read it out
   uint64_t* joined = dempty + 2;                                   // [8] other pairs' parts landed, for a warp
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 8);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_slot + 1);   // the epilogue's: a wait ran out; parts to join
   float* sc = reinterpret_cast<float*>(smem + kScOff);
+  int* slots = reinterpret_cast<int*>(smem + kSlotOff);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), pair = blockIdx.x >> 1;
   const int accs = p.BN <= 128 ? 2 : 1;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < kXRing; ++i) {
       mbar_init(&xfull[i], 1);
-      mbar_init(&used[i], 1);
+      mbar_init(&xempty[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&wfull[i], 1);
       mbar_init(&wempty[i], 4);
       mbar_init(&afull[i], 8);
+      mbar_init(&aempty[i], 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&joined[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -196,6 +220,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
 
+  if (warp < kConv0) {
+  regs_down<kRegsIo>();
   if (warp == 0) {
     // ---------------- tokens
     if (lane == 0) {
@@ -203,27 +229,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Walk k(p, pair);
       const int half = p.BN / 2;
       const uint32_t bytes = static_cast<uint32_t>(half) * 256;
-      int i = 0;
+      int i = 0, s = 0;   // units, stage
+      uint32_t ph = 1;    // parity of its last release
       bool ok = true;
       while (ok && k.next(p)) {
         int nt, mt;
         place(p, k.tile, nt, mt);
         const int m0 = mt * p.BN + rank * half;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (kRing - 1);
-          if (i >= kRing && !mbar_wait_many(&used[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
+          if (i >= p.xring && !mbar_wait_many(&xempty[s], ph)) {
             set_status(p.status, FL_ERR_TIMEOUT, 90);
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&xfull[s], 2 * bytes);
           const uint32_t bar = first_cta(&xfull[s]);
-          tma_load_pair(smem + s * kXStage, &xmap, g * kBlockK, m0, bar);
-          tma_load_pair(smem + s * kXStage + bytes / 2, &xmap, g * kBlockK + 64, m0, bar);
+          uint8_t* dst = smem + static_cast<uint32_t>(s) * bytes;
+          tma_load_pair(dst, &xmap, g * kBlockK, m0, bar);
+          tma_load_pair(dst + bytes / 2, &xmap, g * kBlockK + 64, m0, bar);
+          if (++s == p.xring) s = 0, ph ^= 1u;
         }
       }
-      if (ok)   // (the last arrivals from the pair's MMAs come in before the CTA can end)
-        for (int j = i > kRing ? i - kRing : 0; j < i; ++j) mbar_wait(&used[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
+      // (the last arrivals from the pair's MMAs come in before the CTA can end)
+      for (int j = 0; ok && j < min(i, p.xring); ++j) {
+        if (i < p.xring) s = j, ph = 0;
+        ok = mbar_wait(&xempty[s], ph);
+        if (++s == p.xring) s = 0, ph ^= 1u;
+      }
     }
   } else if (warp == 2) {
     // ---------------- weights: older than the kernel before this one
@@ -257,7 +289,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.BN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
       const uint32_t box = static_cast<uint32_t>(p.BN) * 64;   // bytes of 64 columns of this CTA's tokens
       Walk k(p, pair);
-      int i = 0, j = 0;   // units, tiles
+      int i = 0, j = 0, xs = 0;   // units, tiles, token stage
+      uint32_t xph = 0;
       bool ok = true, there = false;
       while (ok && k.next(p)) {
         const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
@@ -267,29 +300,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint32_t d = tmem + acc * 128;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (kRing - 1), s1 = (i + 1) & (kRing - 1);
-          const uint32_t ph = static_cast<uint32_t>(i >> 2) & 1u, ph1 = static_cast<uint32_t>((i + 1) >> 2) & 1u;
-          if (!there && (!mbar_wait_many(&xfull[s], ph) || !mbar_wait_many(&afull[s], ph))) {
+          const int s = i & (kRing - 1);
+          if (!there && (!mbar_wait_many(&xfull[xs], xph) || !mbar_wait_many(&afull[s], static_cast<uint32_t>(i >> 2) & 1u))) {
             set_status(p.status, FL_ERR_TIMEOUT, 93);
             ok = false;
             break;
           }
-          const bool x1 = mbar_test(&xfull[s1], ph1), a1 = mbar_test(&afull[s1], ph1);
+          const int x = xs;
+          if (++xs == p.xring) xs = 0, xph ^= 1u;
+          const bool x1 = mbar_test(&xfull[xs], xph), a1 = mbar_test(&afull[(i + 1) & (kRing - 1)], static_cast<uint32_t>((i + 1) >> 2) & 1u);
           tc_fence_after();
-          const uint32_t b = smem_u32(smem + s * kXStage), a = tmem + kACols + s * 64;
+          const uint32_t b = smem_u32(smem) + static_cast<uint32_t>(x) * 2 * box, a = tmem + kACols + s * 64;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mma_pair(d, a + h * 32 + q * 8, sw128_desc(b + h * box + q * 32), idesc, g != k.g0 || h != 0 || q != 0);
-          commit_pair(&used[s]);
+          commit_pair(&xempty[x]);
+          commit_pair(&aempty[s]);
           there = x1 && a1;
         }
         if (ok) commit_pair(&dfull[acc]);
         ++j;
       }
     }
-  } else if (warp >= kConv0 && warp < kEpi0) {
+  }
+  } else if (warp < kEpi0) {
+    regs_down<kRegsConv>();
     // ---------------- codes to f16: thread = weight row = tensor memory lane; every other unit
     const int q = warp & 3, mine = (warp - kConv0) >> 2, r = q * 32 + lane;
     const uint32_t ta = tmem + kACols + (static_cast<uint32_t>(q * 32) << 16);
@@ -312,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 8; ++t) c[t] = *reinterpret_cast<const uint4*>(rows + s * kWStage + ((t ^ (r & 7)) << 4));
         __syncwarp();
         if (lane == 0) mbar_arrive(&wempty[s]);
-        if (i >= kRing && !mbar_wait_many(&used[s], ph ^ 1u)) {
+        if (i >= kRing && !mbar_wait_many(&aempty[s], ph ^ 1u)) {
           set_status(p.status, FL_ERR_TIMEOUT, 95);
           ok = false;
           break;
@@ -333,19 +370,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (ok)   // (both groups see the last arrivals in)
       for (int j = i > kRing ? i - kRing : 0; j < i; ++j)
-        if ((j & 1) == mine) mbar_wait(&used[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
+        if ((j & 1) == mine) mbar_wait(&aempty[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
   } else {
-    // ---------------- y: weight rows 32q .. 32q + 31, half of each round's tokens.  Tensor
-    // memory is read in mma's fragments (lane: rows g, g + 8, .. of 32, tokens 2c and
-    // 2c + 1), which stmatrix turns into rows of y; the staging tile has TMA's 128-byte
-    // swizzle, so both sides of it are free of bank conflicts.
-    constexpr int kRound = FP32 ? 64 : 128;          // tokens of a staging tile
-    constexpr int kChunks = kRound / 32;             // 16 tokens each, of a warp and round
+    regs_up<kRegsEpi>();
+    // ---------------- y: weight rows 32q .. 32q + 31, half of the tile's tokens, 16 at a
+    // time.  Tensor memory is read in mma's fragments (lane: rows g, g + 8, .. of 32,
+    // tokens 2c and 2c + 1), which stmatrix turns into rows of y; a warp's staging
+    // buffers have TMA's swizzle, so both sides of them are free of bank conflicts,
+    // and no warp waits for another.
+    constexpr int kBufs = FP32 ? 2 : 4, kBuf = kStaging / 8 / kBufs;   // of 16 tokens x 32 rows
     pdl_wait();
     const int e = warp - kEpi0, q = warp & 3, h = e >> 2, tid = threadIdx.x - kEpi0 * 32;
     const int g = lane >> 2, c2 = 2 * (lane & 3);
-    const uint32_t quad = static_cast<uint32_t>(q * 32) << 16;
-    uint8_t* st = smem + kStgOff;
+    const int mine = p.BN / 2, c0 = h * mine;        // this warp's tokens
+    const int bytes = mine * 128;                    // of its part of a split tile: [16 tokens][4][lane] of 16 bytes
+    int buf = 0;
     Walk k(p, pair);
     for (int j = 0; k.next(p); ++j) {
       const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
@@ -372,40 +411,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const bool own = flags[1] != 0;
       tc_fence_after();
-      const uint32_t d = tmem + acc * 128 + quad;
-      auto issue = [&](int col, uint32_t (&u)[16]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                       : "=r"(u[8 * i]), "=r"(u[8 * i + 1]), "=r"(u[8 * i + 2]), "=r"(u[8 * i + 3]), "=r"(u[8 * i + 4]), "=r"(u[8 * i + 5]),
-                         "=r"(u[8 * i + 6]), "=r"(u[8 * i + 7])
-                       : "r"(d + (static_cast<uint32_t>(16 * i) << 16) + col));
-      };
+      const uint32_t d = tmem + acc * 128 + (static_cast<uint32_t>(q * 32) << 16) + c0;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first(&dempty[acc]);
       };
-      const int bytes = p.BN * 64;                   // of a warp's part of a split tile
-      auto slot = [&](int c) {                       // [chunk][4][lane] of 16 bytes
-        const int which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
-        return reinterpret_cast<float4*>(p.part) + ((static_cast<size_t>(2 * c + which) * 2 + rank) * 8 + e) * (bytes / 16) + lane;
-      };
-      bool room = false;
-      if (!own) {
-        float4* dst = slot(pair);
-        for (int t0 = 0; t0 < p.BN; t0 += kRound) {
-          const int n_t = min(kRound, p.BN - t0), count = n_t / 2, from = t0 + h * count;
-#pragma unroll 1
-          for (int ch = 0; 16 * ch < count; ++ch) {
-            uint32_t u[16];
-            issue(from + 16 * ch, u);
-            tmem_ld_wait(u);
+      auto issue = [&](int t, uint32_t (&u)[16]) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              __stcg(dst + ((t0 / 32 + ch) * 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                                                                      __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
+        for (int i = 0; i < 2; ++i)
+          asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=r"(u[8 * i]), "=r"(u[8 * i + 1]), "=r"(u[8 * i + 2]), "=r"(u[8 * i + 3]), "=r"(u[8 * i + 4]),
+                         "=r"(u[8 * i + 5]), "=r"(u[8 * i + 6]), "=r"(u[8 * i + 7])
+                       : "r"(d + (static_cast<uint32_t>(16 * i) << 16) + t));
+      };
+      // 16 tokens from t on: u[8 i + 4 b + 2 r + k] is row 16 i + 8 r + g, token 8 b + c2 + k
+      auto emit = [&](int t, const uint32_t (&u)[16]) {
+        uint8_t* st = smem + kStgOff + e * (kStaging / 8) + buf * kBuf;
+        buf = (buf + 1) & (kBufs - 1);
+        if (lane == 0) bulk_wait_read<kBufs - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float2 s2 = *reinterpret_cast<const float2*>(sc + c0 + t + 8 * b + c2);
+          uint32_t r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = 8 * (i >> 1) + 4 * b + 2 * (i & 1);
+            const float f0 = __uint_as_float(u[at]) * __fmul_rn(s2.x, ts[i]), f1 = __uint_as_float(u[at + 1]) * __fmul_rn(s2.y, ts[i]);
+            if constexpr (FP32) {
+              const int tok = 8 * b + c2, n = 8 * i + g;
+              *reinterpret_cast<float*>(st + tok * 128 + (((n >> 2) ^ (tok & 7)) << 4) + (n & 3) * 4) = f0;
+              *reinterpret_cast<float*>(st + (tok + 1) * 128 + (((n >> 2) ^ ((tok + 1) & 7)) << 4) + (n & 3) * 4) = f1;
+            } else {
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(f0, f1);
+              r[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
           }
+          if constexpr (!FP32) {
+            const int tok = 8 * b + (lane & 7);
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             smem_u32(st + tok * 64 + (((lane >> 3) ^ ((tok >> 1) & 3)) << 4))),
+                         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                         : "memory");
+          }
+        }
+        const int m = m0 + c0 + t, n = n0 + q * 32;
+        if (p.tma_y) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            if (m < p.M && n < p.N) tma_store_2d(&ymap, st, n, m);
+            bulk_commit();
+          }
+        } else {   // rows of y that do not start and end on 16 bytes
+          __syncwarp();
+          if (n + lane < p.N)
+#pragma unroll 4
+            for (int tok = 0; tok < min(16, p.M - m); ++tok) {
+              const size_t at = static_cast<size_t>(m + tok) * p.y_stride + n + lane;
+              if constexpr (FP32)
+                static_cast<float*>(p.y)[at] = *reinterpret_cast<const float*>(st + tok * 128 + (((lane >> 2) ^ (tok & 7)) << 4) + (lane & 3) * 4);
+              else
+                static_cast<uint16_t*>(p.y)[at] =
+                    *reinterpret_cast<const uint16_t*>(st + tok * 64 + (((lane >> 3) ^ ((tok >> 1) & 3)) << 4) + (lane & 7) * 2);
+            }
+        }
+      };
+      if (!k.split) {
+        uint32_t ua[16], ub[16];
+        issue(0, ua);
+#pragma unroll 1
+        for (int t = 0; t < mine; t += 32) {
+          tmem_ld_wait(ua);
+          if (t + 16 < mine)
+            issue(t + 16, ub);
+          else
+            release();
+          emit(t, ua);
+          if (t + 16 >= mine) break;
+          tmem_ld_wait(ub);
+          if (t + 32 < mine)
+            issue(t + 32, ua);
+          else
+            release();
+          emit(t + 16, ub);
+        }
+        continue;
+      }
+      // a part of a split tile
+      if (tid <= cl - cf) {   // this CTA's parts of it, by pair
+        const int c = cf + tid, which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
+        slots[tid] = (2 * c + which) * 2 + rank;
+      }
+      named_bar(1, 256);
+      auto part = [&](int c) {
+        return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(slots[c - cf]) * 8 + e) * (bytes / 16) + lane;
+      };
+      if (!own) {
+        float4* dst = part(pair);
+#pragma unroll 1
+        for (int t = 0; t < mine; t += 16) {
+          uint32_t u[16];
+          issue(t, u);
+          tmem_ld_wait(u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            __stcg(dst + (t / 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                                       __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
         }
         release();
         named_bar(1, 256);
@@ -413,131 +526,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         named_bar(1, 256);
         if (!flags[1]) continue;
       }
-      if (k.split) {
-        if (tid == 0) *cnt = 0;
-        // at the CTA's last tile the rings are empty and take the parts, all in flight at once
-        const int others = cl - cf + 1 - own;
-        room = k.u >= k.u1 && k.w >= p.waves && others * bytes <= kJoin;
-        if (room) {
-          if (lane == 0) {
-            fence_proxy_async_all();
-            mbar_arrive_expect_tx(&joined[e], static_cast<uint32_t>(others * bytes));
-            for (int c = cf, o = 0; c <= cl; ++c)
-              if (!(own && c == pair)) bulk_g2s(smem + e * kJoin + bytes * o++, slot(c) - lane, bytes, &joined[e]);
-          }
-          __syncwarp();
-          if (!mbar_wait(&joined[e], 0)) set_status(p.status, FL_ERR_TIMEOUT, 98);
+      if (tid == 0) *cnt = 0;
+      // at the CTA's last tile the rings are empty and take the parts, all in flight at once
+      const int others = cl - cf + 1 - own;
+      const bool room = k.u >= k.u1 && k.w >= p.waves && others * bytes <= kJoin;
+      if (room) {
+        if (lane == 0) {
+          fence_proxy_async_all();
+          mbar_arrive_expect_tx(&joined[e], static_cast<uint32_t>(others * bytes));
+          for (int c = cf, o = 0; c <= cl; ++c)
+            if (!(own && c == pair)) bulk_g2s(smem + e * kJoin + bytes * o++, part(c) - lane, bytes, &joined[e]);
         }
+        __syncwarp();
+        if (!mbar_wait(&joined[e], 0)) set_status(p.status, FL_ERR_TIMEOUT, 98);
       }
-      for (int t0 = 0; t0 < p.BN; t0 += kRound) {
-        const int n_t = min(kRound, p.BN - t0), count = n_t / 2, from = t0 + h * count;
-        uint32_t held[32];
-#pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          if (16 * ch < count) {
-            uint32_t u[16];
-            if (own) {
-              issue(from + 16 * ch, u);
-              tmem_ld_wait(u);
-            }
-            if (k.split) {
-              float v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = 0.f;
-              int o = 0;
 #pragma unroll 1
-              for (int c = cf; c <= cl; ++c) {   // (the pairs' order)
-                if (own && c == pair) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(u[i]);
-                  continue;
-                }
-                float4 f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int at = ((t0 / 32 + ch) * 4 + i) * 32;
-                  f[i] = room ? *reinterpret_cast<const float4*>(smem + e * kJoin + bytes * o + (at + lane) * 16) : __ldcg(slot(c) + at);
-                }
-                ++o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[4 * i] += f[i].x, v[4 * i + 1] += f[i].y, v[4 * i + 2] += f[i].z, v[4 * i + 3] += f[i].w;
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
-            }
-            // u[8 i + 4 b + 2 r + k]: row 16 i + 8 r + g, token 8 b + c2 + k of the chunk
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const float2 s2 = *reinterpret_cast<const float2*>(sc + from + 16 * ch + 8 * b + c2);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int at = 8 * (i >> 1) + 4 * b + 2 * (i & 1);
-                const float f0 = __uint_as_float(u[at]) * __fmul_rn(s2.x, ts[i]), f1 = __uint_as_float(u[at + 1]) * __fmul_rn(s2.y, ts[i]);
-                if constexpr (FP32) {
-                  held[16 * ch + at] = __float_as_uint(f0), held[16 * ch + at + 1] = __float_as_uint(f1);
-                } else {
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(f0, f1);
-                  held[8 * ch + 4 * b + i] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-              }
-            }
-          }
+      for (int t = 0; t < mine; t += 16) {
+        uint32_t u[16];
+        float v[16];
+        if (own) {
+          issue(t, u);
+          tmem_ld_wait(u);
+          if (t + 16 >= mine) release();
         }
-        if (own && t0 + kRound >= p.BN) release();
-        if (tid == 0) bulk_wait_read0();   // the round before has left the staging tile
-        named_bar(1, 256);
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          if (16 * ch < count) {
-            const int lt = h * count + 16 * ch;   // token of the round
-            if constexpr (FP32) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int tok = lt + 8 * ((i >> 2) & 1) + c2 + (i & 1), n = 16 * (i >> 3) + 8 * ((i >> 1) & 1) + g;
-                *reinterpret_cast<uint32_t*>(st + q * 8192 + tok * 128 + (((n >> 2) ^ (tok & 7)) << 4) + (n & 3) * 4) = held[16 * ch + i];
-              }
-            } else {
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int tok = lt + 8 * b + (lane & 7), n8 = (q & 1) * 4 + (lane >> 3);
-                const uint32_t* r = held + 8 * ch + 4 * b;
-                asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 smem_u32(st + (q >> 1) * 16384 + tok * 128 + ((n8 ^ (tok & 7)) << 4))),
-                             "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                             : "memory");
-              }
-            }
-          }
-        }
-        fence_proxy_async();
-        named_bar(1, 256);
-        if (p.tma_y) {
-          if (tid == 0) {
-            constexpr int kWide = FP32 ? 32 : 64, kSlab = kRound * 128;   // rows and bytes of 128-byte columns of the tile
-            for (int t = 0; t < n_t && m0 + t0 + t < p.M; t += 32)
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        int o = 0;
 #pragma unroll 1
-              for (int w = 0; w < kRows / kWide && n0 + w * kWide < p.N; ++w)
-                tma_store_2d(&ymap, st + w * kSlab + t * 128, n0 + w * kWide, m0 + t0 + t);
-            bulk_commit();
-          }
-        } else {   // rows of y that do not start on 16 bytes: element by element, a warp a token
-          for (int tok = e; tok < n_t && m0 + t0 + tok < p.M; tok += 8)
+        for (int c = cf; c <= cl; ++c) {   // (the pairs' order)
+          if (own && c == pair) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int n = 32 * w + lane;
-              const size_t at = static_cast<size_t>(m0 + t0 + tok) * p.y_stride + n0 + n;
-              if (n0 + n >= p.N) continue;
-              if constexpr (FP32)
-                static_cast<float*>(p.y)[at] = *reinterpret_cast<const float*>(st + w * 8192 + tok * 128 + (((lane >> 2) ^ (tok & 7)) << 4) + (lane & 3) * 4);
-              else
-                static_cast<uint16_t*>(p.y)[at] = *reinterpret_cast<const uint16_t*>(
-                    st + (n >> 6) * 16384 + tok * 128 + ((((n & 63) >> 3) ^ (tok & 7)) << 4) + (n & 7) * 2);
-            }
-          named_bar(1, 256);
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(u[i]);
+            continue;
+          }
+          float4 f[4];
+          if (room) {
+            const float4* src = reinterpret_cast<const float4*>(smem + e * kJoin + bytes * o++) + t * 8 + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = src[32 * i];
+          } else {
+            const float4* src = part(c) + t * 8;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __ldcg(src + 32 * i);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[4 * i] += f[i].x, v[4 * i + 1] += f[i].y, v[4 * i + 2] += f[i].z, v[4 * i + 3] += f[i].w;
         }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
+        emit(t, u);
       }
     }
-    if (tid == 0) bulk_wait0();
+    if (lane == 0) bulk_wait0();
   }
   tc_fence_before();
   __syncwarp();
@@ -573,7 +613,8 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   p.ntiles = static_cast<int>((c.N + 2 * kRows - 1ll) / (2 * kRows));
   const long long tiles = static_cast<long long>(p.mtiles) * p.ntiles;
   if (tiles > 0x7fffffffll / kGroupM || p.ntiles > 0x7fffffff / kGroupM) return FL_ERR_UNSUPPORTED;
-  const int pairs = flh::sm_count() / 2;
+  p.xring = kXBytes / (p.BN * 128) < kXRing ? kXBytes / (p.BN * 128) : kXRing;
+  const int pairs = flh::sm_count() / 2 < 128 ? flh::sm_count() / 2 : 128;
   p.P = pairs;
   if (tiles * 2 <= pairs) {   // few tiles: each in equal parts
     int parts = pairs / static_cast<int>(tiles);
@@ -611,9 +652,9 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   memset(&ymap, 0, sizeof(ymap));
   if (p.tma_y) {
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.N), static_cast<cuuint64_t>(c.M)}, strides[1] = {static_cast<cuuint64_t>(c.y_stride) * size};
-    const cuuint32_t box[2] = {c.fp32 ? 32u : 64u, 32};
+    const cuuint32_t box[2] = {32, 16};
     if (enc(&ymap, c.fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, c.y, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+            CU_TENSOR_MAP_INTERLEAVE_NONE, c.fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
         CUDA_SUCCESS)
       return FL_ERR_CUDA;
   }
@@ -621,7 +662,10 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !ready[dev]) {
-    if (cudaFuncSetAttribute(k_int8_gemm<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+    cudaFuncAttributes a, b;   // the roles' register counts add up to the launch's
+    if (cudaFuncGetAttributes(&a, k_int8_gemm<false>) != cudaSuccess || cudaFuncGetAttributes(&b, k_int8_gemm<true>) != cudaSuccess ||
+        a.numRegs != kRegs || b.numRegs != kRegs ||
+        cudaFuncSetAttribute(k_int8_gemm<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
         cudaFuncSetAttribute(k_int8_gemm<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
       cudaGetLastError();
       return FL_ERR_CUDA;
