@@ -282,12 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = i - kRing; j < i; ++j) mbar_wait(&wfull[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
     }
   } else if (warp == 1) {
-    // ---------------- MMAs of the pair.  A probe of a barrier takes this thread 200
-    // cycles even if the phase is over, so the next unit's are asked for before the
-    // MMAs of this one and looked at after them (8190 x 4096 x 11008: 487 to 452 us)
-    if (rank == 0 && lane == 0) {
+    // ---------------- MMAs of the pair
+    if (rank == 0) {   // (the whole warp runs the loop: what the MMAs take then lies in uniform registers)
       const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.BN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
-      const uint32_t box = static_cast<uint32_t>(p.BN) * 64;   // bytes of 64 columns of this CTA's tokens
+      const uint32_t stage = static_cast<uint32_t>(p.BN) * 128;   // bytes of this CTA's tokens of a unit
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      const bool one = elect_one();
       Walk k(p, pair);
       int i = 0, j = 0, xs = 0;   // units, tiles, token stage
       uint32_t xph = 0;
@@ -308,19 +308,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           const int x = xs;
           if (++xs == p.xring) xs = 0, xph ^= 1u;
-          const bool x1 = mbar_test(&xfull[xs], xph), a1 = mbar_test(&afull[(i + 1) & (kRing - 1)], static_cast<uint32_t>((i + 1) >> 2) & 1u);
           tc_fence_after();
-          const uint32_t b = smem_u32(smem) + static_cast<uint32_t>(x) * 2 * box, a = tmem + kACols + s * 64;
+          if (one) {
+            const uint64_t b = desc0 + ((static_cast<uint32_t>(x) * stage) >> 4);
+            const uint32_t a = tmem + kACols + s * 64;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              mma_pair(d, a + h * 32 + q * 8, sw128_desc(b + h * box + q * 32), idesc, g != k.g0 || h != 0 || q != 0);
-          commit_pair(&xempty[x]);
-          commit_pair(&aempty[s]);
-          there = x1 && a1;
+              for (int q = 0; q < 4; ++q)
+                mma_pair(d, a + h * 32 + q * 8, b + h * (stage >> 5) + q * 2, idesc, g != k.g0 || h != 0 || q != 0);
+            commit_pair(&xempty[x]);
+            commit_pair(&aempty[s]);
+          }
+          __syncwarp();
+          there = mbar_test(&xfull[xs], xph) && mbar_test(&afull[(i + 1) & (kRing - 1)], static_cast<uint32_t>((i + 1) >> 2) & 1u);
         }
-        if (ok) commit_pair(&dfull[acc]);
+        if (ok && one) commit_pair(&dfull[acc]);
+        __syncwarp();
         ++j;
       }
     }
