@@ -55,18 +55,37 @@ __device__ __forceinline__ uint4 load8(const CodesParams& p, const void* row, in
   return r;
 }
 
+// A row's quotients are x * up * inv (up: a power of two that keeps rows of tiny
+// values clear of subnormal numbers); twice: 2 * scale * up.
 struct Rounding {
-  float up, inv, twice;   // a * up * inv is the quotient; 2 * scale * up
-  bool zero;
+  float up, inv, twice;
 };
-__device__ __forceinline__ int code_of(float x, const Rounding& q) {
-  const float a = fabsf(x) * q.up, t = a * q.inv;
-  float k = rintf(t);
-  if (fabsf(t - k) > 0.4995f) {
-    const float lo = floorf(t), d = __fmaf_rn(-(lo + 0.5f), q.twice, 2.f * a);
-    k = d > 0.f || (d == 0.f && (static_cast<int>(lo) & 1)) ? lo + 1.f : lo;
+// The nearest whole number to the quotient itself, next to a border too.
+__device__ __noinline__ float exact_code(float x, float up, float inv, float twice) {
+  const float a = fabsf(x) * up, t = a * inv, lo = floorf(t);
+  const float d = __fmaf_rn(-(lo + 0.5f), twice, 2.f * a);
+  const float k = d > 0.f || (d == 0.f && (static_cast<int>(lo) & 1)) ? lo + 1.f : lo;
+  return copysignf(k, x);
+}
+// Eight values (bf16 pairs) to whole numbers.  Adding 1.5 * 2^23 rounds to them.
+__device__ __forceinline__ void codes8(const uint4& r, const Rounding& q, float (&k)[8]) {
+  constexpr float kMagic = 12582912.f;
+  float off = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = (&r.x)[i / 2];
+    const float t = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16) * q.up * q.inv;
+    k[i] = __fsub_rn(__fadd_rn(t, kMagic), kMagic);
+    off = fmaxf(off, fabsf(t - k[i]));
   }
-  return static_cast<int>(x < 0.f ? -k : k);
+  if (off > 0.4995f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = (&r.x)[i / 2];
+      const float x = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+      if (fabsf(x * q.up * q.inv - k[i]) > 0.4995f) k[i] = exact_code(x, q.up, q.inv, q.twice);
+    }
+  }
 }
 
 template <int IN, int OUT, int NV>
@@ -83,7 +102,8 @@ __global__ void __launch_bounds__(1024) k_codes(const CodesParams p) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) held[i] = tid + i * T < nv ? load8<IN>(p, row, tid + i * T) : make_uint4(0, 0, 0, 0);
 
-  Rounding q = {1.f, 0.f, 0.f, false};
+  Rounding q = {1.f, 0.f, 0.f};   // (inv 0: every code is 0)
+  bool none = false;
   if constexpr (IN == kInBf16) {
     uint32_t top2 = 0;   // two maxima of |bf16| bits
     auto take = [&](const uint4& r) {
@@ -103,29 +123,24 @@ __global__ void __launch_bounds__(1024) k_codes(const CodesParams p) {
     float scale = __fdiv_rn(largest, 127.f);
     if (top >= 0x7f80u) scale = __uint_as_float(0x7fc00000u);
     if (tid == 0) p.scale[m] = scale;
-    q.zero = top == 0 || top >= 0x7f80u;
+    none = top == 0 || top >= 0x7f80u;
     q.up = largest < 0x1p-60f ? 0x1p64f : 1.f;   // (tiny rows stay clear of subnormal numbers)
-    q.inv = q.zero ? 0.f : __fdiv_rn(127.f, largest * q.up);
+    q.inv = none ? 0.f : __fdiv_rn(127.f, largest * q.up);
     q.twice = 2.f * (scale * q.up);
   }
 
   auto put = [&](int v, const uint4& r) {
-    uint32_t c[2];   // eight int8 codes
-    if constexpr (IN == kInCodes) {
-      c[0] = r.x, c[1] = r.y;
-    } else {
+    if constexpr (OUT == kOutCodes) {
+      float k[8] = {};
+      if (!none) codes8(r, q, k);
+      uint32_t c[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        c[h] = 0;
+        uint32_t b[4];   // (the sum's last byte is the code)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w = (&r.x)[2 * h + i / 2];
-          const float x = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-          c[h] |= static_cast<uint32_t>((q.zero ? 0 : code_of(x, q)) & 0xff) << (8 * i);
-        }
+        for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(k[4 * h + i] + 12582912.f);
+        c[h] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
       }
-    }
-    if constexpr (OUT == kOutCodes) {
       int8_t* out = static_cast<int8_t*>(p.out) + static_cast<size_t>(m) * p.K + 8 * v;
       if ((p.K & 7) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 7) == 0) {
         *reinterpret_cast<uint2*>(out) = make_uint2(c[0], c[1]);
@@ -135,9 +150,19 @@ __global__ void __launch_bounds__(1024) k_codes(const CodesParams p) {
           if (8 * v + i < p.K) out[i] = static_cast<int8_t>(c[i / 4] >> (8 * (i & 3)));
       }
     } else {
-      uint4 f;
-      codes_f16(c[0], f.x, f.y);
-      codes_f16(c[1], f.z, f.w);
+      uint4 f = make_uint4(0, 0, 0, 0);
+      if constexpr (IN == kInCodes) {
+        codes_f16(r.x, f.x, f.y);
+        codes_f16(r.y, f.z, f.w);
+      } else if (!none) {
+        float k[8];
+        codes8(r, q, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __half2 h = __floats2half2_rn(k[2 * i], k[2 * i + 1]);
+          (&f.x)[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
       uint8_t* out = static_cast<uint8_t*>(p.out);
       if constexpr (OUT == kOutRows) {
         *reinterpret_cast<uint4*>(out + (static_cast<size_t>(m) * p.K + 8 * v) * 2) = f;

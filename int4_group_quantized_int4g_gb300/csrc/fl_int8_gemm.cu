@@ -39,7 +39,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kConv0 = 4, kEpi0 = 12;
 // Registers a thread: of the launch, and of the producers and the issuer, the
 // converting warps and the epilogue (which spills its sums with 96).
-constexpr int kRegs = 96, kRegsIo = 64, kRegsConv = 80, kRegsEpi = 128;
+constexpr int kRegs = 96, kRegsIo = 64, kRegsConv = 72, kRegsEpi = 136;
 static_assert(4 * kRegsIo + 8 * kRegsConv + 8 * kRegsEpi <= 20 * kRegs, "the split draws on the launch's registers");
 constexpr int kRing = 4;                       // weight stages and A tiles (even: a slot has one group of converting warps)
 constexpr int kXRing = 8;                      // token stages, at most
@@ -377,12 +377,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if ((j & 1) == mine) mbar_wait(&aempty[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
   } else {
     regs_up<kRegsEpi>();
-    // ---------------- y: weight rows 32q .. 32q + 31, half of the tile's tokens, 16 at a
+    // ---------------- y: weight rows 32q .. 32q + 31, half of the tile's tokens, some at a
     // time.  Tensor memory is read in mma's fragments (lane: rows g, g + 8, .. of 32,
     // tokens 2c and 2c + 1), which stmatrix turns into rows of y; a warp's staging
     // buffers have TMA's swizzle, so both sides of them are free of bank conflicts,
     // and no warp waits for another.
-    constexpr int kBufs = FP32 ? 2 : 4, kBuf = kStaging / 8 / kBufs;   // of 16 tokens x 32 rows
+    constexpr int kStep = FP32 ? 16 : 32;            // tokens of a step; two buffers of 2 KB for them
     pdl_wait();
     const int e = warp - kEpi0, q = warp & 3, h = e >> 2, tid = threadIdx.x - kEpi0 * 32;
     const int g = lane >> 2, c2 = 2 * (lane & 3);
@@ -421,58 +421,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) arrive_first(&dempty[acc]);
       };
-      auto issue = [&](int t, uint32_t (&u)[16]) {
+      auto issue = [&](int t, uint32_t* u) {   // 16 tokens from t on
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          uint32_t* r = u + 8 * i;
           asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                       : "=r"(u[8 * i]), "=r"(u[8 * i + 1]), "=r"(u[8 * i + 2]), "=r"(u[8 * i + 3]), "=r"(u[8 * i + 4]),
-                         "=r"(u[8 * i + 5]), "=r"(u[8 * i + 6]), "=r"(u[8 * i + 7])
+                       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                        : "r"(d + (static_cast<uint32_t>(16 * i) << 16) + t));
+        }
       };
-      // 16 tokens from t on: u[8 i + 4 b + 2 r + k] is row 16 i + 8 r + g, token 8 b + c2 + k
-      auto emit = [&](int t, const uint32_t (&u)[16]) {
-        uint8_t* st = smem + kStgOff + e * (kStaging / 8) + buf * kBuf;
-        buf = (buf + 1) & (kBufs - 1);
-        if (lane == 0) bulk_wait_read<kBufs - 1>();
-        __syncwarp();
+      // 16 tokens from t on, as y: u[8 i + 4 b + 2 r + k] is row 16 i + 8 r + g, token t + 8 b + c2 + k
+      auto scaled = [&](int t, const uint32_t* u, uint32_t* y) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float2 s2 = *reinterpret_cast<const float2*>(sc + c0 + t + 8 * b + c2);
-          uint32_t r[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = 8 * (i >> 1) + 4 * b + 2 * (i & 1);
             const float f0 = __uint_as_float(u[at]) * __fmul_rn(s2.x, ts[i]), f1 = __uint_as_float(u[at + 1]) * __fmul_rn(s2.y, ts[i]);
             if constexpr (FP32) {
-              const int tok = 8 * b + c2, n = 8 * i + g;
-              *reinterpret_cast<float*>(st + tok * 128 + (((n >> 2) ^ (tok & 7)) << 4) + (n & 3) * 4) = f0;
-              *reinterpret_cast<float*>(st + (tok + 1) * 128 + (((n >> 2) ^ ((tok + 1) & 7)) << 4) + (n & 3) * 4) = f1;
+              y[8 * b + 2 * i] = __float_as_uint(f0), y[8 * b + 2 * i + 1] = __float_as_uint(f1);
             } else {
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(f0, f1);
-              r[i] = *reinterpret_cast<const uint32_t*>(&b2);
+              y[4 * b + i] = *reinterpret_cast<const uint32_t*>(&b2);
             }
           }
-          if constexpr (!FP32) {
-            const int tok = 8 * b + (lane & 7);
+        }
+      };
+      uint8_t* st = smem + kStgOff + e * (kStaging / 8);
+      auto buffer = [&]() {   // the next one; the step before the last has left it
+        st = smem + kStgOff + e * (kStaging / 8) + buf * (kStaging / 16);
+        buf ^= 1;
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+      };
+      auto stage = [&](int x, const uint32_t* y) {   // tokens x .. x + 15 of the buffer
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if constexpr (FP32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int tok = x + 8 * b + c2 + (i & 1), n = 8 * (i >> 1) + g;
+              *reinterpret_cast<uint32_t*>(st + tok * 128 + (((n >> 2) ^ (tok & 7)) << 4) + (n & 3) * 4) = y[8 * b + i];
+            }
+          } else {
+            const int tok = x + 8 * b + (lane & 7);
             asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                              smem_u32(st + tok * 64 + (((lane >> 3) ^ ((tok >> 1) & 3)) << 4))),
-                         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                         "r"(y[4 * b]), "r"(y[4 * b + 1]), "r"(y[4 * b + 2]), "r"(y[4 * b + 3])
                          : "memory");
           }
         }
+      };
+      auto store = [&](int t, int count) {   // the buffer's tokens, t .. t + count - 1 of this warp
         const int m = m0 + c0 + t, n = n0 + q * 32;
+        count = min(count, p.M - m);
         if (p.tma_y) {
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            if (m < p.M && n < p.N) tma_store_2d(&ymap, st, n, m);
+            if (n < p.N && count > 0) tma_store_2d(&ymap, st, n, m);
+            if (n < p.N && count > 16) tma_store_2d(&ymap, st + 16 * (FP32 ? 128 : 64), n, m + 16);
             bulk_commit();
           }
         } else {   // rows of y that do not start and end on 16 bytes
           __syncwarp();
           if (n + lane < p.N)
 #pragma unroll 4
-            for (int tok = 0; tok < min(16, p.M - m); ++tok) {
+            for (int tok = 0; tok < count; ++tok) {
               const size_t at = static_cast<size_t>(m + tok) * p.y_stride + n + lane;
               if constexpr (FP32)
                 static_cast<float*>(p.y)[at] = *reinterpret_cast<const float*>(st + tok * 128 + (((lane >> 2) ^ (tok & 7)) << 4) + (lane & 3) * 4);
@@ -482,24 +498,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
       };
+      auto landed = [&](uint32_t (&u)[16]) { tmem_ld_wait(u); };
       if (!k.split) {
-        uint32_t ua[16], ub[16];
+        uint32_t ua[16], ub[16], y[16];
         issue(0, ua);
+        if (16 < mine) issue(16, ub);
 #pragma unroll 1
-        for (int t = 0; t < mine; t += 32) {
-          tmem_ld_wait(ua);
-          if (t + 16 < mine)
-            issue(t + 16, ub);
-          else
-            release();
-          emit(t, ua);
-          if (t + 16 >= mine) break;
-          tmem_ld_wait(ub);
-          if (t + 32 < mine)
-            issue(t + 32, ua);
-          else
-            release();
-          emit(t + 16, ub);
+        for (int t = 0; t < mine; t += kStep) {
+          landed(ua);
+          scaled(t, ua, y);
+          if constexpr (FP32) {   // (16 tokens a step: the buffers hold no more)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ua[i] = ub[i];
+            if (t + 16 >= mine)
+              release();
+            else if (t + 32 < mine)
+              issue(t + 32, ub);
+          } else {
+            landed(ub);
+            if (t + 16 < mine) scaled(t + 16, ub, y + 8);
+            if (t + 32 >= mine) {
+              release();
+            } else {
+              issue(t + 32, ua);
+              if (t + 48 < mine) issue(t + 48, ub);
+            }
+          }
+          buffer();
+          stage(0, y);
+          if constexpr (!FP32)
+            if (t + 16 < mine) stage(16, y + 8);
+          store(t, min(kStep, mine - t));
         }
         continue;
       }
@@ -514,11 +543,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       if (!own) {
         float4* dst = part(pair);
+        uint32_t u[16];
 #pragma unroll 1
         for (int t = 0; t < mine; t += 16) {
-          uint32_t u[16];
           issue(t, u);
-          tmem_ld_wait(u);
+          landed(u);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             __stcg(dst + (t / 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
@@ -548,37 +577,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = 0; t < mine; t += 16) {
         uint32_t u[16];
         float v[16];
-        if (own) {
-          issue(t, u);
-          tmem_ld_wait(u);
-          if (t + 16 >= mine) release();
-        }
+        if (own) issue(t, u);
+        if (own) landed(u);
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        int o = 0;
+        // the pairs' order, the parts of two at once on their way
 #pragma unroll 1
-        for (int c = cf; c <= cl; ++c) {   // (the pairs' order)
-          if (own && c == pair) {
+        for (int c = cf, o = 0; c <= cl; c += 2) {
+          float4 f[2][4];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(u[i]);
-            continue;
+          for (int n = 0; n < 2; ++n) {
+            if (c + n > cl || (own && c + n == pair)) continue;
+            if (room) {
+              const float4* src = reinterpret_cast<const float4*>(smem + e * kJoin + bytes * o++) + t * 8 + lane;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[n][i] = src[32 * i];
+            } else {
+              const float4* src = part(c + n) + t * 8;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[n][i] = __ldcg(src + 32 * i);
+            }
           }
-          float4 f[4];
-          if (room) {
-            const float4* src = reinterpret_cast<const float4*>(smem + e * kJoin + bytes * o++) + t * 8 + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = src[32 * i];
-          } else {
-            const float4* src = part(c) + t * 8;
+          for (int n = 0; n < 2; ++n) {
+            if (c + n > cl) continue;
+            if (own && c + n == pair) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = __ldcg(src + 32 * i);
+              for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(u[i]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[4 * i] += f[n][i].x, v[4 * i + 1] += f[n][i].y, v[4 * i + 2] += f[n][i].z, v[4 * i + 3] += f[n][i].w;
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[4 * i] += f[i].x, v[4 * i + 1] += f[i].y, v[4 * i + 2] += f[i].z, v[4 * i + 3] += f[i].w;
         }
+        if (own && t + 16 >= mine) release();
+        uint32_t y[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[i]);
-        emit(t, u);
+        scaled(t, u, y);
+        buffer();
+        stage(0, y);
+        store(t, 16);
       }
     }
     if (lane == 0) bulk_wait0();
