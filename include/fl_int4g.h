@@ -590,7 +590,7 @@ int fl_int8_linear_workspace(int M, int N, int K, size_t* out);
  * K % 16 == 0, M, N >= 1.  Products and sums are those of the codes: f16
  * operands hold them exactly, sums are fp32 (exact while they stay below
  * 2^24), partial sums of a split K are added in a fixed order, so results do
- * not depend on timing.  M <= 32 streams the weights through mma.sync, larger
+ * not depend on timing.  M <= 16 streams the weights through mma.sync, larger
  * M runs on tcgen05.  A row whose scale is NaN gives NaN. */
 int fl_int8_linear(const void* x, int64_t x_stride, const float* x_scale, int M, int K, const int8_t* w,
                    const float* w_scale, int N, void* y, int64_t y_stride, int y_type, void* ws, size_t ws_bytes,

@@ -41,18 +41,21 @@ constexpr int kConv0 = 4, kEpi0 = 12;
 // converting warps and the epilogue (which spills its sums with 96).
 constexpr int kRegs = 96, kRegsIo = 64, kRegsConv = 72, kRegsEpi = 136;
 static_assert(4 * kRegsIo + 8 * kRegsConv + 8 * kRegsEpi <= 20 * kRegs, "the split draws on the launch's registers");
-constexpr int kRing = 4;                       // weight stages and A tiles (even: a slot has one group of converting warps)
+constexpr int kRing = 4;                       // A tiles (an even number: a slot has one group of converting warps)
+constexpr int kWRing = 8;                      // weight stages, at most (4 or 8)
 constexpr int kXRing = 8;                      // token stages, at most
 constexpr int kRows = 128;                     // weight rows of a CTA
-constexpr int kXBytes = 131072;                // token stages: BN / 2 tokens x 128 columns f16 each, as two boxes
+// Token stages (BN / 2 tokens x 128 columns f16 each, as two boxes), then weight
+// stages: with few tokens, where the weights' bytes bound, the latter get more.
+constexpr int kXBytes = 131072, kXBytesFew = 65536, kFew = 64;
 constexpr int kWStage = kRows * kBlockK;
 constexpr int kStaging = 32768;                // y: 4 KB a warp of the epilogue
-constexpr int kWOff = kXBytes;
-constexpr int kStgOff = kWOff + kRing * kWStage;
+constexpr int kStgOff = kXBytes + 4 * kWStage;
+static_assert(kXBytesFew + 8 * kWStage == kStgOff && kFew * 128 * kXRing <= kXBytesFew, "stages");
 constexpr int kScOff = kStgOff + kStaging;     // 256 token scales
 constexpr int kSlotOff = kScOff + 1024;        // a split tile's parts
 constexpr int kBarOff = kSlotOff + 512;
-constexpr int kBars = 2 * kXRing + 4 * kRing + 4 + 8;
+constexpr int kBars = 2 * kXRing + 2 * kWRing + 2 * kRing + 4 + 8;
 constexpr int kJoin = kStgOff / 8;             // a warp's room for other pairs' parts, when the rings are done
 constexpr int kSmem = kBarOff + kBars * 8 + 16 + 1024;
 static_assert(kSmem <= 232448, "shared memory");
@@ -69,7 +72,7 @@ struct Params {
   int32_t* status;
   int M, N, fp32, tma_y;
   int BN, G, mtiles, ntiles;
-  int xring;         // token stages
+  int xring, wshift, woff;   // token stages, log2 of the weight stages and where these lie
   int P, waves, U;   // pairs, whole tiles of each, units of the rest
 };
 
@@ -175,8 +178,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* xfull = reinterpret_cast<uint64_t*>(smem + kBarOff);   // first CTA: both CTAs' tokens landed
   uint64_t* xempty = xfull + kXRing;                               // the pair's MMAs have read them
   uint64_t* wfull = xempty + kXRing;                                // weights landed
-  uint64_t* wempty = wfull + kRing;                                // 4 converting warps have read them
-  uint64_t* afull = wempty + kRing;                                // first CTA: both CTAs' A tiles are there
+  uint64_t* wempty = wfull + kWRing;                               // 4 converting warps have read them
+  uint64_t* afull = wempty + kWRing;                               // first CTA: both CTAs' A tiles are there
   uint64_t* aempty = afull + kRing;                                // the pair's MMAs have read the A tile
   uint64_t* dfull = aempty + kRing;                                // [2] accumulator final
   uint64_t* dempty = dfull + 2;                                    // [2] first CTA: both CTAs have read it out
@@ -195,9 +198,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&xfull[i], 1);
       mbar_init(&xempty[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) {
+    for (int i = 0; i < kWRing; ++i) {
       mbar_init(&wfull[i], 1);
       mbar_init(&wempty[i], 4);
+    }
+    for (int i = 0; i < kRing; ++i) {
       mbar_init(&afull[i], 8);
       mbar_init(&aempty[i], 1);
     }
@@ -261,6 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------- weights: older than the kernel before this one
     if (lane == 0) {
       Walk k(p, pair);
+      const int wring = 1 << p.wshift;
       int i = 0;
       bool ok = true;
       while (ok && k.next(p)) {
@@ -268,18 +274,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         place(p, k.tile, nt, mt);
         const int n0 = nt * 2 * kRows + rank * kRows;
         for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (kRing - 1);
-          if (i >= kRing && !mbar_wait_many(&wempty[s], static_cast<uint32_t>((i >> 2) - 1) & 1u)) {
+          const int s = i & (wring - 1);
+          if (i >= wring && !mbar_wait_many(&wempty[s], static_cast<uint32_t>((i >> p.wshift) - 1) & 1u)) {
             set_status(p.status, FL_ERR_TIMEOUT, 91);
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&wfull[s], kWStage);
-          tma_load_2d(smem + kWOff + s * kWStage, &wmap, g * kBlockK, n0, &wfull[s]);
+          tma_load_2d(smem + p.woff + s * kWStage, &wmap, g * kBlockK, n0, &wfull[s]);
         }
       }
       if (!ok)
-        for (int j = i - kRing; j < i; ++j) mbar_wait(&wfull[j & (kRing - 1)], static_cast<uint32_t>(j >> 2) & 1u);
+        for (int j = i - wring; j < i; ++j) mbar_wait(&wfull[j & (wring - 1)], static_cast<uint32_t>(j >> p.wshift) & 1u);
     }
   } else if (warp == 1) {
     // ---------------- MMAs of the pair
@@ -334,25 +340,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------- codes to f16: thread = weight row = tensor memory lane; every other unit
     const int q = warp & 3, mine = (warp - kConv0) >> 2, r = q * 32 + lane;
     const uint32_t ta = tmem + kACols + (static_cast<uint32_t>(q * 32) << 16);
-    const uint8_t* rows = smem + kWOff + r * 128;
+    const uint8_t* rows = smem + p.woff + r * 128;
     Walk k(p, pair);
     int i = 0;
     bool ok = true;
     while (ok && k.next(p)) {
       for (int g = k.g0; g < k.g1; ++g, ++i) {
         if ((i & 1) != mine) continue;
-        const int s = i & (kRing - 1);
+        const int s = i & (kRing - 1), ws = i & ((1 << p.wshift) - 1);
         const uint32_t ph = static_cast<uint32_t>(i >> 2) & 1u;
-        if (!mbar_wait_many(&wfull[s], ph)) {
+        if (!mbar_wait_many(&wfull[ws], static_cast<uint32_t>(i >> p.wshift) & 1u)) {
           set_status(p.status, FL_ERR_TIMEOUT, 94);
           ok = false;
           break;
         }
         uint4 c[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) c[t] = *reinterpret_cast<const uint4*>(rows + s * kWStage + ((t ^ (r & 7)) << 4));
+        for (int t = 0; t < 8; ++t) c[t] = *reinterpret_cast<const uint4*>(rows + ws * kWStage + ((t ^ (r & 7)) << 4));
         __syncwarp();
-        if (lane == 0) mbar_arrive(&wempty[s]);
+        if (lane == 0) mbar_arrive(&wempty[ws]);
         if (i >= kRing && !mbar_wait_many(&aempty[s], ph ^ 1u)) {
           set_status(p.status, FL_ERR_TIMEOUT, 95);
           ok = false;
@@ -657,6 +663,8 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   const long long tiles = static_cast<long long>(p.mtiles) * p.ntiles;
   if (tiles > 0x7fffffffll / kGroupM || p.ntiles > 0x7fffffff / kGroupM) return FL_ERR_UNSUPPORTED;
   p.xring = kXBytes / (p.BN * 128) < kXRing ? kXBytes / (p.BN * 128) : kXRing;
+  p.wshift = p.BN <= kFew ? 3 : 2;
+  p.woff = p.BN <= kFew ? kXBytesFew : kXBytes;
   const int pairs = flh::sm_count() / 2 < 128 ? flh::sm_count() / 2 : 128;
   p.P = pairs;
   if (tiles * 2 <= pairs) {   // few tiles: each in equal parts

@@ -1,4 +1,4 @@
-// The linear in 8-bit integers for up to 32 tokens: the weights stream once
+// The linear in 8-bit integers for up to 16 tokens: the weights stream once
 // through shared memory into mma.sync.
 //
 // Work unit = (tile of 256 weight rows, 128 columns): 32 KB by one TMA copy and
@@ -28,7 +28,7 @@ template <int NT>   // tiles of 8 tokens
 struct Cfg {
   static constexpr int kXBytes = NT * 2048;
   static constexpr int kStage = kWBytes + kXBytes;
-  static constexpr int kStages = NT <= 2 ? 6 : 5;
+  static constexpr int kStages = 6;
   static constexpr int kBarOff = kStages * kStage;
   static constexpr int kSmem = kBarOff + 2 * kStages * 8 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
@@ -273,12 +273,7 @@ size_t rows_part_bytes(int M) {
 }
 
 int rows_launch(const Call& c, cudaStream_t s) {
-  switch ((c.M + 7) / 8) {
-    case 1: return launch<1>(c, s);
-    case 2: return launch<2>(c, s);
-    case 3: return launch<3>(c, s);
-    default: return launch<4>(c, s);
-  }
+  return c.M <= 8 ? launch<1>(c, s) : launch<2>(c, s);
 }
 
 }  // namespace fl8
