@@ -2,18 +2,21 @@
 // temperature, a mask of allowed tokens, then the largest, the row's log sum exp
 // and the token's log-probability, in one pass over the logits.
 //
-// A CTA owns a run of a row's vocabulary.  It counts the row's history in shared
-// memory, one word a token of its run: how often it stands in the answer, and the
-// top bit for the prompt (so a word that is not 0 is a token that has been seen).
-// Every CTA of a row reads all of its history, out of L2, and keeps what falls into
-// its run.  Biases note the first entry of their list that names a token; entries
-// that name one again are added in list order, by whoever owns the token.  Then the
-// logits pass through registers once: the rules, the store, and a running maximum
-// and sum of exp (x - max) a thread.  The runs' results are joined by the row's
-// last CTA in their order.  Every step of the rules is one fp32 rounding, so that
-// equal logits stay equal and ties are the formula's.  Bound by HBM: the logits in,
-// fp32 out.
-#include <limits>
+// A CTA owns a run of a row's vocabulary, whose logits come into shared memory by
+// one bulk copy, so that the bytes in flight do not depend on registers.
+// Meanwhile it counts the row's history: one word a token of its run, how often it
+// stands in the answer, the top bit for the prompt; whoever counts a token first
+// puts it on a list.  Every CTA of a row reads all of its history, out of L2, and
+// keeps what falls into its run.  Then the listed tokens, and those that a bias
+// names, are changed in shared memory, a thread a token: one in a hundred has a
+// penalty, but two of three warps meet one, so doing it on the way through the run
+// cost 80 instructions a logit (512 rows of 128003: 261 us).  Last the run passes
+// through registers once: temperature, mask, the store, and a running maximum
+// and sum of exp (x - max) a thread.  The runs' results are joined by the row's last
+// CTA in their order.  Every step of the rules is one fp32 rounding, so that equal
+// logits stay equal and ties are the formula's.  Bound by HBM: the logits in, fp32
+// out.
+#include <type_traits>
 
 #include "fl_common.cuh"
 
@@ -21,9 +24,10 @@ using namespace fl;
 
 namespace {
 
-constexpr int kLead = 8;                       // room before a run's first whole vector
+constexpr int kLead = 32;                      // room before a run's first whole vector
 constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one launch
 constexpr int kRunMin = 1024, kRunMax = 16384;
+constexpr int kRunBytes = 65536;               // shared memory of a run: three CTAs an SM
 
 struct Partial {
   float top, sum;
@@ -38,10 +42,11 @@ struct LogitsParams {
   float* logprob;
   Partial* part;      // [row][run]
   int32_t* cnt;       // [row]
+  int32_t* status;
   int64_t xs, os;
   fl_logits_rules r;
   int V, run, runs;   // a run: tokens after the row's first 16-byte boundary
-  int vec_x, vec_out, vec_h;
+  int vec_out, vec_h;
 };
 
 __device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
@@ -54,94 +59,93 @@ __device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
 struct Best {
   float top, sum;
   int index;
-  __device__ void join(const Best& o) {
+  __device__ __forceinline__ void join(const Best& o) {
     const float t = fmaxf(top, o.top), base = t == -INFINITY ? 0.f : t;
     sum = sum * exp_of(top - base) + o.sum * exp_of(o.top - base);
     if (o.top > top || (o.top == top && static_cast<unsigned>(o.index) < static_cast<unsigned>(index))) index = o.index;
     top = t;
   }
-  __device__ void join_warp() {
+  __device__ __forceinline__ void join_warp() {
+    float t = top;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      Best o;
-      o.top = __shfl_xor_sync(0xffffffffu, top, d);
-      o.sum = __shfl_xor_sync(0xffffffffu, sum, d);
-      o.index = __shfl_xor_sync(0xffffffffu, index, d);
-      // the lower lanes' part first, on both sides of the exchange
-      if (threadIdx.x & d) {
-        const Best mine = *this;
-        *this = o;
-        join(mine);
-      } else {
-        join(o);
-      }
-    }
+    for (int d = 16; d; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+    const float base = t == -INFINITY ? 0.f : t;
+    sum *= exp_of(top - base);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);   // (the same sum in every lane)
+    index = static_cast<int>(__reduce_min_sync(0xffffffffu, top == t ? static_cast<unsigned>(index) : 0xffffffffu));
+    top = t;
   }
 };
 
-template <bool BF16>
-__device__ __forceinline__ float load1(const void* row, int v) {
-  if constexpr (BF16)
-    return __uint_as_float(static_cast<uint32_t>(static_cast<const volatile uint16_t*>(row)[v]) << 16);
-  else
-    return static_cast<const volatile float*>(row)[v];
+// Shared memory of a run, in bytes a token: the logits, for history or biases a
+// word (the count; bf16 logits: the changed value), the list of history's tokens.
+__host__ __device__ constexpr int token_bytes(bool bf16, bool history, bool biases) {
+  return (bf16 ? 2 : 4) + (history || (bf16 && biases) ? 4 : 0) + (history ? 2 : 0);
+}
+// ... and a bit for tokens that a bias names and, with bf16, for changed ones.
+__host__ __device__ constexpr int run_bytes(int room, bool bf16, bool history, bool biases) {
+  return room * token_bytes(bf16, history, biases) + room / 32 * 8 + 16;
 }
 
 template <bool BF16, int T>
 __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
   constexpr int W = BF16 ? 8 : 4;    // tokens of a 16-byte vector
-  constexpr int kAhead = BF16 ? 2 : 4;
-  extern __shared__ uint32_t words[];          // [run + kLead] history, then [run + kLead] biases
+  using Raw = std::conditional_t<BF16, uint16_t, float>;
+  extern __shared__ uint4 raw[];
   __shared__ Best warps[T / 32];
-  __shared__ int again, finish;
-  const int tid = threadIdx.x, b = blockIdx.x / p.runs, run = blockIdx.x - b * p.runs;
+  __shared__ int again, finish, listed;
+  __shared__ uint64_t landed;
+  const int tid = threadIdx.x;
+  const uint32_t b = blockIdx.x / static_cast<uint32_t>(p.runs), run = blockIdx.x - b * p.runs;
   const fl_logits_rules& r = p.r;
   const int room = p.run + kLead;
   const bool counts = r.history != nullptr, biases = r.bias_ids != nullptr;
-  uint32_t* seen = words;
-  int* named = reinterpret_cast<int*>(words + (counts ? room : 0));
+  Raw* x = reinterpret_cast<Raw*>(raw);
+  uint32_t* word = reinterpret_cast<uint32_t*>(x + room);
+  uint32_t* named = word + (counts || (BF16 && biases) ? room : 0);   // bits: a bias names the token
+  uint32_t* changed = named + room / 32 + 1;                          // bits: word holds the token's value
+  uint16_t* list = reinterpret_cast<uint16_t*>(changed + room / 32 + 1);
+  if (tid == 0) {
+    again = listed = 0;
+    mbar_init(&landed, 1);
+    fence_mbar_init();
+  }
   if (counts)
-    for (int i = tid; i < room / 4; i += T) reinterpret_cast<uint4*>(seen)[i] = make_uint4(0, 0, 0, 0);
-  if (biases)
-    for (int i = tid; i < room; i += T) named[i] = std::numeric_limits<int>::max();
-  if (tid == 0) again = 0;
+    for (int i = tid; i < room / 4; i += T) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+  if (BF16 || biases)
+    for (int i = tid; i < 2 * (room / 32 + 1); i += T) named[i] = 0;
 
   pdl_wait();
   pdl_launch_dependents();
   const uint8_t* row = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(b) * p.xs * (BF16 ? 2 : 4);
   float* out = p.out ? p.out + static_cast<int64_t>(b) * p.os : nullptr;
-  // the row's first token on 16 bytes; without such rows every token goes alone
-  const int head = p.vec_x ? min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (BF16 ? 2 : 4), p.V) : 0;
-  const int64_t first = head + static_cast<int64_t>(run) * p.run;      // of the run's vectors
-  const int lo = run == 0 ? 0 : static_cast<int>(min(first, static_cast<int64_t>(p.V)));
-  const int hi = static_cast<int>(min(first + p.run, static_cast<int64_t>(p.V)));
-  const int base = static_cast<int>(min(first, static_cast<int64_t>(p.V))) - kLead;    // token of word 0
-  const int nvec = p.vec_x && hi > base + kLead ? (hi - base - kLead) / W : 0;
-
-  // the first vectors are on their way while the history is counted
-  uint4 ahead[kAhead];
-  auto fetch = [&](int j) {
-    if (j >= nvec) return make_uint4(0, 0, 0, 0);
-    uint4 f;
-    asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(f.x), "=r"(f.y), "=r"(f.z), "=r"(f.w)
-                 : "l"(row + (base + kLead + static_cast<int64_t>(j) * W) * (BF16 ? 2 : 4)));
-    return f;
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) ahead[i] = fetch(tid + i * T);
-
+  // the row's first token on 16 bytes; a run starts there or whole runs behind
+  const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (BF16 ? 2 : 4), p.V);
+  const int64_t first = head + static_cast<int64_t>(run) * p.run;
+  const int start = static_cast<int>(min(first, static_cast<int64_t>(p.V)));
+  const int lo = run == 0 ? 0 : start, hi = static_cast<int>(min(first + p.run, static_cast<int64_t>(p.V)));
+  const int base = start - kLead;    // token 0 of shared memory
+  const int nvec = (hi - start) / W, tail = start + nvec * W;
+  if (tid == 0 && nvec) {
+    mbar_arrive_expect_tx(&landed, nvec * 16);
+    bulk_g2s(x + kLead, row + static_cast<int64_t>(start) * (BF16 ? 2 : 4), nvec * 16, &landed);
+  }
+  // the few tokens before the first vector and after the last
+  const int few = (start - lo) + (hi - tail);
+  auto few_at = [&](int i) { return i < start - lo ? lo + i : tail + (i - (start - lo)); };
+  if (tid < few) x[few_at(tid) - base] = reinterpret_cast<const volatile Raw*>(row)[few_at(tid)];
   __syncthreads();
+
   if (counts) {
     const int n = min(max(r.history_lens[b], 0), r.history_max);
     const int prompt = r.prompt_lens ? min(max(r.prompt_lens[b], 0), n) : 0;
     const int32_t* h = r.history + static_cast<int64_t>(b) * r.history_stride;
+    const uint32_t width = hi - lo;
     auto count = [&](int id, int at) {
-      if (id >= lo && id < hi) {
-        if (at < prompt)
-          atomicOr(seen + (id - base), 0x80000000u);
-        else
-          atomicAdd(seen + (id - base), 1u);
+      if (static_cast<uint32_t>(id - lo) < width) {
+        const uint32_t old = at < prompt ? atomicOr(word + (id - base), 0x80000000u) : atomicAdd(word + (id - base), 1u);
+        if (old == 0) list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(id - base);
       }
     };
     int i0 = 0;
@@ -161,123 +165,129 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
     bias_hi = min(max(r.bias_offsets[b + 1], bias_lo), r.bias_count);
     for (int i = bias_lo + tid; i < bias_hi; i += T) {
       const int id = __ldg(r.bias_ids + i);
-      if (id >= lo && id < hi && atomicMin(named + (id - base), i) != std::numeric_limits<int>::max()) again = 1;
+      if (id >= lo && id < hi) {
+        const uint32_t bit = 1u << ((id - base) & 31);
+        if (atomicOr(named + ((id - base) >> 5), bit) & bit) again = 1;
+      }
     }
   }
-  __syncthreads();
+  if (tid == 0 && nvec && !mbar_wait(&landed, 0)) set_status(p.status, FL_ERR_TIMEOUT, 60);
+  __syncthreads();   // (counted, listed, landed)
 
-  const float rep = r.repetition ? r.repetition[b] : 1.f, freq = r.frequency ? r.frequency[b] : 0.f;
-  const float pres = r.presence ? r.presence[b] : 0.f;
+  auto value = [&](int i) {   // of token base + i
+    if constexpr (BF16) {
+      if (changed[i >> 5] >> (i & 31) & 1) return __uint_as_float(word[i]);
+      return __uint_as_float(static_cast<uint32_t>(x[i]) << 16);
+    } else {
+      return x[i];
+    }
+  };
+  auto change = [&](int i, float v) {
+    if constexpr (BF16) {
+      word[i] = __float_as_uint(v);
+      atomicOr(changed + (i >> 5), 1u << (i & 31));
+    } else {
+      x[i] = v;
+    }
+  };
+  if (counts) {
+    const float rep = r.repetition ? r.repetition[b] : 1.f, freq = r.frequency ? r.frequency[b] : 0.f;
+    const float pres = r.presence ? r.presence[b] : 0.f;
+    for (int j = tid; j < listed; j += T) {
+      const int i = list[j];
+      const uint32_t c = word[i] & 0x7fffffffu;
+      float v = value(i);
+      if (r.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+      if (c) {
+        if (r.frequency) v = __fsub_rn(v, __fmul_rn(freq, static_cast<float>(c)));
+        if (r.presence) v = __fsub_rn(v, pres);
+      }
+      change(i, v);
+    }
+    __syncthreads();
+  }
+  if (biases) {
+    // a token that is named again gets its biases in list order, from one thread
+    const bool several = again != 0;
+    for (int i = several ? bias_lo : bias_lo + tid; i < bias_hi; i += several ? 1 : T) {
+      const int id = __ldg(r.bias_ids + i);
+      if (id >= lo && id < hi && (!several || id % T == tid)) change(id - base, __fadd_rn(value(id - base), __ldg(r.bias + i)));
+    }
+    __syncthreads();
+  }
+
   float inv = 1.f;
   if (r.temperature) {
     const float t = r.temperature[b];
     inv = t > 0.f ? __fdiv_rn(1.f, t) : 1.f;
   }
   const uint32_t* mask = r.allowed ? reinterpret_cast<const uint32_t*>(r.allowed) + static_cast<int64_t>(b) * r.allowed_stride : nullptr;
-  const int several = again;
   Best best = {-INFINITY, 0.f, -1};
-
-  auto penalty = [&](float x, uint32_t w) {
-    if (r.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-    const uint32_t c = w & 0x7fffffffu;
-    if (c) {
-      if (r.frequency) x = __fsub_rn(x, __fmul_rn(freq, static_cast<float>(c)));
-      if (r.presence) x = __fsub_rn(x, pres);
-    }
-    return x;
-  };
-  auto biased = [&](float x, int v, int i) {
-    x = __fadd_rn(x, __ldg(r.bias + i));
-    if (several)
-      for (int j = i + 1; j < bias_hi; ++j)
-        if (__ldg(r.bias_ids + j) == v) x = __fadd_rn(x, __ldg(r.bias + j));
-    return x;
-  };
   auto one = [&](int v) {   // a token outside the vectors
-    float x = load1<BF16>(row, v);
-    if (counts && seen[v - base]) x = penalty(x, seen[v - base]);
-    if (biases && named[v - base] != std::numeric_limits<int>::max()) x = biased(x, v, named[v - base]);
-    x = __fmul_rn(x, inv);
-    if (mask && !(__ldg(mask + (v >> 5)) >> (v & 31) & 1)) x = -INFINITY;
-    if (out) out[v] = x;
-    best.join(Best{x == x ? x : -INFINITY, x == x ? (x == -INFINITY ? 0.f : 1.f) : x, x > -INFINITY ? v : -1});
+    float f = __fmul_rn(value(v - base), inv);
+    if (mask && !(__ldg(mask + (v >> 5)) >> (v & 31) & 1)) f = -INFINITY;
+    if (out) out[v] = f;
+    best.join(Best{f == f ? f : -INFINITY, f == f ? (f == -INFINITY ? 0.f : 1.f) : f, f > -INFINITY ? v : -1});
   };
-  // a run's tokens in ascending order a thread: head, vectors, tail
-  if (tid < base + kLead - lo) one(lo + tid);
-  auto vector = [&](int j, const uint4& f) {
+  auto vector = [&](int j) {
     const int at = kLead + j * W, v = base + at;
-    float x[W];
+    const uint4 u = *reinterpret_cast<const uint4*>(x + at);
+    float f[W];
     if constexpr (BF16) {
 #pragma unroll
-      for (int e = 0; e < W; ++e) x[e] = __uint_as_float(e & 1 ? (&f.x)[e / 2] & 0xffff0000u : (&f.x)[e / 2] << 16);
-    } else {
+      for (int e = 0; e < W; ++e) f[e] = __uint_as_float(e & 1 ? (&u.x)[e / 2] & 0xffff0000u : (&u.x)[e / 2] << 16);
+      if (counts || biases) {
+        const uint32_t bits = reinterpret_cast<const uint8_t*>(changed)[at / 8];
+        if (bits) {
 #pragma unroll
-      for (int e = 0; e < W; ++e) x[e] = __uint_as_float((&f.x)[e]);
-    }
-    if (counts) {
-#pragma unroll
-      for (int q = 0; q < W / 4; ++q) {
-        const uint4 w = reinterpret_cast<const uint4*>(seen + at)[q];
-        if (w.x | w.y | w.z | w.w) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((&w.x)[e]) x[4 * q + e] = penalty(x[4 * q + e], (&w.x)[e]);
+          for (int e = 0; e < W; ++e)
+            if (bits >> e & 1) f[e] = __uint_as_float(word[at + e]);
         }
       }
-    }
-    if (biases) {
+    } else {
 #pragma unroll
-      for (int e = 0; e < W; ++e)
-        if (named[at + e] != std::numeric_limits<int>::max()) x[e] = biased(x[e], v + e, named[at + e]);
+      for (int e = 0; e < W; ++e) f[e] = __uint_as_float((&u.x)[e]);
     }
 #pragma unroll
-    for (int e = 0; e < W; ++e) x[e] = __fmul_rn(x[e], inv);
+    for (int e = 0; e < W; ++e) f[e] = __fmul_rn(f[e], inv);
     if (mask) {
       const uint32_t w0 = __ldg(mask + (v >> 5));
       const uint32_t w1 = (v & 31) + W > 32 ? __ldg(mask + (v >> 5) + 1) : 0;
       const uint32_t bits = __funnelshift_r(w0, w1, v & 31);
 #pragma unroll
       for (int e = 0; e < W; ++e)
-        if (!(bits >> e & 1)) x[e] = -INFINITY;
+        if (!(bits >> e & 1)) f[e] = -INFINITY;
     }
     if (out) {
       if (p.vec_out) {
 #pragma unroll
         for (int q = 0; q < W / 4; ++q)
-          __stcs(reinterpret_cast<float4*>(out + v) + q, make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]));
+          __stcs(reinterpret_cast<float4*>(out + v) + q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
       } else {
 #pragma unroll
-        for (int e = 0; e < W; ++e) out[v + e] = x[e];
+        for (int e = 0; e < W; ++e) out[v + e] = f[e];
       }
     }
-    float top = x[0];
+    float top = f[0];
 #pragma unroll
-    for (int e = 1; e < W; ++e) top = fmaxf(top, x[e]);
+    for (int e = 1; e < W; ++e) top = fmaxf(top, f[e]);
     if (top > best.top) {
       best.sum *= exp_of(best.top - top);
       best.top = top;
 #pragma unroll
       for (int e = W - 1; e >= 0; --e)
-        if (x[e] == top) best.index = v + e;
+        if (f[e] == top) best.index = v + e;
     }
     const float zero = best.top == -INFINITY ? 0.f : best.top;
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < W; ++e) sum += exp_of(x[e] - zero);
+    for (int e = 0; e < W; ++e) sum += exp_of(f[e] - zero);
     best.sum += sum;
   };
-  for (int j = tid; j < nvec; j += kAhead * T) {
-    uint4 now[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      now[i] = ahead[i];
-      ahead[i] = fetch(j + (kAhead + i) * T);
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (j + i * T < nvec) vector(j + i * T, now[i]);
-  }
-  for (int v = base + kLead + nvec * W + tid; v < hi; v += T) one(v);
+  // a thread's tokens in ascending order: before the vectors, these, after them
+  if (tid < start - lo) one(lo + tid);
+  for (int j = tid; j < nvec; j += T) vector(j);
+  if (tid < hi - tail) one(tail + tid);
 
   best.join_warp();
   if ((tid & 31) == 0) warps[tid >> 5] = best;
@@ -323,14 +333,15 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
 
 bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Tokens of a run: the longest that still gives every SM eight of them, so that
-// the history is read by few; short runs where rows are few.
-int run_length(int B, int V) {
+// Tokens of a run: the longest that fits its shared memory and still gives every
+// SM eight of them, so that the history is read by few; short ones where rows are few.
+int run_length(int B, int V, int bytes) {
   const long long want = 8ll * flh::sm_count();
   int run = kRunMax;
-  while (run > kRunMin && (V + run - 1ll) / run * B < want) run /= 2;
+  while (run > kRunMin && (run * bytes > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
 }
+constexpr int kTokenMost = token_bytes(false, true, true);   // the shortest runs
 int run_count(int V, int run) { return static_cast<int>((V + run - 1ll) / run); }
 
 template <bool BF16, int T>
@@ -339,7 +350,7 @@ int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !ready[dev]) {
-    if (cudaFuncSetAttribute(k_logits<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (kRunMax + kLead) * 4) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_logits<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, run_bytes(kRunMax + kLead, BF16, true, true)) != cudaSuccess) {
       cudaGetLastError();
       return FL_ERR_CUDA;
     }
@@ -355,7 +366,7 @@ bool logits_args(int B, int V) { return B >= 1 && V >= 1 && V < (1 << 30) && B <
 extern "C" int fl_logits_process_workspace(int B, int V, size_t* out) {
   if (!out || !logits_args(B, V)) return FL_ERR_ARG;
   const int rows = B < kRowsMax ? B : kRowsMax;
-  *out = kScratchOff + static_cast<size_t>(rows) * run_count(V, run_length(B, V)) * sizeof(Partial);
+  *out = kScratchOff + static_cast<size_t>(rows) * run_count(V, run_length(B, V, kTokenMost)) * sizeof(Partial);
   return FL_OK;
 }
 
@@ -382,19 +393,19 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
 
   LogitsParams p = {};
   p.xs = logits_stride, p.os = out_stride, p.r = r, p.V = V;
-  p.run = run_length(B, V);
+  p.run = run_length(B, V, token_bytes(bf16, r.history, r.bias));
   // a long history is worth longer runs: each of a row's CTAs reads it
   while (r.history && p.run < kRunMax && p.run < r.history_max / 8) p.run *= 2;
   p.runs = run_count(V, p.run);
   p.part = reinterpret_cast<Partial*>(static_cast<uint8_t*>(ws) + kScratchOff);
   p.cnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kTicketOff);
-  p.vec_x = 1;
+  p.status = static_cast<int32_t*>(ws);
   p.vec_h = aligned(r.history, 16) && r.history_stride % 4 == 0;
   // a row's tokens on 16 bytes are so in both (rows shift both alike)
   const int64_t size = bf16 ? 2 : 4;
   const uintptr_t in0 = reinterpret_cast<uintptr_t>(logits) / size, out0 = reinterpret_cast<uintptr_t>(out) / 4;
   p.vec_out = out && (in0 - out0) % 4 == 0 && (logits_stride - out_stride) % 4 == 0;
-  const size_t smem = static_cast<size_t>(p.run + kLead) * 4 * ((r.history ? 1 : 0) + (r.bias ? 1 : 0));
+  const size_t smem = run_bytes(p.run + kLead, bf16, r.history, r.bias);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int b = 0; b < B;) {
     int n = B - b < kRowsMax ? B - b : kRowsMax;
@@ -407,7 +418,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     auto row = [&](auto*& list, int64_t stride) { if (list) list += b * stride; };
     row(q.r.history, r.history_stride), row(q.r.history_lens, 1), row(q.r.prompt_lens, 1), row(q.r.repetition, 1);
     row(q.r.frequency, 1), row(q.r.presence, 1), row(q.r.bias_offsets, 1), row(q.r.allowed, r.allowed_stride), row(q.r.temperature, 1);
-    const int rc = p.run > 2048 ? (bf16 ? launch<true, 512>(q, n, smem, s) : launch<false, 512>(q, n, smem, s))
+    const int rc = p.run > 4096 ? (bf16 ? launch<true, 512>(q, n, smem, s) : launch<false, 512>(q, n, smem, s))
                                 : (bf16 ? launch<true, 256>(q, n, smem, s) : launch<false, 256>(q, n, smem, s));
     if (rc != FL_OK) return rc;
     b += n;
