@@ -27,7 +27,7 @@ namespace {
 constexpr int kLead = 32;                      // room before a run's first whole vector
 constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one launch
 constexpr int kRunMin = 1024, kRunMax = 16384;
-constexpr int kRunBytes = 65536;               // shared memory of a run: three CTAs an SM
+constexpr int kRunBytes = 73728;               // shared memory of a run: three CTAs an SM
 
 struct Partial {
   float top, sum;
@@ -78,19 +78,19 @@ struct Best {
   }
 };
 
-// Shared memory of a run, in bytes a token: the logits, for history or biases a
-// word (the count; bf16 logits: the changed value), the list of history's tokens.
-__host__ __device__ constexpr int token_bytes(bool bf16, bool history, bool biases) {
-  return (bf16 ? 2 : 4) + (history || (bf16 && biases) ? 4 : 0) + (history ? 2 : 0);
-}
-// ... and a bit for tokens that a bias names and, with bf16, for changed ones.
+// Shared memory of a run of `room` tokens: the logits; for history or biases a
+// word a token (its count; with bf16 logits, the changed value); a list of
+// history's tokens, for a quarter of them; a bit a token for those that a bias
+// names, and with bf16 for changed ones.
+__host__ __device__ constexpr bool has_words(bool bf16, bool history, bool biases) { return history || (bf16 && biases); }
 __host__ __device__ constexpr int run_bytes(int room, bool bf16, bool history, bool biases) {
-  return room * token_bytes(bf16, history, biases) + room / 32 * 8 + 16;
+  return room * ((bf16 ? 2 : 4) + (has_words(bf16, history, biases) ? 4 : 0)) + (history ? room / 2 : 0) + room / 32 * 8 + 16;
 }
 
-template <bool BF16, int T>
-__global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
+template <bool BF16, bool LONG>
+__global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams p) {
   constexpr int W = BF16 ? 8 : 4;    // tokens of a 16-byte vector
+  constexpr int T = LONG ? 1024 : 256;
   using Raw = std::conditional_t<BF16, uint16_t, float>;
   extern __shared__ uint4 raw[];
   __shared__ Best warps[T / 32];
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
   const bool counts = r.history != nullptr, biases = r.bias_ids != nullptr;
   Raw* x = reinterpret_cast<Raw*>(raw);
   uint32_t* word = reinterpret_cast<uint32_t*>(x + room);
-  uint32_t* named = word + (counts || (BF16 && biases) ? room : 0);   // bits: a bias names the token
+  uint32_t* named = word + (has_words(BF16, counts, biases) ? room : 0);   // bits: a bias names the token
   uint32_t* changed = named + room / 32 + 1;                          // bits: word holds the token's value
   uint16_t* list = reinterpret_cast<uint16_t*>(changed + room / 32 + 1);
   if (tid == 0) {
@@ -131,6 +131,26 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
     mbar_arrive_expect_tx(&landed, nvec * 16);
     bulk_g2s(x + kLead, row + static_cast<int64_t>(start) * (BF16 ? 2 : 4), nvec * 16, &landed);
   }
+  // the history's entries, four at a time; the first are on their way before the
+  // lengths are known (lists are history_max long whatever of them counts)
+  constexpr int kAhead = 4;
+  int4 ahead[kAhead];
+  int n = 0, prompt = 0;
+  const int32_t* h = r.history + static_cast<int64_t>(b) * r.history_stride;
+  auto fetch = [&](int i) {
+    if (p.vec_h && 4 * i + 4 <= r.history_max) return __ldg(reinterpret_cast<const int4*>(h) + i);
+    int4 f = make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (4 * i + e < r.history_max) (&f.x)[e] = __ldg(h + 4 * i + e);
+    return f;
+  };
+  if (counts) {
+    n = min(max(__ldg(r.history_lens + b), 0), r.history_max);
+    prompt = r.prompt_lens ? max(__ldg(r.prompt_lens + b), 0) : 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ahead[k] = fetch(tid + k * T);
+  }
   // the few tokens before the first vector and after the last
   const int few = (start - lo) + (hi - tail);
   auto few_at = [&](int i) { return i < start - lo ? lo + i : tail + (i - (start - lo)); };
@@ -138,26 +158,35 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
   __syncthreads();
 
   if (counts) {
-    const int n = min(max(r.history_lens[b], 0), r.history_max);
-    const int prompt = r.prompt_lens ? min(max(r.prompt_lens[b], 0), n) : 0;
-    const int32_t* h = r.history + static_cast<int64_t>(b) * r.history_stride;
     const uint32_t width = hi - lo;
-    auto count = [&](int id, int at) {
-      if (static_cast<uint32_t>(id - lo) < width) {
-        const uint32_t old = at < prompt ? atomicOr(word + (id - base), 0x80000000u) : atomicAdd(word + (id - base), 1u);
-        if (old == 0) list[atomicAdd(&listed, 1)] = static_cast<uint16_t>(id - base);
+    for (int i = tid; 4 * i < n; i += kAhead * T) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int id = (&ahead[k].x)[e], at = 4 * (i + k * T) + e;
+          if (static_cast<uint32_t>(id - lo) < width && at < n) {
+            uint32_t* w = word + (id - base);
+            if constexpr (LONG) {
+              if (at < prompt)
+                atomicOr(w, 0x80000000u);
+              else
+                atomicAdd(w, 1u);
+            } else {
+              const uint32_t old = at < prompt ? atomicOr(w, 0x80000000u) : atomicAdd(w, 1u);
+              if (old == 0) {
+                const int to = atomicAdd(&listed, 1);
+                if (to < room / 4) list[to] = static_cast<uint16_t>(id - base);
+              }
+            }
+          }
+        }
       }
-    };
-    int i0 = 0;
-    if (p.vec_h) {
-#pragma unroll 4
-      for (int i = tid; i < n / 4; i += T) {
-        const int4 f = __ldg(reinterpret_cast<const int4*>(h) + i);
-        count(f.x, 4 * i), count(f.y, 4 * i + 1), count(f.z, 4 * i + 2), count(f.w, 4 * i + 3);
+      if (4 * (i + kAhead * T) < n) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) ahead[k] = fetch(i + (kAhead + k) * T);
       }
-      i0 = n / 4 * 4;
     }
-    for (int i = i0 + tid; i < n; i += T) count(__ldg(h + i), i);
   }
   int bias_lo = 0, bias_hi = 0;
   if (biases) {
@@ -193,8 +222,7 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
   if (counts) {
     const float rep = r.repetition ? r.repetition[b] : 1.f, freq = r.frequency ? r.frequency[b] : 0.f;
     const float pres = r.presence ? r.presence[b] : 0.f;
-    for (int j = tid; j < listed; j += T) {
-      const int i = list[j];
+    auto penalise = [&](int i) {
       const uint32_t c = word[i] & 0x7fffffffu;
       float v = value(i);
       if (r.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
@@ -203,7 +231,29 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
         if (r.presence) v = __fsub_rn(v, pres);
       }
       change(i, v);
+    };
+    // a long history comes back to the same tokens again and again: there the counts
+    // are looked through for the tokens, not asked for with every entry
+    if (LONG || listed > room / 4) {
+      __syncthreads();
+      if (tid == 0) listed = 0;
+      __syncthreads();
+      for (int i = tid; i < room / 4; i += T) {
+        const uint4 w = reinterpret_cast<const uint4*>(word)[i];
+        if (!(w.x | w.y | w.z | w.w)) continue;
+#pragma unroll 1
+        for (int e = 0; e < 4; ++e) {
+          if (!(e & 2 ? (e & 1 ? w.w : w.z) : (e & 1 ? w.y : w.x))) continue;
+          const int at = atomicAdd(&listed, 1);
+          if (at < room / 4)
+            list[at] = static_cast<uint16_t>(4 * i + e);
+          else   // (the list is full)
+            penalise(4 * i + e);
+        }
+      }
+      __syncthreads();
     }
+    for (int j = tid; j < min(listed, room / 4); j += T) penalise(list[j]);
     __syncthreads();
   }
   if (biases) {
@@ -333,30 +383,32 @@ __global__ void __launch_bounds__(T) k_logits(const LogitsParams p) {
 
 bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Tokens of a run: the longest that fits its shared memory and still gives every
-// SM eight of them, so that the history is read by few; short ones where rows are few.
-int run_length(int B, int V, int bytes) {
-  const long long want = 8ll * flh::sm_count();
+// Tokens of a run: the longest that fits its shared memory and still gives the
+// GPU CTAs enough; short ones where rows are few.  Each of a row's CTAs reads all of
+// its history: with a long one a CTA an SM is enough.
+constexpr int kLong = 8192;      // entries; from there on 1024 threads
+int run_length(int B, int V, bool bf16, bool history, bool biases, int history_max) {
+  const long long want = (history && history_max >= kLong ? 1ll : 4ll) * flh::sm_count();
   int run = kRunMax;
-  while (run > kRunMin && (run * bytes > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
+  while (run > kRunMin && (run_bytes(run, bf16, history, biases) > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
 }
-constexpr int kTokenMost = token_bytes(false, true, true);   // the shortest runs
+int run_shortest(int B, int V) { return run_length(B, V, false, true, true, 0); }
 int run_count(int V, int run) { return static_cast<int>((V + run - 1ll) / run); }
 
-template <bool BF16, int T>
+template <bool BF16, bool LONG>
 int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
   static bool ready[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !ready[dev]) {
-    if (cudaFuncSetAttribute(k_logits<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, run_bytes(kRunMax + kLead, BF16, true, true)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_logits<BF16, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, run_bytes(kRunMax + kLead, BF16, true, true)) != cudaSuccess) {
       cudaGetLastError();
       return FL_ERR_CUDA;
     }
     ready[dev] = true;
   }
-  return flh::launch_early(k_logits<BF16, T>, dim3(static_cast<unsigned>(B) * p.runs), dim3(T), smem, s, p);
+  return flh::launch_early(k_logits<BF16, LONG>, dim3(static_cast<unsigned>(B) * p.runs), dim3(LONG ? 1024 : 256), smem, s, p);
 }
 
 bool logits_args(int B, int V) { return B >= 1 && V >= 1 && V < (1 << 30) && B <= (1 << 30); }
@@ -366,7 +418,7 @@ bool logits_args(int B, int V) { return B >= 1 && V >= 1 && V < (1 << 30) && B <
 extern "C" int fl_logits_process_workspace(int B, int V, size_t* out) {
   if (!out || !logits_args(B, V)) return FL_ERR_ARG;
   const int rows = B < kRowsMax ? B : kRowsMax;
-  *out = kScratchOff + static_cast<size_t>(rows) * run_count(V, run_length(B, V, kTokenMost)) * sizeof(Partial);
+  *out = kScratchOff + static_cast<size_t>(rows) * run_count(V, run_shortest(B, V)) * sizeof(Partial);
   return FL_OK;
 }
 
@@ -393,9 +445,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
 
   LogitsParams p = {};
   p.xs = logits_stride, p.os = out_stride, p.r = r, p.V = V;
-  p.run = run_length(B, V, token_bytes(bf16, r.history, r.bias));
-  // a long history is worth longer runs: each of a row's CTAs reads it
-  while (r.history && p.run < kRunMax && p.run < r.history_max / 8) p.run *= 2;
+  p.run = run_length(B, V, bf16, r.history, r.bias, r.history_max);
   p.runs = run_count(V, p.run);
   p.part = reinterpret_cast<Partial*>(static_cast<uint8_t*>(ws) + kScratchOff);
   p.cnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kTicketOff);
@@ -418,8 +468,9 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     auto row = [&](auto*& list, int64_t stride) { if (list) list += b * stride; };
     row(q.r.history, r.history_stride), row(q.r.history_lens, 1), row(q.r.prompt_lens, 1), row(q.r.repetition, 1);
     row(q.r.frequency, 1), row(q.r.presence, 1), row(q.r.bias_offsets, 1), row(q.r.allowed, r.allowed_stride), row(q.r.temperature, 1);
-    const int rc = p.run > 4096 ? (bf16 ? launch<true, 512>(q, n, smem, s) : launch<false, 512>(q, n, smem, s))
-                                : (bf16 ? launch<true, 256>(q, n, smem, s) : launch<false, 256>(q, n, smem, s));
+    const bool wide = r.history && r.history_max >= kLong;
+    const int rc = wide ? (bf16 ? launch<true, true>(q, n, smem, s) : launch<false, true>(q, n, smem, s))
+                        : (bf16 ? launch<true, false>(q, n, smem, s) : launch<false, false>(q, n, smem, s));
     if (rc != FL_OK) return rc;
     b += n;
   }
