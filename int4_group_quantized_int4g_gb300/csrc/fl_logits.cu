@@ -79,18 +79,21 @@ struct Best {
 };
 
 // Shared memory of a run of `room` tokens: the logits; for history or biases a
-// word a token (its count; with bf16 logits, the changed value); a list of
-// history's tokens, for a quarter of them; a bit a token for those that a bias
-// names, and with bf16 for changed ones.
-__host__ __device__ constexpr bool has_words(bool bf16, bool history, bool biases) { return history || (bf16 && biases); }
-__host__ __device__ constexpr int run_bytes(int room, bool bf16, bool history, bool biases) {
-  return room * ((bf16 ? 2 : 4) + (has_words(bf16, history, biases) ? 4 : 0)) + (history ? room / 2 : 0) + room / 32 * 8 + 16;
+// word a token (its count, 16 bits with fp32 logits and few entries; with bf16
+// logits the changed value); a list of history's tokens, for a quarter of them; a
+// bit a token for those that a bias names, and with bf16 for changed ones.
+__host__ __device__ constexpr int word_bytes(bool bf16, bool history, bool biases, bool many) {
+  return history ? (bf16 || many ? 4 : 2) : (bf16 && biases ? 4 : 0);
+}
+__host__ __device__ constexpr int run_bytes(int room, bool bf16, bool history, bool biases, bool many) {
+  return room * ((bf16 ? 2 : 4) + word_bytes(bf16, history, biases, many)) + (history ? room / 2 : 0) + room / 32 * 8 + 16;
 }
 
 template <bool BF16, bool LONG>
 __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams p) {
   constexpr int W = BF16 ? 8 : 4;    // tokens of a 16-byte vector
   constexpr int T = LONG ? 1024 : 256;
+  constexpr bool HALF = !BF16 && !LONG;   // counts of 16 bits
   using Raw = std::conditional_t<BF16, uint16_t, float>;
   extern __shared__ uint4 raw[];
   __shared__ Best warps[T / 32];
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
   const bool counts = r.history != nullptr, biases = r.bias_ids != nullptr;
   Raw* x = reinterpret_cast<Raw*>(raw);
   uint32_t* word = reinterpret_cast<uint32_t*>(x + room);
-  uint32_t* named = word + (has_words(BF16, counts, biases) ? room : 0);   // bits: a bias names the token
+  uint32_t* named = word + room * word_bytes(BF16, counts, biases, LONG) / 4;   // bits: a bias names the token
   uint32_t* changed = named + room / 32 + 1;                          // bits: word holds the token's value
   uint16_t* list = reinterpret_cast<uint16_t*>(changed + room / 32 + 1);
   if (tid == 0) {
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
     fence_mbar_init();
   }
   if (counts)
-    for (int i = tid; i < room / 4; i += T) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < room / (HALF ? 8 : 4); i += T) reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
   if (BF16 || biases)
     for (int i = tid; i < 2 * (room / 32 + 1); i += T) named[i] = 0;
 
@@ -166,17 +169,19 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
         for (int e = 0; e < 4; ++e) {
           const int id = (&ahead[k].x)[e], at = 4 * (i + k * T) + e;
           if (static_cast<uint32_t>(id - lo) < width && at < n) {
-            uint32_t* w = word + (id - base);
+            const int i1 = id - base, shift = HALF ? (i1 & 1) * 16 : 0;
+            uint32_t* w = word + (HALF ? i1 >> 1 : i1);
+            const uint32_t flag = HALF ? 0x8000u << shift : 0x80000000u;
             if constexpr (LONG) {
               if (at < prompt)
-                atomicOr(w, 0x80000000u);
+                atomicOr(w, flag);
               else
                 atomicAdd(w, 1u);
             } else {
-              const uint32_t old = at < prompt ? atomicOr(w, 0x80000000u) : atomicAdd(w, 1u);
-              if (old == 0) {
+              const uint32_t old = at < prompt ? atomicOr(w, flag) : atomicAdd(w, 1u << shift);
+              if ((HALF ? old >> shift & 0xffffu : old) == 0) {
                 const int to = atomicAdd(&listed, 1);
-                if (to < room / 4) list[to] = static_cast<uint16_t>(id - base);
+                if (to < room / 4) list[to] = static_cast<uint16_t>(i1);
               }
             }
           }
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
     const float rep = r.repetition ? r.repetition[b] : 1.f, freq = r.frequency ? r.frequency[b] : 0.f;
     const float pres = r.presence ? r.presence[b] : 0.f;
     auto penalise = [&](int i) {
-      const uint32_t c = word[i] & 0x7fffffffu;
+      const uint32_t c = HALF ? word[i >> 1] >> ((i & 1) * 16) & 0x7fffu : word[i] & 0x7fffffffu;
       float v = value(i);
       if (r.repetition) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
       if (c) {
@@ -238,18 +243,13 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
       __syncthreads();
       if (tid == 0) listed = 0;
       __syncthreads();
-      for (int i = tid; i < room / 4; i += T) {
-        const uint4 w = reinterpret_cast<const uint4*>(word)[i];
-        if (!(w.x | w.y | w.z | w.w)) continue;
-#pragma unroll 1
-        for (int e = 0; e < 4; ++e) {
-          if (!(e & 2 ? (e & 1 ? w.w : w.z) : (e & 1 ? w.y : w.x))) continue;
-          const int at = atomicAdd(&listed, 1);
-          if (at < room / 4)
-            list[at] = static_cast<uint16_t>(4 * i + e);
-          else   // (the list is full)
-            penalise(4 * i + e);
-        }
+      for (int i = tid; i < room; i += T) {
+        if (!(HALF ? word[i >> 1] >> ((i & 1) * 16) & 0xffffu : word[i])) continue;
+        const int at = atomicAdd(&listed, 1);
+        if (at < room / 4)
+          list[at] = static_cast<uint16_t>(i);
+        else   // (the list is full)
+          penalise(i);
       }
       __syncthreads();
     }
@@ -387,13 +387,17 @@ bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 // GPU CTAs enough; short ones where rows are few.  Each of a row's CTAs reads all of
 // its history: with a long one a CTA an SM is enough.
 constexpr int kLong = 8192;      // entries; from there on 1024 threads
-int run_length(int B, int V, bool bf16, bool history, bool biases, int history_max) {
-  const long long want = (history && history_max >= kLong ? 1ll : 4ll) * flh::sm_count();
+int run_length(int B, int V, bool bf16, bool history, bool biases, bool many) {
+  const long long want = (many ? 1ll : 4ll) * flh::sm_count();
   int run = kRunMax;
-  while (run > kRunMin && (run_bytes(run, bf16, history, biases) > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
+  while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
 }
-int run_shortest(int B, int V) { return run_length(B, V, false, true, true, 0); }
+int run_shortest(int B, int V) {   // of all types and rules (long histories need fewer CTAs)
+  const int a = run_length(B, V, false, true, true, false), b = run_length(B, V, true, true, true, false);
+  const int c = run_length(B, V, false, true, true, true);
+  return a < b ? (a < c ? a : c) : (b < c ? b : c);
+}
 int run_count(int V, int run) { return static_cast<int>((V + run - 1ll) / run); }
 
 template <bool BF16, bool LONG>
@@ -402,7 +406,7 @@ int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !ready[dev]) {
-    if (cudaFuncSetAttribute(k_logits<BF16, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, run_bytes(kRunMax + kLead, BF16, true, true)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k_logits<BF16, LONG>, cudaFuncAttributeMaxDynamicSharedMemorySize, run_bytes(kRunMax + kLead, BF16, true, true, LONG)) != cudaSuccess) {
       cudaGetLastError();
       return FL_ERR_CUDA;
     }
@@ -445,7 +449,8 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
 
   LogitsParams p = {};
   p.xs = logits_stride, p.os = out_stride, p.r = r, p.V = V;
-  p.run = run_length(B, V, bf16, r.history, r.bias, r.history_max);
+  const bool many = r.history && r.history_max >= kLong;
+  p.run = run_length(B, V, bf16, r.history, r.bias, many);
   p.runs = run_count(V, p.run);
   p.part = reinterpret_cast<Partial*>(static_cast<uint8_t*>(ws) + kScratchOff);
   p.cnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kTicketOff);
@@ -455,7 +460,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
   const int64_t size = bf16 ? 2 : 4;
   const uintptr_t in0 = reinterpret_cast<uintptr_t>(logits) / size, out0 = reinterpret_cast<uintptr_t>(out) / 4;
   p.vec_out = out && (in0 - out0) % 4 == 0 && (logits_stride - out_stride) % 4 == 0;
-  const size_t smem = run_bytes(p.run + kLead, bf16, r.history, r.bias);
+  const size_t smem = run_bytes(p.run + kLead, bf16, r.history, r.bias, many);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int b = 0; b < B;) {
     int n = B - b < kRowsMax ? B - b : kRowsMax;
@@ -468,8 +473,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     auto row = [&](auto*& list, int64_t stride) { if (list) list += b * stride; };
     row(q.r.history, r.history_stride), row(q.r.history_lens, 1), row(q.r.prompt_lens, 1), row(q.r.repetition, 1);
     row(q.r.frequency, 1), row(q.r.presence, 1), row(q.r.bias_offsets, 1), row(q.r.allowed, r.allowed_stride), row(q.r.temperature, 1);
-    const bool wide = r.history && r.history_max >= kLong;
-    const int rc = wide ? (bf16 ? launch<true, true>(q, n, smem, s) : launch<false, true>(q, n, smem, s))
+    const int rc = many ? (bf16 ? launch<true, true>(q, n, smem, s) : launch<false, true>(q, n, smem, s))
                         : (bf16 ? launch<true, false>(q, n, smem, s) : launch<false, false>(q, n, smem, s));
     if (rc != FL_OK) return rc;
     b += n;
