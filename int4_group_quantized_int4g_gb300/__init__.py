@@ -751,6 +751,14 @@ def _matrix(t, dtype, name):
     return t.data_ptr(), st[0] if n > 1 else w   # (the stride of a single row means nothing)
 
 
+def _row(t, dtype, n, name):
+    """Address of a contiguous CUDA tensor of n entries."""
+    if t.numel() != n or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _raise(name, f"expected a contiguous {dtype} CUDA tensor of {n} entries, got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, "
+                     f"on {t.device}")
+    return t.data_ptr()
+
+
 def fl_int8_quantize(x):
     """(codes int8 [M, K], scale fp32 [M]) of bf16 x [M, K]: scale = fp32(max |x| /
     127) of the row, code = the nearest whole number to x / scale, ties to even.
@@ -797,12 +805,8 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         xp, xs = _matrix(x, torch.bfloat16, "x")
     else:
         xp, xs = _matrix(x, torch.int8, "x")
-        if x_scale.numel() != M:
-            _raise("fl_int8_linear", "x_scale is [M]")
-        sp = _ptr(x_scale, torch.float32, "x_scale")
-    if w_scale.numel() != N:
-        _raise("fl_int8_linear", "w_scale is [N]")
-    wp, tp = _ptr(w, torch.int8, "w"), _ptr(w_scale, torch.float32, "w_scale")
+        sp = _row(x_scale, torch.float32, M, "x_scale")
+    wp, tp = _ptr(w, torch.int8, "w"), _row(w_scale, torch.float32, N, "w_scale")
     if y is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16
@@ -856,75 +860,80 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     the largest, -1 where none is left), "lse" and "logprob" (fp32 [B]).
     ws: as for fl_int8_linear."""
     torch = _torch()
+    name = "fl_logits_process"
     if logits.dim() != 2:
-        _raise("fl_logits_process", "logits are [B, V]")
+        _raise(name, "logits are [B, V]")
     B, V = logits.shape
-    device = _here(logits, "fl_logits_process")
+    device = _here(logits, name)
     i32, f32 = torch.int32, torch.float32
     bf16 = logits.dtype is torch.bfloat16
     lp, ls = _matrix(logits, torch.bfloat16 if bf16 else f32, "logits")
-
-    def rows(t, dtype, name, n=B):
-        if t is None:
-            return 0
-        if t.numel() != n:
-            _raise("fl_logits_process", f"{name} has {n} entries")
-        return _ptr(t, dtype, name)
-
-    hp, hs, most, ap, stride = 0, 0, 0, 0, 0
-    if (history is None) != (history_lens is None):
-        _raise("fl_logits_process", "history and history_lens go together")
+    hp = hs = most = nl = np = rp = fp = pp = bo = bi = bp = count = ap = stride = tp = 0
     if history is not None:
+        if history_lens is None:
+            _raise(name, "history and history_lens go together")
         if history.dim() != 2 or history.shape[0] != B:
-            _raise("fl_logits_process", "history is [B, longest]")
+            _raise(name, "history is [B, longest]")
         hp, hs = _matrix(history, i32, "history")
         most = history.shape[1]
-        hp = hp or history_lens.data_ptr()   # (an empty tensor has no address, and nothing is read)
-    elif prompt_lens is not None or repetition is not None or frequency is not None or presence is not None:
-        _raise("fl_logits_process", "penalties need a history")
-    if (bias is None) != (bias_ids is None) or (bias is None) != (bias_offsets is None):
-        _raise("fl_logits_process", "bias, bias_ids and bias_offsets go together")
-    count = 0
-    if bias is not None:
+        nl = _row(history_lens, i32, B, "history_lens")
+        hp = hp or nl                        # (an empty tensor has no address, and nothing is read)
+        if prompt_lens is not None:
+            np = _row(prompt_lens, i32, B, "prompt_lens")
+        if repetition is not None:
+            rp = _row(repetition, f32, B, "repetition")
+        if frequency is not None:
+            fp = _row(frequency, f32, B, "frequency")
+        if presence is not None:
+            pp = _row(presence, f32, B, "presence")
+    elif history_lens is not None or prompt_lens is not None or repetition is not None or frequency is not None or presence is not None:
+        _raise(name, "penalties and lengths need a history")
+    if bias is not None or bias_ids is not None or bias_offsets is not None:
+        if bias is None or bias_ids is None or bias_offsets is None:
+            _raise(name, "bias, bias_ids and bias_offsets go together")
         count = bias.numel()
-        if bias_ids.numel() != count:
-            _raise("fl_logits_process", "bias and bias_ids differ in length")
+        bi, bo = _row(bias_ids, i32, count, "bias_ids"), _row(bias_offsets, i32, B + 1, "bias_offsets")
+        bp = _row(bias, f32, count, "bias")
         if count == 0:
-            bias = bias_ids = bias_offsets = None
+            bo = bi = bp = 0
     if allowed is not None:
         if allowed.dim() != 2 or allowed.shape[0] != B or allowed.shape[1] < (V + 31) // 32:
-            _raise("fl_logits_process", "allowed is [B, ceil(V / 32)]")
+            _raise(name, "allowed is [B, ceil(V / 32)]")
         ap, stride = _matrix(allowed, i32, "allowed")
-    rules = _LOGITS_RULES.pack(
-        hp, rows(history_lens, i32, "history_lens"), rows(prompt_lens, i32, "prompt_lens"), rows(repetition, f32, "repetition"),
-        rows(frequency, f32, "frequency"), rows(presence, f32, "presence"), rows(bias_offsets, i32, "bias_offsets", B + 1),
-        _ptr(bias_ids, i32, "bias_ids") if bias_ids is not None else 0, _ptr(bias, f32, "bias") if bias is not None else 0,
-        ap, rows(temperature, f32, "temperature"), hs, stride, most, count)
+    if temperature is not None:
+        tp = _row(temperature, f32, B, "temperature")
     got = {}
-    op, os_ = None, 0
+    op = os_ = 0
     if out is not None:
         if out.shape != logits.shape:
-            _raise("fl_logits_process", "out and logits differ in shape")
+            _raise(name, "out and logits differ in shape")
         got["logits"] = out
         op, os_ = _matrix(out, f32, "out")
     elif need_logits:
         out = got["logits"] = torch.empty((B, V), dtype=f32, device=device)
         op, os_ = out.data_ptr(), V
-    token = got["token"] = torch.empty((B,), dtype=i32, device=device)
-    lse, logprob = torch.empty((2, B), dtype=f32, device=device).unbind()
-    got["lse"], got["logprob"] = lse, logprob
+    token = got["token"] = torch.empty(B, dtype=i32, device=device)
+    lse = got["lse"] = torch.empty(B, dtype=f32, device=device)
+    logprob = got["logprob"] = torch.empty(B, dtype=f32, device=device)
     if ws is None:
         ws = _workspace(_logits_workspace(device.index, B, V), device)
-    _check("fl_logits_process",
-           lib().fl_logits_process(lp, ls, FL_OUT_BF16 if bf16 else FL_OUT_FP32, B, V, rules, op, os_, token.data_ptr(),
-                                   lse.data_ptr(), logprob.data_ptr(), _p(ws), ws.numel(), _stream()))
+    rc = lib().fl_logits_process(
+        lp, ls, FL_OUT_BF16 if bf16 else FL_OUT_FP32, B, V,
+        _LOGITS_RULES.pack(hp, nl, np, rp, fp, pp, bo, bi, bp, ap, tp, hs, stride, most, count), op, os_, token.data_ptr(),
+        lse.data_ptr(), logprob.data_ptr(), _p(ws), ws.numel(), _stream())
+    if rc:
+        raise Int4gError(name, rc)
     return got
 
 
 # ------------------------------------------------- pages of the 8-bit cache
 
 _KV8_POOL = struct.Struct("PPPiiii")            # struct fl_kv8_pool
-_KV8_CACHES = struct.Struct("PPPPiiiii4x")      # struct fl_kv8_cache in an array
+
+
+@functools.lru_cache(maxsize=256)
+def _kv8_caches(n):
+    return struct.Struct("@" + "PPPPiiiii4x" * n)   # struct fl_kv8_cache [n]
 
 
 def _pool(where, refs, table, kv_lens, block):
@@ -935,12 +944,6 @@ def _pool(where, refs, table, kv_lens, block):
     slots, most = table.shape
     return _KV8_POOL.pack(_ptr(refs, i32, "refs"), _ptr(table, i32, "table"), _ptr(kv_lens, i32, "kv_lens"), refs.numel(),
                           slots, most, block)
-
-
-def _list(where, t, n, name):
-    if t.numel() != n:
-        _raise(where, f"{name} has {n} entries")
-    return _ptr(t, _TORCH.int32, name) if n else None
 
 
 def _status_block(where, status, device):
@@ -960,8 +963,7 @@ def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None)
     pool = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
     n = seqs.numel()
     _check("fl_kv8_pages_free", lib().fl_kv8_pages_free(
-        pool, _list("fl_kv8_pages_free", seqs, n, "seqs"), _list("fl_kv8_pages_free", keep, n, "keep") if keep is not None else None,
-        n, _status_block("fl_kv8_pages_free", status, refs.device), _stream()))
+        pool, _row(seqs, _TORCH.int32, n, "seqs"), _row(keep, _TORCH.int32, n, "keep") if keep is not None else None, n, _status_block("fl_kv8_pages_free", status, refs.device), _stream()))
 
 
 def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=None):
@@ -972,7 +974,7 @@ def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=Non
     pool = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
     n = parents.numel()
     _check("fl_kv8_pages_fork", lib().fl_kv8_pages_fork(
-        pool, _list("fl_kv8_pages_fork", parents, n, "parents"), _list("fl_kv8_pages_fork", children, n, "children"), n,
+        pool, _row(parents, _TORCH.int32, n, "parents"), _row(children, _TORCH.int32, n, "children"), n,
         _status_block("fl_kv8_pages_fork", status, refs.device), _stream()))
 
 
@@ -1007,7 +1009,7 @@ def fl_kv8_pages_alloc(refs, table, kv_lens, seqs, new_tokens, block, ws=None):
     if ws is None:
         ws = _workspace(_pages_workspace(refs.numel(), *table.shape, block), device)
     _check("fl_kv8_pages_alloc", lib().fl_kv8_pages_alloc(
-        pool, _list("fl_kv8_pages_alloc", seqs, n, "seqs"), _list("fl_kv8_pages_alloc", new_tokens, n, "new_tokens"), n,
+        pool, _row(seqs, torch.int32, n, "seqs"), _row(new_tokens, torch.int32, n, "new_tokens"), n,
         granted.data_ptr() or None, pairs.data_ptr() or None, count.data_ptr(), _p(ws), ws.numel(), _stream()))
     return granted, pairs, count
 
@@ -1046,12 +1048,11 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
     nb, heads, block, dim = shape
     device = _here(k_caches[0], where)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    parts = []
+    flat, scales = [], shape[:2]
     for k, v, a, b in zip(k_caches, v_caches, k_scales, v_scales):
-        if k.shape != shape or v.shape != shape or a.shape != shape[:2] or b.shape != shape[:2]:
+        if k.shape != shape or v.shape != shape or a.shape != scales or b.shape != scales:
             _raise(where, "the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
-        parts.append(_KV8_CACHES.pack(_ptr(k, u8, "k_cache"), _ptr(v, u8, "v_cache"), _ptr(a, f32, "k_scale"),
-                                      _ptr(b, f32, "v_scale"), nb, block, heads, dim, 0))
+        flat += (_ptr(k, u8, "k_cache"), _ptr(v, u8, "v_cache"), _ptr(a, f32, "k_scale"), _ptr(b, f32, "v_scale"), nb, block, heads, dim, 0)
     n = pairs.numel() // 2
-    _check(where, lib().fl_kv8_pages_copy(b"".join(parts), layers, _list(where, pairs, 2 * n, "pairs"),
-                                          _ptr(count, i32, "count"), n, _status_block(where, status, device), _stream()))
+    _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, "pairs"),
+                                          _row(count, i32, 1, "count"), n, _status_block(where, status, device), _stream()))

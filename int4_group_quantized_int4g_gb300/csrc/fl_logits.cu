@@ -27,7 +27,7 @@ namespace {
 constexpr int kLead = 32;                      // room before a run's first whole vector
 constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one launch
 constexpr int kRunMin = 1024, kRunMax = 16384;
-constexpr int kRunBytes = 73728;               // shared memory of a run: three CTAs an SM
+constexpr int kRunBytes = 40960;               // shared memory of a run: five CTAs an SM
 
 struct Partial {
   float top, sum;
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
   }
   // the history's entries, four at a time; the first are on their way before the
   // lengths are known (lists are history_max long whatever of them counts)
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 2;
   int4 ahead[kAhead];
   int n = 0, prompt = 0;
   const int32_t* h = r.history + static_cast<int64_t>(b) * r.history_stride;
