@@ -7,7 +7,7 @@
 // CTA scans the list and the pool with prefix sums: with 1024 threads 4096
 // counts a step, and no more of the pool than the pages that are wanted.  They are
 // bound by latency: a dozen dependent loads and barriers.  The copy moves 16-byte
-// vectors, four in flight a thread, over a grid that fills the GPU; it is bound by
+// vectors, eight in flight a thread, over a grid that fills the GPU; it is bound by
 // HBM: every byte of a page once in and once out.
 #include <limits>
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) k_pages_table(const CompactParams c) {
 // ------------------------------------------------------------------- copy
 constexpr int kLayers = 64;           // caches of one launch
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVecs = 4;          // 16-byte vectors of a thread and step
+constexpr int kCopyVecs = 8;          // 16-byte vectors of a thread and step
 
 struct CopyParams {
   uint8_t* codes[kLayers][2];
