@@ -642,7 +642,9 @@ int fl_logits_process_workspace(int B, int V, size_t* out);
 /* Applies the rules to logits [B, V] and chooses each row's token:
  *   logits  type FL_OUT_BF16 or FL_OUT_FP32, row stride in elements
  *   out     fp32 [B, V], row stride out_stride, the logits after the rules; NULL:
- *           not stored; may be the logits themselves (fp32, the same stride)
+ *           not stored; may be the logits themselves (fp32, the same stride); other
+ *           rows of it over rows of the logits are an FL_ERR_ARG, and so are any
+ *           two ranges that meet with different strides
  *   token   int32 [B]: the largest, the lowest index of equals; -1 where no token
  *           is left (all -inf); a NaN is not chosen
  *   lse     fp32 [B]: log sum exp of the row (-inf without a token), or NULL

@@ -56,7 +56,7 @@ __device__ __forceinline__ uint4 load8(const CodesParams& p, const void* row, in
 }
 
 // A row's quotients are x * up * inv (up: a power of two that keeps rows of tiny
-// values clear of subnormal numbers); twice: 2 * scale * up.
+// values clear of subnormal numbers, and twice the largest finite); twice: 2 * scale * up.
 struct Rounding {
   float up, inv, twice;
 };
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(1024) k_codes(const CodesParams p) {
     if (top >= 0x7f80u) scale = __uint_as_float(0x7fc00000u);
     if (tid == 0) p.scale[m] = scale;
     none = top == 0 || top >= 0x7f80u;
-    q.up = largest < 0x1p-60f ? 0x1p64f : 1.f;   // (tiny rows stay clear of subnormal numbers)
+    q.up = largest < 0x1p-60f ? 0x1p64f : largest > 0x1p100f ? 0x1p-64f : 1.f;
     q.inv = none ? 0.f : __fdiv_rn(127.f, largest * q.up);
     q.twice = 2.f * (scale * q.up);
   }
@@ -206,7 +206,8 @@ Layout layout(int M, int N, int K) {
   return l;
 }
 
-bool linear_args(int M, int N, int K) { return M >= 1 && N >= 1 && K >= 16 && K % 16 == 0; }
+constexpr int kMost = 0x7fff0000;   // (tiles behind the last row still have 32-bit numbers)
+bool linear_args(int M, int N, int K) { return M >= 1 && N >= 1 && K >= 16 && K % 16 == 0 && M <= kMost && N <= kMost && K <= kMost; }
 
 }  // namespace
 

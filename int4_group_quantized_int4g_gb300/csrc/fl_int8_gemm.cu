@@ -666,6 +666,7 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   p.wshift = p.BN <= kFew ? 3 : 2;
   p.woff = p.BN <= kFew ? kXBytesFew : kXBytes;
   const int pairs = flh::sm_count() / 2 < 128 ? flh::sm_count() / 2 : 128;
+  if (pairs < 1) return FL_ERR_UNSUPPORTED;
   p.P = pairs;
   if (tiles * 2 <= pairs) {   // few tiles: each in equal parts
     int parts = pairs / static_cast<int>(tiles);

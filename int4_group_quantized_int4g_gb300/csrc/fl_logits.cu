@@ -415,6 +415,19 @@ int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
   return flh::launch_early(k_logits<BF16, LONG>, dim3(static_cast<unsigned>(B) * p.runs), dim3(LONG ? 1024 : 256), smem, s, p);
 }
 
+// Whether rows of `out` would lie over rows of the logits, the logits themselves
+// (the same place and stride, fp32) apart.
+bool over(const void* x, int64_t xs, int size, const float* out, int64_t os, int B, int V) {
+  const auto a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
+  const uint64_t sa = static_cast<uint64_t>(xs) * size, sb = static_cast<uint64_t>(os) * 4;
+  const uint64_t wa = static_cast<uint64_t>(V) * size, wb = static_cast<uint64_t>(V) * 4;
+  if (b >= a + (B - 1) * sa + wa || a >= b + (B - 1) * sb + wb) return false;
+  if (sa != sb) return true;
+  if (a == b && size == 4) return false;
+  const uint64_t d = b >= a ? (b - a) % sa : (sa - (a - b) % sa) % sa;   // where in its stride a row of out begins
+  return d < wa || d + wb > sa;
+}
+
 bool logits_args(int B, int V) { return B >= 1 && V >= 1 && V < (1 << 30) && B <= (1 << 30); }
 
 }  // namespace
@@ -437,7 +450,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
                          r.presence, r.bias_offsets, r.bias_ids, r.bias, r.allowed, r.temperature};
   for (const void* q : lists)
     if (!aligned(q, 4)) return FL_ERR_ARG;
-  if (out == logits && out && (bf16 || out_stride != logits_stride)) return FL_ERR_ARG;
+  if (out && over(logits, logits_stride, bf16 ? 2 : 4, out, out_stride, B, V)) return FL_ERR_ARG;
   if (!r.history != !r.history_lens || (r.history && (r.history_max < 0 || r.history_max >= 1 << 30 || r.history_stride < r.history_max)))
     return FL_ERR_ARG;
   if (!r.history && (r.prompt_lens || r.repetition || r.frequency || r.presence)) return FL_ERR_ARG;

@@ -26,7 +26,7 @@ struct Pool {
   int32_t* lens;
   int blocks, slots, most, block;
   __device__ __forceinline__ int32_t* row(int s) const { return table + static_cast<int64_t>(s) * most; }
-  __device__ __forceinline__ int pages(int tokens) const { return (tokens + block - 1) / block; }
+  __device__ __forceinline__ int pages(int tokens) const { return static_cast<int>((tokens + block - 1ll) / block); }
   __device__ __forceinline__ bool page(int id) const { return id >= 0 && id < blocks; }
 };
 
@@ -71,8 +71,8 @@ __global__ void __launch_bounds__(kListThreads) k_pages_free(const Pool p, const
   // taken out of the table once, whoever comes first
   if (threadIdx.x == 0) was = atomicMin(p.lens + s, left);
   __syncthreads();
-  const long long end = min((static_cast<long long>(max(was, 0)) + p.block - 1) / p.block, static_cast<long long>(p.most));
-  for (long long j = (static_cast<long long>(left) + p.block - 1) / p.block + threadIdx.x; j < end; j += kListThreads) {
+  const int end = min(p.pages(max(was, 0)), p.most);
+  for (int j = p.pages(left) + threadIdx.x; j < end; j += kListThreads) {
     const int id = atomicExch(p.row(s) + j, -1);
     if (id == -1) continue;
     if (!p.page(id)) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(256) k_pages_table(const CompactParams c) {
   if (i >= static_cast<long long>(p.slots) * p.most) return;
   const int s = static_cast<int>(i / p.most), j = static_cast<int>(i - static_cast<long long>(s) * p.most);
   int id = p.table[i];
-  if (j < (static_cast<long long>(max(p.lens[s], 0)) + p.block - 1) / p.block) {
+  if (j < p.pages(max(p.lens[s], 0))) {
     const int to = p.page(id) ? c.moved[id] : -1;
     if (to < 0) missing(c.status, 76);
     id = to;

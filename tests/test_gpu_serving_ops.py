@@ -73,6 +73,16 @@ def test_quantize_borders():
     _codes_check(_bf16(np.array(rows)).to(DEV))
 
 
+@pytest.mark.parametrize("e", [-133, -126, -60, 0, 99, 100, 127])
+def test_quantize_every_value_of_a_binade_over_every_top(e):
+    """Rows of all bf16 values that a largest value of binade e can meet in its own and the next binades."""
+    tops = (128 + np.arange(0, 128, 3)) * 2.0 ** max(e - 7, -140)
+    values = np.concatenate([(128 + np.arange(128)) * 2.0 ** max(e - 7 - i, -140 - i) for i in range(7)])
+    rows = np.minimum(values[None], tops[:, None]) * np.where(np.arange(len(values)) % 2, -1.0, 1.0)
+    rows[:, 0] = tops
+    _codes_check(_bf16(rows).to(DEV))
+
+
 def test_quantize_zeros_and_infinities():
     x = torch.ones((5, 300), dtype=torch.bfloat16, device=DEV)
     x[0] = 0
@@ -374,6 +384,68 @@ def test_logits_repeats_and_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+def test_offsets_past_32_bits():
+    """Rows of the tokens, of y, of the logits and pages of a cache that lie more than 2^31 elements apart."""
+    gap = 1500000000
+    x, w, t = _linear_case(3, 300, 272, 2)
+    want = fl.fl_int8_linear(x, w, t)
+    far = torch.empty(2 * gap + 700, dtype=torch.bfloat16, device=DEV)
+    xs, ys = far.as_strided((3, 272), (gap, 1)), far.as_strided((3, 300), (gap, 1), 300)
+    xs.copy_(x)
+    assert torch.equal(fl.fl_int8_linear(xs, w, t), want)
+    fl.fl_int8_linear(x, w, t, y=ys)
+    assert torch.equal(ys, want)
+    lx, kw = _logits_case(3, 333, 1, torch.bfloat16, history=9)
+    ls = far.as_strided((3, 333), (gap, 1))
+    ls.copy_(lx)
+    _logits_check(lx, kw, fl.fl_logits_process(ls, **{k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}))
+    del far, xs, ys, ls
+    blocks = 70000                                   # of 64 KB of keys
+    codes = [torch.zeros((blocks, 8, 64, 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((blocks, 8), device=DEV) for _ in range(2)]
+    codes[0][blocks - 1], codes[1][2], scales[0][blocks - 1] = 7, 9, 3.0
+    fl.fl_kv8_pages_copy(codes[:1], codes[1:], scales[:1], scales[1:], _i32([(blocks - 1, 1), (2, blocks - 2)]), _i32([2]))
+    assert bool((codes[0][1] == 7).all()) and bool((codes[1][blocks - 2] == 9).all()) and bool((scales[0][1] == 3).all())
+    assert not codes[0][0].any() and not codes[0][blocks - 2].any()
+
+
+def test_linear_from_several_streams_at_once():
+    """Calls that overlap on the GPU, each stream with the workspace that is its own."""
+    cases = [_linear_case(M, N, 1040, M) for M, N in ((1, 3000), (40, 2000), (300, 1500), (20, 5000))]
+    want = [fl.fl_int8_linear(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[] for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(6):
+        for s, c, g in zip(streams, cases, got):
+            with torch.cuda.stream(s):
+                g.append(fl.fl_int8_linear(*c))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, y) for y in g)
+
+
+def test_weights_rounded_just_before():
+    """A linear right behind the kernels that make its weights and its tokens."""
+    rng = np.random.default_rng(3)
+    dense, x = _bf16(rng.standard_normal((900, 512))).to(DEV), _bf16(rng.standard_normal((70, 512))).to(DEV)
+    w, t = fl.fl_int8_quantize(dense)
+    torch.cuda.synchronize()
+    for rows in (x[:3], x):
+        want = fl.fl_int8_linear(rows, w, t)
+        codes, scale = fl.fl_int8_quantize(rows)
+        for _ in range(5):
+            torch.zeros_like(w)                      # (the allocator hands this memory to the next call)
+            w2, t2 = fl.fl_int8_quantize(dense)
+            assert torch.equal(fl.fl_int8_linear(rows, w2, t2), want)
+            del w2
+            torch.zeros_like(w)
+            w3, t3 = fl.fl_int8_quantize(dense)
+            assert torch.equal(fl.fl_int8_linear(codes, w3, t3, x_scale=scale), want)
+            del w3
 
 
 # ------------------------------------------------------------------- pages

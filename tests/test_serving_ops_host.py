@@ -85,6 +85,9 @@ def test_logits_refusals(L):
     assert call(xs=99) == 1 and call(os_=99) == 1
     assert call(x=HALF) == 1 and call(out=HALF) == 1 and call(tok=BYTE) == 1 and call(ws=ODD) == 1
     assert call(t=0) == 1 and call(os_=101) == 1                     # in place: the same type and stride
+    assert call(out=ctypes.c_void_p(0x10000 + 4), os_=100) == 1      # a row over itself, shifted
+    assert call(xs=300, os_=300, out=ctypes.c_void_p(0x10000 + 4 * 250)) == 1     # over the next row
+    assert call(xs=300, os_=200, out=ctypes.c_void_p(0x10000 + 4 * 150)) == 1
     other = ctypes.c_void_p(0x90000)
     for bad in (dict(history_lens=None), dict(history=None), dict(history_stride=49), dict(history_max=-1), dict(history_max=1 << 30),
                 dict(history=None, history_lens=None), dict(bias=None), dict(bias_ids=None), dict(bias_offsets=None),
