@@ -596,6 +596,13 @@ int fl_int8_linear(const void* x, int64_t x_stride, const float* x_scale, int M,
                    const float* w_scale, int N, void* y, int64_t y_stride, int y_type, void* ws, size_t ws_bytes,
                    fl_stream_t stream);
 
+/* Test hook: how the tcgen05 kernel of fl_int8_linear divides a product among sms
+ * / 2 pairs of SMs (host code only).  out[0..7] receives the tokens of a tile, its
+ * units of 128 columns, the token tiles, the tiles of 256 weight rows, the pairs
+ * launched, the whole tiles of each, the units of the tiles before those, and
+ * whether these are taken whole by the first pairs (else in equal runs by all). */
+int fl_int8_test_plan(int M, int N, int K, int sms, long long* out);
+
 /* ------------------------------------------- from logits to the next token */
 
 /* What a row's logits go through before the choice of a token; every list is

@@ -29,7 +29,7 @@ __all__ = [
     "fl_rmsnorm", "fl_rope", "fl_kv8_append", "fl_kv8_attention_workspace", "fl_kv8_attention",
     "fl_kv8_test_pages", "fl_kv8_test_units", "fl_kv8_test_plan",
     "FL_OUT_BF16", "FL_OUT_FP32", "FlLogitsRules", "FlKv8Pool",
-    "fl_int8_quantize", "fl_int8_linear_workspace", "fl_int8_linear", "fl_logits_process_workspace", "fl_logits_process",
+    "fl_int8_quantize", "fl_int8_linear_workspace", "fl_int8_linear", "fl_int8_test_plan", "fl_logits_process_workspace", "fl_logits_process",
     "fl_kv8_pages_free", "fl_kv8_pages_fork", "fl_kv8_pages_workspace", "fl_kv8_pages_alloc", "fl_kv8_pages_compact",
     "fl_kv8_pages_copy",
 ]
@@ -124,6 +124,7 @@ SIGNATURES = {
     "fl_int8_quantize": (_i, [_vp, _l, _i, _i, _vp, _vp, _vp]),
     "fl_int8_linear_workspace": (_i, [_i, _i, _i, _c_size_p]),
     "fl_int8_linear": (_i, [_vp, _l, _vp, _i, _i, _vp, _vp, _i, _vp, _l, _i, _vp, ctypes.c_size_t, _vp]),
+    "fl_int8_test_plan": (_i, [_i, _i, _i, _i, ctypes.POINTER(ctypes.c_longlong)]),
     "fl_logits_process_workspace": (_i, [_i, _i, _c_size_p]),
     "fl_logits_process": (_i, [_vp, _l, _i, _i, _i, _vp, _vp, _l, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "fl_kv8_pages_free": (_i, [_vp, _vp, _vp, _i, _vp, _vp]),
@@ -827,6 +828,13 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         ws = _workspace(_int8_workspace(device.index, M, N, K), device)
     _check("fl_int8_linear", lib().fl_int8_linear(xp, xs, sp, M, K, wp, tp, N, yp, ys, kind, _p(ws), ws.numel(), _stream()))
     return y
+
+
+def fl_int8_test_plan(M, N, K, sms=152):
+    """Test hook: a dict of how the tcgen05 kernel divides a product among SMs."""
+    out = (ctypes.c_longlong * 8)()
+    _check("fl_int8_test_plan", lib().fl_int8_test_plan(M, N, K, sms, out))
+    return dict(zip(("BN", "G", "mtiles", "ntiles", "P", "waves", "units", "whole"), out))
 
 
 # --------------------------------------------- from logits to the next token

@@ -202,7 +202,7 @@ Layout layout(int M, int N, int K) {
   l.scale = kScratch;
   l.x = up(l.scale + static_cast<size_t>(M) * 4);
   l.part = up(l.x + rows * width * 2);
-  l.bytes = l.part + up(M <= kRowsMax ? rows_part_bytes(M) : gemm_part_bytes(M));
+  l.bytes = l.part + up(M <= kRowsMax ? rows_part_bytes(M) : gemm_part_bytes(M, N, K));
   return l;
 }
 
@@ -255,4 +255,12 @@ extern "C" int fl_int8_linear(const void* x, int64_t x_stride, const float* x_sc
   }
   const int rc = x_scale ? launch_codes<kInCodes, kOutRows>(p, s) : launch_codes<kInBf16, kOutRows>(p, s);
   return rc != FL_OK ? rc : gemm_launch(c, s);
+}
+
+extern "C" int fl_int8_test_plan(int M, int N, int K, int sms, long long* out) {
+  if (!out || !linear_args(M, N, K) || sms < 2) return FL_ERR_ARG;
+  const Plan a = gemm_plan(M, N, K, sms / 2);
+  const long long v[8] = {a.BN, a.G, a.mtiles, a.ntiles, a.P, a.waves, a.units, a.whole};
+  for (int i = 0; i < 8; ++i) out[i] = v[i];
+  return FL_OK;
 }

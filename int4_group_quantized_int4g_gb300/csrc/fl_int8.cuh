@@ -45,6 +45,17 @@ struct Call {
 int rows_launch(const Call& c, cudaStream_t s);
 size_t rows_part_bytes(int M);
 int gemm_launch(const Call& c, cudaStream_t s);
-size_t gemm_part_bytes(int M);
+// How the tiles of 256 weight rows x BN tokens (G units of 128 columns each) go to P
+// pairs of SMs: `waves` whole ones each, and `units` of the rest, first, in equal runs
+// or (whole) a tile for each of the first pairs.
+struct Plan {
+  int BN, G;
+  long long mtiles, ntiles;
+  int P, waves;
+  long long units;
+  int whole;
+};
+Plan gemm_plan(int M, int N, int K, int pairs);
+size_t gemm_part_bytes(int M, int N, int K);
 
 }  // namespace fl8

@@ -9,16 +9,13 @@
 // unit's MMAs take 1024 cycles.  The codes become f16, exactly, on the way into
 // tensor memory, where the MMA reads A: shared memory feeds B alone.
 //
-// BN is the tokens divided by the number of tiles that 256 asks for, rounded up to
-// 32, so that 300 tokens cost two tiles of 160, not two of 256.  Up to 128 the
+// BN, a multiple of 32 up to 256, and how tiles meet pairs go by a plan (plan_for): the
+// tiles are taken in waves, all pairs next to one another (8 token tiles by a run of
+// weight tiles, for L2); the rest is taken whole, or cut into equal runs of units,
+// whichever ends sooner.  Cut tiles come first, so that joining them hides behind
+// whole ones.  A split tile is finished by the last pair to come, the parts added
+// in the pairs' order: results do not depend on timing.  Up to BN = 128 the
 // accumulator is doubled and a tile's end overlaps the next tile's MMAs.
-//
-// Tiles are taken in waves, all pairs next to one another (8 token tiles by
-// a run of weight tiles, for L2), as long as every pair gets a whole one; the
-// rest, from one to two tiles a pair, is cut into equal runs of units, and comes
-// first, so that joining its split tiles hides behind the whole ones.  A split
-// tile is finished by the last pair to come, the parts added in the pairs'
-// order: results do not depend on timing.
 //
 // Roles in a CTA:
 //   warp 0        tokens: per unit two TMA boxes of BN / 2 tokens x 64 columns
@@ -39,7 +36,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kConv0 = 4, kEpi0 = 12;
 // Registers a thread: of the launch, and of the producers and the issuer, the
 // converting warps and the epilogue (which spills its sums with 96).
-constexpr int kRegs = 96, kRegsIo = 64, kRegsConv = 72, kRegsEpi = 136;
+constexpr int kRegs = 96, kRegsIo = 48, kRegsConv = 72, kRegsEpi = 144;
 static_assert(4 * kRegsIo + 8 * kRegsConv + 8 * kRegsEpi <= 20 * kRegs, "the split draws on the launch's registers");
 constexpr int kRing = 4;                       // A tiles (an even number: a slot has one group of converting warps)
 constexpr int kWRing = 8;                      // weight stages, at most (4 or 8)
@@ -73,7 +70,8 @@ struct Params {
   int M, N, fp32, tma_y;
   int BN, G, mtiles, ntiles;
   int xring, wshift, woff;   // token stages, log2 of the weight stages and where these lie
-  int P, waves, U;   // pairs, whole tiles of each, units of the rest
+  int P, waves;      // pairs, whole tiles of each
+  int U, whole;      // units of the rest; whether its tiles are taken whole, one by each of the first pairs
 };
 
 __device__ __forceinline__ int unit_begin(int c, int U, int P) { return static_cast<int>(static_cast<long long>(c) * U / P); }
@@ -86,8 +84,10 @@ struct Walk {
   int u, u1, w, c;
   int tile, g0, g1;
   bool split;
-  __device__ Walk(const Params& p, int pair)
-      : u(p.U ? unit_begin(pair, p.U, p.P) : 0), u1(p.U ? unit_begin(pair + 1, p.U, p.P) : 0), w(0), c(pair), tile(0), g0(0), g1(0), split(false) {}
+  __device__ Walk(const Params& p, int pair) : w(0), c(pair), tile(0), g0(0), g1(0), split(false) {
+    u = p.whole ? min(pair, p.U / p.G) * p.G : p.U ? unit_begin(pair, p.U, p.P) : 0;
+    u1 = p.whole ? min(u + p.G, p.U) : p.U ? unit_begin(pair + 1, p.U, p.P) : 0;
+  }
   __device__ bool next(const Params& p) {
     if (u < u1) {
       const int t = u / p.G;
@@ -419,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         set_status(p.status, FL_ERR_TIMEOUT, 97);
         break;
       }
-      const bool own = flags[1] != 0;
+      const bool final = k.u >= k.u1 && k.w >= p.waves;   // the CTA's last tile
+      bool own = flags[1] != 0;      // the sums are in tensor memory, and the others' parts have come
       tc_fence_after();
       const uint32_t d = tmem + acc * 128 + (static_cast<uint32_t>(q * 32) << 16) + c0;
       auto release = [&]() {
@@ -505,15 +506,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       auto landed = [&](uint32_t (&u)[16]) { tmem_ld_wait(u); };
-      if (!k.split) {
+      auto part = [&](int c) {
+        return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(slots[c - cf]) * 8 + e) * (bytes / 16) + lane;
+      };
+      // a part of a split tile
+      int others = 0;
+      bool room = false;
+      if (k.split) {
+        if (tid <= cl - cf) {   // this CTA's parts of it, by pair
+          const int c = cf + tid, which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
+          slots[tid] = (2 * c + which) * 2 + rank;
+        }
+        named_bar(1, 256);
+        if (!own) {
+          float4* dst = part(pair);
+          uint32_t u[16];
+#pragma unroll 1
+          for (int t = 0; t < mine; t += 16) {
+            issue(t, u);
+            landed(u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              __stcg(dst + (t / 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                                         __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
+          }
+          if (!final) release();
+          named_bar(1, 256);
+          if (tid == 0) flags[1] = atom_add_acq_rel_gpu(cnt, 1) == cl - cf;
+          named_bar(1, 256);
+          if (!flags[1]) continue;
+          own = final;   // (no more MMAs: tensor memory still holds them)
+        }
+        if (tid == 0) *cnt = 0;
+        // at the CTA's last tile the rings are empty and take the parts, all in flight at once
+        others = cl - cf + 1 - own;
+        room = final && others * bytes <= kJoin;
+        if (room) {
+          if (lane == 0) {
+            fence_proxy_async_all();
+            mbar_arrive_expect_tx(&joined[e], static_cast<uint32_t>(others * bytes));
+            for (int c = cf, o = 0; c <= cl; ++c)
+              if (!(own && c == pair)) bulk_g2s(smem + e * kJoin + bytes * o++, part(c) - lane, bytes, &joined[e]);
+          }
+          __syncwarp();
+          if (!mbar_wait(&joined[e], 0)) set_status(p.status, FL_ERR_TIMEOUT, 98);
+        }
+      }
+      // whole tiles, and those whose one other part lies in shared memory (a sum of two
+      // has no order)
+      const bool two = room && own && others == 1;
+      if (!k.split || two) {
+        auto add = [&](int t, uint32_t* u) {
+          const float4* src = reinterpret_cast<const float4*>(smem + e * kJoin) + t * 8 + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 f = src[32 * i];
+            u[4 * i] = __float_as_uint(__uint_as_float(u[4 * i]) + f.x), u[4 * i + 1] = __float_as_uint(__uint_as_float(u[4 * i + 1]) + f.y);
+            u[4 * i + 2] = __float_as_uint(__uint_as_float(u[4 * i + 2]) + f.z), u[4 * i + 3] = __float_as_uint(__uint_as_float(u[4 * i + 3]) + f.w);
+          }
+        };
         uint32_t ua[16], ub[16], y[16];
         issue(0, ua);
         if (16 < mine) issue(16, ub);
 #pragma unroll 1
         for (int t = 0; t < mine; t += kStep) {
           landed(ua);
+          if (two) add(t, ua);
           scaled(t, ua, y);
           if constexpr (FP32) {   // (16 tokens a step: the buffers hold no more)
+            landed(ub);
 #pragma unroll
             for (int i = 0; i < 16; ++i) ua[i] = ub[i];
             if (t + 16 >= mine)
@@ -522,7 +583,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               issue(t + 32, ub);
           } else {
             landed(ub);
-            if (t + 16 < mine) scaled(t + 16, ub, y + 8);
+            if (t + 16 < mine) {
+              if (two) add(t + 16, ub);
+              scaled(t + 16, ub, y + 8);
+            }
             if (t + 32 >= mine) {
               release();
             } else {
@@ -537,47 +601,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           store(t, min(kStep, mine - t));
         }
         continue;
-      }
-      // a part of a split tile
-      if (tid <= cl - cf) {   // this CTA's parts of it, by pair
-        const int c = cf + tid, which = unit_begin(c, p.U, p.P) / p.G == T ? 0 : 1;
-        slots[tid] = (2 * c + which) * 2 + rank;
-      }
-      named_bar(1, 256);
-      auto part = [&](int c) {
-        return reinterpret_cast<float4*>(p.part) + (static_cast<size_t>(slots[c - cf]) * 8 + e) * (bytes / 16) + lane;
-      };
-      if (!own) {
-        float4* dst = part(pair);
-        uint32_t u[16];
-#pragma unroll 1
-        for (int t = 0; t < mine; t += 16) {
-          issue(t, u);
-          landed(u);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            __stcg(dst + (t / 4 + i) * 32, make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                                                       __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3])));
-        }
-        release();
-        named_bar(1, 256);
-        if (tid == 0) flags[1] = atom_add_acq_rel_gpu(cnt, 1) == cl - cf;
-        named_bar(1, 256);
-        if (!flags[1]) continue;
-      }
-      if (tid == 0) *cnt = 0;
-      // at the CTA's last tile the rings are empty and take the parts, all in flight at once
-      const int others = cl - cf + 1 - own;
-      const bool room = k.u >= k.u1 && k.w >= p.waves && others * bytes <= kJoin;
-      if (room) {
-        if (lane == 0) {
-          fence_proxy_async_all();
-          mbar_arrive_expect_tx(&joined[e], static_cast<uint32_t>(others * bytes));
-          for (int c = cf, o = 0; c <= cl; ++c)
-            if (!(own && c == pair)) bulk_g2s(smem + e * kJoin + bytes * o++, part(c) - lane, bytes, &joined[e]);
-        }
-        __syncwarp();
-        if (!mbar_wait(&joined[e], 0)) set_status(p.status, FL_ERR_TIMEOUT, 98);
       }
 #pragma unroll 1
       for (int t = 0; t < mine; t += 16) {
@@ -641,13 +664,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 namespace fl8 {
 
-int gemm_bn(int M) {
-  const int tiles = (M + 255) / 256;
-  return ((M + tiles - 1) / tiles + 31) / 32 * 32;
+// The plan of least cycles, as far as these estimates go: a unit's MMAs take 4 BN
+// cycles and 512 at least, a tile's end 16 BN where nothing overlaps it; joining two
+// parts takes 3000 and 1200 for each 32 tokens, more of them 1500 a part (3000 in uneven
+// runs).  BN
+// = 256 moves the fewest bytes for a product and is preferred by 4% for every 32.
+// Measured: 1000 x 4096 x 4096 29 us in 64 whole tiles on 76 pairs, 43 cut into 76
+// runs; 301 x 11008 x 4096 29 us in 86 tiles of 160 cut into 76 runs, 33 in 129 of 128.
+Plan gemm_plan(int M, int N, int K, int pairs) {
+  Plan best = {};
+  double least = 0;
+  const int G = (K + kBlockK - 1) / kBlockK;
+  const long long ntiles = (N + 2 * kRows - 1ll) / (2 * kRows);
+  for (int BN = 256; BN >= 32; BN -= 32) {
+    if (BN < 256 && BN >= M + 32) continue;   // (the next smaller one holds all tokens too)
+    const long long mtiles = (M + BN - 1ll) / BN, tiles = mtiles * ntiles;
+    const double unit = BN > 128 ? 4 * BN : 512, tail = BN > 128 ? 16 * BN : 500, cols = BN / 32, prefer = 1 + 0.04 * (256 - BN) / 32;
+    auto offer = [&](double cycles, int P, int waves, long long rest, int whole) {
+      cycles *= prefer;
+      if (best.BN && cycles >= least) return;
+      least = cycles;
+      best = {BN, G, mtiles, ntiles, P, waves, rest * G, whole};
+    };
+    const long long q = tiles / pairs, rest = tiles % pairs;
+    if (q > 0x7ffffff) continue;
+    const int P = tiles < pairs ? static_cast<int>(tiles) : pairs;
+    offer((q + (rest != 0)) * (G * unit + tail), P, static_cast<int>(tiles < pairs ? 0 : q), tiles < pairs ? tiles : rest, 1);
+    if (rest && tiles * G >= pairs) {
+      const double even = tiles * static_cast<double>(G) / pairs * unit + (q + 1) * tail;
+      const double join = q > 1 ? tail : q == 1 ? 3000 + 1200 * cols : 3000 + 3000 * cols * pairs / tiles;
+      offer(even + join, pairs, static_cast<int>(q ? q - 1 : 0), q ? rest + pairs : rest, 0);
+    }
+    for (int parts = 2; parts <= 8 && tiles * parts <= pairs && parts <= G; ++parts)
+      offer((G + parts - 1) / parts * unit + tail + (parts == 2 ? 3000 + 1200 * cols : 2000 + 1500 * (parts - 1) * cols),
+            static_cast<int>(tiles) * parts, 0, tiles, 0);
+  }
+  return best;
 }
+int gemm_pairs() { return flh::sm_count() / 2 < 128 ? flh::sm_count() / 2 : 128; }
 
-size_t gemm_part_bytes(int M) {
-  return static_cast<size_t>(flh::sm_count() / 2) * 4 * kRows * gemm_bn(M) * 4;
+size_t gemm_part_bytes(int M, int N, int K) {
+  const Plan a = gemm_plan(M, N, K, gemm_pairs());
+  return static_cast<size_t>(a.P) * 4 * kRows * a.BN * 4;
 }
 
 int gemm_launch(const Call& c, cudaStream_t s) {
@@ -656,31 +714,14 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   Params p = {};
   p.x_scale = c.x_scale, p.w_scale = c.w_scale, p.y = c.y, p.y_stride = c.y_stride;
   p.part = c.part, p.cnt = c.cnt, p.status = c.status, p.M = c.M, p.N = c.N, p.fp32 = c.fp32;
-  p.BN = gemm_bn(c.M);
-  p.G = (c.K + kBlockK - 1) / kBlockK;
-  p.mtiles = (c.M + p.BN - 1) / p.BN;
-  p.ntiles = static_cast<int>((c.N + 2 * kRows - 1ll) / (2 * kRows));
-  const long long tiles = static_cast<long long>(p.mtiles) * p.ntiles;
-  if (tiles > 0x7fffffffll / kGroupM || p.ntiles > 0x7fffffff / kGroupM) return FL_ERR_UNSUPPORTED;
+  const int pairs = gemm_pairs();
+  const Plan a = pairs ? gemm_plan(c.M, c.N, c.K, pairs) : Plan{};
+  if (!a.BN || a.mtiles * a.ntiles > 0x7fffffffll / kGroupM || a.units > 0x7fffffffll / (pairs + 1)) return FL_ERR_UNSUPPORTED;
+  p.BN = a.BN, p.G = a.G, p.mtiles = static_cast<int>(a.mtiles), p.ntiles = static_cast<int>(a.ntiles);
+  p.P = a.P, p.waves = a.waves, p.U = static_cast<int>(a.units), p.whole = a.whole;
   p.xring = kXBytes / (p.BN * 128) < kXRing ? kXBytes / (p.BN * 128) : kXRing;
   p.wshift = p.BN <= kFew ? 3 : 2;
   p.woff = p.BN <= kFew ? kXBytesFew : kXBytes;
-  const int pairs = flh::sm_count() / 2 < 128 ? flh::sm_count() / 2 : 128;
-  if (pairs < 1) return FL_ERR_UNSUPPORTED;
-  p.P = pairs;
-  if (tiles * 2 <= pairs) {   // few tiles: each in equal parts
-    int parts = pairs / static_cast<int>(tiles);
-    if (parts > 8) parts = 8;
-    if (parts > p.G) parts = p.G;
-    p.P = static_cast<int>(tiles) * parts;
-  } else if (tiles < pairs && tiles * p.G < pairs) {
-    p.P = static_cast<int>(tiles);
-  }
-  p.waves = static_cast<int>(tiles / p.P);
-  if (tiles % p.P && p.waves) --p.waves;
-  const long long U = (tiles - static_cast<long long>(p.waves) * p.P) * p.G;
-  if (U > 0x7fffffffll / (pairs + 1)) return FL_ERR_UNSUPPORTED;
-  p.U = static_cast<int>(U);
 
   const cuuint32_t estr[2] = {1, 1};
   CUtensorMap wmap, xmap, ymap;

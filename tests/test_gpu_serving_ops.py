@@ -127,7 +127,8 @@ SIZES = [(1, 1, 16), (1, 100, 256), (3, 256, 128), (1, 4096, 1024), (7, 1000, 40
          (17, 128, 2064), (20, 600, 384), (48, 1500, 1536), (65, 700, 2176), (96, 300, 640), (24, 5003, 512), (31, 255, 1024), (32, 700, 4096), (32, 40000, 256), (1, 300, 28672), (2, 40007, 896),
          (33, 127, 128), (40, 1000, 1040), (64, 4096, 512), (100, 129, 16), (128, 2500, 1008), (150, 300, 4096), (257, 777, 400),
          (301, 1100, 2048), (512, 200, 6144), (700, 2049, 272), (1111, 130, 1024), (2050, 384, 528),
-         (2048, 4864, 144), (2304, 4870, 272), (3000, 5000, 256)]   # whole waves of tiles: without a rest, and with one
+         (2048, 4864, 144), (2304, 4870, 272), (3000, 5000, 256), (301, 11008, 272), (700, 4096, 400), (64, 11008, 144),
+         (512, 11008, 272)]   # whole waves of tiles: without a rest, and with one
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)

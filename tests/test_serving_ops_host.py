@@ -62,6 +62,45 @@ def test_int8_linear_refusals(L):
         assert call(M=M, wb=size.value - 1) == 2
 
 
+def _walk(p, c):
+    """The runs of units (tile, first, end) of pair c."""
+    per, units = p["G"], p["units"]
+    if p["whole"]:
+        u = min(c, units // per) * per
+        end = min(u + per, units)
+    else:
+        u, end = (c * units // p["P"], (c + 1) * units // p["P"]) if units else (0, 0)
+    while u < end:
+        t = u // per
+        n = min(per - u % per, end - u)
+        yield p["waves"] * p["P"] + t, u % per, u % per + n
+        u += n
+    for w in range(p["waves"]):
+        yield w * p["P"] + c, 0, per
+
+
+@pytest.mark.parametrize("sms", [152, 148, 20, 2])
+def test_linear_plans_do_every_unit_once(L, sms):
+    for M in (17, 24, 33, 64, 100, 128, 129, 301, 512, 700, 1000, 2048, 8190, 30000):
+        for N, K in ((1, 16), (300, 4096), (4096, 4096), (11008, 4096), (4096, 11008), (16000, 512), (128003, 256)):
+            p = fl.fl_int8_test_plan(M, N, K, sms)
+            tiles = p["mtiles"] * p["ntiles"]
+            assert 32 <= p["BN"] <= 256 and p["BN"] % 32 == 0 and (p["mtiles"] - 1) * p["BN"] < M <= p["mtiles"] * p["BN"]
+            assert p["G"] == -(-K // 128) and p["ntiles"] == -(-N // 256) and 1 <= p["P"] <= sms // 2
+            assert p["waves"] * p["P"] * p["G"] + p["units"] == tiles * p["G"]
+            assert not p["units"] or p["whole"] or p["units"] >= p["P"]      # every run has a unit
+            assert not p["whole"] or p["units"] <= p["P"] * p["G"]
+            done = {}
+            for c in range(p["P"]):
+                for t, a, b in _walk(p, c):
+                    assert 0 <= t < tiles and a < b
+                    done.setdefault(t, []).append((a, b))
+            assert len(done) == tiles
+            for runs in done.values():
+                runs.sort()
+                assert runs[0][0] == 0 and runs[-1][1] == p["G"] and all(x[1] == y[0] for x, y in zip(runs, runs[1:]))
+
+
 def _rules(**kw):
     d = dict(history=0x10000, history_lens=0x10000, prompt_lens=0x10000, repetition=0x10000, frequency=0x10000, presence=0x10000,
              bias_offsets=0x10000, bias_ids=0x10000, bias=0x10000, allowed=0x10000, temperature=0x10000, history_stride=50,
