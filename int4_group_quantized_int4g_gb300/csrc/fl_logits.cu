@@ -27,7 +27,8 @@ namespace {
 constexpr int kLead = 32;                      // room before a run's first whole vector
 constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one launch
 constexpr int kRunMin = 1024, kRunMax = 16384;
-constexpr int kRunBytes = 40960;               // shared memory of a run: five CTAs an SM
+constexpr int kThreads = 256;                  // with short histories
+constexpr int kRunBytes = 40960, kRunBytesLong = 81920;   // shared memory of a run, with short and long histories
 
 struct Partial {
   float top, sum;
@@ -52,6 +53,32 @@ struct LogitsParams {
 __device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269504f));
+  return y;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {   // (a NaN loses)
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -90,9 +117,9 @@ __host__ __device__ constexpr int run_bytes(int room, bool bf16, bool history, b
 }
 
 template <bool BF16, bool LONG>
-__global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams p) {
+__global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsParams p) {
   constexpr int W = BF16 ? 8 : 4;    // tokens of a 16-byte vector
-  constexpr int T = LONG ? 1024 : 256;
+  constexpr int T = LONG ? 1024 : kThreads;
   constexpr bool HALF = !BF16 && !LONG;   // counts of 16 bits
   using Raw = std::conditional_t<BF16, uint16_t, float>;
   extern __shared__ uint4 raw[];
@@ -136,13 +163,14 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
   }
   // the history's entries, four at a time; the first are on their way before the
   // lengths are known (lists are history_max long whatever of them counts)
-  constexpr int kAhead = 2;
+  constexpr int kAhead = LONG ? 2 : 512 / kThreads;
   int4 ahead[kAhead];
   int n = 0, prompt = 0;
   const int32_t* h = r.history + static_cast<int64_t>(b) * r.history_stride;
   auto fetch = [&](int i) {
-    if (p.vec_h && 4 * i + 4 <= r.history_max) return __ldg(reinterpret_cast<const int4*>(h) + i);
     int4 f = make_int4(-1, -1, -1, -1);
+    if (p.vec_h && 4 * i + 4 <= r.history_max) return __ldg(reinterpret_cast<const int4*>(h) + i);
+    if (4 * i >= r.history_max) return f;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (4 * i + e < r.history_max) (&f.x)[e] = __ldg(h + 4 * i + e);
@@ -273,70 +301,104 @@ __global__ void __launch_bounds__(LONG ? 1024 : 256) k_logits(const LogitsParams
   }
   const uint32_t* mask = r.allowed ? reinterpret_cast<const uint32_t*>(r.allowed) + static_cast<int64_t>(b) * r.allowed_stride : nullptr;
   Best best = {-INFINITY, 0.f, -1};
+  float zero = 0.f;   // what is added before exp: the maximum's negative, 0 without one
   auto one = [&](int v) {   // a token outside the vectors
     float f = __fmul_rn(value(v - base), inv);
     if (mask && !(__ldg(mask + (v >> 5)) >> (v & 31) & 1)) f = -INFINITY;
     if (out) out[v] = f;
     best.join(Best{f == f ? f : -INFINITY, f == f ? (f == -INFINITY ? 0.f : 1.f) : f, f > -INFINITY ? v : -1});
   };
-  auto vector = [&](int j) {
-    const int at = kLead + j * W, v = base + at;
-    const uint4 u = *reinterpret_cast<const uint4*>(x + at);
-    float f[W];
-    if constexpr (BF16) {
+  // N vectors, T apart.  What a call has not is decided once, not with every vector
+  auto vectors = [&](int j, auto has_out, auto has_mask, auto count) {
+    constexpr int N = decltype(count)::value;
+    float f[N * W];
 #pragma unroll
-      for (int e = 0; e < W; ++e) f[e] = __uint_as_float(e & 1 ? (&u.x)[e / 2] & 0xffff0000u : (&u.x)[e / 2] << 16);
-      if (counts || biases) {
-        const uint32_t bits = reinterpret_cast<const uint8_t*>(changed)[at / 8];
-        if (bits) {
+    for (int n = 0; n < N; ++n) {
+      const int at = kLead + (j + n * T) * W, v = base + at;
+      const uint4 u = *reinterpret_cast<const uint4*>(x + at);
+      float* g = f + n * W;
+      if constexpr (BF16) {
 #pragma unroll
-          for (int e = 0; e < W; ++e)
-            if (bits >> e & 1) f[e] = __uint_as_float(word[at + e]);
+        for (int e = 0; e < W; ++e) g[e] = __uint_as_float(e & 1 ? (&u.x)[e / 2] & 0xffff0000u : (&u.x)[e / 2] << 16);
+        if (counts || biases) {
+          const uint32_t bits = reinterpret_cast<const uint8_t*>(changed)[at / 8];
+          if (bits) {
+#pragma unroll
+            for (int e = 0; e < W; ++e)
+              if (bits >> e & 1) g[e] = __uint_as_float(word[at + e]);
+          }
         }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < W; ++e) f[e] = __uint_as_float((&u.x)[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < W; ++e) f[e] = __fmul_rn(f[e], inv);
-    if (mask) {
-      const uint32_t w0 = __ldg(mask + (v >> 5));
-      const uint32_t w1 = (v & 31) + W > 32 ? __ldg(mask + (v >> 5) + 1) : 0;
-      const uint32_t bits = __funnelshift_r(w0, w1, v & 31);
-#pragma unroll
-      for (int e = 0; e < W; ++e)
-        if (!(bits >> e & 1)) f[e] = -INFINITY;
-    }
-    if (out) {
-      if (p.vec_out) {
-#pragma unroll
-        for (int q = 0; q < W / 4; ++q)
-          __stcs(reinterpret_cast<float4*>(out + v) + q, make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]));
       } else {
 #pragma unroll
-        for (int e = 0; e < W; ++e) out[v + e] = f[e];
+        for (int e = 0; e < W; ++e) g[e] = __uint_as_float((&u.x)[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < W; e += 2) {
+        const float2 h = mul2(make_float2(g[e], g[e + 1]), make_float2(inv, inv));
+        g[e] = h.x, g[e + 1] = h.y;
+      }
+      if constexpr (decltype(has_mask)::value) {
+        const uint32_t w0 = __ldg(mask + (v >> 5));
+        const uint32_t w1 = (v & 31) + W > 32 ? __ldg(mask + (v >> 5) + 1) : 0;
+        const uint32_t bits = __funnelshift_r(w0, w1, v & 31);
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (!(bits >> e & 1)) g[e] = -INFINITY;
+      }
+      if constexpr (decltype(has_out)::value) {
+        if (p.vec_out) {
+#pragma unroll
+          for (int q = 0; q < W / 4; ++q)
+            __stcs(reinterpret_cast<float4*>(out + v) + q, make_float4(g[4 * q], g[4 * q + 1], g[4 * q + 2], g[4 * q + 3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < W; ++e) out[v + e] = g[e];
+        }
       }
     }
-    float top = f[0];
+    float top = max3(f[0], f[1], f[2]);
 #pragma unroll
-    for (int e = 1; e < W; ++e) top = fmaxf(top, f[e]);
+    for (int e = 3; e + 1 < N * W; e += 2) top = max3(top, f[e], f[e + 1]);
+    top = fmaxf(top, f[N * W - 1]);
     if (top > best.top) {
       best.sum *= exp_of(best.top - top);
       best.top = top;
+      zero = -top;   // (not -inf: it is above another)
 #pragma unroll
-      for (int e = W - 1; e >= 0; --e)
-        if (f[e] == top) best.index = v + e;
+      for (int e = N * W - 1; e >= 0; --e)
+        if (f[e] == top) best.index = base + kLead + (j + e / W * T) * W + e % W;
     }
-    const float zero = best.top == -INFINITY ? 0.f : best.top;
-    float sum = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < W; ++e) sum += exp_of(f[e] - zero);
-    best.sum += sum;
+    for (int e = 0; e < N * W; e += 2) {
+      const float2 d = mul2(add2(make_float2(f[e], f[e + 1]), make_float2(zero, zero)), make_float2(1.44269504f, 1.44269504f));
+      sum = add2(sum, make_float2(ex2(d.x), ex2(d.y)));
+    }
+    best.sum += sum.x + sum.y;
+  };
+  auto all = [&](auto has_out, auto has_mask) {
+    int j = tid;
+    if constexpr (!BF16) {
+#pragma unroll 1
+      for (; j + T < nvec; j += 2 * T) vectors(j, has_out, has_mask, std::integral_constant<int, 2>());
+    }
+    for (; j < nvec; j += T) vectors(j, has_out, has_mask, std::integral_constant<int, 1>());
   };
   // a thread's tokens in ascending order: before the vectors, these, after them
   if (tid < start - lo) one(lo + tid);
-  for (int j = tid; j < nvec; j += T) vector(j);
+  zero = best.top == -INFINITY ? 0.f : -best.top;
+  using Yes = std::true_type;
+  using No = std::false_type;
+  if (out) {
+    if (mask)
+      all(Yes(), Yes());
+    else
+      all(Yes(), No());
+  } else if (mask) {
+    all(No(), Yes());
+  } else {
+    all(No(), No());
+  }
   if (tid < hi - tail) one(tail + tid);
 
   best.join_warp();
@@ -390,7 +452,7 @@ constexpr int kLong = 8192;      // entries; from there on 1024 threads
 int run_length(int B, int V, bool bf16, bool history, bool biases, bool many) {
   const long long want = (many ? 1ll : 4ll) * flh::sm_count();
   int run = kRunMax;
-  while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > kRunBytes || (V + run - 1ll) / run * B < want)) run /= 2;
+  while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > (many ? kRunBytesLong : kRunBytes) || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
 }
 int run_shortest(int B, int V) {   // of all types and rules (long histories need fewer CTAs)
@@ -412,7 +474,7 @@ int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
     }
     ready[dev] = true;
   }
-  return flh::launch_early(k_logits<BF16, LONG>, dim3(static_cast<unsigned>(B) * p.runs), dim3(LONG ? 1024 : 256), smem, s, p);
+  return flh::launch_early(k_logits<BF16, LONG>, dim3(static_cast<unsigned>(B) * p.runs), dim3(LONG ? 1024 : kThreads), smem, s, p);
 }
 
 // Whether rows of `out` would lie over rows of the logits, the logits themselves
