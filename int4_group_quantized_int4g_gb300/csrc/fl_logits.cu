@@ -190,9 +190,37 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
 
   if (counts) {
     const uint32_t width = hi - lo;
+    // four entries of a long history, all of the prompt or all of the answer: an
+    // operation in shared memory for each, without a branch
+    const uint32_t first_word = smem_u32(word + (lo - base));
+    auto four = [&](const int4& f, auto answer) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t off = static_cast<uint32_t>((&f.x)[e] - lo);
+        if constexpr (decltype(answer)::value)
+          asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(off), "r"(width),
+                       "r"(first_word + 4 * off)
+                       : "memory");
+        else
+          asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %0, %1;\n\t@p red.shared.or.b32 [%2], %3;\n\t}" ::"r"(off), "r"(width),
+                       "r"(first_word + 4 * off), "r"(0x80000000u)
+                       : "memory");
+      }
+    };
     for (int i = tid; 4 * i < n; i += kAhead * T) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
+        if constexpr (LONG) {
+          const int at = 4 * (i + k * T);
+          if (at >= prompt && at + 4 <= n) {
+            four(ahead[k], std::true_type());
+            continue;
+          }
+          if (at + 4 <= min(prompt, n)) {
+            four(ahead[k], std::false_type());
+            continue;
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int id = (&ahead[k].x)[e], at = 4 * (i + k * T) + e;
@@ -447,10 +475,11 @@ bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 
 // Tokens of a run: the longest that fits its shared memory and still gives the
 // GPU CTAs enough; short ones where rows are few.  Each of a row's CTAs reads all of
-// its history: with a long one a CTA an SM is enough.
+// its history: with a long one a CTA for two SMs is enough (12 rows of 32000 with 131000
+// entries: 20 us with 96 CTAs, 28 with 192, which L2 feeds no faster).
 constexpr int kLong = 8192;      // entries; from there on 1024 threads
 int run_length(int B, int V, bool bf16, bool history, bool biases, bool many) {
-  const long long want = (many ? 1ll : 4ll) * flh::sm_count();
+  const long long want = (many ? 1ll : 8ll) * flh::sm_count() / 2;
   int run = kRunMax;
   while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > (many ? kRunBytesLong : kRunBytes) || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
