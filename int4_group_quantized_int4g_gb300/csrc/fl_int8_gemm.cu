@@ -1,4 +1,4 @@
-// The linear in 8-bit integers for more than 32 tokens: tcgen05 over pairs of SMs.
+// The linear in 8-bit integers for more than 16 tokens: tcgen05 over pairs of SMs.
 //
 // y^T = W x^T.  A pair of CTAs on two neighbouring SMs multiplies a tile of 256
 // weight rows x BN tokens (tcgen05.mma kind::f16, cta_group::2, 256 x BN x 16,
@@ -7,9 +7,13 @@
 // TMA) and half of the tokens (f16 codes, written by k_codes), so a token tile
 // crosses to the pair once: 48 KB a unit and SM at BN = 256, not 80, where a
 // unit's MMAs take 1024 cycles.  The codes become f16, exactly, on the way into
-// tensor memory, where the MMA reads A: shared memory feeds B alone.
+// tensor memory, where the MMA reads A: shared memory feeds B alone.  Many tokens
+// are bound by the products (8190 x 4096 x 11008 410 us with the rounding of the
+// tokens, 1.80 PFLOP/s), few by the weights' bytes (24 rows of a head of 128003 88 us,
+// 6.1 TB/s), products of a few MB by the way in and out: 4 us before the first MMA
+// (the tokens' kernel, its end and their way here), 2 us after the last.
 //
-// BN, a multiple of 32 up to 256, and how tiles meet pairs go by a plan (plan_for): the
+// BN, a multiple of 32 up to 256, and how tiles meet pairs go by a plan (gemm_plan): the
 // tiles are taken in waves, all pairs next to one another (8 token tiles by a run of
 // weight tiles, for L2); the rest is taken whole, or cut into equal runs of units,
 // whichever ends sooner.  Cut tiles come first, so that joining them hides behind
@@ -19,13 +23,17 @@
 //
 // Roles in a CTA:
 //   warp 0        tokens: per unit two TMA boxes of BN / 2 tokens x 64 columns
-//   warp 1        tensor memory; in the pair's first CTA one thread issues the MMAs
+//   warp 1        tensor memory; in the pair's first CTA it issues the MMAs.  The whole warp
+//                 runs the loop and one thread of it issues: operands then lie in uniform
+//                 registers (eight MMAs in 150 cycles; by a lone thread in 650)
 //   warp 2        weights: per unit a TMA box of 128 rows x 128 columns
 //   warps 4..11   codes to f16 into a ring of A tiles in tensor memory, four warps a
 //                 unit in turn (their arrivals, like the tokens' bytes, are counted on the
 //                 barriers of the first CTA, where the MMAs are issued)
 //   warps 12..19  accumulator times scales -> y, by TMA stores from a staging tile
-//                 where y's rows start and end on 16 bytes
+//                 where y's rows start and end on 16 bytes.  They have more registers
+//                 than the others: what spills comes back from L2, as shared memory
+//                 leaves L1 next to nothing
 #include "fl_int8.cuh"
 
 using namespace fl8;
@@ -226,115 +234,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
 
   if (warp < kConv0) {
-  regs_down<kRegsIo>();
-  if (warp == 0) {
-    // ---------------- tokens
-    if (lane == 0) {
-      pdl_wait();
-      Walk k(p, pair);
-      const int half = p.BN / 2;
-      const uint32_t bytes = static_cast<uint32_t>(half) * 256;
-      int i = 0, s = 0;   // units, stage
-      uint32_t ph = 1;    // parity of its last release
-      bool ok = true;
-      while (ok && k.next(p)) {
-        int nt, mt;
-        place(p, k.tile, nt, mt);
-        const int m0 = mt * p.BN + rank * half;
-        for (int g = k.g0; g < k.g1; ++g, ++i) {
-          if (i >= p.xring && !mbar_wait_many(&xempty[s], ph)) {
-            set_status(p.status, FL_ERR_TIMEOUT, 90);
-            ok = false;
-            break;
+    regs_down<kRegsIo>();
+    if (warp == 0) {
+      // ---------------- tokens
+      if (lane == 0) {
+        pdl_wait();
+        Walk k(p, pair);
+        const int half = p.BN / 2;
+        const uint32_t bytes = static_cast<uint32_t>(half) * 256;
+        int i = 0, s = 0;   // units, stage
+        uint32_t ph = 1;    // parity of its last release
+        bool ok = true;
+        while (ok && k.next(p)) {
+          int nt, mt;
+          place(p, k.tile, nt, mt);
+          const int m0 = mt * p.BN + rank * half;
+          for (int g = k.g0; g < k.g1; ++g, ++i) {
+            if (i >= p.xring && !mbar_wait_many(&xempty[s], ph)) {
+              set_status(p.status, FL_ERR_TIMEOUT, 90);
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&xfull[s], 2 * bytes);
+            const uint32_t bar = first_cta(&xfull[s]);
+            uint8_t* dst = smem + static_cast<uint32_t>(s) * bytes;
+            tma_load_pair(dst, &xmap, g * kBlockK, m0, bar);
+            tma_load_pair(dst + bytes / 2, &xmap, g * kBlockK + 64, m0, bar);
+            if (++s == p.xring) s = 0, ph ^= 1u;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&xfull[s], 2 * bytes);
-          const uint32_t bar = first_cta(&xfull[s]);
-          uint8_t* dst = smem + static_cast<uint32_t>(s) * bytes;
-          tma_load_pair(dst, &xmap, g * kBlockK, m0, bar);
-          tma_load_pair(dst + bytes / 2, &xmap, g * kBlockK + 64, m0, bar);
+        }
+        // (the last arrivals from the pair's MMAs come in before the CTA can end)
+        for (int j = 0; ok && j < min(i, p.xring); ++j) {
+          if (i < p.xring) s = j, ph = 0;
+          ok = mbar_wait(&xempty[s], ph);
           if (++s == p.xring) s = 0, ph ^= 1u;
         }
       }
-      // (the last arrivals from the pair's MMAs come in before the CTA can end)
-      for (int j = 0; ok && j < min(i, p.xring); ++j) {
-        if (i < p.xring) s = j, ph = 0;
-        ok = mbar_wait(&xempty[s], ph);
-        if (++s == p.xring) s = 0, ph ^= 1u;
+    } else if (warp == 2) {
+      // ---------------- weights: older than the kernel before this one
+      if (lane == 0) {
+        Walk k(p, pair);
+        const int wring = 1 << p.wshift;
+        int i = 0;
+        bool ok = true;
+        while (ok && k.next(p)) {
+          int nt, mt;
+          place(p, k.tile, nt, mt);
+          const int n0 = nt * 2 * kRows + rank * kRows;
+          for (int g = k.g0; g < k.g1; ++g, ++i) {
+            const int s = i & (wring - 1);
+            if (i >= wring && !mbar_wait_many(&wempty[s], static_cast<uint32_t>((i >> p.wshift) - 1) & 1u)) {
+              set_status(p.status, FL_ERR_TIMEOUT, 91);
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&wfull[s], kWStage);
+            tma_load_2d(smem + p.woff + s * kWStage, &wmap, g * kBlockK, n0, &wfull[s]);
+          }
+        }
+        if (!ok)
+          for (int j = i - wring; j < i; ++j) mbar_wait(&wfull[j & (wring - 1)], static_cast<uint32_t>(j >> p.wshift) & 1u);
       }
-    }
-  } else if (warp == 2) {
-    // ---------------- weights: older than the kernel before this one
-    if (lane == 0) {
-      Walk k(p, pair);
-      const int wring = 1 << p.wshift;
-      int i = 0;
-      bool ok = true;
-      while (ok && k.next(p)) {
-        int nt, mt;
-        place(p, k.tile, nt, mt);
-        const int n0 = nt * 2 * kRows + rank * kRows;
-        for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (wring - 1);
-          if (i >= wring && !mbar_wait_many(&wempty[s], static_cast<uint32_t>((i >> p.wshift) - 1) & 1u)) {
-            set_status(p.status, FL_ERR_TIMEOUT, 91);
-            ok = false;
+    } else if (warp == 1) {
+      // ---------------- MMAs of the pair
+      if (rank == 0) {   // (the whole warp runs the loop: what the MMAs take then lies in uniform registers)
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.BN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
+        const uint32_t stage = static_cast<uint32_t>(p.BN) * 128;   // bytes of this CTA's tokens of a unit
+        const uint64_t desc0 = sw128_desc(smem_u32(smem));
+        const bool one = elect_one();
+        Walk k(p, pair);
+        int i = 0, j = 0, xs = 0;   // units, tiles, token stage
+        uint32_t xph = 0;
+        bool ok = true, there = false;
+        while (ok && k.next(p)) {
+          const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
+          if (use > 0 && !mbar_wait_many(&dempty[acc], static_cast<uint32_t>(use - 1) & 1u)) {
+            set_status(p.status, FL_ERR_TIMEOUT, 92);
             break;
           }
-          mbar_arrive_expect_tx(&wfull[s], kWStage);
-          tma_load_2d(smem + p.woff + s * kWStage, &wmap, g * kBlockK, n0, &wfull[s]);
-        }
-      }
-      if (!ok)
-        for (int j = i - wring; j < i; ++j) mbar_wait(&wfull[j & (wring - 1)], static_cast<uint32_t>(j >> p.wshift) & 1u);
-    }
-  } else if (warp == 1) {
-    // ---------------- MMAs of the pair
-    if (rank == 0) {   // (the whole warp runs the loop: what the MMAs take then lies in uniform registers)
-      const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(p.BN >> 3) << 17) | (static_cast<uint32_t>(256 >> 4) << 24);
-      const uint32_t stage = static_cast<uint32_t>(p.BN) * 128;   // bytes of this CTA's tokens of a unit
-      const uint64_t desc0 = sw128_desc(smem_u32(smem));
-      const bool one = elect_one();
-      Walk k(p, pair);
-      int i = 0, j = 0, xs = 0;   // units, tiles, token stage
-      uint32_t xph = 0;
-      bool ok = true, there = false;
-      while (ok && k.next(p)) {
-        const int acc = accs == 2 ? j & 1 : 0, use = accs == 2 ? j >> 1 : j;
-        if (use > 0 && !mbar_wait_many(&dempty[acc], static_cast<uint32_t>(use - 1) & 1u)) {
-          set_status(p.status, FL_ERR_TIMEOUT, 92);
-          break;
-        }
-        const uint32_t d = tmem + acc * 128;
-        for (int g = k.g0; g < k.g1; ++g, ++i) {
-          const int s = i & (kRing - 1);
-          if (!there && (!mbar_wait_many(&xfull[xs], xph) || !mbar_wait_many(&afull[s], static_cast<uint32_t>(i >> 2) & 1u))) {
-            set_status(p.status, FL_ERR_TIMEOUT, 93);
-            ok = false;
-            break;
-          }
-          const int x = xs;
-          if (++xs == p.xring) xs = 0, xph ^= 1u;
-          tc_fence_after();
-          if (one) {
-            const uint64_t b = desc0 + ((static_cast<uint32_t>(x) * stage) >> 4);
-            const uint32_t a = tmem + kACols + s * 64;
+          const uint32_t d = tmem + acc * 128;
+          for (int g = k.g0; g < k.g1; ++g, ++i) {
+            const int s = i & (kRing - 1);
+            if (!there && (!mbar_wait_many(&xfull[xs], xph) || !mbar_wait_many(&afull[s], static_cast<uint32_t>(i >> 2) & 1u))) {
+              set_status(p.status, FL_ERR_TIMEOUT, 93);
+              ok = false;
+              break;
+            }
+            const int x = xs;
+            if (++xs == p.xring) xs = 0, xph ^= 1u;
+            tc_fence_after();
+            if (one) {
+              const uint64_t b = desc0 + ((static_cast<uint32_t>(x) * stage) >> 4);
+              const uint32_t a = tmem + kACols + s * 64;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mma_pair(d, a + h * 32 + q * 8, b + h * (stage >> 5) + q * 2, idesc, g != k.g0 || h != 0 || q != 0);
-            commit_pair(&xempty[x]);
-            commit_pair(&aempty[s]);
+                for (int q = 0; q < 4; ++q)
+                  mma_pair(d, a + h * 32 + q * 8, b + h * (stage >> 5) + q * 2, idesc, g != k.g0 || h != 0 || q != 0);
+              commit_pair(&xempty[x]);
+              commit_pair(&aempty[s]);
+            }
+            __syncwarp();
+            there = mbar_test(&xfull[xs], xph) && mbar_test(&afull[(i + 1) & (kRing - 1)], static_cast<uint32_t>((i + 1) >> 2) & 1u);
           }
+          if (ok && one) commit_pair(&dfull[acc]);
           __syncwarp();
-          there = mbar_test(&xfull[xs], xph) && mbar_test(&afull[(i + 1) & (kRing - 1)], static_cast<uint32_t>((i + 1) >> 2) & 1u);
+          ++j;
         }
-        if (ok && one) commit_pair(&dfull[acc]);
-        __syncwarp();
-        ++j;
       }
     }
-  }
   } else if (warp < kEpi0) {
     regs_down<kRegsConv>();
     // ---------------- codes to f16: thread = weight row = tensor memory lane; every other unit

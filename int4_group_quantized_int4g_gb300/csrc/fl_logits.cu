@@ -14,8 +14,11 @@
 // through registers once: temperature, mask, the store, and a running maximum
 // and sum of exp (x - max) a thread.  The runs' results are joined by the row's last
 // CTA in their order.  Every step of the rules is one fp32 rounding, so that equal
-// logits stay equal and ties are the formula's.  Bound by HBM: the logits in, fp32
-// out.
+// logits stay equal and ties are the formula's.  Bound by HBM, the logits in and fp32
+// out, where there is little to look up (512 rows of 128003 without rules 83 us, 6.3
+// TB/s), else by instructions: with histories of 1000 to 2000 entries and 20 biases a
+// row 121 us, 7000 warp instructions for a run of 4096, a third of them for the
+// history, a third for what a CTA does once.
 #include <type_traits>
 
 #include "fl_common.cuh"
