@@ -1060,7 +1060,10 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
     for k, v, a, b in zip(k_caches, v_caches, k_scales, v_scales):
         if k.shape != shape or v.shape != shape or a.shape != scales or b.shape != scales:
             _raise(where, "the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
-        flat += (_ptr(k, u8, "k_cache"), _ptr(v, u8, "v_cache"), _ptr(a, f32, "k_scale"), _ptr(b, f32, "v_scale"), nb, block, heads, dim, 0)
+        if not (k.dtype is u8 and v.dtype is u8 and a.dtype is f32 and b.dtype is f32 and k.is_cuda and v.is_cuda and a.is_cuda
+                and b.is_cuda and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()):
+            _raise(where, "expected contiguous CUDA tensors, caches of uint8 and scales of float32")
+        flat += (k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), nb, block, heads, dim, 0)
     n = pairs.numel() // 2
     _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, "pairs"),
                                           _row(count, i32, 1, "count"), n, _status_block(where, status, device), _stream()))

@@ -292,6 +292,17 @@ def test_logits_many_rows(B, V):
     _logits_check(x, kw)
 
 
+def test_logits_more_rows_than_tickets():
+    """Rows in several launches: a long batch, one run a row and several."""
+    for B, V in ((66000, 33), (65540, 1100)):
+        x, kw = _logits_case(B, V, 1, torch.bfloat16, history=1)
+        dev = {k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}
+        got = fl.fl_logits_process(x, **dev)
+        some = np.concatenate([np.arange(0, B, 997), np.arange(65530, B)])
+        _logits_check(x[torch.from_numpy(some).to(DEV)], {k: v[some] for k, v in kw.items()},
+                      {k: v[torch.from_numpy(some).to(DEV)] for k, v in got.items()})
+
+
 def test_logits_each_rule_alone():
     x, kw = _logits_case(4, 3001, 9, torch.float32, history=200, biases=9, grammar=True)
     base = {k: kw[k] for k in ("history", "history_lens")}
