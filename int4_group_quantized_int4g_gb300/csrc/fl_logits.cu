@@ -12,12 +12,14 @@
 // penalty, but two of three warps meet one, so doing it on the way through the run
 // cost 80 instructions a logit (512 rows of 128003: 261 us).  Last the run passes
 // through registers once: temperature, mask, the store, and a running maximum
-// and sum of exp (x - max) a thread.  The runs' results are joined by the row's last
-// CTA in their order.  Every step of the rules is one fp32 rounding, so that equal
+// and sum of exp (x - max) a thread.  The runs' results are joined in their order, by the
+// row's last CTA, or, with many CTAs, by a kernel of its own: a CTA that takes a ticket
+// waits until its stores are seen (512 rows of 128003 112 us, not 122; of few CTAs the second
+// launch would cost the host more).  Every step of the rules is one fp32 rounding, so that equal
 // logits stay equal and ties are the formula's.  Bound by HBM, the logits in and fp32
 // out, where there is little to look up (512 rows of 128003 without rules 83 us, 6.3
 // TB/s), else by instructions: with histories of 1000 to 2000 entries and 20 biases a
-// row 121 us, 7000 warp instructions for a run of 4096, a third of them for the
+// row 112 us, 7000 warp instructions for a run of 4096, a third of them for the
 // history, a third for what a CTA does once.
 #include <type_traits>
 
@@ -31,7 +33,10 @@ constexpr int kLead = 32;                      // room before a run's first whol
 constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one launch
 constexpr int kRunMin = 1024, kRunMax = 16384;
 constexpr int kThreads = 256;                  // with short histories
+constexpr int kJoinThreads = 64;
+constexpr int kApart = 16;                     // CTAs for each SM from which on a kernel of its own joins the runs
 constexpr int kRunBytes = 40960, kRunBytesLong = 81920;   // shared memory of a run, with short and long histories
+constexpr int kRunBytesRow = 61440;            // of one that is the whole row
 
 struct Partial {
   float top, sum;
@@ -51,6 +56,7 @@ struct LogitsParams {
   fl_logits_rules r;
   int V, run, runs;   // a run: tokens after the row's first 16-byte boundary
   int vec_out, vec_h;
+  int apart;          // a kernel of its own joins the runs
 };
 
 __device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
@@ -107,6 +113,33 @@ struct Best {
     top = t;
   }
 };
+
+// The row's results from `all` of it.
+__device__ __forceinline__ void write_row(const LogitsParams& p, uint32_t b, const Best& all) {
+  const float log_sum = logf(all.sum);
+  const bool none = all.top == -INFINITY;
+  p.token[b] = all.index;
+  if (p.lse) p.lse[b] = all.sum == 0.f ? -INFINITY : (none ? 0.f : all.top) + log_sum;
+  if (p.logprob) p.logprob[b] = all.sum == 0.f ? -INFINITY : -log_sum;
+}
+// Joins the row's runs, with T threads, and writes the row's results.
+template <int T>
+__device__ __forceinline__ void join_runs(const LogitsParams& p, uint32_t b, Best* warps) {
+  const int tid = threadIdx.x;
+  Best best = {-INFINITY, 0.f, -1};
+  for (int i = tid; i < p.runs; i += T) {
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(b) * p.runs + i));
+    best.join(Best{f.x, f.y, __float_as_int(f.z)});
+  }
+  best.join_warp();
+  if ((tid & 31) == 0) warps[tid >> 5] = best;
+  __syncthreads();
+  if (tid < 32) {
+    best = tid < T / 32 ? warps[tid] : Best{-INFINITY, 0.f, -1};
+    best.join_warp();
+    if (tid == 0) write_row(p, b, best);
+  }
+}
 
 // Shared memory of a run of `room` tokens: the logits; for history or biases a
 // word a token (its count, 16 bits with fp32 logits and few entries; with bf16
@@ -435,43 +468,34 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
   best.join_warp();
   if ((tid & 31) == 0) warps[tid >> 5] = best;
   __syncthreads();
-  auto write = [&](const Best& all) {
-    const float log_sum = logf(all.sum);
-    const bool none = all.top == -INFINITY;
-    p.token[b] = all.index;
-    if (p.lse) p.lse[b] = all.sum == 0.f ? -INFINITY : (none ? 0.f : all.top) + log_sum;
-    if (p.logprob) p.logprob[b] = all.sum == 0.f ? -INFINITY : -log_sum;
-  };
+  if (p.apart && tid >= 32) return;
   if (tid < 32) {
     best = tid < T / 32 ? warps[tid] : Best{-INFINITY, 0.f, -1};
     best.join_warp();
     if (tid == 0) {
       finish = 0;
       if (p.runs == 1) {
-        write(best);
+        write_row(p, b, best);
       } else {
         __stcg(reinterpret_cast<float4*>(p.part + static_cast<int64_t>(b) * p.runs + run),
                make_float4(best.top, best.sum, __int_as_float(best.index), 0.f));
-        finish = atom_add_acq_rel_gpu(p.cnt + b, 1) == p.runs - 1;
-        if (finish) p.cnt[b] = 0;
+        if (!p.apart) {
+          finish = atom_add_acq_rel_gpu(p.cnt + b, 1) == p.runs - 1;
+          if (finish) p.cnt[b] = 0;
+        }
       }
     }
   }
+  if (p.apart) return;
   __syncthreads();
-  if (!finish) return;
-  best = {-INFINITY, 0.f, -1};
-  for (int i = tid; i < p.runs; i += T) {
-    const float4 f = __ldcg(reinterpret_cast<const float4*>(p.part + static_cast<int64_t>(b) * p.runs + i));
-    best.join(Best{f.x, f.y, __float_as_int(f.z)});
-  }
-  best.join_warp();
-  if ((tid & 31) == 0) warps[tid >> 5] = best;
-  __syncthreads();
-  if (tid < 32) {
-    best = tid < T / 32 ? warps[tid] : Best{-INFINITY, 0.f, -1};
-    best.join_warp();
-    if (tid == 0) write(best);
-  }
+  if (finish) join_runs<T>(p, b, warps);
+}
+
+__global__ void __launch_bounds__(kJoinThreads) k_logits_join(const LogitsParams p) {
+  __shared__ Best warps[kJoinThreads / 32];
+  pdl_wait();
+  pdl_launch_dependents();
+  join_runs<kJoinThreads>(p, blockIdx.x, warps);
 }
 
 bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -479,12 +503,15 @@ bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 // Tokens of a run: the longest that fits its shared memory and still gives the
 // GPU CTAs enough; short ones where rows are few.  Each of a row's CTAs reads all of
 // its history: with a long one a CTA for two SMs is enough (12 rows of 32000 with 131000
-// entries: 20 us with 96 CTAs, 28 with 192, which L2 feeds no faster).
+// entries: 20 us with 96 CTAs, 28 with 192, which L2 feeds no faster).  With short ones
+// five CTAs an SM are best (runs of 8192, three an SM: 512 rows of 128003 117 us, not 112),
+// but for a row that one run holds (2000 rows of 5000: 27 us, not 35 in two runs).
 constexpr int kLong = 8192;      // entries; from there on 1024 threads
 int run_length(int B, int V, bool bf16, bool history, bool biases, bool many) {
   const long long want = (many ? 1ll : 8ll) * flh::sm_count() / 2;
+  auto most = [&](int run) { return many ? kRunBytesLong : run >= V ? kRunBytesRow : kRunBytes; };
   int run = kRunMax;
-  while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > (many ? kRunBytesLong : kRunBytes) || (V + run - 1ll) / run * B < want)) run /= 2;
+  while (run > kRunMin && (run_bytes(run, bf16, history, biases, many) > most(run) || (V + run - 1ll) / run * B < want)) run /= 2;
   return run;
 }
 int run_shortest(int B, int V) {   // of all types and rules (long histories need fewer CTAs)
@@ -567,6 +594,7 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
   const int64_t size = bf16 ? 2 : 4;
   const uintptr_t in0 = reinterpret_cast<uintptr_t>(logits) / size, out0 = reinterpret_cast<uintptr_t>(out) / 4;
   p.vec_out = out && (in0 - out0) % 4 == 0 && (logits_stride - out_stride) % 4 == 0;
+  p.apart = p.runs > 1 && static_cast<long long>(B) * p.runs > kApart * flh::sm_count();
   const size_t smem = run_bytes(p.run + kLead, bf16, r.history, r.bias, many);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   for (int b = 0; b < B;) {
@@ -583,6 +611,10 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     const int rc = many ? (bf16 ? launch<true, true>(q, n, smem, s) : launch<false, true>(q, n, smem, s))
                         : (bf16 ? launch<true, false>(q, n, smem, s) : launch<false, false>(q, n, smem, s));
     if (rc != FL_OK) return rc;
+    if (p.apart) {
+      const int rj = flh::launch_early(k_logits_join, dim3(n), dim3(kJoinThreads), 0, s, q);
+      if (rj != FL_OK) return rj;
+    }
     b += n;
   }
   return FL_OK;

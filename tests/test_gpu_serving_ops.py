@@ -303,6 +303,47 @@ def test_logits_more_rows_than_tickets():
                       {k: v[torch.from_numpy(some).to(DEV)] for k, v in got.items()})
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_logits_many_rows_of_several_runs(dtype):
+    """As many CTAs as take a kernel of their own to join the runs: rows without a token, with a NaN, with the
+    largest in several runs; the same bits replayed; then few rows with the same workspace."""
+    B, V = 1000, 20003
+    x, kw = _logits_case(B, V, 4, dtype, history=30, biases=3, grammar=True)
+    x[3, 12345], x[4, 19999], x[5] = float("nan"), float("inf"), -float("inf")
+    x[6, 50:20000:997] = 80.0
+    kw["allowed"][6], kw["allowed"][7] = -1, 0
+    kw["bias"][18:21] = 0
+    dev = {k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}
+    ws = torch.zeros(fl.fl_logits_process_workspace(B, V), dtype=torch.uint8, device=DEV)
+    got = fl.fl_logits_process(x, **dev, ws=ws)
+    some = np.concatenate([np.arange(20), np.arange(20, B, 37), [B - 1]])
+    at = torch.from_numpy(some).to(DEV)
+    pick = {k: v[some] for k, v in kw.items() if not k.startswith("bias")}
+    pick["bias_offsets"] = (3 * np.arange(len(some) + 1)).astype(np.int32)
+    pick["bias_ids"], pick["bias"] = kw["bias_ids"].reshape(B, 3)[some].ravel(), kw["bias"].reshape(B, 3)[some].ravel()
+    _logits_check(x[at], pick, {k: v[at] for k, v in got.items()})
+    assert got["token"][5] == -1 and got["token"][7] == -1
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = fl.fl_logits_process(x, **dev, ws=ws)
+    for _ in range(3):
+        for v in again.values():
+            v.zero_()
+        graph.replay()
+    torch.cuda.synchronize()
+    for k, v in got.items():
+        assert torch.equal(again[k].view(torch.int32), v.view(torch.int32)), k
+    few, kf = _logits_case(3, V, 5, dtype, history=30)
+    _logits_check(few, kf, fl.fl_logits_process(few, **{k: torch.from_numpy(v).to(DEV) for k, v in kf.items()}, ws=ws))
+    assert fl.fl_int4g_status(ws) == 0
+
+
+@pytest.mark.parametrize("V", [4097, 5000, 8191, 8192, 8193])
+def test_logits_rows_of_one_long_run(V):
+    _logits_check(*_logits_case(700, V, V, torch.float32, history=60, biases=2, grammar=True))
+    _logits_check(*_logits_case(650, V, V + 1, torch.bfloat16, history=90))
+
+
 def test_logits_each_rule_alone():
     x, kw = _logits_case(4, 3001, 9, torch.float32, history=200, biases=9, grammar=True)
     base = {k: kw[k] for k in ("history", "history_lens")}
