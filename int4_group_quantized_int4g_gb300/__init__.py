@@ -204,13 +204,14 @@ def _p(t):
 
 
 _WS = {}
+_SCRATCH = 262400   # bytes of a workspace's status block and counters
 _OUTGROWN = []   # workspaces that a larger one has replaced: a captured graph may hold them
 
 
 def _workspace(nbytes, device):
     """A zero-filled workspace per (device, stream), grown on demand.  One that
-    is made while the stream is captured is zero-filled by the graph's replay
-    alone, so it serves that one call."""
+    is made while the stream is captured is zero-filled (its status and counters:
+    scratch need not be) by the graph's replay alone, so it serves that one call."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     key = (device.index, raw(device.index) if raw is not None and device.index is not None
@@ -218,7 +219,9 @@ def _workspace(nbytes, device):
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         if torch.cuda.is_current_stream_capturing():
-            return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            buf[:_SCRATCH].zero_()
+            return buf
         if buf is not None:
             _OUTGROWN.append(buf)
             nbytes = max(nbytes, 2 * buf.numel())   # (so that those kept are smaller together than the last)

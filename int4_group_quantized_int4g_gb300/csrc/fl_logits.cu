@@ -7,20 +7,21 @@
 // Meanwhile it counts the row's history: one word a token of its run, how often it
 // stands in the answer, the top bit for the prompt; whoever counts a token first
 // puts it on a list.  Every CTA of a row reads all of its history, out of L2, and
-// keeps what falls into its run.  Then the listed tokens, and those that a bias
-// names, are changed in shared memory, a thread a token: one in a hundred has a
-// penalty, but two of three warps meet one, so doing it on the way through the run
-// cost 80 instructions a logit (512 rows of 128003: 261 us).  Last the run passes
-// through registers once: temperature, mask, the store, and a running maximum
-// and sum of exp (x - max) a thread.  The runs' results are joined in their order, by the
-// row's last CTA, or, with many CTAs, by a kernel of its own: a CTA that takes a ticket
-// waits until its stores are seen (512 rows of 128003 112 us, not 122; of few CTAs the second
-// launch would cost the host more).  Every step of the rules is one fp32 rounding, so that equal
-// logits stay equal and ties are the formula's.  Bound by HBM, the logits in and fp32
-// out, where there is little to look up (512 rows of 128003 without rules 83 us, 6.3
-// TB/s), else by instructions: with histories of 1000 to 2000 entries and 20 biases a
-// row 112 us, 7000 warp instructions for a run of 4096, a third of them for the
-// history, a third for what a CTA does once.
+// keeps what falls into its run; where that is much, a kernel before puts the history in
+// the order of the runs, while the logits are already on their way (512 rows of 128003
+// with 2000 entries 106 us, not 112, with 7000 104 and 152, with 16000 117 and 248).  Then
+// the listed tokens, and those that a bias names, are changed in shared memory, a thread
+// a token: one in a hundred has a penalty, but two of three warps meet one, so doing it
+// on the way through the run cost 80 instructions a logit (512 rows of 128003: 261 us).
+// Last the run passes through registers once: temperature, mask, the store, and a
+// running maximum and sum of exp (x - max) a thread.  The runs' results are joined in
+// their order, by the row's last CTA, or, with many CTAs, by a kernel of its own: a CTA
+// that takes a ticket waits until its stores are seen (512 rows of 128003 112 us, not 122;
+// of few CTAs the second launch would cost the host more).  Every step of the rules is
+// one fp32 rounding, so that equal logits stay equal and ties are the formula's.  Bound
+// by HBM, the logits in and fp32 out, where there is little to look up (512 rows of 128003
+// without rules 81 us, 6.5 TB/s), else by instructions: with histories of 1000 to 2000
+// entries and 20 biases a row 106 us.
 #include <type_traits>
 
 #include "fl_common.cuh"
@@ -34,6 +35,14 @@ constexpr int kRowsMax = kTicketTiles * kTicketWarps;   // tickets: rows of one 
 constexpr int kRunMin = 1024, kRunMax = 16384;
 constexpr int kThreads = 256;                  // with short histories
 constexpr int kJoinThreads = 64;
+// A history of 1024 to 23040 entries (48 KB and counts of 16 bits hold them) is sorted by
+// run where a row's CTAs, kApart an SM or more, would read 65536 entries an SM otherwise:
+// there that is as much as the third launch costs the host.
+constexpr int kSortThreads = 512;              // as many runs at most are sorted by
+constexpr int kSortLeast = 1024, kSortMost = 23040;
+constexpr long long kSortWork = 65536;
+constexpr int kSortRows = 8192;                // rows of a launch then,
+constexpr int kSortRoom = 1 << 23;             // and entries of all of them
 constexpr int kApart = 16;                     // CTAs for each SM from which on a kernel of its own joins the runs
 constexpr int kRunBytes = 40960, kRunBytesLong = 81920;   // shared memory of a run, with short and long histories
 constexpr int kRunBytesRow = 61440;            // of one that is the whole row
@@ -57,6 +66,9 @@ struct LogitsParams {
   int V, run, runs;   // a run: tokens after the row's first 16-byte boundary
   int vec_out, vec_h;
   int apart;          // a kernel of its own joins the runs
+  uint16_t* sorted;   // [row][sorted_stride] history by run, or NULL: place in the run's shared memory, top bit: prompt
+  int32_t* begin;     // [row][runs + 1] where in it each run's entries begin
+  int sorted_stride, shift;   // run is 1 << shift
 };
 
 __device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
@@ -113,6 +125,12 @@ struct Best {
     top = t;
   }
 };
+
+// Tokens of a row before its first 16-byte boundary: run 0 begins there, and holds them too.
+template <typename Raw>
+__device__ __forceinline__ int row_head(const void* row, int V) {
+  return min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<int>(sizeof(Raw)), V);
+}
 
 // The row's results from `all` of it.
 __device__ __forceinline__ void write_row(const LogitsParams& p, uint32_t b, const Best& all) {
@@ -182,12 +200,12 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
   if (BF16 || biases)
     for (int i = tid; i < 2 * (room / 32 + 1); i += T) named[i] = 0;
 
-  pdl_wait();
-  pdl_launch_dependents();
+  // (after k_logits_sort, which has waited for all kernels before it, the logits are there)
+  if (LONG || !p.sorted) pdl_wait();
   const uint8_t* row = static_cast<const uint8_t*>(p.x) + static_cast<int64_t>(b) * p.xs * (BF16 ? 2 : 4);
   float* out = p.out ? p.out + static_cast<int64_t>(b) * p.os : nullptr;
   // the row's first token on 16 bytes; a run starts there or whole runs behind
-  const int head = min(static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / (BF16 ? 2 : 4), p.V);
+  const int head = row_head<Raw>(row, p.V);
   const int64_t first = head + static_cast<int64_t>(run) * p.run;
   const int start = static_cast<int>(min(first, static_cast<int64_t>(p.V)));
   const int lo = run == 0 ? 0 : start, hi = static_cast<int>(min(first + p.run, static_cast<int64_t>(p.V)));
@@ -197,6 +215,8 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
     mbar_arrive_expect_tx(&landed, nvec * 16);
     bulk_g2s(x + kLead, row + static_cast<int64_t>(start) * (BF16 ? 2 : 4), nvec * 16, &landed);
   }
+  if (!LONG && p.sorted) pdl_wait();
+  pdl_launch_dependents();
   // the history's entries, four at a time; the first are on their way before the
   // lengths are known (lists are history_max long whatever of them counts)
   constexpr int kAhead = LONG ? 2 : 512 / kThreads;
@@ -212,7 +232,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
       if (4 * i + e < r.history_max) (&f.x)[e] = __ldg(h + 4 * i + e);
     return f;
   };
-  if (counts) {
+  if (counts && (LONG || !p.sorted)) {
     n = min(max(__ldg(r.history_lens + b), 0), r.history_max);
     prompt = r.prompt_lens ? max(__ldg(r.prompt_lens + b), 0) : 0;
 #pragma unroll
@@ -224,7 +244,25 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
   if (tid < few) x[few_at(tid) - base] = reinterpret_cast<const volatile Raw*>(row)[few_at(tid)];
   __syncthreads();
 
-  if (counts) {
+  // an entry of a short history: counts it, and lists its token
+  auto count = [&](int i1, bool asked) {
+    const int shift = HALF ? (i1 & 1) * 16 : 0;
+    uint32_t* w = word + (HALF ? i1 >> 1 : i1);
+    const uint32_t old = asked ? atomicOr(w, HALF ? 0x8000u << shift : 0x80000000u) : atomicAdd(w, 1u << shift);
+    if ((HALF ? old >> shift & 0xffffu : old) == 0) {
+      const int to = atomicAdd(&listed, 1);
+      if (to < room / 4) list[to] = static_cast<uint16_t>(i1);
+    }
+  };
+  if (!LONG && p.sorted) {
+    const int32_t* begin = p.begin + static_cast<int64_t>(b) * (p.runs + 1) + run;
+    const uint16_t* ids = p.sorted + static_cast<int64_t>(b) * p.sorted_stride;
+    const int end = __ldcg(begin + 1);
+    for (int i = __ldcg(begin) + tid; i < end; i += T) {
+      const uint32_t id = __ldcg(ids + i);
+      count(id & 0x7fff, id >> 15);
+    }
+  } else if (counts) {
     const uint32_t width = hi - lo;
     // four entries of a long history, all of the prompt or all of the answer: an
     // operation in shared memory for each, without a branch
@@ -261,20 +299,14 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
         for (int e = 0; e < 4; ++e) {
           const int id = (&ahead[k].x)[e], at = 4 * (i + k * T) + e;
           if (static_cast<uint32_t>(id - lo) < width && at < n) {
-            const int i1 = id - base, shift = HALF ? (i1 & 1) * 16 : 0;
-            uint32_t* w = word + (HALF ? i1 >> 1 : i1);
-            const uint32_t flag = HALF ? 0x8000u << shift : 0x80000000u;
             if constexpr (LONG) {
+              uint32_t* w = word + (id - base);
               if (at < prompt)
-                atomicOr(w, flag);
+                atomicOr(w, 0x80000000u);
               else
                 atomicAdd(w, 1u);
             } else {
-              const uint32_t old = at < prompt ? atomicOr(w, flag) : atomicAdd(w, 1u << shift);
-              if ((HALF ? old >> shift & 0xffffu : old) == 0) {
-                const int to = atomicAdd(&listed, 1);
-                if (to < room / 4) list[to] = static_cast<uint16_t>(i1);
-              }
+              count(id - base, at < prompt);
             }
           }
         }
@@ -491,6 +523,67 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
   if (finish) join_runs<T>(p, b, warps);
 }
 
+// Puts the history of a row (a CTA's) in the order of the runs, each entry as what a run's
+// CTA makes of it.
+template <typename Raw>
+__global__ void __launch_bounds__(kSortThreads) k_logits_sort(const LogitsParams p) {
+  extern __shared__ uint4 raw[];
+  __shared__ int at[kSortThreads], sums[kSortThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.x;
+  at[tid] = 0;
+  pdl_wait();
+  pdl_launch_dependents();   // (after the wait: k_logits, started now, finds the logits)
+  const fl_logits_rules& r = p.r;
+  const int head = row_head<Raw>(static_cast<const Raw*>(p.x) + b * p.xs, p.V);
+  const int n = min(max(r.history_lens[b], 0), r.history_max), prompt = r.prompt_lens ? r.prompt_lens[b] : 0;
+  const int32_t* h = r.history + b * r.history_stride;
+  auto fetch = [&](int i) {
+    int4 f = make_int4(-1, -1, -1, -1);
+    if (p.vec_h && i + 4 <= r.history_max) return *reinterpret_cast<const int4*>(h + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < r.history_max) (&f.x)[e] = h[i + e];
+    return f;
+  };
+  const int4 first = fetch(4 * tid);
+  auto each = [&](auto take) {   // (run, entry of the sorted list)
+    for (int i = 4 * tid; i < n; i += 4 * kSortThreads) {
+      const int4 f = i == 4 * tid ? first : fetch(i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int id = (&f.x)[e];
+        if (i + e >= n || id < 0 || id >= p.V) continue;
+        const int run = max(id - head, 0) >> p.shift;
+        // (its shared memory holds the tokens from head + run's first less kLead on)
+        take(run, static_cast<uint16_t>(id - head - (run << p.shift) + kLead) | (i + e < prompt ? 0x8000u : 0u));
+      }
+    }
+  };
+  __syncthreads();
+  each([&](int run, uint32_t) { atomicAdd(&at[run], 1); });
+  __syncthreads();
+  const int v = at[tid];
+  int inc = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += u;
+  }
+  if (lane == 31) sums[tid >> 5] = inc;
+  __syncthreads();
+  for (int w = 0; w < tid >> 5; ++w) inc += sums[w];
+  int32_t* begin = p.begin + static_cast<int64_t>(b) * (p.runs + 1);
+  if (tid < p.runs) begin[tid + 1] = inc;
+  if (tid == 0) begin[0] = 0;
+  at[tid] = inc - v;
+  __syncthreads();
+  uint16_t* ids = reinterpret_cast<uint16_t*>(raw);
+  each([&](int run, uint32_t id) { ids[atomicAdd(&at[run], 1)] = static_cast<uint16_t>(id); });
+  __syncthreads();
+  uint4* to = reinterpret_cast<uint4*>(p.sorted + static_cast<int64_t>(b) * p.sorted_stride);
+  for (int i = tid; 8 * i < at[p.runs - 1]; i += kSortThreads) to[i] = raw[i];   // (whole vectors: the stride has room)
+}
+
 __global__ void __launch_bounds__(kJoinThreads) k_logits_join(const LogitsParams p) {
   __shared__ Best warps[kJoinThreads / 32];
   pdl_wait();
@@ -549,14 +642,30 @@ bool over(const void* x, int64_t xs, int size, const float* out, int64_t os, int
   return d < wa || d + wb > sa;
 }
 
+// Workspace: the runs' results, where each run's entries of a sorted history begin, these.
+struct LogitsLayout {
+  size_t begin, sorted, bytes;
+};
+LogitsLayout layout(int B, int V) {
+  const long long runs = run_count(V, run_shortest(B, V));
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  LogitsLayout l;
+  l.begin = up(kScratchOff + static_cast<size_t>(B < kRowsMax ? B : kRowsMax) * runs * sizeof(Partial));
+  l.sorted = l.bytes = l.begin;
+  if (B * runs > kApart * flh::sm_count()) {
+    l.sorted = l.begin + up(static_cast<size_t>(B < kSortRows ? B : kSortRows) * ((runs < kSortThreads ? runs : kSortThreads) + 1) * 4);
+    l.bytes = l.sorted + kSortRoom * 2;
+  }
+  return l;
+}
+
 bool logits_args(int B, int V) { return B >= 1 && V >= 1 && V < (1 << 30) && B <= (1 << 30); }
 
 }  // namespace
 
 extern "C" int fl_logits_process_workspace(int B, int V, size_t* out) {
   if (!out || !logits_args(B, V)) return FL_ERR_ARG;
-  const int rows = B < kRowsMax ? B : kRowsMax;
-  *out = kScratchOff + static_cast<size_t>(rows) * run_count(V, run_shortest(B, V)) * sizeof(Partial);
+  *out = layout(B, V).bytes;
   return FL_OK;
 }
 
@@ -577,15 +686,26 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
   if (!r.history && (r.prompt_lens || r.repetition || r.frequency || r.presence)) return FL_ERR_ARG;
   if (!r.bias_offsets != !r.bias_ids || !r.bias_ids != !r.bias || (r.bias && r.bias_count < 0)) return FL_ERR_ARG;
   if (r.allowed && r.allowed_stride < (V + 31) / 32) return FL_ERR_ARG;
-  size_t need = 0;
-  fl_logits_process_workspace(B, V, &need);
-  if (ws_bytes < need) return FL_ERR_WORKSPACE;
+  const LogitsLayout l = layout(B, V);
+  if (ws_bytes < l.bytes) return FL_ERR_WORKSPACE;
 
   LogitsParams p = {};
   p.xs = logits_stride, p.os = out_stride, p.r = r, p.V = V;
-  const bool many = r.history && r.history_max >= kLong;
-  p.run = run_length(B, V, bf16, r.history, r.bias, many);
+  bool many = r.history && r.history_max >= kLong;
+  p.run = run_length(B, V, bf16, r.history, r.bias, false);
   p.runs = run_count(V, p.run);
+  if (r.history && r.history_max >= kSortLeast && r.history_max <= kSortMost && p.runs > 1 && p.runs <= kSortThreads &&
+      static_cast<long long>(B) * p.runs > kApart * flh::sm_count() &&
+      static_cast<long long>(B) * p.runs * r.history_max > kSortWork * flh::sm_count()) {
+    many = false;
+    p.sorted = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + l.sorted);
+    p.begin = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + l.begin);
+    p.sorted_stride = (r.history_max + 7) / 8 * 8;
+    while (1 << p.shift < p.run) ++p.shift;
+  } else if (many) {
+    p.run = run_length(B, V, bf16, r.history, r.bias, true);
+    p.runs = run_count(V, p.run);
+  }
   p.part = reinterpret_cast<Partial*>(static_cast<uint8_t*>(ws) + kScratchOff);
   p.cnt = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(ws) + kTicketOff);
   p.status = static_cast<int32_t*>(ws);
@@ -601,6 +721,8 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     int n = B - b < kRowsMax ? B - b : kRowsMax;
     const long long most = 0x7fffffffll / p.runs;
     if (n > most) n = static_cast<int>(most);
+    if (p.sorted && n > kSortRows) n = kSortRows;
+    if (p.sorted && n > kSortRoom / p.sorted_stride) n = kSortRoom / p.sorted_stride;
     LogitsParams q = p;
     q.x = static_cast<const uint8_t*>(logits) + static_cast<int64_t>(b) * logits_stride * size;
     q.out = out ? out + static_cast<int64_t>(b) * out_stride : nullptr;
@@ -608,6 +730,10 @@ extern "C" int fl_logits_process(const void* logits, int64_t logits_stride, int 
     auto row = [&](auto*& list, int64_t stride) { if (list) list += b * stride; };
     row(q.r.history, r.history_stride), row(q.r.history_lens, 1), row(q.r.prompt_lens, 1), row(q.r.repetition, 1);
     row(q.r.frequency, 1), row(q.r.presence, 1), row(q.r.bias_offsets, 1), row(q.r.allowed, r.allowed_stride), row(q.r.temperature, 1);
+    if (p.sorted) {
+      const int rs = flh::launch_early(bf16 ? k_logits_sort<uint16_t> : k_logits_sort<float>, dim3(n), dim3(kSortThreads), p.sorted_stride * 2, s, q);
+      if (rs != FL_OK) return rs;
+    }
     const int rc = many ? (bf16 ? launch<true, true>(q, n, smem, s) : launch<false, true>(q, n, smem, s))
                         : (bf16 ? launch<true, false>(q, n, smem, s) : launch<false, false>(q, n, smem, s));
     if (rc != FL_OK) return rc;

@@ -344,6 +344,73 @@ def test_logits_rows_of_one_long_run(V):
     _logits_check(*_logits_case(650, V, V + 1, torch.bfloat16, history=90))
 
 
+def _logits_some(x, kw, biases, some, got):
+    """The rows `some` of a call against the formula's; lists of biases of one length."""
+    at = torch.from_numpy(some).to(DEV)
+    pick = {k: v[some] for k, v in kw.items() if not k.startswith("bias")}
+    if biases:
+        pick["bias_offsets"] = (biases * np.arange(len(some) + 1)).astype(np.int32)
+        pick["bias_ids"], pick["bias"] = (kw[k].reshape(-1, biases)[some].ravel() for k in ("bias_ids", "bias"))
+    _logits_check(x[at], pick, {k: v[at] for k, v in got.items()})
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("history", [1023, 1999, 2048, 2501, 5003, 20000, 23040, 23041, 32768])
+def test_logits_many_rows_with_histories(history, dtype):
+    """Histories that are sorted by run first, in one launch or several, and those beside their limits: rows on and off
+    16 bytes, padding, tokens outside the vocabulary, one token throughout, all of prompt or answer, none."""
+    B, V = 1000, 20003
+    x, kw = _logits_case(B, V, history, dtype, history=history, biases=2)
+    h, lens, prompt = kw["history"], kw["history_lens"], kw["prompt_lens"]
+    lens[1], prompt[1] = history, history
+    lens[2], prompt[2] = history, 0
+    h[2] = 17
+    h[3, ::3], h[4, 1::2] = -1, V
+    lens[3], lens[4] = history, history
+    h[5] = np.arange(history) % 9           # the tokens before a row's first 16 bytes among them
+    lens[5], lens[6], lens[7], prompt[8] = history, 0, -3, 2 * history
+    h[9, 0], h[9, -1], lens[9] = V - 1, 2 ** 31 - 1, history
+    h[10], lens[10] = np.where(np.arange(history) % 2, 4095 + np.arange(history) % 9, -2 ** 31), history + 5
+    dev = {k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}
+    some = np.concatenate([np.arange(16), np.arange(16, B, 83), [418, 419, 420, 999]])
+    got = fl.fl_logits_process(x, **dev)
+    _logits_some(x, kw, 2, some, got)
+    wide = torch.zeros((B, V + 14), dtype=dtype, device=DEV)[:, 3:3 + V]
+    wide.copy_(x)
+    other = fl.fl_logits_process(wide, **dev)
+    for k, v in got.items():
+        if k in ("logits", "token"):
+            assert torch.equal(other[k], v), k
+    _logits_some(wide, kw, 2, some[:16], other)
+
+
+def test_logits_made_just_before_with_sorted_histories():
+    """The logits by the kernel before, on another stream too, again and again, in place."""
+    B, V, K = 700, 32000, 64
+    w = torch.randint(-127, 128, (V, K), device=DEV, dtype=torch.int8)
+    t = torch.full((V,), 1e-2, device=DEV)
+    _, kw = _logits_case(B, V, 8, torch.float32, history=2400)
+    dev = {k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}
+    xs = [torch.randn((B, K), device=DEV).to(torch.bfloat16) for _ in range(4)]
+    want = []
+    for x in xs:
+        y = fl.fl_int8_linear(x, w, t, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in fl.fl_logits_process(y, **dev).items()})
+        torch.cuda.synchronize()
+    y = torch.empty((B, V), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (torch.cuda.current_stream(), side):
+        with torch.cuda.stream(stream):
+            for i in range(12):
+                fl.fl_int8_linear(xs[i % 4], w, t, y=y)
+                got = fl.fl_logits_process(y, **dev, out=y if i % 2 else None)
+                for k, v in got.items():
+                    assert torch.equal(v, want[i % 4][k]), (i, k)
+        stream.synchronize()
+
+
 def test_logits_each_rule_alone():
     x, kw = _logits_case(4, 3001, 9, torch.float32, history=200, biases=9, grammar=True)
     base = {k: kw[k] for k in ("history", "history_lens")}
