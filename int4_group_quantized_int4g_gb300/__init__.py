@@ -219,7 +219,9 @@ def _workspace(nbytes, device):
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         if torch.cuda.is_current_stream_capturing():
-            buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            if nbytes <= _SCRATCH:
+                return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
             buf[:_SCRATCH].zero_()
             return buf
         if buf is not None:
