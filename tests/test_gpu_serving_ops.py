@@ -411,6 +411,26 @@ def test_logits_made_just_before_with_sorted_histories():
         stream.synchronize()
 
 
+def test_captured_calls_without_a_workspace():
+    """Scratch is the graph's own and not cleared: the second replay finds what the first has left."""
+    x, kw = _logits_case(700, 32000, 3, torch.float32, history=2400)
+    dev = {k: torch.from_numpy(v).to(DEV) for k, v in kw.items()}
+    a, w, t = _linear_case(90, 1500, 1024, 2)
+    b = a[:1]
+    want = fl.fl_logits_process(x, **dev), fl.fl_int8_linear(a, w, t), fl.fl_int8_linear(b, w, t)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one, two, three = fl.fl_logits_process(x, **dev), fl.fl_int8_linear(a, w, t), fl.fl_int8_linear(b, w, t)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in want[0].items():
+            assert torch.equal(one[k], v), k
+        assert torch.equal(two, want[1]) and torch.equal(three, want[2])
+        for v in (*one.values(), two, three):
+            v.zero_()
+
+
 def test_logits_each_rule_alone():
     x, kw = _logits_case(4, 3001, 9, torch.float32, history=200, biases=9, grammar=True)
     base = {k: kw[k] for k in ("history", "history_lens")}
