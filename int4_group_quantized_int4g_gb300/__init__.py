@@ -741,11 +741,23 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
 # -------------------------------------------------- linear in 8-bit integers
 
 def _here(t, name):
-    """The tensor's device, which has to be the current one: its streams take the call."""
+    """The tensor's device, which has to be the current one, and its current stream's handle."""
     device = t.device
-    if not t.is_cuda or device.index != _device():
+    index = device.index
+    if not t.is_cuda or index != _device():
         _raise(name, f"expected tensors of the current CUDA device, got one on {device}")
-    return device
+    raw = getattr(_TORCH._C, "_cuda_getCurrentRawStream", None)
+    return device, raw(index) if raw is not None else _TORCH.cuda.current_stream(device).cuda_stream
+
+
+def _space(ws, nbytes, device, stream):
+    """The caller's workspace or the stream's (to be held until the call), its address and bytes."""
+    if ws is not None:
+        return ws, _p(ws), ws.numel()
+    ws = _WS.get((device.index, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspace(nbytes, device)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def _matrix(t, dtype, name):
@@ -773,11 +785,11 @@ def fl_int8_quantize(x):
     if x.dim() != 2:
         _raise("fl_int8_quantize", "x is [M, K]")
     M, K = x.shape
-    device = _here(x, "fl_int8_quantize")
+    device, stream = _here(x, "fl_int8_quantize")
     xp, xs = _matrix(x, torch.bfloat16, "x")
     codes = torch.empty((M, K), dtype=torch.int8, device=device)
     scale = torch.empty((M,), dtype=torch.float32, device=device)
-    _check("fl_int8_quantize", lib().fl_int8_quantize(xp, xs, M, K, codes.data_ptr(), scale.data_ptr(), _stream()))
+    _check("fl_int8_quantize", lib().fl_int8_quantize(xp, xs, M, K, codes.data_ptr(), scale.data_ptr(), stream))
     return codes, scale
 
 
@@ -805,7 +817,7 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         _raise("fl_int8_linear", "x is [M, K], w [N, K]")
     M, K = x.shape
     N = w.shape[0]
-    device = _here(x, "fl_int8_linear")
+    device, stream = _here(x, "fl_int8_linear")
     sp = None
     if x_scale is None:
         xp, xs = _matrix(x, torch.bfloat16, "x")
@@ -829,9 +841,8 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         kind = FL_OUT_FP32
     else:
         _raise("fl_int8_linear", "y is bfloat16 or float32")
-    if ws is None:
-        ws = _workspace(_int8_workspace(device.index, M, N, K), device)
-    _check("fl_int8_linear", lib().fl_int8_linear(xp, xs, sp, M, K, wp, tp, N, yp, ys, kind, _p(ws), ws.numel(), _stream()))
+    ws, wsp, wsn = _space(ws, _int8_workspace(device.index, M, N, K), device, stream)
+    _check("fl_int8_linear", lib().fl_int8_linear(xp, xs, sp, M, K, wp, tp, N, yp, ys, kind, wsp, wsn, stream))
     return y
 
 
@@ -877,7 +888,7 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     if logits.dim() != 2:
         _raise(name, "logits are [B, V]")
     B, V = logits.shape
-    device = _here(logits, name)
+    device, stream = _here(logits, name)
     i32, f32 = torch.int32, torch.float32
     bf16 = logits.dtype is torch.bfloat16
     lp, ls = _matrix(logits, torch.bfloat16 if bf16 else f32, "logits")
@@ -928,12 +939,11 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     token = got["token"] = torch.empty(B, dtype=i32, device=device)
     lse = got["lse"] = torch.empty(B, dtype=f32, device=device)
     logprob = got["logprob"] = torch.empty(B, dtype=f32, device=device)
-    if ws is None:
-        ws = _workspace(_logits_workspace(device.index, B, V), device)
+    ws, wsp, wsn = _space(ws, _logits_workspace(device.index, B, V), device, stream)
     rc = lib().fl_logits_process(
         lp, ls, FL_OUT_BF16 if bf16 else FL_OUT_FP32, B, V,
         _LOGITS_RULES.pack(hp, nl, np, rp, fp, pp, bo, bi, bp, ap, tp, hs, stride, most, count), op, os_, token.data_ptr(),
-        lse.data_ptr(), logprob.data_ptr(), _p(ws), ws.numel(), _stream())
+        lse.data_ptr(), logprob.data_ptr(), wsp, wsn, stream)
     if rc:
         raise Int4gError(name, rc)
     return got
@@ -950,18 +960,19 @@ def _kv8_caches(n):
 
 
 def _pool(where, refs, table, kv_lens, block):
+    """(struct fl_kv8_pool, device, its current stream)"""
     i32 = _torch().int32
-    _here(refs, where)
+    device, stream = _here(refs, where)
     if table.dim() != 2 or kv_lens.numel() != table.shape[0]:
         _raise(where, "table is [slots, max_blocks], kv_lens [slots]")
     slots, most = table.shape
     return _KV8_POOL.pack(_ptr(refs, i32, "refs"), _ptr(table, i32, "table"), _ptr(kv_lens, i32, "kv_lens"), refs.numel(),
-                          slots, most, block)
+                          slots, most, block), device, stream
 
 
-def _status_block(where, status, device):
+def _status_block(where, status, device, stream):
     if status is None:
-        return _workspace(256, device).data_ptr()
+        return _space(None, 256, device, stream)[1]
     if status.numel() * status.element_size() < 16:
         _raise(where, "the status block has 16 bytes")
     return _p(status)
@@ -973,10 +984,11 @@ def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None)
     page; table int32 [slots, max_blocks], kv_lens int32 [slots]: those of
     fl_kv8_append and fl_kv8_attention; block: tokens of a page.  All three are
     updated.  status: as for fl_kv8_append."""
-    pool = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
+    pool, device, stream = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
     n = seqs.numel()
     _check("fl_kv8_pages_free", lib().fl_kv8_pages_free(
-        pool, _row(seqs, _TORCH.int32, n, "seqs"), _row(keep, _TORCH.int32, n, "keep") if keep is not None else None, n, _status_block("fl_kv8_pages_free", status, refs.device), _stream()))
+        pool, _row(seqs, _TORCH.int32, n, "seqs"), _row(keep, _TORCH.int32, n, "keep") if keep is not None else None, n,
+        _status_block("fl_kv8_pages_free", status, device, stream), stream))
 
 
 def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=None):
@@ -984,11 +996,11 @@ def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=Non
     of slot parents[i] (int32 lists; the rest as in fl_kv8_pages_free).  A child
     that is not empty, that the list names again or that is a parent in it is left
     out, and the status block says so."""
-    pool = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
+    pool, device, stream = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
     n = parents.numel()
     _check("fl_kv8_pages_fork", lib().fl_kv8_pages_fork(
         pool, _row(parents, _TORCH.int32, n, "parents"), _row(children, _TORCH.int32, n, "children"), n,
-        _status_block("fl_kv8_pages_fork", status, refs.device), _stream()))
+        _status_block("fl_kv8_pages_fork", status, device, stream), stream))
 
 
 def fl_kv8_pages_workspace(num_blocks, slots, max_blocks, block):
@@ -1014,16 +1026,15 @@ def fl_kv8_pages_alloc(refs, table, kv_lens, seqs, new_tokens, block, ws=None):
     again, or whose table is too short, is left out, and the status block at the
     start of ws says so.  ws: as for fl_int8_linear."""
     torch = _torch()
-    pool = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
-    n, device = seqs.numel(), refs.device
+    pool, device, stream = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
+    n = seqs.numel()
     granted = torch.empty((n,), dtype=torch.int32, device=device)
     pairs = torch.empty((n, 2), dtype=torch.int32, device=device)
     count = torch.empty((1,), dtype=torch.int32, device=device)
-    if ws is None:
-        ws = _workspace(_pages_workspace(refs.numel(), *table.shape, block), device)
+    ws, wsp, wsn = _space(ws, _pages_workspace(refs.numel(), *table.shape, block), device, stream)
     _check("fl_kv8_pages_alloc", lib().fl_kv8_pages_alloc(
         pool, _row(seqs, torch.int32, n, "seqs"), _row(new_tokens, torch.int32, n, "new_tokens"), n,
-        granted.data_ptr() or None, pairs.data_ptr() or None, count.data_ptr(), _p(ws), ws.numel(), _stream()))
+        granted.data_ptr() or None, pairs.data_ptr() or None, count.data_ptr(), wsp, wsn, stream))
     return granted, pairs, count
 
 
@@ -1034,8 +1045,8 @@ def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None
     False new ones), the copies for fl_kv8_pages_copy, and int32 [blocks] where each
     page is now, -1 for free ones."""
     torch = _torch()
-    pool = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
-    device, blocks = refs.device, refs.numel()
+    pool, device, stream = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
+    blocks = refs.numel()
     if not in_place:
         table, refs = torch.empty_like(table), torch.empty_like(refs)
     pairs = torch.empty((blocks // 2, 2), dtype=torch.int32, device=device)
@@ -1043,7 +1054,7 @@ def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None
     moved = torch.empty((blocks,), dtype=torch.int32, device=device)
     _check("fl_kv8_pages_compact", lib().fl_kv8_pages_compact(
         pool, table.data_ptr(), refs.data_ptr(), moved.data_ptr(), pairs.data_ptr() or None, count.data_ptr(),
-        _status_block("fl_kv8_pages_compact", status, device), _stream()))
+        _status_block("fl_kv8_pages_compact", status, device, stream), stream))
     return table, refs, pairs, count, moved
 
 
@@ -1059,7 +1070,7 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
     if len(shape) != 4:
         _raise(where, "the caches are [blocks, kv_heads, block, head_dim]")
     nb, heads, block, dim = shape
-    device = _here(k_caches[0], where)
+    device, stream = _here(k_caches[0], where)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
     flat, scales = [], shape[:2]
     for k, v, a, b in zip(k_caches, v_caches, k_scales, v_scales):
@@ -1071,4 +1082,4 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
         flat += (k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), nb, block, heads, dim, 0)
     n = pairs.numel() // 2
     _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, "pairs"),
-                                          _row(count, i32, 1, "count"), n, _status_block(where, status, device), _stream()))
+                                          _row(count, i32, 1, "count"), n, _status_block(where, status, device, stream), stream))
