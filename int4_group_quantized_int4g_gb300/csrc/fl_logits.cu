@@ -103,14 +103,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A maximum, the sum of exp(x - maximum), the first index that has the maximum.
+// A maximum, the first index that has it, and the sum of exp(x - maximum) of all others:
+// where one token has nearly all of the probability, its logarithm is this sum, and would
+// be lost in 1 + sum.
 struct Best {
   float top, sum;
   int index;
+  __device__ __forceinline__ float all() const { return top > -INFINITY ? sum + 1.f : sum; }   // (the maximum's own with it)
   __device__ __forceinline__ void join(const Best& o) {
+    const bool other = o.top > top || (o.top == top && static_cast<unsigned>(o.index) < static_cast<unsigned>(index));
     const float t = fmaxf(top, o.top), base = t == -INFINITY ? 0.f : t;
-    sum = sum * exp_of(top - base) + o.sum * exp_of(o.top - base);
-    if (o.top > top || (o.top == top && static_cast<unsigned>(o.index) < static_cast<unsigned>(index))) index = o.index;
+    sum = other ? o.sum + all() * exp_of(top - base) : sum + o.all() * exp_of(o.top - base);
+    if (other) index = o.index;
     top = t;
   }
   __device__ __forceinline__ void join_warp() {
@@ -118,10 +122,11 @@ struct Best {
 #pragma unroll
     for (int d = 16; d; d >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
     const float base = t == -INFINITY ? 0.f : t;
-    sum *= exp_of(top - base);
+    const unsigned first = __reduce_min_sync(0xffffffffu, top == t ? static_cast<unsigned>(index) : 0xffffffffu);
+    if (top != t || static_cast<unsigned>(index) != first) sum = all() * exp_of(top - base);
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);   // (the same sum in every lane)
-    index = static_cast<int>(__reduce_min_sync(0xffffffffu, top == t ? static_cast<unsigned>(index) : 0xffffffffu));
+    index = static_cast<int>(first);
     top = t;
   }
 };
@@ -134,11 +139,11 @@ __device__ __forceinline__ int row_head(const void* row, int V) {
 
 // The row's results from `all` of it.
 __device__ __forceinline__ void write_row(const LogitsParams& p, uint32_t b, const Best& all) {
-  const float log_sum = logf(all.sum);
   const bool none = all.top == -INFINITY;
+  const float l = none ? (all.sum == 0.f ? INFINITY : NAN) : all.top == INFINITY ? NAN : log1pf(all.sum);
   p.token[b] = all.index;
-  if (p.lse) p.lse[b] = all.sum == 0.f ? -INFINITY : (none ? 0.f : all.top) + log_sum;
-  if (p.logprob) p.logprob[b] = all.sum == 0.f ? -INFINITY : -log_sum;
+  if (p.lse) p.lse[b] = none ? -l : all.top + l;
+  if (p.logprob) p.logprob[b] = -l;
 }
 // Joins the row's runs, with T threads, and writes the row's results.
 template <int T>
@@ -402,7 +407,7 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
     float f = __fmul_rn(value(v - base), inv);
     if (mask && !(__ldg(mask + (v >> 5)) >> (v & 31) & 1)) f = -INFINITY;
     if (out) out[v] = f;
-    best.join(Best{f == f ? f : -INFINITY, f == f ? (f == -INFINITY ? 0.f : 1.f) : f, f > -INFINITY ? v : -1});
+    best.join(Best{f == f ? f : -INFINITY, f == f ? 0.f : f, f > -INFINITY ? v : -1});
   };
   // N vectors, T apart.  What a call has not is decided once, not with every vector
   auto vectors = [&](int j, auto has_out, auto has_mask, auto count) {
@@ -457,12 +462,17 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
     for (int e = 3; e + 1 < N * W; e += 2) top = max3(top, f[e], f[e + 1]);
     top = fmaxf(top, f[N * W - 1]);
     if (top > best.top) {
-      best.sum *= exp_of(best.top - top);
+      best.sum = best.all() * exp_of(best.top - top);
       best.top = top;
       zero = -top;   // (not -inf: it is above another)
+      int at = 0;
 #pragma unroll
       for (int e = N * W - 1; e >= 0; --e)
-        if (f[e] == top) best.index = base + kLead + (j + e / W * T) * W + e % W;
+        if (f[e] == top) at = e;
+#pragma unroll
+      for (int e = 0; e < N * W; ++e)
+        if (at == e) f[e] = -INFINITY;   // (not in the sum)
+      best.index = base + kLead + (j + at / W * T) * W + at % W;
     }
     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll

@@ -411,6 +411,27 @@ def test_logits_made_just_before_with_sorted_histories():
         stream.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B,V", [(9, 2), (12, 33), (40, 5000), (30, 20003), (5, 128003), (900, 24001)])
+def test_logits_logprob_of_nearly_certain_tokens(B, V, dtype):
+    """One token far above the others: its log-probability is -log(1 + rest), good relative to itself."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy((-14 - 8 * rng.random((B, V))).astype(np.float32)).to(DEV).to(dtype)
+    spots = np.concatenate([[0, V - 1, V // 2], rng.integers(0, V, B)])[:B]
+    at = torch.from_numpy(spots).to(DEV)
+    x[torch.arange(B, device=DEV), at] = 1.0
+    x[B - 1, V - 1 - spots[B - 1]] = 1.0            # (one row with two of them, mostly)
+    got = fl.fl_logits_process(x)
+    y = _np(x.float())
+    rest = np.exp(y - 1).sum(1) - 1
+    rest = np.where(rest > 0.5, rest, np.exp(np.where(y < 1, y, -np.inf) - 1).sum(1))
+    # a term exp(d), |d| <= 24: three roundings of d, 2^-24 each, and exp's own 2^-22 make 2^-17.5; additions and
+    # log1p fit into the rest of 2^-17
+    assert np.all(np.abs(_np(got["logprob"]) + np.log1p(rest)) <= 2.0 ** -17 * np.log1p(rest))
+    assert np.all(np.abs(_np(got["lse"]) - 1 - np.log1p(rest)) <= 2.0 ** -23 + 2.0 ** -17 * np.log1p(rest))
+    assert np.array_equal(got["token"].cpu().numpy(), y.argmax(1))
+
+
 def test_captured_calls_without_a_workspace():
     """Scratch is the graph's own and not cleared: the second replay finds what the first has left."""
     x, kw = _logits_case(700, 32000, 3, torch.float32, history=2400)
