@@ -9,19 +9,19 @@
 // puts it on a list.  Every CTA of a row reads all of its history, out of L2, and
 // keeps what falls into its run; where that is much, a kernel before puts the history in
 // the order of the runs, while the logits are already on their way (512 rows of 128003
-// with 2000 entries 106 us, not 112, with 7000 104 and 152, with 16000 117 and 248).  Then
+// with 2000 entries 107 us, not 117, with 7000 104 and 157, with 16000 120 and 255).  Then
 // the listed tokens, and those that a bias names, are changed in shared memory, a thread
 // a token: one in a hundred has a penalty, but two of three warps meet one, so doing it
 // on the way through the run cost 80 instructions a logit (512 rows of 128003: 261 us).
 // Last the run passes through registers once: temperature, mask, the store, and a
 // running maximum and sum of exp (x - max) a thread.  The runs' results are joined in
 // their order, by the row's last CTA, or, with many CTAs, by a kernel of its own: a CTA
-// that takes a ticket waits until its stores are seen (512 rows of 128003 112 us, not 122;
+// that takes a ticket waits until its stores are seen (512 rows of 128003 117 us, not 125;
 // of few CTAs the second launch would cost the host more).  Every step of the rules is
 // one fp32 rounding, so that equal logits stay equal and ties are the formula's.  Bound
 // by HBM, the logits in and fp32 out, where there is little to look up (512 rows of 128003
-// without rules 81 us, 6.5 TB/s), else by instructions: with histories of 1000 to 2000
-// entries and 20 biases a row 106 us.
+// without rules 82 us, 6.4 TB/s), else by instructions: with histories of 1000 to 2000
+// entries and 20 biases a row 107 us.
 #include <type_traits>
 
 #include "fl_common.cuh"
