@@ -5,6 +5,11 @@ kernels.  PyTorch supplies device memory and the current stream.  The library
 is loaded lazily and a missing library is an error: there is no fallback.
 
 Function names match the C entry points.
+
+A call without a workspace of the caller's takes one that the binding keeps for the
+current stream and the calling thread.  A captured call does so too, where there is
+one: graphs of such calls are replayed on the stream that they were captured on, one
+at a time, or given workspaces of their own.
 """
 from __future__ import annotations
 
@@ -12,6 +17,7 @@ import ctypes
 import functools
 import os
 import struct
+from threading import get_ident as _thread
 
 from . import _build
 
@@ -209,13 +215,15 @@ _OUTGROWN = []   # workspaces that a larger one has replaced: a captured graph m
 
 
 def _workspace(nbytes, device):
-    """A zero-filled workspace per (device, stream), grown on demand.  One that
-    is made while the stream is captured is zero-filled (its status and counters:
-    scratch need not be) by the graph's replay alone, so it serves that one call."""
+    """A zero-filled workspace per (device, stream, thread), grown on demand: a call
+    of several launches hands over through it, and two threads' launches on one
+    stream may come in any order.  One that is made while the stream is captured is
+    zero-filled (its status and counters: scratch need not be) by the graph's replay
+    alone, so it serves that one call."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     key = (device.index, raw(device.index) if raw is not None and device.index is not None
-           else torch.cuda.current_stream(device).cuda_stream)
+           else torch.cuda.current_stream(device).cuda_stream, _thread())
     buf = _WS.get(key)
     if buf is None or buf.numel() < nbytes:
         if torch.cuda.is_current_stream_capturing():
@@ -751,10 +759,10 @@ def _here(t, name):
 
 
 def _space(ws, nbytes, device, stream):
-    """The caller's workspace or the stream's (to be held until the call), its address and bytes."""
+    """The caller's workspace or this thread's of the stream (to be held until the call), its address and bytes."""
     if ws is not None:
         return ws, _p(ws), ws.numel()
-    ws = _WS.get((device.index, stream))
+    ws = _WS.get((device.index, stream, _thread()))
     if ws is None or ws.numel() < nbytes:
         ws = _workspace(nbytes, device)
     return ws, ws.data_ptr(), ws.numel()
