@@ -75,24 +75,30 @@ class Generator:
         fl.fl_kv8_pages_copy([x.cache[0] for x in one], [x.cache[1] for x in one], [x.scales[0] for x in one],
                              [x.scales[1] for x in one], pairs, count, status=ws)
 
-    def layers_forward(self, tokens, positions, ws, keep=None, **seqs):
+    def layers_forward(self, tokens, positions, kv_lens, ws, keep=None, **seqs):
         """The stream after all layers, normed."""
         x = self.embedding.index_select(0, tokens)
         residual = torch.zeros_like(x)
         for i, one in enumerate(self.layers):
-            x, residual = one.forward(x, residual, positions, self.kv_lens, ws, keep=keep[i] if keep else None, **seqs)
+            x, residual = one.forward(x, residual, positions, kv_lens, ws, keep=keep[i] if keep else None, **seqs)
         return fl.fl_rmsnorm(x, self.norm_out, residual=residual)["y"]
 
-    def choose(self, hidden, ws, keep=None):
-        """The next token of every slot, and its place in the history."""
+    def choose(self, hidden, ws, moved=None, keep=None):
+        """The next token of every slot, and its place in the history; slots that
+        have not moved on (moved, truth values; None: all have) keep the one they have."""
         logits = fl.fl_int8_linear(hidden, self.head, self.head_scale, out_dtype=torch.float32, ws=ws)
         got = fl.fl_logits_process(logits, history=self.history, history_lens=self.kv_lens, prompt_lens=self.prompt_lens, **self.rules,
                                    ws=ws)
         if keep is not None:
             keep.update(hidden=hidden, logits=logits, history=self.history.clone(), history_lens=self.kv_lens.clone(), chosen=got)
-        self.token.copy_(got["token"])
         at = self.kv_lens.long().clamp(max=self.history.shape[1] - 1)[:, None]
-        self.history.scatter_(1, at, self.token[:, None])
+        token = got["token"]
+        if moved is None:
+            self.token.copy_(token)
+        else:
+            self.token.copy_(torch.where(moved, token, self.token))
+            token = torch.where(moved, token, self.history.gather(1, at)[:, 0])
+        self.history.scatter_(1, at, token[:, None])
         return got
 
     def start(self, prompts, ws):
@@ -109,7 +115,7 @@ class Generator:
         if not bool(granted.all()):
             raise RuntimeError("the pool has too few pages for the prompts")
         positions = torch.cat([torch.arange(len(p), dtype=torch.int32) for p in prompts]).to(dev)
-        hidden = self.layers_forward(flat, positions, ws, cu_q=cu_q, max_q=max(len(p) for p in prompts))
+        hidden = self.layers_forward(flat, positions, self.kv_lens, ws, cu_q=cu_q, max_q=max(len(p) for p in prompts))
         if self.ways > 1:
             children = self.seqs.view(-1, self.ways)[:, 1:].contiguous()
             fl.fl_kv8_pages_fork(*self.pool, firsts[:, None].expand_as(children).contiguous(), children, BLOCK, status=ws)
@@ -120,15 +126,21 @@ class Generator:
         return self.choose(hidden.index_select(0, last), ws)
 
     def step(self, new, ws, keep=None):
-        """One token of every slot; new int32 [slots]: 1, or 0 for ended ones."""
+        """One token of every slot; new int32 [slots]: 1, or 0 for those that stay as
+        they are.  A slot that gets no room (the pool is full, or its table) stays so
+        too, and goes on with the token that it has when a later step finds room."""
         granted, pairs, count = fl.fl_kv8_pages_alloc(*self.pool, self.seqs, new, BLOCK, ws=ws)
         self.copy_pages(pairs, count, ws)
-        positions = (self.kv_lens - 1).clamp(min=0)
+        # the others' rows are there, but of no token: nothing is written for them, and their
+        # last tokens and the pages that they share stay
+        moved = (granted > 0) & (new > 0)
+        lens = self.kv_lens * moved
+        positions = (lens - 1).clamp(min=0)
         steps = [{} for _ in self.layers] if keep is not None else None
-        hidden = self.layers_forward(self.token.clamp(min=0), positions, ws, keep=steps, max_q=1)
+        hidden = self.layers_forward(self.token.clamp(min=0), positions, lens, ws, keep=steps, max_q=1)
         if keep is not None:
             keep.update(granted=granted, pairs=pairs, count=count, layers=steps)
-        return self.choose(hidden, ws, keep)
+        return self.choose(hidden, ws, moved, keep)
 
     def end(self, slots, ws):
         """The sequences in these slots end; the pages in use move together."""

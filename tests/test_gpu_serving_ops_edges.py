@@ -1,0 +1,73 @@
+"""The serving operators and the example around them at the edges of their use, on
+the GPU: pools that are full, sums past 2^24."""
+import numpy as np
+import pytest
+import torch
+
+import int4_group_quantized_int4g_gb300 as fl
+from examples.generate import BLOCK, Generator
+from oracle import serving_oracle as O
+from test_gpu_generate import _books, _check_step, _values
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from int4_group_quantized_int4g_gb300 import _build
+    _build.build()
+    fl.lib()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_continuations_without_room_wait_for_it(captured):
+    """A prompt of 70 tokens, three continuations and a pool of three pages: one copies
+    the last page, the others get no room until it ends."""
+    gen = Generator(prompts=1, ways=3, room=192, layers=2, vocab=500, pages=3, hidden=128, heads=2, kv_heads=1, dim=64, experts=2,
+                    inter=128, top_k=1)
+    pool = O.Pool(3, 3, gen.table.shape[1], BLOCK)
+    ws = gen.workspace(70)
+    gen.start([list(range(70))], ws)
+    pool.alloc([0], [70])
+    pool.fork([0, 0], [1, 2])
+    _books(gen, pool)
+    new = torch.ones(3, dtype=torch.int32, device=DEV)
+    keep = {}
+    if captured:
+        gen.step(torch.zeros_like(new), ws)          # (first calls of every kernel; nobody moves)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            gen.step(new, ws, keep)
+
+    def step(values):
+        new.copy_(torch.tensor(values, dtype=torch.int32))
+        if captured:
+            graph.replay()
+        else:
+            gen.step(new, ws, keep)
+        granted, pairs = pool.alloc([0, 1, 2], values)
+        assert keep["granted"].tolist() == granted and int(keep["count"]) == len(pairs)
+        _books(gen, pool)
+        return granted
+    held = [[_values(gen, i, s) for i in range(2)] for s in range(3)]
+    token, history = gen.token.clone(), gen.history.clone()
+    for _ in range(2):
+        assert step([1, 1, 1]) == [1, 0, 0]
+        _check_step(gen, keep, (0,))
+        for s in (1, 2):
+            assert all(np.array_equal(_values(gen, i, s), held[s][i]) for i in range(2))
+        assert torch.equal(gen.token[1:], token[1:]) and torch.equal(gen.history[1:], history[1:])
+    # (tokens of the page that is written next may be rounded again)
+    assert all(np.array_equal(_values(gen, i, 0)[:, :, :64], held[0][i][:, :, :64]) for i in range(2))
+    gen.end(torch.tensor([0], dtype=torch.int32, device=DEV), ws)
+    pool.free([0])
+    pool.compact()
+    for _ in range(2):
+        assert step([0, 1, 1])[1:] == [1, 1]
+        _check_step(gen, keep, (1, 2))
+    assert gen.kv_lens.tolist() == [0, 72, 72]
+    assert torch.equal(gen.history[1:, 70], token[1:])
+    assert all(np.array_equal(_values(gen, i, s)[:, :, :64], held[s][i][:, :, :64]) for i in range(2) for s in (1, 2))
+    assert fl.fl_int4g_status(ws) == 0

@@ -6,6 +6,8 @@ import types
 import torch
 
 import int4_group_quantized_int4g_gb300 as fl
+from examples import generate
+from oracle import serving_oracle as O
 
 
 # ------------------------------------------------------------ workspaces
@@ -54,3 +56,98 @@ def test_threads_on_one_stream_have_workspaces_of_their_own(monkeypatch):
         assert mine[0] is mine[1] and mine[2] is mine[3] and mine[2].numel() >= 9000
     mine = fl._workspace(9000, dev)
     assert fl._space(None, 9000, dev, 77)[0] is mine and fl._workspace(100, dev) is mine
+
+
+# ------------------------------------------------------------- generation
+
+def _generator(monkeypatch, blocks, lens, ways):
+    """examples/generate.py's books and steps on the CPU, the library's calls replaced by
+    the oracle's pool and a layer that notes which token each place of the cache holds."""
+    pool = O.Pool(blocks, len(lens) * ways, 2, generate.BLOCK)
+    cache = {}
+
+    def to_tensors(gen):
+        gen.refs.copy_(torch.tensor(pool.refs)), gen.kv_lens.copy_(torch.tensor(pool.lens)), gen.table.copy_(torch.tensor(pool.table))
+
+    def alloc(refs, table, kv_lens, seqs, new, block, ws=None):
+        granted, pairs = pool.alloc(seqs.tolist(), new.tolist())
+        to_tensors(gen)
+        flat = pairs + [(-1, -1)] * (len(granted) - len(pairs))
+        return (torch.tensor(granted, dtype=torch.int32), torch.tensor(flat, dtype=torch.int32),
+                torch.tensor([len(pairs)], dtype=torch.int32))
+
+    def copy(k, v, a, b, pairs, count, status=None):
+        for f, t in pairs[:int(count)].tolist():
+            for off in range(generate.BLOCK):
+                cache.pop((t, off), None)
+                if (f, off) in cache:
+                    cache[t, off] = cache[f, off]
+
+    class Layer:
+        cache, scales = [None, None], [None, None]
+
+        def forward(self, x, residual, positions, kv_lens, ws, keep=None, max_q=None, **seqs):
+            for s, n in enumerate(kv_lens.tolist()):     # a row a slot, the last of its tokens; none of an empty one
+                if n:
+                    place = (pool.table[s][(n - 1) // generate.BLOCK], (n - 1) % generate.BLOCK)
+                    assert pool.refs[place[0]] == 1, "written into a shared page"
+                    cache[place] = (s, n - 1, int(gen.token[s]))
+            return x, residual
+    gen = object.__new__(generate.Generator)
+    slots = len(lens) * ways
+    gen.prompts, gen.ways, gen.vocab, gen.slots, gen.layers, gen.device = len(lens), ways, 50, slots, [Layer()], torch.device("cpu")
+    gen.refs, gen.table = torch.zeros(blocks, dtype=torch.int32), torch.full((slots, 2), -1, dtype=torch.int32)
+    gen.kv_lens, gen.token = torch.zeros(slots, dtype=torch.int32), torch.arange(30, 30 + slots, dtype=torch.int32)
+    gen.embedding, gen.norm_out, gen.head, gen.head_scale, gen.rules = torch.zeros((50, 8)), None, None, None, {}
+    gen.history = torch.zeros((slots, 2 * generate.BLOCK + 4), dtype=torch.int32)
+    gen.prompt_lens, gen.seqs = torch.zeros(slots, dtype=torch.int32), torch.arange(slots, dtype=torch.int32)
+    calls = [0]
+
+    def process(logits, **kw):
+        calls[0] += 1
+        return {"token": torch.arange(slots, dtype=torch.int32) + 10 * calls[0] % 40}
+    stub = types.SimpleNamespace(fl_kv8_pages_alloc=alloc, fl_kv8_pages_copy=copy, fl_logits_process=process,
+                                 fl_rmsnorm=lambda x, w, residual=None: {"y": x}, fl_int8_linear=lambda x, *a, **kw: x)
+    monkeypatch.setattr(generate, "fl", stub)
+    firsts = list(range(0, slots, ways))
+    pool.alloc(firsts, list(lens))
+    for s, n in zip(firsts, lens):
+        for j in range(n):
+            cache[pool.table[s][j // generate.BLOCK], j % generate.BLOCK] = ("prompt", j, 0)
+        children = [s + i for i in range(1, ways)]
+        pool.fork([s] * len(children), children)
+        for c in [s] + children:
+            gen.history[c, n] = gen.token[c]
+    to_tensors(gen)
+    return gen, pool, cache, lambda: to_tensors(gen)
+
+
+def test_a_slot_without_room_stays_as_it_is(monkeypatch):
+    """Three continuations of 20 tokens and one page left: the first copies, the others
+    get no room, write nothing and keep their tokens until the first one ends."""
+    gen, pool, cache, sync = _generator(monkeypatch, 2, (20,), 3)
+    new = torch.ones(3, dtype=torch.int32)
+    before, tokens, history = dict(cache), gen.token.clone(), gen.history.clone()
+    keep = {}
+    gen.step(new, None, keep)
+    assert keep["granted"].tolist() == [1, 0, 0] and gen.kv_lens.tolist() == [21, 20, 20]
+    assert {k: v for k, v in cache.items() if k[0] == 0} == before                    # the prompt's page
+    assert cache[1, 20] == (0, 20, 30)
+    assert torch.equal(gen.token[1:], tokens[1:]) and torch.equal(gen.history[1:], history[1:])
+    assert int(gen.history[0, 21]) == int(gen.token[0]) == 10
+    pool.free([0])
+    sync()
+    gen.step(torch.tensor([0, 1, 1], dtype=torch.int32), None, keep)
+    assert keep["granted"].tolist() == [1, 1, 1] and gen.kv_lens.tolist() == [0, 21, 21]
+    assert cache[1, 20] == (1, 20, 31) and cache[0, 20] == (2, 20, 32)
+    assert gen.history[1:, 20].tolist() == [31, 32] and torch.equal(gen.history[1:, 21], gen.token[1:])
+
+
+def test_a_live_slot_that_takes_no_token_stays_as_it_is(monkeypatch):
+    gen, pool, cache, _ = _generator(monkeypatch, 6, (20, 64), 2)
+    before, tokens, history = dict(cache), gen.token.clone(), gen.history.clone()
+    gen.step(torch.tensor([0, 1, 0, 0], dtype=torch.int32), None)
+    assert {k: v for k, v in cache.items() if k in before} == before and len(cache) == len(before) + 21
+    still = [0, 2, 3]
+    assert torch.equal(gen.token[still], tokens[still]) and torch.equal(gen.history[still], history[still])
+    assert gen.kv_lens.tolist() == [20, 21, 64, 64]
