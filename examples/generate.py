@@ -48,7 +48,8 @@ class Generator:
         self.norm_out = torch.ones(hidden, dtype=torch.bfloat16, device=self.device)
         self.head, self.head_scale = fl.fl_int8_quantize((torch.randn((vocab, hidden), generator=g, device=self.device)
                                                           * hidden ** -0.5).to(torch.bfloat16))
-        self.history = torch.zeros((self.slots, room), dtype=torch.int32, device=self.device)
+        # (all that a slot's table holds, and the token chosen behind them; rows of whole 16 bytes)
+        self.history = torch.zeros((self.slots, self.table.shape[1] * BLOCK + 4), dtype=torch.int32, device=self.device)
         self.prompt_lens = torch.zeros(self.slots, dtype=torch.int32, device=self.device)
         # continuations differ in what a repeated token costs them, and in some tokens that each prefers
         way = torch.arange(self.slots, device=self.device) % ways
@@ -91,7 +92,7 @@ class Generator:
                                    ws=ws)
         if keep is not None:
             keep.update(hidden=hidden, logits=logits, history=self.history.clone(), history_lens=self.kv_lens.clone(), chosen=got)
-        at = self.kv_lens.long().clamp(max=self.history.shape[1] - 1)[:, None]
+        at = self.kv_lens.long()[:, None]
         token = got["token"]
         if moved is None:
             self.token.copy_(token)

@@ -151,3 +151,30 @@ def test_a_live_slot_that_takes_no_token_stays_as_it_is(monkeypatch):
     still = [0, 2, 3]
     assert torch.equal(gen.token[still], tokens[still]) and torch.equal(gen.history[still], history[still])
     assert gen.kv_lens.tolist() == [20, 21, 64, 64]
+
+
+def test_the_last_token_of_a_full_table_has_a_place(monkeypatch):
+    """A slot may fill its table's last page; the token chosen then stands behind its
+    tokens, not over the last one."""
+    made = {}
+
+    class Layer:
+        hidden, device = 8, torch.device("cpu")
+
+        def __init__(self, batch, room, seed, **kw):
+            per = -(-room // generate.BLOCK)
+            self.cache = [torch.zeros((batch * per, 1, 1, 1), dtype=torch.uint8) for _ in range(2)]
+            self.scales = [torch.zeros((batch * per, 1)) for _ in range(2)]
+    monkeypatch.setattr(generate, "DecoderLayer", Layer)
+    monkeypatch.setattr(generate, "fl", types.SimpleNamespace(
+        fl_int8_quantize=lambda x: (x, x), fl_int8_linear=lambda x, *a, **kw: x,
+        fl_logits_process=lambda x, **kw: made.update(kw) or {"token": torch.full((2,), 7, dtype=torch.int32)}))
+    for room in (100, 128):
+        gen = generate.Generator(prompts=1, ways=2, room=room, layers=1, vocab=20)
+        full = gen.table.shape[1] * generate.BLOCK
+        gen.history.fill_(3)
+        gen.kv_lens.copy_(torch.tensor([full, room]))
+        gen.choose(torch.zeros((2, 8)), None)
+        assert gen.history[0, :full].tolist() == [3] * full and int(gen.history[0, full]) == 7
+        assert gen.history[1, :room].tolist() == [3] * room and int(gen.history[1, room]) == 7
+        assert made["history"].stride(0) % 4 == 0          # (rows of whole 16 bytes)
