@@ -104,6 +104,10 @@ class Generator:
 
     def start(self, prompts, ws):
         """prompts: a list of token lists.  Reads them and lets each have `ways` continuations."""
+        if len(prompts) != self.prompts or not all(prompts):
+            raise ValueError(f"expected {self.prompts} prompts of at least a token each")
+        if min(map(min, prompts)) < 0 or max(map(max, prompts)) >= self.vocab:
+            raise ValueError(f"a prompt's tokens are those of a vocabulary of {self.vocab}")
         dev = self.device
         lens = torch.zeros(self.slots, dtype=torch.int32)
         lens[::self.ways] = torch.tensor([len(p) for p in prompts], dtype=torch.int32)

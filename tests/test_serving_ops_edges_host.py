@@ -3,6 +3,7 @@ tensors of other devices, outputs over inputs, pools that are full.  No GPU."""
 import threading
 import types
 
+import pytest
 import torch
 
 import int4_group_quantized_int4g_gb300 as fl
@@ -178,3 +179,14 @@ def test_the_last_token_of_a_full_table_has_a_place(monkeypatch):
         assert gen.history[0, :full].tolist() == [3] * full and int(gen.history[0, full]) == 7
         assert gen.history[1, :room].tolist() == [3] * room and int(gen.history[1, room]) == 7
         assert made["history"].stride(0) % 4 == 0          # (rows of whole 16 bytes)
+
+
+@pytest.mark.parametrize("prompts", [[[1, 2], []], [[], [1]], [[1, 2]], [[1], [2], [3]], [[1, 50], [2]], [[1], [-1]]])
+def test_prompts_that_cannot_be_read_are_refused(monkeypatch, prompts):
+    """None, too few or too many, or tokens outside the vocabulary, before any call: an
+    empty one has no last token to go on from, and others are read as indices."""
+    gen, pool, cache, _ = _generator(monkeypatch, 6, (20, 64), 2)
+    books = [t.clone() for t in gen.pool]
+    with pytest.raises(ValueError):
+        gen.start(prompts, None)
+    assert all(torch.equal(a, b) for a, b in zip(gen.pool, books))
