@@ -565,8 +565,9 @@ int fl_kv8_attention(const void* q, int64_t q_stride, int Hq, const fl_kv8_cache
  * (of the quotient itself, not of a rounded one); a row of zeros: scale 0,
  * codes 0; a row with an infinity or NaN: scale NaN, codes 0.
  *   codes  int8 [M, K] device        scale  fp32 [M] device
- * M >= 1, K >= 1.  Rows of x that start on 16 bytes are read 16 bytes at a
- * time, others element by element; pointers need their elements' alignment. */
+ * M >= 1, K >= 1.  codes and scale may lie neither over x nor over each other
+ * (FL_ERR_ARG).  Rows of x that start on 16 bytes are read 16 bytes at a time,
+ * others element by element; pointers need their elements' alignment. */
 int fl_int8_quantize(const void* x, int64_t x_stride, int M, int K, int8_t* codes, float* scale, fl_stream_t stream);
 
 #define FL_OUT_BF16 0
@@ -586,7 +587,8 @@ int fl_int8_linear_workspace(int M, int N, int K, size_t* out);
  *   w        int8 [N, K] device, row-major, any of the 256 codes, 16-byte
  *            aligned         w_scale  fp32 [N] device
  *   y        [M, N], row stride y_stride in elements; y_type FL_OUT_BF16 or
- *            FL_OUT_FP32.  y may not lie over an input.
+ *            FL_OUT_FP32.  y may not lie over an input: FL_ERR_ARG, where rows
+ *            meet or, with strides of x and y that differ in bytes, ranges
  * K % 16 == 0, M, N >= 1.  Products and sums are those of the codes: f16
  * operands hold them exactly, sums are fp32 (exact while they stay below
  * 2^24), partial sums of a split K are added in a fixed order, so results do

@@ -816,8 +816,9 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
     """y [M, N] = x . w^T with int8 weights w [N, K], a scale w_scale fp32 [N] for
     each output channel and one for each token.  x: bf16 [M, K], rounded to 8 bits
     within the call as by fl_int8_quantize, or with x_scale (fp32 [M]) its codes,
-    int8.  y: bf16 or fp32, out_dtype when y is not given (bf16 by default).  Rows
-    of x and y may be those of wider matrices.  K is a multiple of 16.
+    int8.  y: bf16 or fp32, out_dtype when y is not given (bf16 by default); it may not
+    lie over an input.  Rows of x and y may be those of wider matrices.  K is a
+    multiple of 16.
     ws: a workspace of the caller's, zero-filled before its first use (for calls
     that are captured in a graph, as for fl_kv8_attention)."""
     torch = _torch()

@@ -271,6 +271,16 @@ namespace flh {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether na rows of wa bytes, sa apart, meet nb of wb bytes, sb apart.  Rows of one
+// stride may alternate in one buffer; ranges of different strides meet as a whole.
+inline bool rows_meet(const void* pa, uint64_t sa, uint64_t wa, uint64_t na, const void* pb, uint64_t sb, uint64_t wb, uint64_t nb) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+  if (b >= a + (na - 1) * sa + wa || a >= b + (nb - 1) * sb + wb) return false;
+  if (sa != sb || na == 1 || nb == 1) return true;
+  const uint64_t d = b >= a ? (b - a) % sa : (sa - (a - b) % sa) % sa;   // where in its stride a row of b begins
+  return d < wa || d + wb > sa;
+}
+
 int sm_count();  // cached per device (fl_abi.cu)
 
 // Launches a kernel whose CTAs may start while the kernel before it in the

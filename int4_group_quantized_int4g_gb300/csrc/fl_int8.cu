@@ -215,6 +215,12 @@ extern "C" int fl_int8_quantize(const void* x, int64_t x_stride, int M, int K, i
                                 fl_stream_t stream) {
   if (!x || !codes || !scale || M < 1 || K < 1 || x_stride < K || K > 0x7fffff00 || !aligned(x, 2) || !aligned(scale, 4))
     return FL_ERR_ARG;
+  // (a row's codes are written while others are still read)
+  const uint64_t rows = M, width = K;
+  if (flh::rows_meet(x, 2 * x_stride, 2 * width, rows, codes, 0, rows * width, 1) ||
+      flh::rows_meet(x, 2 * x_stride, 2 * width, rows, scale, 0, 4 * rows, 1) ||
+      flh::rows_meet(codes, 0, rows * width, 1, scale, 0, 4 * rows, 1))
+    return FL_ERR_ARG;
   CodesParams p = {x, x_stride, codes, scale, M, K, aligned(x, 16) && x_stride % 8 == 0, 0};
   return launch_codes<kInBf16, kOutCodes>(p, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -235,6 +241,13 @@ extern "C" int fl_int8_linear(const void* x, int64_t x_stride, const float* x_sc
     return FL_ERR_ARG;
   const Layout l = layout(M, N, K);
   if (ws_bytes < l.bytes) return FL_ERR_WORKSPACE;
+  const uint64_t out = y_type == FL_OUT_FP32 ? 4 : 2, in = x_scale ? 1 : 2;
+  auto under = [&](const void* p, uint64_t stride, uint64_t width, uint64_t rows) {
+    return flh::rows_meet(p, stride, width, rows, y, y_stride * out, N * out, M);
+  };
+  if (under(x, x_stride * in, K * in, M) || under(w, 0, static_cast<uint64_t>(N) * K, 1) || under(w_scale, 0, 4ull * N, 1) ||
+      (x_scale && under(x_scale, 0, 4ull * M, 1)))
+    return FL_ERR_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* base = static_cast<uint8_t*>(ws);
   Call c;

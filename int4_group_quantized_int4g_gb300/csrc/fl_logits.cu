@@ -642,14 +642,8 @@ int launch(const LogitsParams& p, int B, size_t smem, cudaStream_t s) {
 // Whether rows of `out` would lie over rows of the logits, the logits themselves
 // (the same place and stride, fp32) apart.
 bool over(const void* x, int64_t xs, int size, const float* out, int64_t os, int B, int V) {
-  const auto a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(out);
-  const uint64_t sa = static_cast<uint64_t>(xs) * size, sb = static_cast<uint64_t>(os) * 4;
-  const uint64_t wa = static_cast<uint64_t>(V) * size, wb = static_cast<uint64_t>(V) * 4;
-  if (b >= a + (B - 1) * sa + wa || a >= b + (B - 1) * sb + wb) return false;
-  if (sa != sb) return true;
-  if (a == b && size == 4) return false;
-  const uint64_t d = b >= a ? (b - a) % sa : (sa - (a - b) % sa) % sa;   // where in its stride a row of out begins
-  return d < wa || d + wb > sa;
+  if (x == out && size == 4 && xs == os) return false;
+  return flh::rows_meet(x, xs * size, static_cast<uint64_t>(V) * size, B, out, os * 4, static_cast<uint64_t>(V) * 4, B);
 }
 
 // Workspace: the runs' results, where each run's entries of a sorted history begin, these.

@@ -1,5 +1,6 @@
 """Host side of the serving operators at the edges of their use: several threads,
 tensors of other devices, outputs over inputs, pools that are full.  No GPU."""
+import ctypes
 import threading
 import types
 
@@ -8,6 +9,7 @@ import torch
 
 import int4_group_quantized_int4g_gb300 as fl
 from examples import generate
+from int4_group_quantized_int4g_gb300 import _build
 from oracle import serving_oracle as O
 
 
@@ -190,3 +192,52 @@ def test_prompts_that_cannot_be_read_are_refused(monkeypatch, prompts):
     with pytest.raises(ValueError):
         gen.start(prompts, None)
     assert all(torch.equal(a, b) for a, b in zip(gen.pool, books))
+
+
+# ------------------------------------------------- outputs over inputs
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return fl.lib()
+
+
+def _runs(rc):
+    """Right as far as overlap goes: the call fails later, as there is no GPU."""
+    return rc == 4
+
+
+def test_linear_refuses_an_output_over_an_input(L):
+    at = 1 << 24
+
+    def call(x=1 << 30, xs=256, sx=None, M=4, K=256, w=1 << 32, sw=1 << 33, N=64, y=at, ys=64, t=0):
+        return L.fl_int8_linear(ctypes.c_void_p(x), xs, ctypes.c_void_p(sx) if sx else None, M, K, ctypes.c_void_p(w), ctypes.c_void_p(sw),
+                                N, ctypes.c_void_p(y), ys, t, ctypes.c_void_p(1 << 34), 1 << 40, None)
+    for t, size in ((0, 2), (1, 4)):
+        for M in (4, 1, 40):
+            end = M * 64 * size                               # bytes of y, rows without gaps
+            for d in (0, 16, -16, end - 16):                  # w, the scales, x: y's range meets theirs
+                assert call(w=at + d, M=M, t=t) == 1 and call(sw=at + d, M=M, t=t) == 1 and call(x=at + d, M=M, t=t) == 1
+                assert call(x=at + d, sx=1 << 35, M=M, t=t) == 1
+            assert call(sx=at + end - 4, M=M, t=t) == 1 and call(sx=at - 4 * M + 4, M=M, t=t) == 1
+            assert call(w=at - 64 * 256 + 16, M=M, t=t) == 1 and call(sw=at - 64 * 4 + 4, M=M, t=t) == 1
+    # columns of one wide matrix: x in the first 256 of 320, y behind them or over their end
+    for M in (1, 4, 40):
+        assert call(x=at, xs=320, y=at + 2 * 255, ys=320, M=M) == 1 and call(x=at, xs=320, y=at - 2, ys=320, M=M) == 1
+        if not torch.cuda.is_available():                     # (the addresses are no memory)
+            assert _runs(call(x=at, xs=320, y=at + 2 * 256, ys=320, M=M)) and _runs(call(x=at + 2 * 64, xs=320, ys=320, M=M))
+            assert _runs(call(x=at + 4 * 64 * M, M=M)) and _runs(call(w=at + 2 * 64 * M, M=M)) and _runs(call(w=at - 64 * 256, M=M))
+            assert _runs(call(sw=at - 64 * 4, M=M)) and _runs(call(sx=at + 2 * 64 * M, M=M))
+    assert call(x=at, xs=320, y=at + 4 * 200, ys=320, t=1) == 1   # strides of 640 and 1280 bytes that meet
+
+
+def test_quantize_refuses_outputs_that_meet(L):
+    at, far, M, K = 1 << 24, 1 << 30, 4, 64
+
+    def call(x=at, xs=64, c=far, s=1 << 31):
+        return L.fl_int8_quantize(ctypes.c_void_p(x), xs, M, K, ctypes.c_void_p(c), ctypes.c_void_p(s), None)
+    for d in (0, 64, 511, -255):
+        assert call(c=at + d) == 1
+    assert call(s=at) == 1 and call(s=at + 508) == 1 and call(s=at - 12) == 1 and call(s=far) == 1 and call(s=far + 252) == 1
+    if not torch.cuda.is_available():
+        assert _runs(call()) and _runs(call(c=at + 512)) and _runs(call(c=at - 256)) and _runs(call(s=far + 256)) and _runs(call(s=far - 16))
