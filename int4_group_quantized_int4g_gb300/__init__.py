@@ -749,18 +749,21 @@ def fl_kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
 # -------------------------------------------------- linear in 8-bit integers
 
 def _here(t, name):
-    """The tensor's device, which has to be the current one, and its current stream's handle."""
+    """The tensor's device, which has to be the current one, its index, and its current
+    stream's handle.  The call's other tensors are checked for that index."""
     device = t.device
     index = device.index
     if not t.is_cuda or index != _device():
         _raise(name, f"expected tensors of the current CUDA device, got one on {device}")
     raw = getattr(_TORCH._C, "_cuda_getCurrentRawStream", None)
-    return device, raw(index) if raw is not None else _TORCH.cuda.current_stream(device).cuda_stream
+    return device, index, raw(index) if raw is not None else _TORCH.cuda.current_stream(device).cuda_stream
 
 
 def _space(ws, nbytes, device, stream):
     """The caller's workspace or this thread's of the stream (to be held until the call), its address and bytes."""
     if ws is not None:
+        if ws.get_device() != device.index:
+            _raise("ws", f"expected a workspace on {device}, got one on {ws.device}")
         return ws, _p(ws), ws.numel()
     ws = _WS.get((device.index, stream, _thread()))
     if ws is None or ws.numel() < nbytes:
@@ -768,20 +771,20 @@ def _space(ws, nbytes, device, stream):
     return ws, ws.data_ptr(), ws.numel()
 
 
-def _matrix(t, dtype, name):
-    """(address, row stride) of [rows, columns] whose columns are packed; the
-    rows may be those of a wider matrix."""
+def _matrix(t, dtype, index, name):
+    """(address, row stride) of [rows, columns] on CUDA device `index` whose columns
+    are packed; the rows may be those of a wider matrix."""
     st, (n, w) = t.stride(), t.shape
-    if t.dtype is not dtype or not t.is_cuda or (st[1] != 1 and w > 1):
-        _raise(name, f"expected a {dtype} CUDA matrix with packed columns, got {t.dtype}, strides {st}, on {t.device}")
+    if t.dtype is not dtype or t.get_device() != index or (st[1] != 1 and w > 1):
+        _raise(name, f"expected a {dtype} matrix with packed columns on cuda:{index}, got {t.dtype}, strides {st}, on {t.device}")
     return t.data_ptr(), st[0] if n > 1 else w   # (the stride of a single row means nothing)
 
 
-def _row(t, dtype, n, name):
-    """Address of a contiguous CUDA tensor of n entries."""
-    if t.numel() != n or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _raise(name, f"expected a contiguous {dtype} CUDA tensor of {n} entries, got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, "
-                     f"on {t.device}")
+def _row(t, dtype, n, index, name):
+    """Address of a contiguous tensor of n entries (None: any number) on CUDA device `index`."""
+    if (n is not None and t.numel() != n) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        _raise(name, f"expected a contiguous {dtype} tensor{'' if n is None else f' of {n} entries'} on cuda:{index}, got {t.dtype}, "
+                     f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
     return t.data_ptr()
 
 
@@ -793,8 +796,8 @@ def fl_int8_quantize(x):
     if x.dim() != 2:
         _raise("fl_int8_quantize", "x is [M, K]")
     M, K = x.shape
-    device, stream = _here(x, "fl_int8_quantize")
-    xp, xs = _matrix(x, torch.bfloat16, "x")
+    device, index, stream = _here(x, "fl_int8_quantize")
+    xp, xs = _matrix(x, torch.bfloat16, index, "x")
     codes = torch.empty((M, K), dtype=torch.int8, device=device)
     scale = torch.empty((M,), dtype=torch.float32, device=device)
     _check("fl_int8_quantize", lib().fl_int8_quantize(xp, xs, M, K, codes.data_ptr(), scale.data_ptr(), stream))
@@ -826,14 +829,14 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         _raise("fl_int8_linear", "x is [M, K], w [N, K]")
     M, K = x.shape
     N = w.shape[0]
-    device, stream = _here(x, "fl_int8_linear")
+    device, index, stream = _here(x, "fl_int8_linear")
     sp = None
     if x_scale is None:
-        xp, xs = _matrix(x, torch.bfloat16, "x")
+        xp, xs = _matrix(x, torch.bfloat16, index, "x")
     else:
-        xp, xs = _matrix(x, torch.int8, "x")
-        sp = _row(x_scale, torch.float32, M, "x_scale")
-    wp, tp = _ptr(w, torch.int8, "w"), _row(w_scale, torch.float32, N, "w_scale")
+        xp, xs = _matrix(x, torch.int8, index, "x")
+        sp = _row(x_scale, torch.float32, M, index, "x_scale")
+    wp, tp = _row(w, torch.int8, None, index, "w"), _row(w_scale, torch.float32, N, index, "w_scale")
     if y is None:
         if out_dtype is None:
             out_dtype = torch.bfloat16
@@ -843,7 +846,7 @@ def fl_int8_linear(x, w, w_scale, x_scale=None, y=None, out_dtype=None, ws=None)
         if y.dim() != 2 or y.shape != (M, N) or out_dtype not in (None, y.dtype):
             _raise("fl_int8_linear", "y is [M, N] of out_dtype")
         out_dtype = y.dtype
-        yp, ys = _matrix(y, out_dtype, "y")
+        yp, ys = _matrix(y, out_dtype, index, "y")
     if out_dtype is torch.bfloat16:
         kind = FL_OUT_BF16
     elif out_dtype is torch.float32:
@@ -897,51 +900,51 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     if logits.dim() != 2:
         _raise(name, "logits are [B, V]")
     B, V = logits.shape
-    device, stream = _here(logits, name)
+    device, index, stream = _here(logits, name)
     i32, f32 = torch.int32, torch.float32
     bf16 = logits.dtype is torch.bfloat16
-    lp, ls = _matrix(logits, torch.bfloat16 if bf16 else f32, "logits")
+    lp, ls = _matrix(logits, torch.bfloat16 if bf16 else f32, index, "logits")
     hp = hs = most = nl = np = rp = fp = pp = bo = bi = bp = count = ap = stride = tp = 0
     if history is not None:
         if history_lens is None:
             _raise(name, "history and history_lens go together")
         if history.dim() != 2 or history.shape[0] != B:
             _raise(name, "history is [B, longest]")
-        hp, hs = _matrix(history, i32, "history")
+        hp, hs = _matrix(history, i32, index, "history")
         most = history.shape[1]
-        nl = _row(history_lens, i32, B, "history_lens")
+        nl = _row(history_lens, i32, B, index, "history_lens")
         hp = hp or nl                        # (an empty tensor has no address, and nothing is read)
         if prompt_lens is not None:
-            np = _row(prompt_lens, i32, B, "prompt_lens")
+            np = _row(prompt_lens, i32, B, index, "prompt_lens")
         if repetition is not None:
-            rp = _row(repetition, f32, B, "repetition")
+            rp = _row(repetition, f32, B, index, "repetition")
         if frequency is not None:
-            fp = _row(frequency, f32, B, "frequency")
+            fp = _row(frequency, f32, B, index, "frequency")
         if presence is not None:
-            pp = _row(presence, f32, B, "presence")
+            pp = _row(presence, f32, B, index, "presence")
     elif history_lens is not None or prompt_lens is not None or repetition is not None or frequency is not None or presence is not None:
         _raise(name, "penalties and lengths need a history")
     if bias is not None or bias_ids is not None or bias_offsets is not None:
         if bias is None or bias_ids is None or bias_offsets is None:
             _raise(name, "bias, bias_ids and bias_offsets go together")
         count = bias.numel()
-        bi, bo = _row(bias_ids, i32, count, "bias_ids"), _row(bias_offsets, i32, B + 1, "bias_offsets")
-        bp = _row(bias, f32, count, "bias")
+        bi, bo = _row(bias_ids, i32, count, index, "bias_ids"), _row(bias_offsets, i32, B + 1, index, "bias_offsets")
+        bp = _row(bias, f32, count, index, "bias")
         if count == 0:
             bo = bi = bp = 0
     if allowed is not None:
         if allowed.dim() != 2 or allowed.shape[0] != B or allowed.shape[1] < (V + 31) // 32:
             _raise(name, "allowed is [B, ceil(V / 32)]")
-        ap, stride = _matrix(allowed, i32, "allowed")
+        ap, stride = _matrix(allowed, i32, index, "allowed")
     if temperature is not None:
-        tp = _row(temperature, f32, B, "temperature")
+        tp = _row(temperature, f32, B, index, "temperature")
     got = {}
     op = os_ = 0
     if out is not None:
         if out.shape != logits.shape:
             _raise(name, "out and logits differ in shape")
         got["logits"] = out
-        op, os_ = _matrix(out, f32, "out")
+        op, os_ = _matrix(out, f32, index, "out")
     elif need_logits:
         out = got["logits"] = torch.empty((B, V), dtype=f32, device=device)
         op, os_ = out.data_ptr(), V
@@ -969,21 +972,21 @@ def _kv8_caches(n):
 
 
 def _pool(where, refs, table, kv_lens, block):
-    """(struct fl_kv8_pool, device, its current stream)"""
+    """(struct fl_kv8_pool, device, its index and current stream)"""
     i32 = _torch().int32
-    device, stream = _here(refs, where)
+    device, index, stream = _here(refs, where)
     if table.dim() != 2 or kv_lens.numel() != table.shape[0]:
         _raise(where, "table is [slots, max_blocks], kv_lens [slots]")
     slots, most = table.shape
-    return _KV8_POOL.pack(_ptr(refs, i32, "refs"), _ptr(table, i32, "table"), _ptr(kv_lens, i32, "kv_lens"), refs.numel(),
-                          slots, most, block), device, stream
+    return _KV8_POOL.pack(_row(refs, i32, None, index, "refs"), _row(table, i32, None, index, "table"),
+                          _row(kv_lens, i32, None, index, "kv_lens"), refs.numel(), slots, most, block), device, index, stream
 
 
 def _status_block(where, status, device, stream):
     if status is None:
         return _space(None, 256, device, stream)[1]
-    if status.numel() * status.element_size() < 16:
-        _raise(where, "the status block has 16 bytes")
+    if status.numel() * status.element_size() < 16 or status.get_device() != device.index:
+        _raise(where, f"the status block has 16 bytes on {device}")
     return _p(status)
 
 
@@ -993,10 +996,10 @@ def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None)
     page; table int32 [slots, max_blocks], kv_lens int32 [slots]: those of
     fl_kv8_append and fl_kv8_attention; block: tokens of a page.  All three are
     updated.  status: as for fl_kv8_append."""
-    pool, device, stream = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
+    pool, device, index, stream = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
     n = seqs.numel()
     _check("fl_kv8_pages_free", lib().fl_kv8_pages_free(
-        pool, _row(seqs, _TORCH.int32, n, "seqs"), _row(keep, _TORCH.int32, n, "keep") if keep is not None else None, n,
+        pool, _row(seqs, _TORCH.int32, n, index, "seqs"), _row(keep, _TORCH.int32, n, index, "keep") if keep is not None else None, n,
         _status_block("fl_kv8_pages_free", status, device, stream), stream))
 
 
@@ -1005,10 +1008,10 @@ def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=Non
     of slot parents[i] (int32 lists; the rest as in fl_kv8_pages_free).  A child
     that is not empty, that the list names again or that is a parent in it is left
     out, and the status block says so."""
-    pool, device, stream = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
+    pool, device, index, stream = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
     n = parents.numel()
     _check("fl_kv8_pages_fork", lib().fl_kv8_pages_fork(
-        pool, _row(parents, _TORCH.int32, n, "parents"), _row(children, _TORCH.int32, n, "children"), n,
+        pool, _row(parents, _TORCH.int32, n, index, "parents"), _row(children, _TORCH.int32, n, index, "children"), n,
         _status_block("fl_kv8_pages_fork", status, device, stream), stream))
 
 
@@ -1035,14 +1038,14 @@ def fl_kv8_pages_alloc(refs, table, kv_lens, seqs, new_tokens, block, ws=None):
     again, or whose table is too short, is left out, and the status block at the
     start of ws says so.  ws: as for fl_int8_linear."""
     torch = _torch()
-    pool, device, stream = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
+    pool, device, index, stream = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
     n = seqs.numel()
     granted = torch.empty((n,), dtype=torch.int32, device=device)
     pairs = torch.empty((n, 2), dtype=torch.int32, device=device)
     count = torch.empty((1,), dtype=torch.int32, device=device)
     ws, wsp, wsn = _space(ws, _pages_workspace(refs.numel(), *table.shape, block), device, stream)
     _check("fl_kv8_pages_alloc", lib().fl_kv8_pages_alloc(
-        pool, _row(seqs, torch.int32, n, "seqs"), _row(new_tokens, torch.int32, n, "new_tokens"), n,
+        pool, _row(seqs, torch.int32, n, index, "seqs"), _row(new_tokens, torch.int32, n, index, "new_tokens"), n,
         granted.data_ptr() or None, pairs.data_ptr() or None, count.data_ptr(), wsp, wsn, stream))
     return granted, pairs, count
 
@@ -1054,7 +1057,7 @@ def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None
     False new ones), the copies for fl_kv8_pages_copy, and int32 [blocks] where each
     page is now, -1 for free ones."""
     torch = _torch()
-    pool, device, stream = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
+    pool, device, index, stream = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
     blocks = refs.numel()
     if not in_place:
         table, refs = torch.empty_like(table), torch.empty_like(refs)
@@ -1079,16 +1082,17 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
     if len(shape) != 4:
         _raise(where, "the caches are [blocks, kv_heads, block, head_dim]")
     nb, heads, block, dim = shape
-    device, stream = _here(k_caches[0], where)
+    device, index, stream = _here(k_caches[0], where)
     u8, f32, i32 = torch.uint8, torch.float32, torch.int32
     flat, scales = [], shape[:2]
     for k, v, a, b in zip(k_caches, v_caches, k_scales, v_scales):
         if k.shape != shape or v.shape != shape or a.shape != scales or b.shape != scales:
             _raise(where, "the caches are [blocks, kv_heads, block, head_dim], their scales [blocks, kv_heads]")
-        if not (k.dtype is u8 and v.dtype is u8 and a.dtype is f32 and b.dtype is f32 and k.is_cuda and v.is_cuda and a.is_cuda
-                and b.is_cuda and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()):
-            _raise(where, "expected contiguous CUDA tensors, caches of uint8 and scales of float32")
+        if not (k.dtype is u8 and v.dtype is u8 and a.dtype is f32 and b.dtype is f32
+                and k.get_device() == v.get_device() == a.get_device() == b.get_device() == index
+                and k.is_contiguous() and v.is_contiguous() and a.is_contiguous() and b.is_contiguous()):
+            _raise(where, f"expected contiguous tensors on {device}, caches of uint8 and scales of float32")
         flat += (k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), nb, block, heads, dim, 0)
     n = pairs.numel() // 2
-    _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, "pairs"),
-                                          _row(count, i32, 1, "count"), n, _status_block(where, status, device, stream), stream))
+    _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, index, "pairs"),
+                                          _row(count, i32, 1, index, "count"), n, _status_block(where, status, device, stream), stream))

@@ -241,3 +241,98 @@ def test_quantize_refuses_outputs_that_meet(L):
     assert call(s=at) == 1 and call(s=at + 508) == 1 and call(s=at - 12) == 1 and call(s=far) == 1 and call(s=far + 252) == 1
     if not torch.cuda.is_available():
         assert _runs(call()) and _runs(call(c=at + 512)) and _runs(call(c=at - 256)) and _runs(call(s=far + 256)) and _runs(call(s=far - 16))
+
+
+# --------------------------------------------------------------- devices
+
+class On:
+    """A tensor that says it lies on a CUDA device."""
+    is_cuda = True
+
+    def __init__(self, t, index=0):
+        self.t, self.index = t, index
+        self.device = torch.device("cuda", index)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.index
+
+    def __getitem__(self, i):
+        return On(self.t[i], self.index)
+
+
+def _empty(shape, dtype=None, device=None):
+    return On(torch.empty(shape, dtype=dtype))
+
+
+def _zeros(*shape, dtype=torch.int32):
+    return On(torch.zeros(shape, dtype=dtype))
+
+
+@pytest.fixture
+def gpu0(monkeypatch):
+    """The binding as on a machine with GPUs, of which 0 is the current one; returns the
+    library's calls, none of which runs."""
+    calls = []
+
+    def entry(name):
+        if name.endswith("_workspace"):
+            return lambda *a: 0
+        return lambda *a: calls.append(name) or 0
+    library = type("L", (), {"__getattr__": lambda self, name: entry(name)})()
+    state = {"capturing": False}
+    fake = types.SimpleNamespace(empty=_empty, empty_like=lambda t: On(torch.empty_like(t.t)),
+                                 zeros=lambda n, dtype=None, device=None: On(torch.zeros(n, dtype=dtype)),
+                                 _C=types.SimpleNamespace(_cuda_getDevice=lambda: 0, _cuda_getCurrentRawStream=lambda i: 77),
+                                 cuda=types.SimpleNamespace(is_current_stream_capturing=lambda: state["capturing"]),
+                                 **{n: getattr(torch, n) for n in ("int8", "uint8", "int32", "float32", "float64", "bfloat16")})
+    monkeypatch.setattr(fl, "_TORCH", fake)
+    monkeypatch.setattr(fl, "lib", lambda: library)
+    monkeypatch.setattr(fl, "_WS", {})
+    monkeypatch.setattr(fl, "_OUTGROWN", [])
+    return types.SimpleNamespace(calls=calls, state=state)
+
+
+def _calls():
+    """Every serving call with all of its tensors: (name, function, arguments)."""
+    f32, bf16, u8, i8 = torch.float32, torch.bfloat16, torch.uint8, torch.int8
+    ws = dict(ws=_zeros(4096, dtype=u8))
+    pool = dict(refs=_zeros(6), table=_zeros(3, 4), kv_lens=_zeros(3))
+    status = dict(status=_zeros(4))
+
+    def copy(**kw):
+        lists = [[kw.pop(f"{name}{i}") for i in range(2)] for name in ("k", "v", "a", "b")]
+        return fl.fl_kv8_pages_copy(*lists, **kw)
+    caches = {f"{name}{i}": _zeros(6, 1, 16, 64, dtype=u8) if name in "kv" else _zeros(6, 1, dtype=f32) for i in range(2) for name in "kvab"}
+    return [
+        ("quantize", fl.fl_int8_quantize, dict(x=_zeros(2, 32, dtype=bf16)), {}),
+        ("linear", fl.fl_int8_linear, dict(x=_zeros(2, 32, dtype=bf16), w=_zeros(4, 32, dtype=i8), w_scale=_zeros(4, dtype=f32),
+                                           y=_zeros(2, 4, dtype=bf16), **ws), {}),
+        ("linear", fl.fl_int8_linear, dict(x=_zeros(2, 32, dtype=i8), x_scale=_zeros(2, dtype=f32), w=_zeros(4, 32, dtype=i8),
+                                           w_scale=_zeros(4, dtype=f32)), {}),
+        ("logits", fl.fl_logits_process, dict(
+            logits=_zeros(2, 40, dtype=f32), history=_zeros(2, 8), history_lens=_zeros(2), prompt_lens=_zeros(2),
+            repetition=_zeros(2, dtype=f32), frequency=_zeros(2, dtype=f32), presence=_zeros(2, dtype=f32), bias_offsets=_zeros(3),
+            bias_ids=_zeros(5), bias=_zeros(5, dtype=f32), allowed=_zeros(2, 2), temperature=_zeros(2, dtype=f32),
+            out=_zeros(2, 40, dtype=f32), **ws), {}),
+        ("free", fl.fl_kv8_pages_free, dict(**pool, seqs=_zeros(2), keep=_zeros(2), **status), dict(block=16)),
+        ("fork", fl.fl_kv8_pages_fork, dict(**pool, parents=_zeros(2), children=_zeros(2), **status), dict(block=16)),
+        ("alloc", fl.fl_kv8_pages_alloc, dict(**pool, seqs=_zeros(2), new_tokens=_zeros(2), **ws), dict(block=16)),
+        ("compact", fl.fl_kv8_pages_compact, dict(**pool, **status), dict(block=16)),
+        ("copy", copy, dict(**caches, pairs=_zeros(2, 2), count=_zeros(1), **status), {}),
+    ]
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_tensors_of_another_device_are_refused(gpu0, which):
+    name, call, tensors, rest = _calls()[which]
+    call(**tensors, **rest)
+    assert len(gpu0.calls) == 1 and name in gpu0.calls[0]
+    for other, t in tensors.items():
+        with pytest.raises(ValueError):
+            call(**{**tensors, other: On(t.t, 1)}, **rest)
+    with pytest.raises(ValueError):
+        call(**{k: On(t.t, 1) for k, t in tensors.items()}, **rest)      # all on one that is not the current one
+    assert len(gpu0.calls) == 1
