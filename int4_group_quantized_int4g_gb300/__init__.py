@@ -983,11 +983,13 @@ def _pool(where, refs, table, kv_lens, block):
 
 
 def _status_block(where, status, device, stream):
+    """The caller's status block or that of this thread's workspace (to be held until
+    the call), and its address."""
     if status is None:
-        return _space(None, 256, device, stream)[1]
+        return _space(None, 256, device, stream)[:2]
     if status.numel() * status.element_size() < 16 or status.get_device() != device.index:
         _raise(where, f"the status block has 16 bytes on {device}")
-    return _p(status)
+    return status, _p(status)
 
 
 def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None):
@@ -995,24 +997,28 @@ def fl_kv8_pages_free(refs, table, kv_lens, seqs, block, keep=None, status=None)
     gives their other pages back.  refs int32 [blocks]: the holders of each
     page; table int32 [slots, max_blocks], kv_lens int32 [slots]: those of
     fl_kv8_append and fl_kv8_attention; block: tokens of a page.  All three are
-    updated.  status: as for fl_kv8_append."""
+    updated.  A slot or page that is not there is left out; only the status block says
+    so.  status: the status block (an int32 or uint8 CUDA tensor of 16 bytes, zero-filled
+    before its first use, or a workspace), for fl_int4g_status; None: one that cannot
+    be read, so that nothing tells of what was left out."""
     pool, device, index, stream = _pool("fl_kv8_pages_free", refs, table, kv_lens, block)
     n = seqs.numel()
+    status, sp = _status_block("fl_kv8_pages_free", status, device, stream)
     _check("fl_kv8_pages_free", lib().fl_kv8_pages_free(
         pool, _row(seqs, _TORCH.int32, n, index, "seqs"), _row(keep, _TORCH.int32, n, index, "keep") if keep is not None else None, n,
-        _status_block("fl_kv8_pages_free", status, device, stream), stream))
+        sp, stream))
 
 
 def fl_kv8_pages_fork(refs, table, kv_lens, parents, children, block, status=None):
     """Slot children[i], which is empty, becomes a sequence that shares all pages
     of slot parents[i] (int32 lists; the rest as in fl_kv8_pages_free).  A child
     that is not empty, that the list names again or that is a parent in it is left
-    out, and the status block says so."""
+    out, and only the status block says so (status: as for fl_kv8_pages_free)."""
     pool, device, index, stream = _pool("fl_kv8_pages_fork", refs, table, kv_lens, block)
     n = parents.numel()
+    status, sp = _status_block("fl_kv8_pages_fork", status, device, stream)
     _check("fl_kv8_pages_fork", lib().fl_kv8_pages_fork(
-        pool, _row(parents, _TORCH.int32, n, index, "parents"), _row(children, _TORCH.int32, n, index, "children"), n,
-        _status_block("fl_kv8_pages_fork", status, device, stream), stream))
+        pool, _row(parents, _TORCH.int32, n, index, "parents"), _row(children, _TORCH.int32, n, index, "children"), n, sp, stream))
 
 
 def fl_kv8_pages_workspace(num_blocks, slots, max_blocks, block):
@@ -1035,8 +1041,8 @@ def fl_kv8_pages_alloc(refs, table, kv_lens, seqs, new_tokens, block, ws=None):
     which the free pages do not suffice; pairs int32 [n, 2] and count int32 [1],
     the pages that fl_kv8_pages_copy has to copy before the new tokens are written:
     pages that others hold too are not written into.  A slot that the list names
-    again, or whose table is too short, is left out, and the status block at the
-    start of ws says so.  ws: as for fl_int8_linear."""
+    again, or whose table is too short, is left out: granted is 0, and the status block
+    at the start of ws says so.  ws: as for fl_int8_linear."""
     torch = _torch()
     pool, device, index, stream = _pool("fl_kv8_pages_alloc", refs, table, kv_lens, block)
     n = seqs.numel()
@@ -1055,7 +1061,8 @@ def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None
     goes to the k-th free page before.  Returns (table, refs, pairs, count, moved): the
     table and counts after the moves (the given ones, updated, or with in_place
     False new ones), the copies for fl_kv8_pages_copy, and int32 [blocks] where each
-    page is now, -1 for free ones."""
+    page is now, -1 for free ones.  A table's entry that names no page in use becomes
+    -1, and the status block says so (status: as for fl_kv8_pages_free)."""
     torch = _torch()
     pool, device, index, stream = _pool("fl_kv8_pages_compact", refs, table, kv_lens, block)
     blocks = refs.numel()
@@ -1064,16 +1071,17 @@ def fl_kv8_pages_compact(refs, table, kv_lens, block, in_place=True, status=None
     pairs = torch.empty((blocks // 2, 2), dtype=torch.int32, device=device)
     count = torch.empty((1,), dtype=torch.int32, device=device)
     moved = torch.empty((blocks,), dtype=torch.int32, device=device)
+    status, sp = _status_block("fl_kv8_pages_compact", status, device, stream)
     _check("fl_kv8_pages_compact", lib().fl_kv8_pages_compact(
-        pool, table.data_ptr(), refs.data_ptr(), moved.data_ptr(), pairs.data_ptr() or None, count.data_ptr(),
-        _status_block("fl_kv8_pages_compact", status, device, stream), stream))
+        pool, table.data_ptr(), refs.data_ptr(), moved.data_ptr(), pairs.data_ptr() or None, count.data_ptr(), sp, stream))
     return table, refs, pairs, count, moved
 
 
 def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, status=None):
     """Copies the pages pairs[i] = (from, to), i < count[0] (int32 [n, 2], [1]; at
     most n), in every layer's cache: lists of the tensors of fl_kv8_append, all of
-    one shape."""
+    one shape.  A pair that names no page is left out, and only the status block says
+    so (status: as for fl_kv8_pages_free)."""
     torch = _torch()
     where, layers = "fl_kv8_pages_copy", len(k_caches)
     if layers < 1 or len(v_caches) != layers or len(k_scales) != layers or len(v_scales) != layers:
@@ -1094,5 +1102,6 @@ def fl_kv8_pages_copy(k_caches, v_caches, k_scales, v_scales, pairs, count, stat
             _raise(where, f"expected contiguous tensors on {device}, caches of uint8 and scales of float32")
         flat += (k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), nb, block, heads, dim, 0)
     n = pairs.numel() // 2
+    status, sp = _status_block(where, status, device, stream)
     _check(where, lib().fl_kv8_pages_copy(_kv8_caches(layers).pack(*flat), layers, _row(pairs, i32, 2 * n, index, "pairs"),
-                                          _row(count, i32, 1, index, "count"), n, _status_block(where, status, device, stream), stream))
+                                          _row(count, i32, 1, index, "count"), n, sp, stream))

@@ -3,6 +3,7 @@ tensors of other devices, outputs over inputs, pools that are full.  No GPU."""
 import ctypes
 import threading
 import types
+import weakref
 
 import pytest
 import torch
@@ -336,3 +337,25 @@ def test_tensors_of_another_device_are_refused(gpu0, which):
     with pytest.raises(ValueError):
         call(**{k: On(t.t, 1) for k, t in tensors.items()}, **rest)      # all on one that is not the current one
     assert len(gpu0.calls) == 1
+
+
+# ---------------------------------------------------------- status blocks
+
+@pytest.mark.parametrize("which", [4, 5, 7, 8])
+def test_status_blocks_of_captured_calls_live_until_the_launch(gpu0, monkeypatch, which):
+    """Without a status block a captured call makes one; it is not given back before
+    the library has it."""
+    made, alive = [], []
+    name, call, tensors, rest = _calls()[which]
+    zeros = fl._TORCH.zeros
+
+    def noted(*a, **kw):
+        t = zeros(*a, **kw)
+        made.append(weakref.ref(t))
+        return t
+    fl._TORCH.zeros = noted
+    library = type("L", (), {"__getattr__": lambda self, n: lambda *a: alive.append([r() is not None for r in made]) or 0})()
+    monkeypatch.setattr(fl, "lib", lambda: library)
+    gpu0.state["capturing"] = True
+    call(**{**tensors, "status": None}, **rest)
+    assert alive == [[True]]
