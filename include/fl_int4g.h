@@ -590,10 +590,13 @@ int fl_int8_linear_workspace(int M, int N, int K, size_t* out);
  *            FL_OUT_FP32.  y may not lie over an input: FL_ERR_ARG, where rows
  *            meet or, with strides of x and y that differ in bytes, ranges
  * K % 16 == 0, M, N >= 1.  Products and sums are those of the codes: f16
- * operands hold them exactly, sums are fp32 (exact while they stay below
- * 2^24), partial sums of a split K are added in a fixed order, so results do
- * not depend on timing.  M <= 16 streams the weights through mma.sync, larger
- * M runs on tcgen05.  A row whose scale is NaN gives NaN. */
+ * operands hold them exactly, sums are fp32, exact while all parts of them stay
+ * below 2^24 (with codes of any sign and size: up to K = 1024).  Larger ones
+ * round as they grow, and a partial sum of K ends where M, N, K and the SMs put
+ * it: the same call always gives the same bits (parts are added in a fixed
+ * order), but such a row may differ by roundings from the same row in another
+ * batch.  M <= 16 streams the weights through mma.sync, larger M runs on
+ * tcgen05.  A row whose scale is NaN gives NaN. */
 int fl_int8_linear(const void* x, int64_t x_stride, const float* x_scale, int M, int K, const int8_t* w,
                    const float* w_scale, int N, void* y, int64_t y_stride, int y_type, void* ws, size_t ws_bytes,
                    fl_stream_t stream);

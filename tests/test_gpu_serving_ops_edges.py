@@ -71,3 +71,42 @@ def test_continuations_without_room_wait_for_it(captured):
     assert torch.equal(gen.history[1:, 70], token[1:])
     assert all(np.array_equal(_values(gen, i, s)[:, :, :64], held[s][i][:, :, :64]) for i in range(2) for s in (1, 2))
     assert fl.fl_int4g_status(ws) == 0
+
+
+# ------------------------------------------------------------------ linear
+
+def _in_batches(x, w, t):
+    """The first row's product, alone and in batches whose sums are divided otherwise."""
+    return [fl.fl_int8_linear(x[:M], w, t, out_dtype=torch.float32)[0].double().cpu().numpy() for M in (1, 8, 16, 17, 64, 300, 1000)]
+
+
+def test_a_row_is_the_same_in_every_batch_while_sums_are_below_2_24():
+    """1040 products of 127 and 127, of one sign: 16.774e6 of 2^24 = 16.777e6."""
+    x = torch.full((1000, 1040), 3.0, dtype=torch.bfloat16, device=DEV)
+    w = torch.full((300, 1040), 127, dtype=torch.int8, device=DEV)
+    w[1::2] = -127
+    w[5] = torch.arange(1040, device=DEV) % 255 - 127
+    t = torch.linspace(0.5, 2.0, 300, device=DEV) * 1e-3
+    got = _in_batches(x, w, t)
+    assert all(np.array_equal(g, got[0]) for g in got)
+
+
+@pytest.mark.parametrize("K", [8192, 16384])
+def test_a_row_in_batches_past_2_24(K):
+    """Sums of 15e6, below 2^24, and of 30e6.  Past 2^24 a sum is rounded, where
+    depends on the batch: each of the K / 16 steps and of joining the parts by at
+    most a step, 2^-23 of it, on either side, and both results by three roundings to
+    fp32 more."""
+    rng = np.random.default_rng(5)
+    x = torch.from_numpy(np.abs(rng.standard_normal((1000, K))).astype(np.float32)).to(torch.bfloat16).to(DEV)
+    w = torch.from_numpy(rng.integers(0, 128, (300, K)).astype(np.int8)).to(DEV)
+    t = torch.from_numpy((np.exp(0.3 * rng.standard_normal(300)) * 1e-3).astype(np.float32)).to(DEV)
+    q, s = O.quantize8(x[:1].double().cpu().numpy())
+    dot, scale = O.linear8(q, s, w.cpu().numpy(), t.double().cpu().numpy())
+    assert dot.max() < 2 ** 24 if K == 8192 else dot.min() > 2 ** 24
+    ref = (dot * scale)[0]
+    step = ref * ((K / 16 + 20) * 2.0 ** -23 + 3 * 2.0 ** -24)
+    got = _in_batches(x, w, t)
+    for g, again in zip(got, _in_batches(x, w, t)):
+        assert np.array_equal(g, again) and (K == 16384 or np.array_equal(g, got[0]))
+        assert np.all(np.abs(g - ref) <= step) and np.all(np.abs(g - got[0]) <= 2 * step)
