@@ -75,7 +75,7 @@ struct Params {
   float* part;       // [pair][2][rank] slots of [column][row]
   int32_t* cnt;      // [pair][rank]
   int32_t* status;
-  int M, N, fp32, tma_y;
+  int M, N, tma_y;
   int BN, G, mtiles, ntiles;
   int xring, wshift, woff;   // token stages, log2 of the weight stages and where these lie
   int P, waves;      // pairs, whole tiles of each
@@ -721,7 +721,7 @@ int gemm_launch(const Call& c, cudaStream_t s) {
   if (!enc) return FL_ERR_CUDA;
   Params p = {};
   p.x_scale = c.x_scale, p.w_scale = c.w_scale, p.y = c.y, p.y_stride = c.y_stride;
-  p.part = c.part, p.cnt = c.cnt, p.status = c.status, p.M = c.M, p.N = c.N, p.fp32 = c.fp32;
+  p.part = c.part, p.cnt = c.cnt, p.status = c.status, p.M = c.M, p.N = c.N;
   const int pairs = gemm_pairs();
   const Plan a = pairs ? gemm_plan(c.M, c.N, c.K, pairs) : Plan{};
   if (!a.BN || a.mtiles * a.ntiles > 0x7fffffffll / kGroupM || a.units > 0x7fffffffll / (pairs + 1)) return FL_ERR_UNSUPPORTED;

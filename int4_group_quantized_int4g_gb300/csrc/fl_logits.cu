@@ -71,11 +71,12 @@ struct LogitsParams {
   int sorted_stride, shift;   // run is 1 << shift
 };
 
-__device__ __forceinline__ float exp_of(float d) {   // exp(d), d <= 0
+__device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * 1.44269504f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp_of(float d) { return ex2(d * 1.44269504f); }   // exp(d), d <= 0, relative to within |d| 2^-24 + 2^-22
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -96,11 +97,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {   // (a NaN l
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // A maximum, the first index that has it, and the sum of exp(x - maximum) of all others:
