@@ -75,11 +75,13 @@ struct Params {
   float* part;       // [pair][2][rank] slots of [column][row]
   int32_t* cnt;      // [pair][rank]
   int32_t* status;
-  int M, N, tma_y;
+  // (in pairs of 8 bytes that are used together: with `whole` last, which shifts them by
+  // one, 301 x 11008 x 4096 31.1 us, not 30.5)
+  int M, N;
+  int whole, tma_y;  // whether the rest's tiles are taken whole, one by each of the first pairs
   int BN, G, mtiles, ntiles;
   int xring, wshift, woff;   // token stages, log2 of the weight stages and where these lie
-  int P, waves;      // pairs, whole tiles of each
-  int U, whole;      // units of the rest; whether its tiles are taken whole, one by each of the first pairs
+  int P, waves, U;   // pairs, whole tiles of each, units of the rest
 };
 
 __device__ __forceinline__ int unit_begin(int c, int U, int P) { return static_cast<int>(static_cast<long long>(c) * U / P); }
