@@ -577,8 +577,8 @@ int fl_int8_quantize(const void* x, int64_t x_stride, int M, int K, int8_t* code
 int fl_int8_linear_workspace(int M, int N, int K, size_t* out);
 
 /* The linear layer with weights and tokens in 8-bit integers, a scale for each
- * output channel and one for each token (fastllm's --dtype int8; the layers
- * that do not stand 4 bits, the head above all):
+ * output channel and one for each token, without zero points (for layers that
+ * do not stand 4 bits, the head above all):
  *   y[m, n] = (sum_k q[m, k] * w[n, k]) * (s[m] * w_scale[n])
  *   x        x_scale NULL: bf16 [M, K], rounded to codes q and scales s as
  *            fl_int8_quantize does, within the call;
@@ -616,7 +616,8 @@ int fl_int8_test_plan(int M, int N, int K, int sms, long long* out);
  *                answer, history_lens int32 [B] of them, the first prompt_lens
  *                int32 [B] (NULL: none) being the prompt.  Lengths are cut to
  *                0 .. history_max, and tokens outside the vocabulary (a padding
- *                of -1) count for nothing
+ *                of -1) count for nothing.  The kernel is chosen by history_max:
+ *                a bound near the lengths is faster than one far above
  *   repetition   fp32: of a token seen in prompt or answer, l > 0 becomes l / r,
  *                any other l * r
  *   frequency, presence  fp32: a token that stands c > 0 times in the answer

@@ -888,7 +888,8 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     history int32 [B, longest], of which history_lens [B] count, the first
     prompt_lens [B] the prompt: repetition [B] divides (or, not above 0,
     multiplies) tokens of either, frequency [B] times the count and presence [B]
-    are taken off tokens of the answer.  bias_offsets int32 [B + 1], bias_ids
+    are taken off tokens of the answer.  (The kernel is chosen by `longest`: a view that
+    ends near the lengths, history[:, :n], is faster than a much wider one.)  bias_offsets int32 [B + 1], bias_ids
     int32, bias: what row b adds to which tokens.  temperature [B] divides.  allowed
     int32 [B, ceil(V / 32)]: tokens without a bit become -inf.  Any may be left out.
     Returns a dict: "logits" (fp32 [B, V], unless need_logits is False; `out` if

@@ -8,8 +8,10 @@
 // the order in which mma.sync lanes read them.  A code is the nearest whole
 // number to the quotient itself: fp32's a * (127 / top) is within 2^-15 of it, and
 // next to a border the sign of 2a - (2k + 1) scale decides, which one fma gives
-// without a rounding that could hide it.  Bound by HBM: 2 + 1 (or 2) bytes an
-// element (2048 x 4096 12 us from cold caches, 50 MB), small ones by latency (3 us).
+// without a rounding that could hide it.  Large ones are bound by instructions, 19 an
+// element: 8190 x 4096 to int8 27 us in a chain, where the bytes (2 + 1 an element)
+// take 15; a scheduler issues in 0.70 of the cycles.  2048 x 4096 takes 10 us (bytes 3.8),
+// small ones are bound by latency (1 x 4096 1.6 us, 301 x 4096 3.2).
 #include "fl_int8.cuh"
 
 using namespace fl8;

@@ -9,15 +9,16 @@
 // puts it on a list.  Every CTA of a row reads all of its history, out of L2, and
 // keeps what falls into its run; where that is much, a kernel before puts the history in
 // the order of the runs, while the logits are already on their way (512 rows of 128003
-// with 2000 entries 107 us, not 117, with 7000 104 and 157, with 16000 120 and 255).  Then
+// with 2000 entries 108 us, not 116, with 7000 112 and 166, with 16000 127 and 277).  Then
 // the listed tokens, and those that a bias names, are changed in shared memory, a thread
 // a token: one in a hundred has a penalty, but two of three warps meet one, so doing it
-// on the way through the run cost 80 instructions a logit (512 rows of 128003: 261 us).
+// on the way through the run cost 80 instructions a logit (512 rows of 128003: 261 us, and
+// 161 with this change alone).
 // Last the run passes through registers once: temperature, mask, the store, and a
 // running maximum and sum of exp (x - max) a thread.  The runs' results are joined in
 // their order, by the row's last CTA, or, with many CTAs, by a kernel of its own: a CTA
-// that takes a ticket waits until its stores are seen (512 rows of 128003 117 us, not 125;
-// of few CTAs the second launch would cost the host more).  Every step of the rules is
+// that takes a ticket waits until its stores are seen (512 rows of 128003, unsorted, 116
+// us, not 125; of few CTAs the second launch would cost the host more).  Every step of the rules is
 // one fp32 rounding, so that equal logits stay equal and ties are the formula's.  Bound
 // by HBM, the logits in and fp32 out, where there is little to look up (512 rows of 128003
 // without rules 82 us, 6.4 TB/s), else by instructions: with histories of 1000 to 2000
@@ -37,13 +38,20 @@ constexpr int kThreads = 256;                  // with short histories
 constexpr int kJoinThreads = 64;
 // A history of 1024 to 23040 entries (48 KB and counts of 16 bits hold them) is sorted by
 // run where a row's CTAs, kApart an SM or more, would read 65536 entries an SM otherwise:
-// there that is as much as the third launch costs the host.
+// there that is as much as the third launch costs the host.  512 rows of 128003 with 500
+// entries 104 us unsorted, 105 sorted, with 1000 108 and 107, with 2000 116 and 108; 128
+// rows with 1000 33 and 34, with 2000 36 and 34.  Fewer rows would gain in a captured
+// graph alone: 48 rows with 4000 20 and 18 us of kernels, but 22 and 25 a call; 48 of
+// 151655 with 4100, a grammar and biases 24 and 21, but 24 and 30.
 constexpr int kSortThreads = 512;              // as many runs at most are sorted by
 constexpr int kSortLeast = 1024, kSortMost = 23040;
 constexpr long long kSortWork = 65536;
 constexpr int kSortRows = 8192;                // rows of a launch then,
 constexpr int kSortRoom = 1 << 23;             // and entries of all of them
-constexpr int kApart = 16;                     // CTAs for each SM from which on a kernel of its own joins the runs
+// CTAs for each SM from which on a kernel of its own joins the runs: 64 rows of 128003
+// (2048 CTAs) 21.2 us without, 20.1 with it, but 23.0 and 25.6 a call; 100 rows 29.9 and
+// 28.6, and the same a call.
+constexpr int kApart = 16;
 constexpr int kRunBytes = 40960, kRunBytesLong = 81920;   // shared memory of a run, with short and long histories
 constexpr int kRunBytesRow = 61440;            // of one that is the whole row
 
@@ -602,10 +610,16 @@ bool aligned(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n =
 // Tokens of a run: the longest that fits its shared memory and still gives the
 // GPU CTAs enough; short ones where rows are few.  Each of a row's CTAs reads all of
 // its history: with a long one a CTA for two SMs is enough (12 rows of 32000 with 131000
-// entries: 20 us with 96 CTAs, 28 with 192, which L2 feeds no faster).  With short ones
-// five CTAs an SM are best (runs of 8192, three an SM: 512 rows of 128003 117 us, not 112),
-// but for a row that one run holds (2000 rows of 5000: 27 us, not 35 in two runs).
-constexpr int kLong = 8192;      // entries; from there on 1024 threads
+// entries: 19 us with 96 CTAs, 27 with 192, which L2 feeds no faster).  With short ones
+// five CTAs an SM are best (512 rows of 128003 108 us; runs of 8192, three an SM, 114; runs
+// of 2048 156), but for a row that one run holds (2000 rows of 5000: 24 us, in two runs 28).
+// From kLong entries on, by the width of the list, as the lengths are on the device: 1024
+// threads.  With as many entries 12 rows of 32000 take 8.2 us with 256 threads and 9.0 with
+// 1024 at 2000, 9.3 and 9.0 at 4100, 11.4 and 9.2 at 8192, 17.7 and 10.4 at 20000; 48 rows of
+// 128003 18.7 and 28.5 at 4100, 23.6 and 29.4 at 8192, 30.0 and 31.5 at 12000, 40.5 and 33.8 at
+// 20000.  A wide list with short lengths pays for that: 512 rows of 128003 with up to 2000
+// entries take 107 us in lists of up to 23040, 229 in wider ones; one row 7.5 and 8.5.
+constexpr int kLong = 8192;
 int run_length(int B, int V, bool bf16, bool history, bool biases, bool many) {
   const long long want = (many ? 1ll : 8ll) * flh::sm_count() / 2;
   auto most = [&](int run) { return many ? kRunBytesLong : run >= V ? kRunBytesRow : kRunBytes; };
