@@ -651,8 +651,8 @@ def fl_kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens
     whose lists name rows, or tokens past its table, that are not there is left
     out: nothing of it is written, and the status block says so.
     status: the status block to record device-side errors in (an int32 or uint8
-    CUDA tensor of 16 bytes or a workspace; None: this stream's workspace, whose
-    status nobody reads)."""
+    CUDA tensor of 16 bytes or a workspace; None: this thread's workspace of the
+    stream, whose status nobody reads)."""
     _torch()
     T, h, d = k.shape
     if v.shape != k.shape:
@@ -889,9 +889,10 @@ def fl_logits_process(logits, history=None, history_lens=None, prompt_lens=None,
     prompt_lens [B] the prompt: repetition [B] divides (or, not above 0,
     multiplies) tokens of either, frequency [B] times the count and presence [B]
     are taken off tokens of the answer.  (The kernel is chosen by `longest`: a view that
-    ends near the lengths, history[:, :n], is faster than a much wider one.)  bias_offsets int32 [B + 1], bias_ids
-    int32, bias: what row b adds to which tokens.  temperature [B] divides.  allowed
-    int32 [B, ceil(V / 32)]: tokens without a bit become -inf.  Any may be left out.
+    ends near the lengths, history[:, :n], is faster than a much wider one.)
+    bias_offsets int32 [B + 1], bias_ids int32, bias: what row b adds to which tokens.
+    temperature [B] divides.  allowed int32 [B, ceil(V / 32)]: tokens without a bit
+    become -inf.  Any may be left out.
     Returns a dict: "logits" (fp32 [B, V], unless need_logits is False; `out` if
     given, which may be fp32 logits themselves), "token" (int32 [B], the first of
     the largest, -1 where none is left), "lse" and "logprob" (fp32 [B]).

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(LONG ? 1024 : kThreads) k_logits(const LogitsP
     __syncthreads();
   }
   if (biases) {
-    // a token that is named again gets its biases in list order, from one thread
+    // a token that is named again gets its biases in list order, from one thread (which
+    // looks through all of the list: 48 rows of 128003 with 4000 biases 272 us, not 19)
     const bool several = again != 0;
     for (int i = several ? bias_lo : bias_lo + tid; i < bias_hi; i += several ? 1 : T) {
       const int id = __ldg(r.bias_ids + i);

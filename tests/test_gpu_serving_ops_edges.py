@@ -1,5 +1,7 @@
 """The serving operators and the example around them at the edges of their use, on
-the GPU: pools that are full, sums past 2^24."""
+the GPU: threads on one stream, pools that are full, sums past 2^24."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -110,3 +112,39 @@ def test_a_row_in_batches_past_2_24(K):
     for g, again in zip(got, _in_batches(x, w, t)):
         assert np.array_equal(g, again) and (K == 16384 or np.array_equal(g, got[0]))
         assert np.all(np.abs(g - ref) <= step) and np.all(np.abs(g - got[0]) <= 2 * step)
+
+
+# ----------------------------------------------------------------- threads
+
+def test_threads_on_one_stream():
+    """Calls of several launches from four threads at once, without workspaces of the
+    callers', give what they give one after another."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    w = torch.randint(-127, 128, (1000, 512), generator=g, device=DEV, dtype=torch.int8)
+    t = torch.rand(1000, generator=g, device=DEV)
+    xs = [torch.randn((m, 512), generator=g, device=DEV).to(torch.bfloat16) for m in (1, 9, 40, 150)]
+    rows = [torch.randn((m, 20011), generator=g, device=DEV) for m in (1, 5, 300, 600)]
+
+    def both(i):
+        got = fl.fl_logits_process(rows[i])
+        return [fl.fl_int8_linear(xs[i], w, t), got["logits"], got["token"], got["lse"]]
+    want = [both(i) for i in range(4)]
+    torch.cuda.synchronize()
+    barrier = threading.Barrier(4)
+    same, errors = [True] * 4, []
+
+    def run(i):
+        try:
+            torch.cuda.set_device(DEV)
+            barrier.wait()
+            for _ in range(100):
+                same[i] &= all(torch.equal(a, b) for a, b in zip(both(i), want[i]))
+        except Exception as e:       # noqa: BLE001 (told by the test)
+            errors.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors and all(same)
